@@ -363,6 +363,140 @@ gemm_status gemm_skinny_noalloc(int64_t M, int64_t N, int64_t K, int dtype_is_bf
                                 int out, float alpha, float beta, void *stream);
 
 /*
+ * Gated feed-forward block: with G = A * Bg^T and U = A * Bu^T (float32 sums),
+ *     D[i][j] = act(G[i][j]) * U[i][j],
+ * both products, the activation and the multiplication in one kernel that reads
+ * A once.  D is formed from the float32 sums and rounded once to `out`.
+ *
+ *  dtype_is_bf16  0: A, Bg, Bu are f16; 1: bf16.
+ *  A, lda         M x K, as in gemm_f16.
+ *  Bg, ldbg       N x K gate weights, as B in gemm_f16; Bu, ldbu the same (up weights).
+ *  G, ldg         NULL, or M x N in the operand type: receives G rounded to it, for
+ *                 gemm_gated_backward; ldg >= N, 2-byte aligned.  U, ldu the same.
+ *                 (With either kept, M <= 64 runs on the tile kernel.)
+ *  D, ldd, out    M x N, as in gemm_f16.
+ *  act            a gemm_act_t value.
+ *  M == 0 or N == 0: nothing is done.  K == 0: D = act(0) * 0 = 0 (G and U zero).
+ *  D, G and U must not overlap A, Bg, Bu or one another (GEMM_ERR_ALIAS).
+ *  Other errors, alignment and execution as gemm_f16.
+ *
+ * Activations: SILU g sigmoid(g); GELU g Phi(g) (with erf); GELU_TANH its tanh
+ * form; RELU max(g, 0); SIGMOID sigmoid(g).
+ */
+typedef enum {
+    GEMM_ACT_SILU = 0,
+    GEMM_ACT_GELU = 1,
+    GEMM_ACT_GELU_TANH = 2,
+    GEMM_ACT_RELU = 3,
+    GEMM_ACT_SIGMOID = 4
+} gemm_act_t;
+
+gemm_status gemm_gated(int64_t M, int64_t N, int64_t K, int dtype_is_bf16,
+                       const void *A, int64_t lda,
+                       const void *Bg, int64_t ldbg,
+                       const void *Bu, int64_t ldbu,
+                       void *G, int64_t ldg, void *U, int64_t ldu,
+                       void *D, int64_t ldd,
+                       int out, int act, void *stream);
+
+/*
+ * gemm_gated with all three operands FP4: A (M x K), Bg and Bu (N x K) as packed
+ * E2M1 codes with UE8M0 scales per 32 elements, as gemm_e2m1 takes them
+ * (GEMM_FP4_PACKED: codes 16-byte aligned with pitches that are multiples of
+ * 16; K a multiple of 32).  Scales that are not 16-byte aligned with a pitch
+ * that is a multiple of 16 are copied first, as there.  Other arguments as
+ * gemm_gated; no kept products.
+ */
+gemm_status gemm_gated_e2m1(int64_t M, int64_t N, int64_t K,
+                            const uint8_t *Aq, int64_t ldaq,
+                            const uint8_t *As, int64_t ldas,
+                            const uint8_t *Bgq, int64_t ldbgq,
+                            const uint8_t *Bgs, int64_t ldbgs,
+                            const uint8_t *Buq, int64_t ldbuq,
+                            const uint8_t *Bus, int64_t ldbus,
+                            void *D, int64_t ldd,
+                            int out, int act, void *stream);
+
+/*
+ * Gradients of gemm_gated.  From dD (the gradient of D) and the kept G and U,
+ * with all arithmetic in float32:
+ *     dG = dD * U * act'(G),  dU = dD * act(G)   (rounded to the operand type)
+ *     dA = dG * Bg + dU * Bu,  dBg = dG^T * A,  dBu = dU^T * A.
+ * dG and dU are operands of the tensor-core products, which take 16-bit
+ * operands, so the three products use them as rounded.
+ *
+ *  dtype_is_bf16  type of dD, G, U, A, Bg, Bu, dG and dU: 0 f16, 1 bf16.
+ *  dD, G, U       M x N, pitches >= N, 2-byte aligned.
+ *  A, lda         M x K, as in gemm_gated; may be NULL when dBg and dBu are.
+ *  Bg, Bu         N x K, as in gemm_gated; may be NULL when dA is.
+ *  dG, dU         M x N, caller-owned: 16-byte aligned, pitches >= N and
+ *                 multiples of 8.  dG may be G and dU may be U exactly (same
+ *                 pointer and pitch), which then hold the gradients.
+ *  dA, ldda       M x K of type `out`, or NULL (not wanted).
+ *  dBg, dBu       N x K of type `out`, both or neither NULL (not wanted).
+ *  M == 0: dBg = dBu = 0.  N == 0: dA = 0.  K == 0: only dG and dU.
+ *  Outputs must not overlap inputs or one another otherwise (GEMM_ERR_ALIAS).
+ *  relu'(0) is 0.  Other errors and execution as gemm_f16 (up to three kernels).
+ */
+gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf16,
+                                const void *dD, int64_t lddd,
+                                const void *G, int64_t ldg,
+                                const void *U, int64_t ldu,
+                                const void *A, int64_t lda,
+                                const void *Bg, int64_t ldbg,
+                                const void *Bu, int64_t ldbu,
+                                void *dG, int64_t lddg, void *dU, int64_t lddu,
+                                void *dA, int64_t ldda,
+                                void *dBg, int64_t lddbg, void *dBu, int64_t lddbu,
+                                int out, int act, void *stream);
+
+/*
+ * Operands in either storage: D = fma.rn(alpha, op(A) * op(B), beta * C), M x N,
+ * the sum over K.  trans_a == 0: A is stored M x K (as gemm_f16); 1: K x M.
+ * trans_b == 0: B is stored N x K (as gemm_f16); 1: K x N.  Both 0 is
+ * gemm_f16 / gemm_bf16 itself.  These are the products of a linear layer's
+ * backward pass: Y = X * W^T has dX = dY * W (trans_b) and dW = dY^T * X
+ * (trans_a and trans_b), read as they lie in memory.
+ *
+ *  A, lda    16-byte aligned, lda a multiple of 8 and >= the stored row length
+ *            (K, or M when trans_a); B, ldb the same (K, or N when trans_b).
+ *  Other arguments, errors and execution as gemm_f16 (dtype_is_bf16 as in
+ *  gemm_gated).
+ */
+gemm_status gemm_trans(int64_t M, int64_t N, int64_t K, int dtype_is_bf16,
+                       int trans_a, const void *A, int64_t lda,
+                       int trans_b, const void *B, int64_t ldb,
+                       const float *C, int64_t ldc,
+                       void *D, int64_t ldd,
+                       int out, float alpha, float beta, void *stream);
+
+/*
+ * Rows of X to FP4 as gemm_e2m1 and gemm_gated_e2m1 take them.  Per row and 32
+ * elements along K, with m = max |x|: the scale byte is
+ *     s = max(0, floor(log2(m)) - 2 + 127)   (a block of zeros: 0),
+ * and each code is x * 2^(127 - s) rounded to the nearest E2M1 value (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives; ties to the even code), magnitudes
+ * above 6 to 6.  A block that holds an infinity or a NaN gets s = 255 (NaN) and
+ * zero codes.  Every step is exact but the rounding to E2M1.
+ *
+ *  type      gemm_out_t of X (and Y): float32, bf16 or f16.
+ *  X, ldx    M x K, aligned to its element size (16-byte aligned with a pitch
+ *            that is a multiple of 16 bytes is read faster).
+ *  K         a multiple of 32 (GEMM_ERR_UNSUPPORTED otherwise).
+ *  Q, ldq    M rows of K/2 code bytes: 16-byte aligned, ldq >= K/2 and a
+ *            multiple of 16.
+ *  S, lds    K/32 rows of M scale bytes, lds >= M.
+ *  Y, ldy    NULL, or M x K of X's type: the values the codes and scales stand
+ *            for (exact in every type; NaN where s = 255).  Y may be X exactly.
+ *  Outputs must not overlap X (but for Y) or one another (GEMM_ERR_ALIAS).
+ */
+gemm_status gemm_quantize_e2m1(int64_t M, int64_t K, int type,
+                               const void *X, int64_t ldx,
+                               uint8_t *Q, int64_t ldq,
+                               uint8_t *S, int64_t lds,
+                               void *Y, int64_t ldy, void *stream);
+
+/*
  * Synchronises `stream`, then returns and clears the first error the device
  * recorded since the last call on the current device (GEMM_OK if none).
  * Returns GEMM_ERR_CUDA if the synchronisation itself failed.  After a
@@ -382,8 +516,12 @@ const char *gemm_status_string(int status);
  * (gemm_scatter_rows), 3 = seeded (gemm_seeded), 4 = FP4 weights
  * (gemm_bf16_e2m1), 5 = gemm_skinny_noalloc (kernel 0 where it returns
  * GEMM_ERR_UNSUPPORTED for the shape), 6 / 7 = gemm_e2m1 with packed codes /
- * the 16U4_ALIGN16B image; any other value is GEMM_ERR_INVALID_ARG.
- * has_c: C is given and beta != 0.
+ * the 16U4_ALIGN16B image, 16 = gemm_gated, 17 = gemm_gated_e2m1, 18 / 19 / 20 =
+ * gemm_trans with trans_a / trans_b / both; any other value is
+ * GEMM_ERR_INVALID_ARG.
+ * has_c: C is given and beta != 0 (gemm_gated: G or U is kept).
+ * Gated forms: bn counts accumulator columns, G's and U's; D's tile is bn / 2
+ * (kernels 2 and 15: 64) columns wide.
  *
  * With M <= 64 rows (bf16 / f16 B; not gathered, not seeded) the skinny
  * kernel runs where it measured faster than the tile kernel: M <= 16 with

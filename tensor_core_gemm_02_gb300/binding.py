@@ -59,6 +59,16 @@ def load_library(path: str = LIB_PATH):
                                    i32, f32, f32, vp]
     lib.gemm_e2m1.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
                               i32, f32, f32, i32, vp]
+    lib.gemm_gated.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                               i32, i32, vp]
+    lib.gemm_gated_e2m1.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                    vp, i64, i32, i32, vp]
+    lib.gemm_gated_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                        vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32,
+                                        vp]
+    lib.gemm_trans.argtypes = [i64, i64, i64, i32, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, f32,
+                               f32, vp]
+    lib.gemm_quantize_e2m1.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp]
     lib.gemm_seeded.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp]
     lib.gemm_accumulate.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, f32, vp]
     lib.gemm_scatter_rows.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64,
@@ -74,7 +84,8 @@ def load_library(path: str = LIB_PATH):
     lib.gemm_debug_force_tile.argtypes = [i32, i32]
     for name in ("gemm_f16", "gemm_bf16", "gemm_gather_rows", "gemm_scatter_rows", "gemm_accumulate",
                  "gemm_seeded", "gemm_bf16_e2m1", "gemm_e2m1",
-                 "gemm_skinny_noalloc",
+                 "gemm_gated", "gemm_gated_e2m1", "gemm_gated_backward", "gemm_trans",
+                 "gemm_quantize_e2m1", "gemm_skinny_noalloc",
                  "gemm_check_device_status",
                  "gemm_query_plan", "gemm_set_wait_timeout", "gemm_debug_inject",
                  "gemm_debug_force_tile"):
@@ -89,7 +100,9 @@ def gemm_status_string(status: int) -> str:
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object around it
+        # (2.8 us of every call's host time on a GB300's Grace cores)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -251,6 +264,171 @@ def gemm_e2m1(Aq, As, Bq, Bs, C=None, D=None, *, alpha=1.0, beta=1.0, out=OUT_F3
     return D
 
 
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = 0, 1, 2, 3, 4
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU,
+         "sigmoid": ACT_SIGMOID}
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)}")
+        return _ACTS[act]
+    return int(act)
+
+
+def _bf16_flag(name, dtype) -> int:
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is not torch.float16:
+        raise TypeError(f"{name} must be f16 or bf16")
+    return 0
+
+
+def _mat(name, t, rows, cols, dtype):
+    """(pointer, leading dimension) of a rows x cols matrix argument of that dtype."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {rows} x {cols}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), (ld if rows > 1 else max(ld, cols)) if cols else 0
+
+
+def _mat_or_null(name, t, rows, cols, dtype):
+    return (None, 0) if t is None else _mat(name, t, rows, cols, dtype)
+
+
+def _padded(rows, cols, dtype, device):
+    """An uninitialised matrix whose row pitch is a multiple of 16 bytes."""
+    per = 16 // dtype.itemsize
+    return torch.empty_strided((rows, cols), ((cols + per - 1) // per * per, 1), dtype=dtype, device=device)
+
+
+def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, stream=None):
+    """D = act(A @ Bg.T) * (A @ Bu.T) with f16 or bf16 A (M x K), Bg and Bu (N x K), in one
+    kernel.  act: an ACT_ value or its name ("silu", "gelu", "gelu_tanh", "relu", "sigmoid").
+    G, U: M x N tensors of A's dtype that receive the two products, for
+    gemm_gated_backward."""
+    dt = A.dtype
+    bf16 = _bf16_flag("A", dt)
+    M, K = A.shape
+    N = Bg.shape[0]
+    if D is None:
+        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+    st = load_library().gemm_gated(
+        M, N, K, bf16, *_mat("A", A, M, K, dt), *_mat("Bg", Bg, N, K, dt), *_mat("Bu", Bu, N, K, dt),
+        *_mat_or_null("G", G, M, N, dt), *_mat_or_null("U", U, M, N, dt),
+        *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act), _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_gated")
+    return D
+
+
+def gemm_gated_e2m1(Aq, As, Bgq, Bgs, Buq, Bus, D=None, *, act=ACT_SILU, out=OUT_F32, stream=None):
+    """gemm_gated with FP4 operands: packed E2M1 codes Aq (M x K/2), Bgq and Buq (N x K/2) and
+    UE8M0 block scales As (K/32 x M), Bgs and Bus (K/32 x N), as gemm_e2m1 takes them."""
+    M, half = Aq.shape
+    N = Bgq.shape[0]
+    blocks, u8 = half // 16, torch.uint8
+    if D is None:
+        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=Aq.device)
+    st = load_library().gemm_gated_e2m1(
+        M, N, 2 * half, *_mat("Aq", Aq, M, half, u8), *_mat("As", As, blocks, M, u8),
+        *_mat("Bgq", Bgq, N, half, u8), *_mat("Bgs", Bgs, blocks, N, u8), *_mat("Buq", Buq, N, half, u8),
+        *_mat("Bus", Bus, blocks, N, u8), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act),
+        _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_gated_e2m1")
+    return D
+
+
+def gemm_gated_backward(dD, G, U, A, Bg, Bu, *, dG=None, dU=None, dA=None, dBg=None, dBu=None,
+                        need_input=True, need_weights=True, act=ACT_SILU, out=OUT_F32, stream=None):
+    """Gradients of gemm_gated from dD and the products it kept (all of A's dtype):
+    dG = dD * U * act'(G) and dU = dD * act(G), rounded to that dtype, then
+    dA = dG @ Bg + dU @ Bu, dBg = dG.T @ A and dBu = dU.T @ A in `out`'s type.
+    dG may be G and dU may be U.  need_input / need_weights leave out dA / dBg
+    and dBu (then None).  Returns (dA, dBg, dBu, dG, dU)."""
+    dt, dev, ot = dD.dtype, dD.device, _DTYPE_OF_OUT[out]
+    bf16 = _bf16_flag("dD", dt)
+    M, N = dD.shape
+    K = A.shape[1] if need_weights else (Bg.shape[1] if need_input else 0)
+    null = (None, 0)
+    dG = _padded(M, N, dt, dev) if dG is None else dG
+    dU = _padded(M, N, dt, dev) if dU is None else dU
+    a = bg = bu = pa = pbg = pbu = null
+    if need_input:
+        bg, bu = _mat("Bg", Bg, N, K, dt), _mat("Bu", Bu, N, K, dt)
+        dA = torch.empty((M, K), dtype=ot, device=dev) if dA is None else dA
+        pa = _mat("dA", dA, M, K, ot)
+    else:
+        dA = None
+    if need_weights:
+        a = _mat("A", A, M, K, dt)
+        dBg = torch.empty((N, K), dtype=ot, device=dev) if dBg is None else dBg
+        dBu = torch.empty((N, K), dtype=ot, device=dev) if dBu is None else dBu
+        pbg, pbu = _mat("dBg", dBg, N, K, ot), _mat("dBu", dBu, N, K, ot)
+    else:
+        dBg = dBu = None
+    st = load_library().gemm_gated_backward(
+        M, N, K, bf16, *_mat("dD", dD, M, N, dt), *_mat("G", G, M, N, dt), *_mat("U", U, M, N, dt),
+        *a, *bg, *bu, *_mat("dG", dG, M, N, dt), *_mat("dU", dU, M, N, dt), *pa, *pbg, *pbu, out,
+        _act(act), _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_gated_backward")
+    return dA, dBg, dBu, dG, dU
+
+
+def gemm_trans(A, B, C=None, D=None, *, trans_a=False, trans_b=False, alpha=1.0, beta=1.0, out=OUT_F32,
+               stream=None):
+    """D = fma.rn(alpha, op(A) @ op(B), beta * C), f16 or bf16: A is M x K, or K x M with
+    trans_a; B is N x K, or K x N with trans_b (so trans_b alone is A @ B and both are
+    A.T @ B of the tensors as given)."""
+    dt = A.dtype
+    bf16 = _bf16_flag("A", dt)
+    ra, ca = A.shape
+    rb, cb = B.shape
+    K, M = (ra, ca) if trans_a else (ca, ra)
+    Kb, N = (rb, cb) if trans_b else (cb, rb)
+    if K != Kb:
+        raise ValueError("A and B disagree on K")
+    if D is None:
+        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+    st = load_library().gemm_trans(
+        M, N, K, bf16, 1 if trans_a else 0, *_mat("A", A, ra, ca, dt), 1 if trans_b else 0,
+        *_mat("B", B, rb, cb, dt), *_mat_or_null("C", C, M, N, torch.float32),
+        *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, alpha, beta, _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_trans")
+    return D
+
+
+def gemm_quantize_e2m1(X, Q=None, S=None, *, Y=None, stream=None):
+    """Rows of X (M x K float32, bf16 or f16, K a multiple of 32) to packed E2M1 codes Q
+    (M x K/2 uint8) and UE8M0 block scales S (K/32 x M uint8), as gemm_e2m1 and
+    gemm_gated_e2m1 take them.  Y, of X's shape and dtype, receives the values they
+    stand for (Y may be X).  Returns (Q, S)."""
+    dt, u8 = X.dtype, torch.uint8
+    kind = _OUT_OF_DTYPE.get(dt)
+    if kind is None:
+        raise TypeError("X must be float32, bfloat16 or float16")
+    M, K = X.shape
+    half, blocks = K // 2, K // 32
+    if Q is None:
+        Q = torch.empty((M, half), dtype=u8, device=X.device)
+    if S is None:
+        S = _padded(blocks, M, u8, X.device)
+    st = load_library().gemm_quantize_e2m1(
+        M, K, kind, *_mat("X", X, M, K, dt), *_mat("Q", Q, M, half, u8), *_mat("S", S, blocks, M, u8),
+        *_mat_or_null("Y", Y, M, K, dt), _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_quantize_e2m1")
+    return Q, S
+
+
 def gemm_seeded(A, B, C, D=None, *, out=OUT_F32, stream=None):
     """D = C + A @ B.T with C (float32 M x N) as the accumulator's starting value:
     every K step of the tensor-core sum accumulates onto it."""
@@ -321,12 +499,18 @@ def gemm_check_device_status(stream=None) -> int:
 
 
 def gemm_query_plan(M, N, K, gather=False, has_c=False, sm_count=148, scatter=False,
-                    seeded=False, fp4=False, noalloc=False, e2m1=None) -> Plan:
-    """e2m1: None, or FP4_PACKED / FP4_ALIGN16B for gemm_e2m1's plan."""
+                    seeded=False, fp4=False, noalloc=False, e2m1=None, gated=None, trans=None) -> Plan:
+    """e2m1: None, or FP4_PACKED / FP4_ALIGN16B for gemm_e2m1's plan; gated: "16" or "e2m1"
+    for gemm_gated's (has_c: a product is kept) or gemm_gated_e2m1's; trans: (trans_a,
+    trans_b), not both False, for gemm_trans's."""
     p = Plan()
     form = 1 if gather else (2 if scatter else (3 if seeded else (4 if fp4 else (5 if noalloc else 0))))
     if e2m1 is not None:
         form = 6 + int(e2m1)
+    if gated is not None:
+        form = {"16": 16, "e2m1": 17}[gated]
+    if trans is not None:
+        form = 17 + int(bool(trans[0])) + 2 * int(bool(trans[1]))
     _check(load_library().gemm_query_plan(M, N, K, form, int(bool(has_c)),
                                           sm_count, ctypes.byref(p)), "gemm_query_plan")
     return p

@@ -1,0 +1,85 @@
+// act.cuh -- the activations of the gated form and their slopes, in float32.
+//
+// sigmoid(x) = 1 / (1 + e^-x) with the fast exponential and division: e^-x
+// overflows to infinity for x below about -88, where the quotient is 0 as it
+// should be; __fdividef also returns 0 for denominators in 2^126 .. 2^128,
+// where the true quotient is below 2^-126.  Relative error a few units in
+// the last place, well below the rounding of the tensor-core sums that go in.
+#pragma once
+
+#include <stdint.h>
+
+namespace tcg {
+
+// (the values of gemm_act_t)
+enum : int32_t { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid = 4 };
+
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// gelu_tanh: 0.5 g (1 + tanh(y)) = g sigmoid(2 y), y = sqrt(2 / pi) (g + 0.044715 g^3)
+constexpr float kGeluTanh1 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluTanh3 = 0.07135481282720802f;  // 0.044715 of that
+constexpr float kSqrtHalf = 0.7071067811865476f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g)
+{
+    if (ACT == kActSilu)
+        return __fdividef(g, 1.f + __expf(-g));
+    if (ACT == kActGelu)
+        return 0.5f * g * (1.f + erff(g * kSqrtHalf));
+    if (ACT == kActGeluTanh)
+        return g * sigmoid_f32(g * (kGeluTanh1 + kGeluTanh3 * g * g));
+    if (ACT == kActRelu)
+        return g <= 0.f ? 0.f : g;  // (a NaN stays one)
+    return sigmoid_f32(g);
+}
+
+// act(g) and act'(g)
+template <int ACT>
+__device__ __forceinline__ void act_value_slope(float g, float &a, float &s)
+{
+    if (ACT == kActSilu) {
+        const float p = sigmoid_f32(g);
+        a = g * p;
+        s = p * (1.f + g * (1.f - p));
+    } else if (ACT == kActGelu) {
+        const float c = 0.5f * (1.f + erff(g * kSqrtHalf));
+        a = g * c;
+        s = c + g * kInvSqrt2Pi * __expf(-0.5f * g * g);
+    } else if (ACT == kActGeluTanh) {
+        const float p = sigmoid_f32(g * (kGeluTanh1 + kGeluTanh3 * g * g));
+        a = g * p;
+        // (past |g| = 30, p is 0 or 1 and the second term 0: keep g^3 finite there)
+        const float c = fminf(fmaxf(g, -30.f), 30.f);
+        s = p + c * p * (1.f - p) * (kGeluTanh1 + 3.f * kGeluTanh3 * c * c);
+    } else if (ACT == kActRelu) {
+        a = g <= 0.f ? 0.f : g;
+        s = g <= 0.f ? 0.f : (g > 0.f ? 1.f : g);
+    } else {
+        const float p = sigmoid_f32(g);
+        a = p;
+        s = p * (1.f - p);
+    }
+}
+
+// Call f with the activation as a compile-time constant (decltype(tag)::value).
+template <int ACT>
+struct ActTag {
+    static constexpr int value = ACT;
+};
+
+template <typename F>
+__device__ __forceinline__ void with_act(int32_t act, F f)
+{
+    switch (act) {
+    case kActSilu: f(ActTag<kActSilu>{}); break;
+    case kActGelu: f(ActTag<kActGelu>{}); break;
+    case kActGeluTanh: f(ActTag<kActGeluTanh>{}); break;
+    case kActRelu: f(ActTag<kActRelu>{}); break;
+    default: f(ActTag<kActSigmoid>{}); break;
+    }
+}
+
+}  // namespace tcg

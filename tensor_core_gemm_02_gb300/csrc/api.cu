@@ -341,11 +341,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // N = K = 4096, f32 out: 256 x 256 pairs 0.326 ms, 256 x 512 pairs 0.355 ms --
 // eight scatter4 issues per 32-column chunk make the epilogue long enough that
 // it must overlap the next tile's mainloop, which needs two accumulators.)
-struct TileChoice {
-    int kernel;  // 1 single, 3 pair 256, 4 pair 512
-    int bn;
-};
-
 TileChoice choose_tile(int64_t M, int64_t N, int64_t K, bool gather, bool c_used, bool scatter,
                        int sm_count)
 {
@@ -1104,8 +1099,20 @@ gemm_status gemm_query_plan(int64_t M, int64_t N, int64_t K, int form, int has_c
 {
     if (!plan || sm_count < 1 || M < 0 || N < 0 || K < 0)
         return GEMM_ERR_INVALID_ARG;
-    if (form < 0 || form > 7)
+    if (form < 0 || (form > 7 && form < 16) || form > 20)
         return GEMM_ERR_INVALID_ARG;
+    if (form == 16) {
+        *plan = gated_plan(M, N, K, has_c != 0, sm_count);
+        return GEMM_OK;
+    }
+    if (form == 17) {
+        *plan = gated_e2m1_plan(M, N, K, sm_count);
+        return GEMM_OK;
+    }
+    if (form >= 18) {
+        *plan = trans_plan(M, N, K, 1, has_c != 0, sm_count);
+        return GEMM_OK;
+    }
     if (form == 5) {
         *plan = noalloc_plan(M, N, K, has_c != 0, sm_count);
         return GEMM_OK;

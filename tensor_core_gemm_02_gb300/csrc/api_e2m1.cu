@@ -112,29 +112,6 @@ gemm_status validate_e2m1(const E2m1Problem &p, bool *empty)
     return GEMM_OK;
 }
 
-// Scales with an unaligned base or a pitch that is not a multiple of 16 bytes
-// are first copied into a padded per-stream buffer (TMA needs both).
-gemm_status tma_scales(const DeviceInfo *dev, cudaStream_t stream, int use, const uint8_t *s,
-                       int64_t ld, int64_t cols, int64_t rows, const uint8_t **out, int64_t *ld_out)
-{
-    if (aligned16(s) && ld % 16 == 0) {
-        *out = s;
-        *ld_out = ld;
-        return GEMM_OK;
-    }
-    const int64_t pitch = (cols + 15) / 16 * 16;
-    void *buf = nullptr;
-    gemm_status st = get_dequant_buffer(dev->index, stream, use, static_cast<size_t>(pitch) * rows, &buf);
-    if (st != GEMM_OK)
-        return st;
-    if (cudaMemcpy2DAsync(buf, pitch, s, ld, cols, rows, cudaMemcpyDeviceToDevice, stream) !=
-        cudaSuccess)
-        return GEMM_ERR_CUDA;
-    *out = static_cast<const uint8_t *>(buf);
-    *ld_out = pitch;
-    return GEMM_OK;
-}
-
 // Few rows of A, packed codes: the swap-AB stream-K skinny kernel with
 // block-scaled MMAs (128 rows of B on the MMA's M side, the padded rows of A on
 // its N side, the K blocks of all tiles shared out over the SMs).
@@ -288,6 +265,46 @@ gemm_status run_e2m1(const E2m1Problem &p)
 
 }  // namespace
 
+// Scales with an unaligned base or a pitch that is not a multiple of 16 bytes
+// are first copied into a padded per-stream buffer (TMA needs both).
+gemm_status tma_scales(const DeviceInfo *dev, cudaStream_t stream, int use, const uint8_t *s,
+                       int64_t ld, int64_t cols, int64_t rows, const uint8_t **out, int64_t *ld_out)
+{
+    if (aligned16(s) && ld % 16 == 0) {
+        *out = s;
+        *ld_out = ld;
+        return GEMM_OK;
+    }
+    const int64_t pitch = (cols + 15) / 16 * 16;
+    void *buf = nullptr;
+    gemm_status st = get_dequant_buffer(dev->index, stream, use, static_cast<size_t>(pitch) * rows, &buf);
+    if (st != GEMM_OK)
+        return st;
+    if (cudaMemcpy2DAsync(buf, pitch, s, ld, cols, rows, cudaMemcpyDeviceToDevice, stream) !=
+        cudaSuccess)
+        return GEMM_ERR_CUDA;
+    *out = static_cast<const uint8_t *>(buf);
+    *ld_out = pitch;
+    return GEMM_OK;
+}
+
+void set_e2m1_skinny_plan(gemm_plan &p, int64_t M, int64_t tiles, int64_t K, int sm_count)
+{
+    const int mp = skinny_rows(M);
+    const int64_t nkb = ceil_div(K, tcg::skinny_mx_kstage());
+    // at least kSkinnyMinBlocks K blocks (of 256 elements) per CTA
+    constexpr int64_t kSkinnyMinBlocks = 4;
+    const int64_t want = ceil_div(tiles * nkb, kSkinnyMinBlocks);
+    const int64_t G = want < sm_count ? want : sm_count;
+    p.kernel = 15;
+    p.bm = mp;
+    p.bn = 128;
+    p.stages = tcg::skinny_mx_stages(mp);
+    p.tiles = tiles;
+    p.splits = tcg::skinny_max_parts(tiles, nkb, G);
+    p.grid = static_cast<int32_t>(G);
+}
+
 // Forms: M <= 64 with packed codes: the skinny kernel (kernel 15).  Otherwise
 // CTA pairs with 256 x 256 tiles (each SM moves 2/3 of the operand bytes
 // per MMA that a single CTA with a 128 x 256 tile moves, which FP4 operands,
@@ -312,20 +329,7 @@ gemm_plan e2m1_plan(int64_t M, int64_t N, int64_t K, int image, int sm_count)
     // 64 x 1024^2 5.3 / 6.7.
     const bool skinny_ok = image == 0 && M <= 64 && K > 0;
     if (skinny_ok && (fk == 15 || !(fk >= 11 && fk <= 14))) {
-        const int mp = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
-        const int64_t tiles = ceil_div(N, 128);
-        const int64_t nkb = ceil_div(K, tcg::skinny_mx_kstage());
-        // at least kSkinnyMinBlocks K blocks (of 256 elements) per CTA
-        constexpr int64_t kSkinnyMinBlocks = 4;
-        const int64_t want = ceil_div(tiles * nkb, kSkinnyMinBlocks);
-        const int64_t G = want < sm_count ? want : sm_count;
-        p.kernel = 15;
-        p.bm = mp;
-        p.bn = 128;
-        p.stages = tcg::skinny_mx_stages(mp);
-        p.tiles = tiles;
-        p.splits = tcg::skinny_max_parts(tiles, nkb, G);
-        p.grid = static_cast<int32_t>(G);
+        set_e2m1_skinny_plan(p, M, ceil_div(N, 128), K, sm_count);
         return p;
     }
     const int mx = image == 0 ? 1 : 2;

@@ -1,0 +1,766 @@
+// api_gated.cu -- the gated feed-forward entry points: gemm_gated and
+// gemm_gated_e2m1 (both products, the activation and the product in one
+// kernel), gemm_gated_backward, gemm_trans (operands stored K x M / K x N, the
+// products of a backward pass) and gemm_quantize_e2m1 (include/tcgemm.h has
+// the contracts).  Checks run before any CUDA call, as everywhere.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstring>
+#include <initializer_list>
+
+#include "host_internal.h"
+
+namespace tcg {
+namespace host {
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int kGroupM = 16;  // block rows per tile-order group, as the plain forms
+
+struct Span {
+    const void *p;
+    uint64_t bytes;
+};
+
+// Whether any of the outputs overlaps an input or another output.
+bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (overlap(o->p, o->bytes, i.p, i.bytes))
+                return true;
+        for (const Span *q = o + 1; q != outs.end(); ++q)
+            if (overlap(o->p, o->bytes, q->p, q->bytes))
+                return true;
+    }
+    return false;
+}
+
+bool out_ok(int out) { return out == GEMM_OUT_F32 || out == GEMM_OUT_BF16 || out == GEMM_OUT_F16; }
+bool act_ok(int act) { return act >= GEMM_ACT_SILU && act <= GEMM_ACT_SIGMOID; }
+bool elem_aligned(const void *p, int size)
+{
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(size - 1)) == 0;
+}
+
+// A matrix argument: pointer, leading dimension, rows and columns of `esize`-byte
+// elements; `mma`: it is a TMA operand (16-byte base and pitch).
+struct Mat {
+    const void *p;
+    int64_t ld;
+    int64_t rows, cols;
+    int esize;
+    bool mma;
+};
+
+gemm_status check_mats(std::initializer_list<Mat> mats)
+{
+    for (const Mat &m : mats)
+        if (m.rows > 0 && m.cols > 0 && (!m.p || m.ld < m.cols))
+            return GEMM_ERR_INVALID_ARG;
+    for (const Mat &m : mats)
+        if (m.ld > kMaxDim)
+            return GEMM_ERR_UNSUPPORTED;
+    for (const Mat &m : mats)
+        if (m.rows > 0 && m.cols > 0 &&
+            (m.mma ? !aligned16(m.p) || (m.ld * m.esize) % 16 != 0 : !elem_aligned(m.p, m.esize)))
+            return GEMM_ERR_ALIGNMENT;
+    return GEMM_OK;
+}
+
+Span span_of(const Mat &m) { return Span{m.p, span_bytes(m.rows, m.cols, m.ld, m.esize)}; }
+
+CUtensorMapDataType out_type(int out)
+{
+    return out == GEMM_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                               : (out == GEMM_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+}
+
+// 32 x 32 boxes of an output matrix
+bool encode_out(CUtensorMap *m, const void *p, int out, int64_t rows, int64_t cols, int64_t ld)
+{
+    return encode_2d(m, out_type(out), p, cols, rows, ld * out_size(out), 32, 32,
+                     out == GEMM_OUT_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+bool out_tma(const void *p, int64_t ld, int out) { return aligned16(p) && (ld * out_size(out)) % 16 == 0; }
+
+// ---------------------------------------------------------------- gated form
+
+struct GatedProblem {
+    int64_t M, N, K;
+    bool bf16, fp4;
+    const void *A;
+    int64_t lda;
+    const void *Bg;
+    int64_t ldbg;
+    const void *Bu;
+    int64_t ldbu;
+    const uint8_t *As, *Bgs, *Bus;  // (fp4) block scales
+    int64_t ldas, ldbgs, ldbus;
+    void *G;
+    int64_t ldg;
+    void *U;
+    int64_t ldu;
+    void *D;
+    int64_t ldd;
+    int out, act;
+    cudaStream_t stream;
+};
+
+gemm_status validate_gated(const GatedProblem &p, bool *empty)
+{
+    *empty = false;
+    if (p.M < 0 || p.N < 0 || p.K < 0 || !out_ok(p.out) || !act_ok(p.act))
+        return GEMM_ERR_INVALID_ARG;
+    if (p.M > kMaxDim || p.N > kMaxDim || p.K > kMaxDim)
+        return GEMM_ERR_UNSUPPORTED;
+    if (p.fp4 && p.K % 32 != 0)
+        return GEMM_ERR_UNSUPPORTED;  // whole scale blocks only
+    if (p.M == 0 || p.N == 0) {
+        *empty = true;
+        return GEMM_OK;
+    }
+    const int64_t cols = p.fp4 ? p.K / 2 : p.K;
+    const int es = p.fp4 ? 1 : 2;
+    const Mat a{p.A, p.lda, p.M, cols, es, true}, bg{p.Bg, p.ldbg, p.N, cols, es, true},
+        bu{p.Bu, p.ldbu, p.N, cols, es, true}, d{p.D, p.ldd, p.M, p.N, out_size(p.out), false};
+    const int64_t sf = p.fp4 ? p.K / 32 : 0;
+    const Mat as{p.As, p.ldas, sf, p.M, 1, false}, bgs{p.Bgs, p.ldbgs, sf, p.N, 1, false},
+        bus{p.Bus, p.ldbus, sf, p.N, 1, false};
+    const Mat g{p.G, p.ldg, p.G ? p.M : 0, p.N, 2, false}, u{p.U, p.ldu, p.U ? p.M : 0, p.N, 2, false};
+    gemm_status st = check_mats({a, bg, bu, d, as, bgs, bus, g, u});
+    if (st != GEMM_OK)
+        return st;
+    if (any_overlap({span_of(d), span_of(g), span_of(u)},
+                    {span_of(a), span_of(bg), span_of(bu), span_of(as), span_of(bgs), span_of(bus)}))
+        return GEMM_ERR_ALIAS;
+    return GEMM_OK;
+}
+
+// Tiles of the gated form: D tiles half as wide as the accumulator tile.
+void set_gated_tile_plan(gemm_plan &p, int kernel, int bn, int64_t M, int64_t N, int sm_count)
+{
+    p.kernel = kernel;
+    p.bn = bn;
+    p.bm = kernel == 3 ? 256 : 128;
+    p.stages = tcg::tile_stages(bn, kernel == 3, 1, 1);
+    p.tiles = ceil_div(M, p.bm) * ceil_div(N, bn / 2);
+    p.splits = 1;
+    const int64_t cl = kernel == 3 ? 2 : 1, sets = sm_count / cl;
+    p.grid = static_cast<int32_t>(cl * (p.tiles < sets ? p.tiles : sets));
+}
+
+// Kernel arguments both forms share.
+void fill_gated(GemmArgs &a, const GatedProblem &p, const DeviceInfo *dev)
+{
+    Problem q{};  // (the fields fill_common reads)
+    q.M = p.M;
+    q.N = p.N;
+    q.K = p.K;
+    q.bf16 = p.bf16;
+    q.D = p.D;
+    q.ldd = p.ldd;
+    q.out = p.out;
+    q.alpha = 1.0f;
+    fill_common(a, q, dev);
+    a.act = p.act;
+    a.group_m = 1;
+    a.splits = 1;
+    a.k2_block = INT_MAX;
+    a.m2_block = INT_MAX;
+    a.d_tma = out_tma(p.D, p.ldd, p.out) ? 1 : 0;
+    a.d_tail_direct = (p.N * out_size(p.out)) % 16 != 0 ? 1 : 0;
+    a.G = p.G;
+    a.ldg = p.ldg;
+    a.U = p.U;
+    a.ldu = p.ldu;
+    const int kind = p.bf16 ? GEMM_OUT_BF16 : GEMM_OUT_F16;
+    a.keep_tma = (!p.G || out_tma(p.G, p.ldg, kind)) && (!p.U || out_tma(p.U, p.ldu, kind)) ? 1 : 0;
+    a.keep_tail_direct = (p.N * 2) % 16 != 0 ? 1 : 0;
+}
+
+gemm_status run_gated_skinny(const GatedProblem &p, const gemm_plan &plan, const DeviceInfo *dev)
+{
+    const int mp = plan.bm;
+    GemmMaps maps;
+    TileMapsTwo two;
+    std::memset(&maps, 0, sizeof(maps));
+    std::memset(&two, 0, sizeof(two));
+    gemm_status st;
+    const int kstage = p.fp4 ? tcg::skinny_mx_kstage() : tcg::skinny_kstage();
+    if (p.fp4) {
+        const uint8_t *as = nullptr, *bgs = nullptr, *bus = nullptr;
+        int64_t ldas = 0, ldbgs = 0, ldbus = 0;
+        if ((st = tma_scales(dev, p.stream, kBufScalesA, p.As, p.ldas, p.M, p.K / 32, &as, &ldas)) != GEMM_OK ||
+            (st = tma_scales(dev, p.stream, kBufScalesB, p.Bgs, p.ldbgs, p.N, p.K / 32, &bgs, &ldbgs)) != GEMM_OK ||
+            (st = tma_scales(dev, p.stream, kBufScalesB2, p.Bus, p.ldbus, p.N, p.K / 32, &bus, &ldbus)) != GEMM_OK)
+            return st;
+        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        const uint32_t sf_rows = static_cast<uint32_t>(kstage / 32);
+        if (!encode_2d(&maps.a, u8, p.A, p.K / 2, p.M, p.lda, 128, static_cast<uint32_t>(mp),
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&maps.b, u8, p.Bg, p.K / 2, p.N, p.ldbg, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&two.b2, u8, p.Bu, p.K / 2, p.N, p.ldbu, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&maps.c, u8, bgs, p.N, p.K / 32, ldbgs, 64, sf_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode_2d(&two.sfb2, u8, bus, p.N, p.K / 32, ldbus, 64, sf_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode_2d(&maps.sfa, u8, as, p.M, p.K / 32, ldas, static_cast<uint32_t>(mp), sf_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE))
+            return GEMM_ERR_CUDA;
+    } else if (!encode_2d(&maps.a, ab_type(p.bf16), p.A, p.K, p.M, p.lda * 2, 64, static_cast<uint32_t>(mp),
+                          CU_TENSOR_MAP_SWIZZLE_128B) ||
+               !encode_2d(&maps.b, ab_type(p.bf16), p.Bg, p.K, p.N, p.ldbg * 2, 64, 64,
+                          CU_TENSOR_MAP_SWIZZLE_128B) ||
+               !encode_2d(&two.b2, ab_type(p.bf16), p.Bu, p.K, p.N, p.ldbu * 2, 64, 64,
+                          CU_TENSOR_MAP_SWIZZLE_128B)) {
+        return GEMM_ERR_CUDA;
+    }
+    GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    fill_gated(a, p, dev);
+    a.num_m_blocks = 1;
+    a.num_n_blocks = static_cast<int32_t>(plan.tiles);
+    a.num_k_blocks = static_cast<int32_t>(ceil_div(p.K, kstage));
+    a.num_tiles = static_cast<int32_t>(plan.tiles);
+    a.sk_tiles = static_cast<int32_t>(plan.tiles);  // every tile shared block by block
+    a.splits = plan.splits;
+    if (plan.splits > 1) {
+        Workspace w;
+        const size_t bytes = static_cast<size_t>(plan.tiles) * plan.splits * 128 * mp * sizeof(float);
+        if ((st = get_workspace(dev->index, p.stream, bytes, static_cast<size_t>(plan.tiles), &w)) != GEMM_OK)
+            return st;
+        a.workspace = w.partials;
+        a.counters = w.counters;
+    }
+    const cudaError_t e = tcg::launch_skinny_gated(mp, p.fp4, maps, two, a, plan.grid, p.stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status run_gated(const GatedProblem &p)
+{
+    bool empty = false;
+    gemm_status st = validate_gated(p, &empty);
+    if (st != GEMM_OK || empty)
+        return st;
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const gemm_plan plan = p.fp4 ? gated_e2m1_plan(p.M, p.N, p.K, dev->sm_count)
+                                 : gated_plan(p.M, p.N, p.K, p.G || p.U, dev->sm_count);
+    if (plan.kernel == 2 || plan.kernel == 15)
+        return run_gated_skinny(p, plan, dev);
+    const bool pair = plan.kernel == 3;
+    const int bn = plan.bn;
+    const uint32_t half = static_cast<uint32_t>(bn / 2);  // rows of Bg (Bu) per box
+    int grid = plan.grid;
+    if (pair) {
+        // never more pairs than can be resident together
+        const int resident = tcg::tile_max_clusters(256, true, 1, 1);
+        if (resident <= 0)
+            return GEMM_ERR_CUDA;
+        grid = static_cast<int>(2 * (plan.tiles < resident ? plan.tiles : resident));
+    }
+    GemmMaps maps;
+    TileMapsTwo two;
+    std::memset(&maps, 0, sizeof(maps));
+    std::memset(&two, 0, sizeof(two));
+    const int kstage = p.fp4 ? tcg::tile_mx_kstage(1) : 64;
+    if (p.K > 0 && p.fp4) {
+        const uint8_t *as = nullptr, *bgs = nullptr, *bus = nullptr;
+        int64_t ldas = 0, ldbgs = 0, ldbus = 0;
+        if ((st = tma_scales(dev, p.stream, kBufScalesA, p.As, p.ldas, p.M, p.K / 32, &as, &ldas)) != GEMM_OK ||
+            (st = tma_scales(dev, p.stream, kBufScalesB, p.Bgs, p.ldbgs, p.N, p.K / 32, &bgs, &ldbgs)) != GEMM_OK ||
+            (st = tma_scales(dev, p.stream, kBufScalesB2, p.Bus, p.ldbus, p.N, p.K / 32, &bus, &ldbus)) != GEMM_OK)
+            return st;
+        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        const uint32_t sf_rows = static_cast<uint32_t>(kstage / 32);
+        if (!encode_2d(&maps.a, u8, p.A, p.K / 2, p.M, p.lda, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&maps.b, u8, p.Bg, p.K / 2, p.N, p.ldbg, 128, half, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&two.b2, u8, p.Bu, p.K / 2, p.N, p.ldbu, 128, half, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&maps.sfa, u8, as, p.M, p.K / 32, ldas, 128, sf_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode_2d(&maps.sfb, u8, bgs, p.N, p.K / 32, ldbgs, half, sf_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode_2d(&two.sfb2, u8, bus, p.N, p.K / 32, ldbus, half, sf_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return GEMM_ERR_CUDA;
+    } else if (p.K > 0) {
+        const CUtensorMapDataType t = ab_type(p.bf16);
+        if (!encode_2d(&maps.a, t, p.A, p.K, p.M, p.lda * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&maps.b, t, p.Bg, p.K, p.N, p.ldbg * 2, 64, half, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d(&two.b2, t, p.Bu, p.K, p.N, p.ldbu * 2, 64, half, CU_TENSOR_MAP_SWIZZLE_128B))
+            return GEMM_ERR_CUDA;
+    }
+    GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    fill_gated(a, p, dev);
+    const int keep = p.bf16 ? GEMM_OUT_BF16 : GEMM_OUT_F16;
+    if ((a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd)) ||
+        (a.keep_tma && p.G && !encode_out(&two.d2, p.G, keep, p.M, p.N, p.ldg)) ||
+        (a.keep_tma && p.U && !encode_out(&two.d3, p.U, keep, p.M, p.N, p.ldu)))
+        return GEMM_ERR_CUDA;
+    a.num_m_blocks = static_cast<int32_t>(ceil_div(p.M, plan.bm));
+    a.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, bn / 2));
+    a.num_k_blocks = static_cast<int32_t>(ceil_div(p.K, kstage));
+    a.num_tiles = static_cast<int32_t>(plan.tiles);
+    a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
+    const cudaError_t e = p.fp4 ? tcg::launch_tile_gated_mx(bn, maps, two, a, grid, p.stream)
+                                : tcg::launch_tile_gated(bn, pair, maps, two, a, grid, p.stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- transposed storage
+
+// D = fma.rn(alpha, op(A) op(B), beta C).  A second source: K blocks that follow
+// (A2, B2: D also gets op(A2) op(B2)), or block rows that follow (A2, D2: D2
+// = op(A2) op(B)).
+struct TransProblem {
+    int64_t M, N, K;
+    bool bf16, ta, tb;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    const float *C;
+    int64_t ldc;
+    void *D;
+    int64_t ldd;
+    int out;
+    float alpha, beta;
+    cudaStream_t stream;
+    const void *A2 = nullptr;
+    int64_t lda2 = 0;
+    const void *B2 = nullptr;
+    int64_t ldb2 = 0;
+    void *D2 = nullptr;
+    int64_t ldd2 = 0;
+};
+
+// Launch (arguments already checked; M, N > 0).
+gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
+{
+    const bool c_used = p.C != nullptr && p.beta != 0.0f;
+    const gemm_plan plan = trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, c_used, dev->sm_count);
+    const bool pair = plan.kernel != 1;
+    const int nsub = plan.kernel == 4 ? 2 : 1;
+    const int bn = pair ? 256 : plan.bn;
+    int grid = plan.grid;
+    if (pair) {
+        const int resident = tcg::tile_max_clusters(256, true, nsub, 1);
+        if (resident <= 0)
+            return GEMM_ERR_CUDA;
+        grid = static_cast<int>(2 * (plan.tiles < resident ? plan.tiles : resident));
+    }
+    GemmMaps maps;
+    TileMapsTwo two;
+    std::memset(&maps, 0, sizeof(maps));
+    std::memset(&two, 0, sizeof(two));
+    const CUtensorMapDataType t = ab_type(p.bf16);
+    const uint32_t b_rows = static_cast<uint32_t>(pair ? bn / 2 : bn);
+    // K-major: boxes of 64 K x the tile's rows; stored the other way: 64 columns x 64 K
+    auto map_a = [&](CUtensorMap *m, const void *A, int64_t lda) {
+        return p.ta ? encode_2d(m, t, A, p.M, p.K, lda * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                    : encode_2d(m, t, A, p.K, p.M, lda * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto map_b = [&](CUtensorMap *m, const void *B, int64_t ldb) {
+        return p.tb ? encode_2d(m, t, B, p.N, p.K, ldb * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                    : encode_2d(m, t, B, p.K, p.N, ldb * 2, 64, b_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (p.K > 0 && (!map_a(&maps.a, p.A, p.lda) || !map_b(&maps.b, p.B, p.ldb) ||
+                    (p.A2 && !map_a(&two.a2, p.A2, p.lda2)) || (p.B2 && !map_b(&two.b2, p.B2, p.ldb2))))
+        return GEMM_ERR_CUDA;
+    Problem q{};  // (the fields fill_common reads)
+    q.M = p.M;
+    q.N = p.N;
+    q.K = p.K;
+    q.bf16 = p.bf16;
+    q.C = p.C;
+    q.ldc = p.ldc;
+    q.D = p.D;
+    q.ldd = p.ldd;
+    q.out = p.out;
+    q.alpha = p.alpha;
+    q.beta = p.beta;
+    GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    fill_common(a, q, dev);
+    const int64_t m_blocks = ceil_div(p.M, plan.bm), k_blocks = ceil_div(p.K, 64);
+    const bool more_k = p.B2 != nullptr, more_m = p.D2 != nullptr;
+    a.num_m_blocks = static_cast<int32_t>(more_m ? 2 * m_blocks : m_blocks);
+    a.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, bn * nsub));
+    a.num_k_blocks = static_cast<int32_t>(more_k ? 2 * k_blocks : k_blocks);
+    a.num_tiles = a.num_m_blocks * a.num_n_blocks;
+    a.k2_block = more_k ? static_cast<int32_t>(k_blocks) : INT_MAX;
+    a.m2_block = more_m ? static_cast<int32_t>(m_blocks) : INT_MAX;
+    a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
+    a.splits = 1;
+    a.c_tma = c_used && aligned16(p.C) && (p.ldc * 4) % 16 == 0 ? 1 : 0;
+    a.d_tma = out_tma(p.D, p.ldd, p.out) && (!more_m || out_tma(p.D2, p.ldd2, p.out)) ? 1 : 0;
+    a.d_tail_direct = (p.N * out_size(p.out)) % 16 != 0 ? 1 : 0;
+    a.D2 = p.D2;
+    a.ldd2 = p.ldd2;
+    if ((a.c_tma && !encode_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.C, p.N, p.M, p.ldc * 4, 32, 32,
+                               CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd)) ||
+        (a.d_tma && more_m && !encode_out(&two.d2, p.D2, p.out, p.M, p.N, p.ldd2)))
+        return GEMM_ERR_CUDA;
+    const int maj = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
+    const cudaError_t e = tcg::launch_tile_major(maj, bn, pair, nsub, maps, two, a, grid, p.stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status check_trans(const TransProblem &p)
+{
+    if (p.M < 0 || p.N < 0 || p.K < 0 || !out_ok(p.out))
+        return GEMM_ERR_INVALID_ARG;
+    if (p.M > kMaxDim || p.N > kMaxDim || p.K > kMaxDim)
+        return GEMM_ERR_UNSUPPORTED;
+    if (p.M == 0 || p.N == 0)
+        return GEMM_OK;
+    const bool c_used = p.C != nullptr && p.beta != 0.0f;
+    const Mat a{p.A, p.lda, p.ta ? p.K : p.M, p.ta ? p.M : p.K, 2, true};
+    const Mat b{p.B, p.ldb, p.tb ? p.K : p.N, p.tb ? p.N : p.K, 2, true};
+    const Mat c{p.C, p.ldc, c_used ? p.M : 0, p.N, 4, false};
+    const Mat d{p.D, p.ldd, p.M, p.N, out_size(p.out), false};
+    gemm_status st = check_mats({a, b, c, d});
+    if (st != GEMM_OK)
+        return st;
+    if (any_overlap({span_of(d)}, {span_of(a), span_of(b)}))
+        return GEMM_ERR_ALIAS;
+    const bool in_place = c_used && static_cast<const void *>(p.C) == p.D && p.out == GEMM_OUT_F32 &&
+                          p.ldc == p.ldd;
+    if (c_used && !in_place && any_overlap({span_of(d)}, {span_of(c)}))
+        return GEMM_ERR_ALIAS;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+gemm_plan gated_plan(int64_t M, int64_t N, int64_t K, bool keep, int sm_count)
+{
+    gemm_plan p;
+    std::memset(&p, 0, sizeof(p));
+    if (M == 0 || N == 0)
+        return p;
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    // M <= 64 rows: as the plain form decides between the two kernels, for the
+    // 2 N rows of both weight matrices (the skinny kernel keeps no products)
+    const bool skinny_ok = M <= 64 && K > 0 && !keep;
+    if (skinny_ok && (fk == 2 || (fk != 1 && fk != 3 && skinny_wins(M, 2 * N, K)))) {
+        set_skinny_plan(p, M, 128 * ceil_div(N, 64), K, sm_count, false);
+        return p;
+    }
+    if (fk == 1 || (fk == 3 && K > 0)) {
+        set_gated_tile_plan(p, fk, fbn, M, N, sm_count);
+        return p;
+    }
+    // waves of CTAs (pairs) x accumulator width plus a fixed cost per tile, pairs
+    // at 0.9 (each SM moves 2/3 of the operand bytes), as choose_tile weighs them
+    int kernel = 1, bn = 256;
+    double best = -1.0;
+    for (int w : {256, 128, 64}) {
+        const int64_t tiles = ceil_div(M, 128) * ceil_div(N, w / 2);
+        const double cost = static_cast<double>(ceil_div(tiles, sm_count) * (w + 32));
+        if (best < 0 || cost < best) {
+            best = cost;
+            bn = w;
+        }
+    }
+    const int pairs = sm_count / 2;
+    if (K > 0 && pairs > 0) {
+        const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 128);
+        if (0.9 * static_cast<double>(ceil_div(tiles, pairs) * (256 + 32)) <= best) {
+            kernel = 3;
+            bn = 256;
+        }
+    }
+    set_gated_tile_plan(p, kernel, bn, M, N, sm_count);
+    return p;
+}
+
+gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
+{
+    gemm_plan p;
+    std::memset(&p, 0, sizeof(p));
+    if (M == 0 || N == 0)
+        return p;
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    if (M <= 64 && K > 0 && fk != 11) {
+        set_e2m1_skinny_plan(p, M, ceil_div(N, 64), K, sm_count);
+        return p;
+    }
+    int bn = 256;
+    if (fk == 11) {
+        bn = fbn;
+    } else {
+        const int64_t w256 = ceil_div(ceil_div(M, 128) * ceil_div(N, 128), sm_count);
+        const int64_t w128 = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
+        if (w128 * (128 + 32) < w256 * (256 + 32))
+            bn = 128;
+    }
+    p.kernel = 11;
+    p.bm = 128;
+    p.bn = bn;
+    p.stages = tcg::tile_mx_stages(1, bn, false);
+    p.tiles = ceil_div(M, 128) * ceil_div(N, bn / 2);
+    p.splits = 1;
+    p.grid = static_cast<int32_t>(p.tiles < sm_count ? p.tiles : sm_count);
+    return p;
+}
+
+// Block rows of both stacked sources (sources = 2) count as one problem's.
+gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int sources, bool c_used, int sm_count)
+{
+    gemm_plan p;
+    std::memset(&p, 0, sizeof(p));
+    if (M == 0 || N == 0)
+        return p;
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    TileChoice c = choose_tile(sources * M, N, K, false, c_used, false, sm_count);
+    if (fk == 1 || ((fk == 3 || fk == 4) && K > 0))
+        c = TileChoice{fk, fbn};
+    set_tile_plan(p, c.kernel, c.bn, M, N, sm_count);
+    if (sources > 1) {
+        p.tiles *= sources;
+        const int64_t cl = c.kernel == 1 ? 1 : 2, sets = sm_count / cl;
+        p.grid = static_cast<int32_t>(cl * (p.tiles < sets ? p.tiles : sets));
+    }
+    return p;
+}
+
+}  // namespace host
+}  // namespace tcg
+
+using namespace tcg::host;
+
+extern "C" {
+
+gemm_status gemm_gated(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, const void *A, int64_t lda,
+                       const void *Bg, int64_t ldbg, const void *Bu, int64_t ldbu, void *G, int64_t ldg,
+                       void *U, int64_t ldu, void *D, int64_t ldd, int out, int act, void *stream)
+{
+    if (dtype_is_bf16 != 0 && dtype_is_bf16 != 1)
+        return GEMM_ERR_INVALID_ARG;
+    GatedProblem p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.bf16 = dtype_is_bf16 == 1;
+    p.A = A;
+    p.lda = lda;
+    p.Bg = Bg;
+    p.ldbg = ldbg;
+    p.Bu = Bu;
+    p.ldbu = ldbu;
+    p.G = G;
+    p.ldg = ldg;
+    p.U = U;
+    p.ldu = ldu;
+    p.D = D;
+    p.ldd = ldd;
+    p.out = out;
+    p.act = act;
+    p.stream = static_cast<cudaStream_t>(stream);
+    return run_gated(p);
+}
+
+gemm_status gemm_gated_e2m1(int64_t M, int64_t N, int64_t K, const uint8_t *Aq, int64_t ldaq,
+                            const uint8_t *As, int64_t ldas, const uint8_t *Bgq, int64_t ldbgq,
+                            const uint8_t *Bgs, int64_t ldbgs, const uint8_t *Buq, int64_t ldbuq,
+                            const uint8_t *Bus, int64_t ldbus, void *D, int64_t ldd, int out, int act,
+                            void *stream)
+{
+    GatedProblem p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.fp4 = true;
+    p.A = Aq;
+    p.lda = ldaq;
+    p.As = As;
+    p.ldas = ldas;
+    p.Bg = Bgq;
+    p.ldbg = ldbgq;
+    p.Bgs = Bgs;
+    p.ldbgs = ldbgs;
+    p.Bu = Buq;
+    p.ldbu = ldbuq;
+    p.Bus = Bus;
+    p.ldbus = ldbus;
+    p.D = D;
+    p.ldd = ldd;
+    p.out = out;
+    p.act = act;
+    p.stream = static_cast<cudaStream_t>(stream);
+    return run_gated(p);
+}
+
+gemm_status gemm_trans(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, int trans_a, const void *A,
+                       int64_t lda, int trans_b, const void *B, int64_t ldb, const float *C, int64_t ldc,
+                       void *D, int64_t ldd, int out, float alpha, float beta, void *stream)
+{
+    if ((dtype_is_bf16 != 0 && dtype_is_bf16 != 1) || (trans_a != 0 && trans_a != 1) ||
+        (trans_b != 0 && trans_b != 1))
+        return GEMM_ERR_INVALID_ARG;
+    if (trans_a == 0 && trans_b == 0) {
+        const Problem q{M, N, K, dtype_is_bf16 == 1, A, M, lda, nullptr, B, ldb, C, ldc, D, ldd,
+                        out, alpha, beta, false, static_cast<cudaStream_t>(stream)};
+        return run(q);
+    }
+    TransProblem p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.bf16 = dtype_is_bf16 == 1;
+    p.ta = trans_a == 1;
+    p.tb = trans_b == 1;
+    p.A = A;
+    p.lda = lda;
+    p.B = B;
+    p.ldb = ldb;
+    p.C = C;
+    p.ldc = ldc;
+    p.D = D;
+    p.ldd = ldd;
+    p.out = out;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.stream = static_cast<cudaStream_t>(stream);
+    gemm_status st = check_trans(p);
+    if (st != GEMM_OK || M == 0 || N == 0)
+        return st;
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    return run_trans(p, dev);
+}
+
+gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, const void *dD,
+                                int64_t lddd, const void *G, int64_t ldg, const void *U, int64_t ldu,
+                                const void *A, int64_t lda, const void *Bg, int64_t ldbg, const void *Bu,
+                                int64_t ldbu, void *dG, int64_t lddg, void *dU, int64_t lddu, void *dA,
+                                int64_t ldda, void *dBg, int64_t lddbg, void *dBu, int64_t lddbu, int out,
+                                int act, void *stream)
+{
+    if ((dtype_is_bf16 != 0 && dtype_is_bf16 != 1) || M < 0 || N < 0 || K < 0 || !out_ok(out) || !act_ok(act))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return GEMM_ERR_UNSUPPORTED;
+    // which gradients are asked for (an empty one needs no pointer)
+    const bool want_a = dA != nullptr && M > 0 && K > 0;
+    const bool want_b = (dBg != nullptr || dBu != nullptr) && N > 0 && K > 0;
+    const int es = out_size(out);
+    const Mat dd{dD, lddd, M, N, 2, false}, g{G, ldg, M, N, 2, false}, u{U, ldu, M, N, 2, false};
+    const Mat dg{dG, lddg, M, N, 2, true}, du{dU, lddu, M, N, 2, true};
+    const Mat a{A, lda, want_b ? M : 0, K, 2, true};
+    const Mat bg{Bg, ldbg, want_a ? N : 0, K, 2, true}, bu{Bu, ldbu, want_a ? N : 0, K, 2, true};
+    const Mat da{dA, ldda, want_a ? M : 0, K, es, false};
+    const Mat dbg{dBg, lddbg, want_b ? N : 0, K, es, false}, dbu{dBu, lddbu, want_b ? N : 0, K, es, false};
+    gemm_status st = check_mats({dd, g, u, dg, du, a, bg, bu, da, dbg, dbu});
+    if (st != GEMM_OK)
+        return st;
+    // dG may take G's place and dU U's, exactly
+    const Span sg = dG == G && lddg == ldg ? Span{nullptr, 0} : span_of(g);
+    const Span su = dU == U && lddu == ldu ? Span{nullptr, 0} : span_of(u);
+    if (any_overlap({span_of(dg), span_of(du), span_of(da), span_of(dbg), span_of(dbu)},
+                    {span_of(dd), span_of(a), span_of(bg), span_of(bu)}) ||
+        any_overlap({span_of(dg)}, {sg, span_of(u)}) || any_overlap({span_of(du)}, {span_of(g), su}) ||
+        any_overlap({span_of(da)}, {span_of(g), span_of(u)}) ||
+        any_overlap({span_of(dbg)}, {span_of(g), span_of(u)}) ||
+        any_overlap({span_of(dbu)}, {span_of(g), span_of(u)}))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype_is_bf16 == 1;
+    if (M > 0 && N > 0 &&
+        tcg::launch_gated_slope(dD, lddd, G, ldg, U, ldu, dG, lddg, dU, lddu, static_cast<int32_t>(M),
+                                static_cast<int32_t>(N), bf16, act, cs) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    if (want_a) {
+        // dA = [dG dU] [Bg; Bu]: one sum over 2 N, Bg and Bu read as stored (K columns contiguous)
+        TransProblem p{};
+        p.M = M;
+        p.N = K;
+        p.K = N;
+        p.bf16 = bf16;
+        p.tb = true;
+        p.A = dG;
+        p.lda = lddg;
+        p.B = Bg;
+        p.ldb = ldbg;
+        p.A2 = dU;
+        p.lda2 = lddu;
+        p.B2 = Bu;
+        p.ldb2 = ldbu;
+        p.D = dA;
+        p.ldd = ldda;
+        p.out = out;
+        p.alpha = 1.0f;
+        p.stream = cs;
+        if ((st = run_trans(p, dev)) != GEMM_OK)
+            return st;
+    }
+    if (want_b) {
+        // [dBg; dBu] = [dG dU]^T A: both gradients' tiles in one launch
+        TransProblem p{};
+        p.M = N;
+        p.N = K;
+        p.K = M;
+        p.bf16 = bf16;
+        p.ta = true;
+        p.tb = true;
+        p.A = dG;
+        p.lda = lddg;
+        p.A2 = dU;
+        p.lda2 = lddu;
+        p.B = A;
+        p.ldb = lda;
+        p.D = dBg;
+        p.ldd = lddbg;
+        p.D2 = dBu;
+        p.ldd2 = lddbu;
+        p.out = out;
+        p.alpha = 1.0f;
+        p.stream = cs;
+        if ((st = run_trans(p, dev)) != GEMM_OK)
+            return st;
+    }
+    return GEMM_OK;
+}
+
+gemm_status gemm_quantize_e2m1(int64_t M, int64_t K, int type, const void *X, int64_t ldx, uint8_t *Q,
+                               int64_t ldq, uint8_t *S, int64_t lds, void *Y, int64_t ldy, void *stream)
+{
+    if (M < 0 || K < 0 || !out_ok(type))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || K > kMaxDim || K % 32 != 0)
+        return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0)
+        return GEMM_OK;
+    const int es = out_size(type);
+    const Mat x{X, ldx, M, K, es, false}, q{Q, ldq, M, K / 2, 1, true}, s{S, lds, K / 32, M, 1, false},
+        y{Y, ldy, Y ? M : 0, K, es, false};
+    gemm_status st = check_mats({x, q, s, y});
+    if (st != GEMM_OK)
+        return st;
+    // Y may take X's place, exactly
+    const Span sy = Y == X && ldy == ldx ? Span{nullptr, 0} : span_of(y);
+    if (any_overlap({span_of(q), span_of(s), sy}, {span_of(x)}) ||
+        any_overlap({span_of(q), span_of(s)}, {span_of(y)}))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const cudaError_t e =
+        tcg::launch_quantize_e2m1(X, ldx, type, Q, ldq, S, lds, Y, ldy, static_cast<int32_t>(M),
+                                  static_cast<int32_t>(K), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // extern "C"

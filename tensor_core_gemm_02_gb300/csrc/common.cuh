@@ -58,6 +58,25 @@ struct GemmArgs {
     int64_t ldd;
     float *workspace;       // per-split partial tiles
     uint32_t *counters;     // per-tile arrival counters (zero between calls)
+    // gated form (D = act(G) * U from two weight matrices)
+    int32_t act;            // gemm_act_t
+    int32_t keep_tma;       // G and U boxes go out through TMA stores; else plain stores
+    int32_t keep_tail_direct;  // as d_tail_direct, for the 16-bit G and U
+    void *G, *U;            // the two products, in the operand type; NULL: not kept
+    int64_t ldg, ldu;
+    // products with two sources: K blocks from k2_block on read the second pair
+    // of operands, block rows from m2_block on the second A and D
+    int32_t k2_block, m2_block;
+    void *D2;
+    int64_t ldd2;
+};
+
+// Descriptors of the tile kernel's two-source forms beyond the plain form's: the
+// gated form's Bu (b2), its scales (sfb2) and the kept products (d2: G, d3: U);
+// or the second source of a product with two (a2, b2: K blocks from
+// args.k2_block on; a2, d2: block rows from args.m2_block on).
+struct TileMapsTwo {
+    CUtensorMap a2, b2, d2, d3, sfb2;
 };
 
 __device__ __forceinline__ void record_error(uint32_t *status, uint32_t code, uint32_t where)

@@ -99,7 +99,7 @@ gemm_status reset_static_scratch(int device);
 // Buffers the library keeps per (device, stream, use), grown geometrically:
 // bf16 weights converted from FP4, and block scales copied to a 16-byte row
 // pitch for TMA (B's for gemm_bf16_e2m1; A's and B's for gemm_e2m1).
-enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3 };
+enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4 };
 gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t bytes, void **out);
 
 // The form forced by gemm_debug_force_tile (kernel 0: none).
@@ -109,6 +109,36 @@ bool aligned16(const void *p);
 uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esize);
 bool overlap(const void *a, uint64_t an, const void *b, uint64_t bn);
 int out_size(int out);
+
+// Any problem of the A * B^T entry points: validate, choose a kernel, launch.
+gemm_status run(const Problem &p);
+
+// Block scales as TMA needs them (16-byte aligned base and pitch): the caller's
+// own, or a copy in the per-stream buffer `use`.
+gemm_status tma_scales(const DeviceInfo *dev, cudaStream_t stream, int use, const uint8_t *s,
+                       int64_t ld, int64_t cols, int64_t rows, const uint8_t **out, int64_t *ld_out);
+
+// Rows of A the skinny kernel pads m to (16, 32 or 64).
+int skinny_rows(int64_t m);
+// Whether the skinny kernel beats the tile kernel at M <= 64 (16-bit operands).
+bool skinny_wins(int64_t M, int64_t N, int64_t K);
+// The tile kernel's form for a problem (api.cu says how it is chosen), its plan,
+// and the clusters of a form that fit the device at once.
+struct TileChoice {
+    int kernel;  // 1 single CTAs, 3 pairs of 256 x 256, 4 pairs of 256 x 512 (and the clustered forms)
+    int bn;
+};
+TileChoice choose_tile(int64_t M, int64_t N, int64_t K, bool gather, bool c_used, bool scatter,
+                       int sm_count);
+void set_tile_plan(gemm_plan &p, int kernel, int bn, int64_t M, int64_t N, int sm_count);
+// The both-FP4 skinny kernel's plan: `tiles` tiles of 128 rows of B, M <= 64.
+void set_e2m1_skinny_plan(gemm_plan &p, int64_t M, int64_t tiles, int64_t K, int sm_count);
+
+// Plans of gemm_gated (16-bit), gemm_gated_e2m1 and gemm_trans, with a forced
+// form applied.
+gemm_plan gated_plan(int64_t M, int64_t N, int64_t K, bool keep, int sm_count);
+gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count);
+gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int sources, bool c_used, int sm_count);
 
 // Plan of gemm_e2m1 (kernel 11: packed codes, kind::mxf4; 12: the 16U4 image,
 // kind::mxf8f6f4), with a forced form applied.

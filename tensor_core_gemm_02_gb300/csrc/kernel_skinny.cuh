@@ -35,14 +35,23 @@
 //              coalesced plain loads/stores (lanes walk along N); with
 //              scattered rows, row m of the result lands in row idx[m] of D;
 //              in the accumulating form every part is added into D with
-//              float32 atomic adds instead (no workspace, no last arriver)
+//              float32 atomic adds instead (no workspace, no last arriver);
+//              gated form: below
 //   the rest   (FP4 B) converters: E2M1 codes and UE8M0 scales to bf16 rows
 //              in tensor memory (tcgen05.st), the MMA's A operand; or (both
 //              operands FP4, MX) one scale warp: the stage's scale rows of B
 //              and A rearranged into the tiles tcgen05.cp copies into tensor
 //              memory, where the block-scaled MMA (kind::mxf4) reads them
+//
+// Gated form (D = act(A Bg^T) * (A Bu^T)): a tile's 128 rows are 64 rows of Bg
+// followed by the 64 rows of Bu with the same numbers, so both matrices stream
+// through the same ring and MMAs and a tile's sums hold G and U of 64 columns
+// of D.  They lie in different TMEM lanes: once a tile's sums are whole, thread n
+// < 64 (a column of G) and thread n + 64 (the same column of U) swap half of
+// their rows through shared memory, and each finishes half of the rows.
 #pragma once
 
+#include "act.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 
@@ -70,7 +79,7 @@ __host__ __device__ constexpr uint32_t tmem_cols_for(uint32_t cols)
     return cols <= 32u ? 32u : (cols <= 64u ? 64u : (cols <= 128u ? 128u : (cols <= 256u ? 256u : 512u)));
 }
 
-template <int MP_, int KBOX_, bool W4_ = false, bool MX_ = false>
+template <int MP_, int KBOX_, bool W4_ = false, bool MX_ = false, bool GATED_ = false>
 struct SkinnyCfg {
     static constexpr int MP = MP_;      // padded rows of A = MMA N
     static constexpr int BN = 128;      // rows of B per tile = MMA M
@@ -170,7 +179,9 @@ struct SkinnyCfg {
     static constexpr uint32_t SF_COLS = MX ? ISSUERS * 8 : 0;  // a stage's
     static constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t OFF_ROWS = OFF_MISC + 16;  // MP destination rows (scattered rows)
-    static constexpr uint32_t SMEM_BYTES = OFF_ROWS + MP * 4;
+    // (gated) sums that change threads: MP / 2 rows of 128 floats
+    static constexpr uint32_t OFF_SWAP = OFF_ROWS + MP * 4;
+    static constexpr uint32_t SMEM_BYTES = OFF_SWAP + (GATED_ ? MP / 2 * 512 : 0);
     static constexpr uint32_t SMEM_ALLOC = SMEM_BYTES + 1024;
 
     static_assert(!W4 || KBOX == 4, "W4 stages hold 128-byte runs of codes");
@@ -204,6 +215,22 @@ template <int N>
 __device__ __forceinline__ void epi_bar_sync()
 {
     asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
+// The same barrier, agreeing on whether any thread found `p`.
+template <int N>
+__device__ __forceinline__ bool epi_bar_any(bool p)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(p ? 1u : 0u), "n"(N)
+        : "memory");
+    return r != 0;
 }
 
 // Row of C and D for row m of A: m itself, or (scattered rows) the entry
@@ -338,14 +365,51 @@ __device__ __forceinline__ void skinny_add(const GemmArgs &a, const int32_t *dro
             atomicAdd(p + static_cast<int64_t>(m) * a.ldd, d[m]);
 }
 
-template <int MP, int KBOX, bool W4, bool MX = false>
-__global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
-    skinny_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                       const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmS,
-                       const __grid_constant__ CUtensorMap tmSA, const GemmArgs args)
+// Gated form: thread n_local (column n_local % 64 of the tile; < 64: its sums are
+// G's, else U's) swaps half of its CH rows with thread n_local ^ 64 and stores
+// D[m][n] = act(G) * U for the other half: rows m0 .. m0 + CH / 2 - 1, or the
+// next CH / 2.  Every epilogue thread takes part; the barrier before the next
+// tile's sums are read keeps its swap apart from this one.
+template <int CH, int THREADS>
+__device__ __forceinline__ void skinny_store_gated(const GemmArgs &a, float *swap, int32_t n_local,
+                                                   int32_t n, int m0, const float (&v)[CH])
 {
-    using Cfg = SkinnyCfg<MP, KBOX, W4, MX>;
+    constexpr int H = CH / 2;
+    const bool is_g = n_local < 64;
+    float *mine = swap + (m0 / 2) * 128 + n_local;
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        mine[i * 128] = is_g ? v[H + i] : v[i];
+    epi_bar_sync<THREADS>();
+    if (n >= a.N)
+        return;
+    const float *theirs = swap + (m0 / 2) * 128 + (n_local ^ 64);
+    float d[H];
+    with_act(a.act, [&](auto tag) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float x = theirs[i * 128];
+            const float g = is_g ? v[i] : x, u = is_g ? x : v[H + i];
+            d[i] = act_value<decltype(tag)::value>(g) * u;
+        }
+    });
+    const int m = is_g ? m0 : m0 + H;
+    if (a.out_kind == kOutF32)
+        skinny_store_rows<float>(a, nullptr, n, m, d, [](float x) { return x; });
+    else if (a.out_kind == kOutBF16)
+        skinny_store_rows<unsigned short>(a, nullptr, n, m, d, [](float x) { return f32_to_bf16_rn(x); });
+    else
+        skinny_store_rows<unsigned short>(a, nullptr, n, m, d, [](float x) { return f32_to_f16_rn(x); });
+}
+
+template <int MP, int KBOX, bool W4, bool MX, bool GATED>
+__device__ __forceinline__ void skinny_gemm_body(const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                                 const CUtensorMap &tmS, const CUtensorMap &tmSA,
+                                                 const CUtensorMap *tmB2, const CUtensorMap *tmS2,
+                                                 const GemmArgs &args)
+{
+    using Cfg = SkinnyCfg<MP, KBOX, W4, MX, GATED>;
+    static_assert(!GATED || !W4, "gated form: 16-bit operands, or both FP4");
     constexpr int STAGES = Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -456,11 +520,19 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
         if constexpr (MX) {
             // one 128-byte box of codes of B (128 rows) and of A (MP rows), x in
             // bytes; the stage's scale rows of B (128 columns) and of A (MP)
-            tma_load_2d(base + Cfg::OFF_B + st * Cfg::B_BYTES, &tmB, full_bar(st), kb * 128,
-                        t * Cfg::BN);
+            const uint32_t sb = base + Cfg::OFF_B + st * Cfg::B_BYTES;
+            const uint32_t ss = base + Cfg::OFF_SC + st * Cfg::SCALE_B;
+            if constexpr (GATED) {
+                // 64 rows of each matrix, and their scales as two images
+                tma_load_2d(sb, &tmB, full_bar(st), kb * 128, t * 64);
+                tma_load_2d(sb + 64u * 128u, tmB2, full_bar(st), kb * 128, t * 64);
+                tma_load_2d(ss, &tmS, full_bar(st), t * 64, kb * Cfg::SF_KB);
+                tma_load_2d(ss + Cfg::SF_KB * 64u, tmS2, full_bar(st), t * 64, kb * Cfg::SF_KB);
+            } else {
+                tma_load_2d(sb, &tmB, full_bar(st), kb * 128, t * Cfg::BN);
+                tma_load_2d(ss, &tmS, full_bar(st), t * Cfg::BN, kb * Cfg::SF_KB);
+            }
             tma_load_2d(base + Cfg::OFF_A + st * Cfg::A_BYTES, &tmA, full_bar(st), kb * 128, 0);
-            tma_load_2d(base + Cfg::OFF_SC + st * Cfg::SCALE_B, &tmS, full_bar(st), t * Cfg::BN,
-                        kb * Cfg::SF_KB);
             tma_load_2d(base + Cfg::OFF_SCA + st * Cfg::SCALE_A, &tmSA, full_bar(st), 0,
                         kb * Cfg::SF_KB);
         } else if constexpr (W4) {
@@ -476,8 +548,13 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
         } else {
             for (int j = 0; j < KBOX; ++j) {
                 const int32_t k0 = kb * Cfg::KSTAGE + j * Cfg::BK;
-                tma_load_2d(base + Cfg::OFF_B + st * Cfg::B_BYTES + j * Cfg::B_BOX, &tmB,
-                            full_bar(st), k0, t * Cfg::BN);
+                const uint32_t sb = base + Cfg::OFF_B + st * Cfg::B_BYTES + j * Cfg::B_BOX;
+                if constexpr (GATED) {
+                    tma_load_2d(sb, &tmB, full_bar(st), k0, t * 64);
+                    tma_load_2d(sb + Cfg::B_BOX / 2, tmB2, full_bar(st), k0, t * 64);
+                } else {
+                    tma_load_2d(sb, &tmB, full_bar(st), k0, t * Cfg::BN);
+                }
                 tma_load_2d(base + Cfg::OFF_A + st * Cfg::A_BYTES + j * Cfg::A_BOX, &tmA,
                             full_bar(st), k0, 0);
             }
@@ -511,6 +588,10 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
             tma_prefetch_desc(&tmS);
         if (MX)
             tma_prefetch_desc(&tmSA);
+        if (GATED)
+            tma_prefetch_desc(tmB2);
+        if (GATED && MX)
+            tma_prefetch_desc(tmS2);
         // inputs are read only once the previous kernel in the stream is done
         grid_dependency_wait();
         // the ring is empty: start the B stream now instead of after the
@@ -698,6 +779,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
         // scattered rows: D row of each row of A, read once (after the set-up
         // barrier, so after the previous kernel in the stream has finished)
         int32_t *drow = reinterpret_cast<int32_t *>(gbase + Cfg::OFF_ROWS);
+        [[maybe_unused]] float *swap = reinterpret_cast<float *>(gbase + Cfg::OFF_SWAP);
         if (args.scatter) {
             const int32_t e = static_cast<int32_t>(threadIdx.x) - 32 * Cfg::EPI_WARP0;  // epilogue thread
             if (e < MP) {
@@ -718,7 +800,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
         for (int64_t i = 0; i < n_steps;) {
             const int32_t t = static_cast<int32_t>(order(i) / nkb);
             i = piece_end(i);
-            const int32_t n = t * Cfg::BN + n_local;
+            const int32_t n = GATED ? t * 64 + (n_local & 63) : t * Cfg::BN + n_local;
             // FP4 weights with MP > 16 finish the MP rows of A in chunks of 16,
             // so the epilogue's registers stay those of MP = 16 and leave room
             // for the converter warps; otherwise one chunk of the warp's MPH
@@ -795,9 +877,15 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
             const bool ok = warp_wait_bounded_inline(accf_bar(ab), aph, abort_flag, args.status,
                                                      args.timeout_ns, kWhereEpiAccFull);
             // all epilogue warps agree before the named barriers below
-            epi_bar_sync<EPI_THREADS>();
-            if (!ok || *abort_flag)
-                break;
+            // (gated: every thread takes the same way to the barriers that follow)
+            if constexpr (GATED) {
+                if (epi_bar_any<EPI_THREADS>(!ok || *abort_flag))
+                    break;
+            } else {
+                epi_bar_sync<EPI_THREADS>();
+                if (!ok || *abort_flag)
+                    break;
+            }
             tc_fence_after_sync();
             float v[CH];  // this chunk's sums (with one chunk: the CTA's whole part)
 #pragma unroll 1
@@ -848,9 +936,13 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
                 if (args.reduce) {
                     skinny_add<CH>(args, drow, n, mb + CH * g, v);  // every part adds itself into D
                 } else if (parts == 1) {
-                    float cb[CH];
-                    chunk_cb(g, cb);
-                    skinny_store<CH>(args, drow, n, mb + CH * g, v, cb);
+                    if constexpr (GATED) {
+                        skinny_store_gated<CH, EPI_THREADS>(args, swap, n_local, n, mb + CH * g, v);
+                    } else {
+                        float cb[CH];
+                        chunk_cb(g, cb);
+                        skinny_store<CH>(args, drow, n, mb + CH * g, v, cb);
+                    }
                 } else if (!last_known) {
 #pragma unroll
                     for (int m = 0; m < CH; ++m)
@@ -915,9 +1007,13 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
                     for (int m = 0; m < CH; ++m)
                         sum[m] += part[m];
                 }
-                float cb[CH];
-                chunk_cb(g, cb);
-                skinny_store<CH>(args, drow, n, mb + CH * g, sum, cb);
+                if constexpr (GATED) {
+                    skinny_store_gated<CH, EPI_THREADS>(args, swap, n_local, n, mb + CH * g, sum);
+                } else {
+                    float cb[CH];
+                    chunk_cb(g, cb);
+                    skinny_store<CH>(args, drow, n, mb + CH * g, sum, cb);
+                }
             }
             if (leader)
                 args.counters[t] = 0u;  // ready for the next call
@@ -1039,8 +1135,13 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
             for (int ti = 0; ti < Cfg::SF_TILES; ++ti) {
                 const bool b_tile = ti < Cfg::SF_TILES / 2;
                 const int c = ti % (Cfg::SF_TILES / 2);
-                const uint32_t pitch = b_tile ? static_cast<uint32_t>(Cfg::BN) : static_cast<uint32_t>(MP);
+                uint32_t pitch = b_tile ? static_cast<uint32_t>(Cfg::BN) : static_cast<uint32_t>(MP);
                 const uint8_t *src = (b_tile ? srcb : srca) + 4u * c * pitch + 4u * lane;
+                if (GATED && b_tile) {
+                    // rows 0-63 of the tile in Bg's image, 64-127 in Bu's
+                    pitch = 64u;
+                    src = srcb + (lane / 16u) * (Cfg::SF_KB * 64u) + 4u * c * 64u + 4u * (lane % 16u);
+                }
                 const bool have = b_tile || 4u * lane < static_cast<uint32_t>(MP);
                 uint32_t w[4];
 #pragma unroll
@@ -1074,6 +1175,29 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
     }
+}
+
+template <int MP, int KBOX, bool W4, bool MX = false>
+__global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
+    skinny_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmS,
+                       const __grid_constant__ CUtensorMap tmSA, const GemmArgs args)
+{
+    skinny_gemm_body<MP, KBOX, W4, MX, false>(tmA, tmB, tmS, tmSA, nullptr, nullptr, args);
+}
+
+// The gated form: Bg and Bu (tmB, tmB2), (MX) their scales (tmS, tmS2).
+template <int MP, int KBOX, bool MX>
+__global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, false, MX, true>::THREADS, 1)
+    skinny_gated_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmS,
+                        const __grid_constant__ CUtensorMap tmSA,
+                        const __grid_constant__ CUtensorMap tmB2,
+                        const __grid_constant__ CUtensorMap tmS2, const GemmArgs args)
+{
+    skinny_gemm_body<MP, KBOX, false, MX, true>(tmA, tmB, tmS, tmSA, &tmB2, &tmS2, args);
 }
 
 }  // namespace tcg

@@ -20,7 +20,8 @@
 //               scattered rows, C comes in by tile::gather4 and D goes out by
 //               tile::scatter4 at the rows idx[m] (section "Gather4 and
 //               scatter4").  In the accumulating form the box is added into
-//               D by a TMA reduce-add instead of stored.
+//               D by a TMA reduce-add instead of stored.  In the gated form
+//               the two halves of the columns make one output tile.
 //
 // PAIR = true runs the same roles on a CTA pair (ranks 2p, 2p+1 of a cluster) sharing
 // one tcgen05.mma.cta_group::2 of M = 256: each CTA loads its own 128 rows of
@@ -41,6 +42,7 @@
 // kernel returns with the error recorded.
 #pragma once
 
+#include "act.cuh"
 #include "common.cuh"
 
 // Evict-first L2 policy on the epilogue's C loads and D stores (0 or 1;
@@ -159,19 +161,33 @@ __device__ __forceinline__ uint32_t swz_off(uint32_t row, uint32_t chunk, uint32
 
 // Epilogue modes, a template parameter so that each kernel carries only its own:
 // the fma.rn epilogue with optional C, rows scattered through idx, reduce-add
-// into D, and accumulators seeded with C.
-enum : int { kModePlain = 0, kModeScatter = 1, kModeReduce = 2, kModeSeed = 3 };
+// into D, accumulators seeded with C, and the gated form.
+//
+// Gated form: D = act(G) * U with G = A Bg^T and U = A Bu^T.  The left half of
+// a tile's accumulator columns holds G, the right half the same columns of U:
+// the tile's rows of B are BN / 2 rows of Bg followed by the BN / 2 rows of Bu
+// with the same numbers (a CTA pair: the leader's half of B comes from Bg, the
+// peer's from Bu), so A is read once for both products, the MMAs are those of a
+// plain tile, and an epilogue thread finds G and U of its row in its own TMEM
+// lane.  The output tile is BN / 2 columns wide.
+enum : int { kModePlain = 0, kModeScatter = 1, kModeReduce = 2, kModeSeed = 3, kModeGated = 4 };
 
-template <int BN, int STAGES, bool PAIR, int NSUB, int MC, int MODE, int MX = 0>
-__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREADS, 1)
-    tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                     const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC,
-                     const __grid_constant__ CUtensorMap tmD,
-                     const __grid_constant__ CUtensorMap tmSFA,
-                     const __grid_constant__ CUtensorMap tmSFB, const GemmArgs args)
+// Storage of the 16-bit operands: A stored K x M, B stored K x N (bits); the
+// boxes are then 64 columns x 64 K rows and the MMA reads them as MN-major.
+enum : int { kMajA = 1, kMajB = 2 };
+
+template <int BN, int STAGES, bool PAIR, int NSUB, int MC, int MODE, int MX, int MAJ>
+__device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                               const CUtensorMap &tmC, const CUtensorMap &tmD,
+                                               const CUtensorMap &tmSFA, const CUtensorMap &tmSFB,
+                                               const TileMapsTwo *two, const GemmArgs &args)
 {
     using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>;
+    constexpr bool kGated = MODE == kModeGated;
+    constexpr bool kTwo = kGated || MAJ != 0;  // loads go through load_stage_two
+    static_assert(!kTwo || MC == 1, "two-source forms: no A multicast");
+    static_assert(!kGated || (NSUB == 1 && MAJ == 0), "gated form: one MMA half, K-major operands");
+    static_assert(MAJ == 0 || (MX == 0 && MODE == kModePlain), "K x M / K x N storage: 16-bit, plain epilogue");
     constexpr int CL = Cfg::CLUSTER;
     // issuers in use: one for seeded accumulators (C is the start value of the
     // one chain of K steps, as the pages' recurrence has it)
@@ -230,6 +246,67 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
     // `pre` stages; the producer skips them.
     constexpr bool kPrefill = !PAIR && MC == 1;
     int pre = 0;
+
+    // Two-source forms: the boxes of stage st <- K block kb of tile (mb, nb), this
+    // CTA's part, counted on `bar` (one thread).
+    auto load_stage_two = [&](int st, int32_t kb, int32_t mb, int32_t nb, uint32_t bar) {
+        if constexpr (kTwo) {
+            const uint32_t sa = base + Cfg::OFF_A + st * Cfg::A_BYTES;
+            const uint32_t sb = base + Cfg::OFF_B + st * Cfg::B_BYTES;
+            auto load = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) {
+                if (PAIR)
+                    tma_load_2d_pair(dst, m, bar, x, y);
+                else
+                    tma_load_2d(dst, m, bar, x, y);
+            };
+            const bool second_k = MAJ != 0 && kb >= args.k2_block;
+            const bool second_m = MAJ != 0 && mb >= args.m2_block;
+            const CUtensorMap *ma = second_k || second_m ? &two->a2 : &tmA;
+            const CUtensorMap *mbp = second_k ? &two->b2 : &tmB;
+            const int32_t k0 = (MX ? 128 : Cfg::BK) * (second_k ? kb - args.k2_block : kb);
+            const int32_t m0 = (second_m ? mb - args.m2_block : mb) * Cfg::TILE_M +
+                               static_cast<int32_t>(role) * Cfg::BM;
+            if constexpr ((MAJ & kMajA) != 0) {
+                for (int j = 0; j < Cfg::BM / 64; ++j)
+                    load(sa + j * 8192u, ma, m0 + 64 * j, k0);
+            } else {
+                load(sa, ma, k0, m0);
+            }
+            if constexpr (kGated) {
+                if (PAIR) {
+                    load(sb, role == 0u ? &tmB : &two->b2, k0, nb * Cfg::BN_LOCAL);
+                } else {
+                    load(sb, &tmB, k0, nb * (BN / 2));
+                    load(sb + BN / 2 * Cfg::ROW_BYTES, &two->b2, k0, nb * (BN / 2));
+                }
+            } else {
+                for (int j = 0; j < NSUB; ++j) {
+                    const int32_t n = nb * TILE_N + static_cast<int32_t>(role) * Cfg::BN_LOCAL + j * BN;
+                    if constexpr ((MAJ & kMajB) != 0) {
+                        for (int i = 0; i < Cfg::BN_LOCAL / 64; ++i)
+                            load(sb + j * Cfg::B_SUB_BYTES + i * 8192u, mbp, n + 64 * i, k0);
+                    } else {
+                        load(sb + j * Cfg::B_SUB_BYTES, mbp, k0, n);
+                    }
+                }
+            }
+        }
+    };
+    // (FP4) the scale rows of a stage: this CTA's rows of A, and all of the tile's
+    // rows of B (gated: the rows of Bg, then those of Bu, as two images)
+    auto load_scales = [&](int st, int32_t kb, int32_t m0, int32_t nb) {
+        const uint32_t sfs = base + Cfg::OFF_SFS + st * Cfg::SF_STAGE_BYTES;
+        const uint32_t sfb = sfs + Cfg::SF_KB * Cfg::BM;
+        mbar_arrive_expect_tx(sf_full_bar(st), Cfg::SF_STAGE_BYTES);
+        tma_load_2d(sfs, &tmSFA, sf_full_bar(st), m0, kb * Cfg::SF_KB);
+        if constexpr (kGated) {
+            tma_load_2d(sfb, &tmSFB, sf_full_bar(st), nb * (TILE_N / 2), kb * Cfg::SF_KB);
+            tma_load_2d(sfb + Cfg::SF_KB * (TILE_N / 2), &two->sfb2, sf_full_bar(st),
+                        nb * (TILE_N / 2), kb * Cfg::SF_KB);
+        } else {
+            tma_load_2d(sfb, &tmSFB, sf_full_bar(st), nb * TILE_N, kb * Cfg::SF_KB);
+        }
+    };
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
@@ -273,14 +350,13 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                 const int32_t n = min(STAGES, args.num_k_blocks);
                 for (; pre < n; ++pre) {
                     const int32_t k0 = MX ? pre * 128 : pre * Cfg::BK;
-                    if (MX) {
-                        const uint32_t sfs = base + Cfg::OFF_SFS + pre * Cfg::SF_STAGE_BYTES;
-                        mbar_arrive_expect_tx(sf_full_bar(pre), Cfg::SF_STAGE_BYTES);
-                        tma_load_2d(sfs, &tmSFA, sf_full_bar(pre), m0, pre * Cfg::SF_KB);
-                        tma_load_2d(sfs + Cfg::SF_KB * Cfg::BM, &tmSFB, sf_full_bar(pre), nb * TILE_N,
-                                    pre * Cfg::SF_KB);
-                    }
+                    if (MX)
+                        load_scales(pre, pre, m0, nb);
                     mbar_arrive_expect_tx(full_bar(pre), Cfg::STAGE_TX + (pre == 0 ? args.extra_tx : 0u));
+                    if constexpr (kTwo) {
+                        load_stage_two(pre, pre, mb, nb, full_bar(pre));
+                        continue;
+                    }
                     tma_load_2d(base + Cfg::OFF_A + pre * Cfg::A_BYTES, &tmA, full_bar(pre), k0, m0);
                     for (int j = 0; j < NSUB; ++j)
                         tma_load_2d(base + Cfg::OFF_B + pre * Cfg::B_BYTES + j * Cfg::B_SUB_BYTES, &tmB,
@@ -380,13 +456,12 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                 if (MX && lane == 0) {
                     // FP4: the stage's SF_KB rows of block scales, this CTA's rows of A
                     // and all of the tile's rows of B, on this CTA's own barrier
-                    const uint32_t sfs = base + Cfg::OFF_SFS + s * Cfg::SF_STAGE_BYTES;
-                    mbar_arrive_expect_tx(sf_full_bar(s), Cfg::SF_STAGE_BYTES);
-                    tma_load_2d(sfs, &tmSFA, sf_full_bar(s), m0, kb * Cfg::SF_KB);
-                    tma_load_2d(sfs + Cfg::SF_KB * Cfg::BM, &tmSFB, sf_full_bar(s), nb * TILE_N,
-                                kb * Cfg::SF_KB);
+                    load_scales(s, kb, m0, nb);
                 }
-                if (PAIR) {
+                if constexpr (kTwo) {
+                    if (lane == 0)
+                        load_stage_two(s, kb, mb, nb, lead(full_bar(s)));
+                } else if (PAIR) {
                     const uint32_t fb = lead(full_bar(s));
                     if (MC > 1) {
                         if (args.gather) {
@@ -464,7 +539,8 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
         // ------------------------------------------------------------ MMA issuers
         const int e = warp == 1 ? 0 : 1;  // issuer e takes the K blocks kb = e (mod kIss)
         if (lane == 0 && leader && e < kIss) {
-            const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, Cfg::TILE_M, BN);
+            const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, Cfg::TILE_M, BN,
+                                                    (MAJ & kMajA) != 0, (MAJ & kMajB) != 0);
             const int32_t nkb = args.num_k_blocks;
             int s = 0;
             uint32_t ph = 0;
@@ -476,9 +552,14 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
             // accumulated onto from the first K step on
             constexpr bool seeded = MODE == kModeSeed;
             auto issue_half = [&](int st, int32_t kb, int j, uint32_t d_tmem) {
-                const uint64_t ad = sdesc_k_sw128(base + Cfg::OFF_A + st * Cfg::A_BYTES);
-                const uint64_t bd =
-                    sdesc_k_sw128(base + Cfg::OFF_B + st * Cfg::B_BYTES + j * Cfg::B_SUB_BYTES);
+                const uint32_t sa = base + Cfg::OFF_A + st * Cfg::A_BYTES;
+                const uint32_t sb = base + Cfg::OFF_B + st * Cfg::B_BYTES + j * Cfg::B_SUB_BYTES;
+                const uint64_t ad = (MAJ & kMajA) != 0 ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+                const uint64_t bd = (MAJ & kMajB) != 0 ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
+                // descriptor step of one K step: 32 bytes along a K-major row, or 16
+                // rows of 128 bytes
+                constexpr uint32_t kStepA = (MAJ & kMajA) != 0 ? 128u : 2u;
+                constexpr uint32_t kStepB = (MAJ & kMajB) != 0 ? 128u : 2u;
                 const uint32_t dj = d_tmem + static_cast<uint32_t>(j * BN);
                 if constexpr (MX != 0) {
                     // the stage's scale tiles into its TMEM columns, then four
@@ -513,13 +594,13 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < Cfg::BK / 16; ++k) {  // +32 B per K=16 step
+                    for (int k = 0; k < Cfg::BK / 16; ++k) {  // one K=16 step each
                         // (the first K step of this issuer's chain starts from zero)
                         if (PAIR)
-                            tc_mma_f16_pair(dj, ad + 2u * k, bd + 2u * k, idesc,
+                            tc_mma_f16_pair(dj, ad + kStepA * k, bd + kStepB * k, idesc,
                                             (seeded || ((kb / kIss) | k) != 0) ? 1u : 0u);
                         else
-                            tc_mma_f16(dj, ad + 2u * k, bd + 2u * k, idesc,
+                            tc_mma_f16(dj, ad + kStepA * k, bd + kStepB * k, idesc,
                                        (seeded || ((kb / kIss) | k) != 0) ? 1u : 0u);
                     }
                 }
@@ -694,9 +775,17 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                         const bool a_tile = ti < Cfg::SF_CHUNKS;
                         const int c = a_tile ? ti : (ti - Cfg::SF_CHUNKS) / Cfg::SF_B_ROWTILES;
                         const int rt = a_tile ? 0 : (ti - Cfg::SF_CHUNKS) % Cfg::SF_B_ROWTILES;
-                        const uint32_t pitch = a_tile ? Cfg::BM : Cfg::TILE_N;
-                        const uint8_t *rows = src + (a_tile ? 0u : Cfg::SF_KB * Cfg::BM) + 128u * rt +
-                                              4u * c * pitch + 4u * lane;
+                        uint32_t pitch = a_tile ? Cfg::BM : Cfg::TILE_N;
+                        const uint8_t *rows = src + (a_tile ? 0u : Cfg::SF_KB * Cfg::BM);
+                        if (kGated && !a_tile) {
+                            // Bg's image, then Bu's, each of half the tile's rows: rows
+                            // 128 rt + 4 lane ... of the tile lie in one of the two
+                            pitch = Cfg::TILE_N / 2;
+                            const uint32_t r = 128u * rt + 4u * lane;
+                            rows += (r / pitch) * Cfg::SF_KB * pitch + 4u * c * pitch + r % pitch;
+                        } else {
+                            rows += 128u * rt + 4u * c * pitch + 4u * lane;
+                        }
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             w[ti][b] = *reinterpret_cast<const uint32_t *>(rows + b * pitch);
@@ -812,11 +901,143 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
         uint32_t aph = 0;
         uint32_t cph[2] = {0u, 0u};
         bool alive = true;
-        for (int32_t t = cta_set; t < args.num_tiles && alive; t += cta_sets) {
+
+        // Gated form: per 32 columns of D, G from the left half of the accumulator
+        // and U from the right half (with two issuers, both partial sums of each),
+        // kept copies of G and U if asked for, then D = act(G) * U.  Returns false
+        // when a wait gave up.
+        auto gated_epilogue = [&]() -> bool {
+            constexpr int32_t kCols = TILE_N / 2;  // columns of D per tile
+            const int keep_kind = args.ab_bf16 != 0 ? kOutBF16 : kOutF16;
+            const bool acc_none = args.num_k_blocks == 0;
+            int slot = 0;
+            for (int32_t t = cta_set; t < args.num_tiles; t += cta_sets) {
+                int32_t mb, nb;
+                tile_coords(t, args, mb, nb);
+                const int32_t n0 = nb * kCols;
+                const int32_t row0 = mb * Cfg::TILE_M + static_cast<int32_t>(role) * Cfg::BM +
+                                     32 * static_cast<int32_t>(q);
+                const int32_t my_row = row0 + static_cast<int32_t>(lane);
+                const int32_t nchunks = min(kCols / 32, (args.N - n0 + 31) / 32);
+                // 32 columns from col0 of this warp's rows of one output matrix
+                auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, bool tail,
+                                void *ptr, int64_t ld, int kind, int32_t col0) {
+                    if (!tma || (tail && col0 + 32 > args.N)) {
+                        if (my_row >= args.M)
+                            return;
+                        const int64_t o = static_cast<int64_t>(my_row) * ld + col0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (col0 + i < args.N) {
+                                if (kind == kOutF32)
+                                    static_cast<float *>(ptr)[o + i] = v[i];
+                                else
+                                    static_cast<unsigned short *>(ptr)[o + i] =
+                                        kind == kOutBF16 ? f32_to_bf16_rn(v[i]) : f32_to_f16_rn(v[i]);
+                            }
+                        }
+                        return;
+                    }
+                    const uint32_t buf = buf0 + static_cast<uint32_t>(slot) * Cfg::EPI_BUF;
+                    slot ^= 1;
+                    if (lane == 0)
+                        bulk_wait_group_read<1>();  // the store before the last has left this buffer
+                    __syncwarp();
+                    if (kind == kOutF32) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(buf + swz_off(lane, i, 128u), __float_as_uint(v[4 * i]),
+                                         __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                         __float_as_uint(v[4 * i + 3]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = kind == kOutBF16 ? pack_bf16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1])
+                                                        : pack_f16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+                            st_shared_v4(buf + swz_off(lane, i, 64u), w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d_hint(map, buf, col0, row0, epi_policy);
+                        bulk_commit_group();
+                    }
+                };
+                if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status,
+                                             args.timeout_ns, kWhereEpiAccFull))
+                    return false;
+                tc_fence_after_sync();
+                for (int32_t c = 0; c < kCols / 32; ++c) {
+                    float g[32], u[32];
+                    if (c < nchunks) {
+                        const uint32_t col = tmem_base + ((32u * q) << 16) +
+                                             static_cast<uint32_t>(ab * kIss * TILE_N + 32 * c);
+                        uint32_t rg[32], ru[32];
+                        tc_ld_32x32b_x32(col, rg);
+                        tc_ld_32x32b_x32(col + kCols, ru);
+                        tc_wait_ld(rg);
+                        tc_wait_ld(ru);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            g[i] = acc_none ? 0.f : __uint_as_float(rg[i]);
+                            u[i] = acc_none ? 0.f : __uint_as_float(ru[i]);
+                        }
+                        if (kIss > 1 && args.num_k_blocks > 1) {
+                            tc_ld_32x32b_x32(col + TILE_N, rg);
+                            tc_ld_32x32b_x32(col + TILE_N + kCols, ru);
+                            tc_wait_ld(rg);
+                            tc_wait_ld(ru);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                g[i] = __fadd_rn(g[i], __uint_as_float(rg[i]));
+                                u[i] = __fadd_rn(u[i], __uint_as_float(ru[i]));
+                            }
+                        }
+                    }
+                    if (c == kCols / 32 - 1)
+                        release_unit(ab);
+                    if (c >= nchunks || row0 >= args.M)
+                        continue;
+                    const int32_t col0 = n0 + 32 * c;
+                    if (args.G != nullptr)
+                        emit(g, &two->d2, args.keep_tma, args.keep_tail_direct, args.G, args.ldg,
+                             keep_kind, col0);
+                    if (args.U != nullptr)
+                        emit(u, &two->d3, args.keep_tma, args.keep_tail_direct, args.U, args.ldu,
+                             keep_kind, col0);
+                    with_act(args.act, [&](auto tag) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            g[i] = act_value<decltype(tag)::value>(g[i]) * u[i];
+                    });
+                    emit(g, &tmD, args.d_tma, args.d_tail_direct, args.D, args.ldd, out_kind, col0);
+                }
+                if (++ab == Cfg::NUM_ACC) {
+                    ab = 0;
+                    aph ^= 1u;
+                }
+            }
+            return true;
+        };
+        if constexpr (kGated) {
+            alive = gated_epilogue();
+        }
+        for (int32_t t = cta_set; !kGated && t < args.num_tiles && alive; t += cta_sets) {
             int32_t mb, nb;
             tile_coords(t, args, mb, nb);
             if (MC > 1)
                 nb = nb * MC + static_cast<int32_t>(share);
+            // (two sources stacked along M: the second has its own rows and D)
+            const bool second_m = MAJ != 0 && mb >= args.m2_block;
+            const CUtensorMap *const map_d = second_m ? &two->d2 : &tmD;
+            void *const out_d = second_m ? args.D2 : args.D;
+            const int64_t out_ld = second_m ? args.ldd2 : args.ldd;
+            if (second_m)
+                mb -= args.m2_block;
             const int32_t m0 = mb * Cfg::TILE_M + static_cast<int32_t>(role) * Cfg::BM;
             const int32_t n0 = nb * TILE_N;
             const int32_t row0 = m0 + 32 * (int32_t)q;
@@ -877,18 +1098,18 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
             auto store_direct = [&](const float(&v)[32], int32_t col0) {
                 if (d_row < 0)
                     return;
-                const int64_t o = static_cast<int64_t>(d_row) * args.ldd + col0;
+                const int64_t o = static_cast<int64_t>(d_row) * out_ld + col0;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     if (col0 + i < args.N) {
                         if (reduce)
-                            atomicAdd(static_cast<float *>(args.D) + o + i, v[i]);
+                            atomicAdd(static_cast<float *>(out_d) + o + i, v[i]);
                         else if (out_kind == kOutF32)
-                            static_cast<float *>(args.D)[o + i] = v[i];
+                            static_cast<float *>(out_d)[o + i] = v[i];
                         else if (out_kind == kOutBF16)
-                            static_cast<unsigned short *>(args.D)[o + i] = f32_to_bf16_rn(v[i]);
+                            static_cast<unsigned short *>(out_d)[o + i] = f32_to_bf16_rn(v[i]);
                         else
-                            static_cast<unsigned short *>(args.D)[o + i] = f32_to_f16_rn(v[i]);
+                            static_cast<unsigned short *>(out_d)[o + i] = f32_to_f16_rn(v[i]);
                     }
                 }
             };
@@ -1016,11 +1237,11 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                     if (!scatter) {
                         if (lane == 0) {
                             if (reduce)
-                                tma_reduce_add_2d_hint(&tmD, buf, col0, row0, epi_policy);
+                                tma_reduce_add_2d_hint(map_d, buf, col0, row0, epi_policy);
                             else if (TCG_EPI_EVICT_FIRST)
-                                tma_store_2d_hint(&tmD, buf, col0, row0, epi_policy);
+                                tma_store_2d_hint(map_d, buf, col0, row0, epi_policy);
                             else
-                                tma_store_2d(&tmD, buf, col0, row0);
+                                tma_store_2d(map_d, buf, col0, row0);
                             bulk_commit_group();
                         }
                     } else {
@@ -1028,7 +1249,7 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
                         // float32 output, 128-byte swizzled image)
                         if (lane < 8) {
                             if (issue_group_whole)
-                                tma_scatter4_hint(&tmD, buf + 512u * lane, col0, grp_rows[0],
+                                tma_scatter4_hint(map_d, buf + 512u * lane, col0, grp_rows[0],
                                                   grp_rows[1], grp_rows[2], grp_rows[3], epi_policy);
                             bulk_commit_group();
                         }
@@ -1089,6 +1310,35 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
     // kernel in the stream, which waits for this grid, waits for both
     if (args.co_tail)
         grid_dependency_wait();
+}
+
+template <int BN, int STAGES, bool PAIR, int NSUB, int MC, int MODE, int MX = 0>
+__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREADS, 1)
+    tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC,
+                     const __grid_constant__ CUtensorMap tmD,
+                     const __grid_constant__ CUtensorMap tmSFA,
+                     const __grid_constant__ CUtensorMap tmSFB, const GemmArgs args)
+{
+    tile_gemm_body<BN, STAGES, PAIR, NSUB, MC, MODE, MX, 0>(tmA, tmB, tmC, tmD, tmSFA, tmSFB, nullptr,
+                                                            args);
+}
+
+// The gated form, and operands stored K x M / K x N (MAJ), with the second
+// source's descriptors.
+template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
+__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, 1, MX>::THREADS, 1)
+    tile_gemm2_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmC,
+                      const __grid_constant__ CUtensorMap tmD,
+                      const __grid_constant__ CUtensorMap tmSFA,
+                      const __grid_constant__ CUtensorMap tmSFB,
+                      const __grid_constant__ TileMapsTwo two, const GemmArgs args)
+{
+    tile_gemm_body<BN, STAGES, PAIR, NSUB, 1, MODE, MX, MAJ>(tmA, tmB, tmC, tmD, tmSFA, tmSFB, &two,
+                                                             args);
 }
 
 }  // namespace tcg

@@ -59,6 +59,37 @@ inline int tile_max_pairs_or(int mx, int fallback)
 cudaError_t launch_tile_mx(int mx, int bn, bool pair, const GemmMaps &maps, const GemmArgs &args,
                            int grid, cudaStream_t stream);
 
+// Gated form (D = act(A Bg^T) * (A Bu^T)): single CTAs with 128 x bn accumulator
+// tiles (bn 64, 128, 256), or CTA pairs with 256 x 256 ones; D tiles are bn / 2
+// wide.  maps.b / two.b2: Bg / Bu in boxes of bn / 2 rows; maps.d, two.d2,
+// two.d3: D, G, U.  The mx form takes packed FP4 codes (maps.sfa, maps.sfb,
+// two.sfb2: scales of A, Bg and Bu; single CTAs, bn 128 or 256).
+cudaError_t launch_tile_gated(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
+                              const GemmArgs &args, int grid, cudaStream_t stream);
+cudaError_t launch_tile_gated_mx(int bn, const GemmMaps &maps, const TileMapsTwo &two,
+                                 const GemmArgs &args, int grid, cudaStream_t stream);
+
+// Operands stored K x M (maj bit 0) or K x N (bit 1), boxes of 64 columns x 64 K
+// rows; two: the second source along K or M.  Forms: single CTAs (bn 64, 128,
+// 256) and CTA pairs (256 x 256, or 256 x 512 with nsub = 2).
+cudaError_t launch_tile_major(int maj, int bn, bool pair, int nsub, const GemmMaps &maps,
+                              const TileMapsTwo &two, const GemmArgs &args, int grid,
+                              cudaStream_t stream);
+
+// dG = dD * U * act'(G), dU = dD * act(G) over M x N, 16-bit (bf16 or f16)
+// matrices; dG may be G and dU may be U.
+cudaError_t launch_gated_slope(const void *dD, int64_t lddd, const void *G, int64_t ldg,
+                               const void *U, int64_t ldu, void *dG, int64_t lddg, void *dU,
+                               int64_t lddu, int32_t M, int32_t N, bool bf16, int32_t act,
+                               cudaStream_t stream);
+
+// X (M x K; type kOutF32 / kOutBF16 / kOutF16) -> E2M1 codes Q (rows of K / 2
+// bytes) and UE8M0 scales S (K / 32 rows of M bytes); Y (NULL: none): the
+// values they stand for, in X's type.
+cudaError_t launch_quantize_e2m1(const void *X, int64_t ldx, int type, uint8_t *Q, int64_t ldq,
+                                 uint8_t *S, int64_t lds, void *Y, int64_t ldy, int32_t M, int32_t K,
+                                 cudaStream_t stream);
+
 // Warp-level tiny-GEMM kernel: one 16 x 8 block of D per warp.
 int tiny_warps_per_cta();
 cudaError_t launch_tiny(const void *A, int64_t lda, const void *B, int64_t ldb,
@@ -88,6 +119,11 @@ cudaError_t launch_skinny_mx(int mp, const GemmMaps &maps, const GemmArgs &args,
                              cudaStream_t stream);
 cudaError_t launch_skinny(int mp, const GemmMaps &maps, const GemmArgs &args, int grid,
                           cudaStream_t stream);
+// The gated form of the 16-bit and (mx) both-FP4 kernels: maps.b / two.b2: Bg / Bu
+// in boxes of 64 rows; (mx) maps.c / two.sfb2: their scales in boxes of 64
+// columns, maps.sfa: A's.  Tiles are 64 columns of D.
+cudaError_t launch_skinny_gated(int mp, bool mx, const GemmMaps &maps, const TileMapsTwo &two,
+                                const GemmArgs &args, int grid, cudaStream_t stream);
 
 // Stream-K split of the skinny kernel: the CTA that owns linear k-block x
 // when W blocks are shared by G CTAs as [W g / G, W (g+1) / G).

@@ -1,0 +1,51 @@
+// launch_skinny_gated.cu -- the swap-AB stream-K kernel's gated-form
+// instantiations (16-bit operands, or both FP4 on the block-scaled MMA).
+#include <cuda_runtime.h>
+
+#include "kernel_skinny.cuh"
+#include "launch.h"
+
+namespace tcg {
+
+namespace {
+
+template <int MP, bool MX>
+cudaError_t launch_skinny_gated_impl(const GemmMaps &maps, const TileMapsTwo &two, const GemmArgs &args,
+                                     int grid, cudaStream_t stream)
+{
+    using Cfg = SkinnyCfg<MP, 1, false, MX, true>;
+    auto kfn = skinny_gated_kernel<MP, 1, MX>;
+    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Cfg::SMEM_ALLOC));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_ALLOC;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = TCG_PDL;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kfn, maps.a, maps.b, maps.c, maps.sfa, two.b2, two.sfb2, args);
+}
+
+}  // namespace
+
+cudaError_t launch_skinny_gated(int mp, bool mx, const GemmMaps &maps, const TileMapsTwo &two,
+                                const GemmArgs &args, int grid, cudaStream_t stream)
+{
+    switch (mp) {
+    case 16: return mx ? launch_skinny_gated_impl<16, true>(maps, two, args, grid, stream)
+                       : launch_skinny_gated_impl<16, false>(maps, two, args, grid, stream);
+    case 32: return mx ? launch_skinny_gated_impl<32, true>(maps, two, args, grid, stream)
+                       : launch_skinny_gated_impl<32, false>(maps, two, args, grid, stream);
+    case 64: return mx ? launch_skinny_gated_impl<64, true>(maps, two, args, grid, stream)
+                       : launch_skinny_gated_impl<64, false>(maps, two, args, grid, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tcg

@@ -56,6 +56,54 @@ cudaError_t tile_launch_impl(const GemmMaps &maps, const GemmArgs &args, int gri
     return cudaLaunchKernelEx(&cfg, kfn, maps.a, maps.b, maps.c, maps.d, maps.sfa, maps.sfb, args);
 }
 
+// The two-source kernels (gated form; operands stored K x M / K x N).
+template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
+cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, const GemmArgs &args,
+                              int grid, cudaStream_t stream)
+{
+    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, 1, MX>;
+    auto kfn = tile_gemm2_kernel<BN, STAGES, PAIR, NSUB, MODE, MX, MAJ>;
+    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Cfg::SMEM_ALLOC));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    tile_fill_config<BN, STAGES, PAIR, NSUB, 1, MX>(cfg, attr, grid, stream);
+    return cudaLaunchKernelEx(&cfg, kfn, maps.a, maps.b, maps.c, maps.d, maps.sfa, maps.sfb, two, args);
+}
+
+template <int MAJ>
+cudaError_t launch_tile_major_impl(int bn, bool pair, int nsub, const GemmMaps &maps,
+                                   const TileMapsTwo &two, const GemmArgs &args, int grid,
+                                   cudaStream_t stream)
+{
+    if (pair) {
+        if (bn != 256)
+            return cudaErrorInvalidValue;
+        return nsub == 2
+                   ? tile_launch2_impl<256, 4, true, 2, kModePlain, 0, MAJ>(maps, two, args, grid, stream)
+                   : tile_launch2_impl<256, 6, true, 1, kModePlain, 0, MAJ>(maps, two, args, grid, stream);
+    }
+    switch (bn) {
+    case 256: return tile_launch2_impl<256, 4, false, 1, kModePlain, 0, MAJ>(maps, two, args, grid, stream);
+    case 128: return tile_launch2_impl<128, 6, false, 1, kModePlain, 0, MAJ>(maps, two, args, grid, stream);
+    case 64: return tile_launch2_impl<64, 8, false, 1, kModePlain, 0, MAJ>(maps, two, args, grid, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+// (defined, one storage each, in launch_tile_major_{a,b,ab}.cu)
+extern template cudaError_t launch_tile_major_impl<kMajA>(int, bool, int, const GemmMaps &,
+                                                          const TileMapsTwo &, const GemmArgs &, int,
+                                                          cudaStream_t);
+extern template cudaError_t launch_tile_major_impl<kMajB>(int, bool, int, const GemmMaps &,
+                                                          const TileMapsTwo &, const GemmArgs &, int,
+                                                          cudaStream_t);
+extern template cudaError_t launch_tile_major_impl<kMajA | kMajB>(int, bool, int, const GemmMaps &,
+                                                                  const TileMapsTwo &, const GemmArgs &,
+                                                                  int, cudaStream_t);
+
 // Every form of the tile kernel, for epilogue mode MODE.
 template <int MODE>
 cudaError_t launch_tile_mode(int bn, bool pair, int nsub, int mc, const GemmMaps &maps,

@@ -697,6 +697,26 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t smem_addr)
     return d;
 }
 
+// Shared-memory matrix descriptor for an operand stored K x MN (the M or N
+// index contiguous, "MN-major"), as a TMA load with CU_TENSOR_MAP_SWIZZLE_128B
+// writes its boxes of 64 columns x 64 K rows: rows of 64 x 16-bit elements
+// (128 B), one per K index, in 8-row groups of 1024 B; boxes side by side along
+// MN are 8192 B apart.  A K step of 16 is two 8-row groups: +2048 bytes on the
+// start address, which stays 1024-byte aligned.
+//   bits 16-29  leading-dimension byte offset >> 4 (8192 B to the next 64 of MN)
+//   bits 32-45  stride byte offset >> 4 (1024 B to the next 8 of K)
+//   the rest as in sdesc_k_sw128
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 // Shared-memory descriptor of an unswizzled image made of 8-row groups of
 // 16-byte rows, the groups 128 bytes apart (the source of tcgen05.cp 32x128b:
 // 32 rows of 16 bytes, contiguous).  16-byte aligned base; layout 0 = none.
@@ -729,13 +749,14 @@ __host__ __device__ constexpr uint32_t idesc_mx(uint32_t fmt, uint32_t m, uint32
 //   bits  4-5   D format (1 = f32)
 //   bits  7-9   A format (0 = f16, 1 = bf16)
 //   bits 10-12  B format (same code)
-//   bit  15/16  A/B major (0 = K-major)
+//   bit  15/16  A/B major (0 = K-major, 1 = MN-major)
 //   bits 17-22  N >> 3
 //   bits 24-28  M >> 4
-__host__ __device__ constexpr uint32_t idesc_f16_f32acc(bool bf16, uint32_t m, uint32_t n)
+__host__ __device__ constexpr uint32_t idesc_f16_f32acc(bool bf16, uint32_t m, uint32_t n,
+                                                        bool a_mn = false, bool b_mn = false)
 {
-    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((n >> 3) << 17) |
-           ((m >> 4) << 24);
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // ---------------------------------------------------------------- epilogue math

@@ -1,0 +1,124 @@
+"""gemm_trans (operands stored K x M / K x N) on the GPU (needs a GB300): quarter-integers
+compare bit for bit with 64-bit sums (every partial sum is exact in float32), normal
+inputs within gated_ref's sum bound."""
+import numpy as np
+import pytest
+import torch
+
+import gated_ref as ref
+from gated_ref import assert_close, wide
+from gpu_helpers import device_status
+from tensor_core_gemm_02_gb300 import binding
+from tensor_core_gemm_02_gb300.workloads import OUT_BF16, OUT_F16, OUT_F32
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+STORED = [(False, True), (True, True), (True, False), (False, False)]
+FORMS = {"auto": (0, 0), "single64": (1, 64), "single128": (1, 128), "single256": (1, 256),
+         "pair256": (3, 256), "pair512": (4, 512)}
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    binding.gemm_debug_force_tile(0, 0)
+    assert device_status() == binding.GEMM_OK
+    yield
+    binding.gemm_debug_force_tile(0, 0)
+    assert device_status() == binding.GEMM_OK
+
+
+def operands(seed, M, N, K, ta, tb, dtype, exact):
+    r = torch.Generator().manual_seed(seed)
+    A = wide(K if ta else M, M if ta else K, dtype, r, exact=exact)
+    B = wide(K if tb else N, N if tb else K, dtype, r, exact=exact)
+    return A, B, wide(M, N, torch.float32, r, exact=exact)
+
+
+def product(A, B, ta, tb):
+    a, b = A.cpu().double(), B.cpu().double()
+    a, b = (a.T if ta else a), (b if tb else b.T)
+    return a @ b, a.abs() @ b.abs()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+def test_exact_every_form(form, ta, tb):
+    binding.gemm_debug_force_tile(*FORMS[form])
+    for M, N, K in ((1, 1, 1), (128, 256, 64), (129, 70, 63), (300, 520, 65), (40, 1030, 328), (513, 515, 200)):
+        for dtype, out in ((BF16, OUT_F32), (F16, OUT_BF16), (BF16, OUT_F16)):
+            A, B, C = operands(M + N + K, M, N, K, ta, tb, dtype, True)
+            s, _ = product(A, B, ta, tb)
+            got = binding.gemm_trans(A, B, C, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=out)
+            want = (0.5 * s + 2.0 * C.cpu().double()).float().to(ref.out_dtype(out))
+            assert torch.equal(got.cpu(), want), (form, M, N, K, dtype, out)
+            got = binding.gemm_trans(A, B, trans_a=ta, trans_b=tb, out=out)
+            assert torch.equal(got.cpu(), s.float().to(ref.out_dtype(out))), (form, M, N, K, dtype, out)
+
+
+@pytest.mark.parametrize("ta,tb", STORED)
+@pytest.mark.parametrize("M,N,K,dtype,out", [(1, 300, 4096, BF16, OUT_F32), (64, 4096, 1000, F16, OUT_F16),
+                                             (500, 264, 4100, BF16, OUT_BF16)])
+def test_random_within_bound(ta, tb, M, N, K, dtype, out):
+    A, B, C = operands(K, M, N, K, ta, tb, dtype, False)
+    s, t = product(A, B, ta, tb)
+    d = 0.5 * s + C.cpu().double()
+    e = 0.5 * ref.sum_bound(K) * t + (d.abs() + t) * 2.0 ** -23
+    got = binding.gemm_trans(A, B, C, trans_a=ta, trans_b=tb, alpha=0.5, out=out)
+    assert_close(got, d, e + ref.rounding(d.abs() + e, out), f"{ta} {tb}")
+
+
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+def test_in_place_unaligned_and_k_zero(ta, tb):
+    M, N, K = 70, 45, 96
+    A, B, C = operands(3, M, N, K, ta, tb, F16, True)
+    s, _ = product(A, B, ta, tb)
+    want = (s + C.cpu().double()).float()
+    acc = C.clone()
+    binding.gemm_trans(A, B, acc, acc, trans_a=ta, trans_b=tb)  # accumulated onto D itself
+    assert torch.equal(acc.cpu(), want)
+    buf = torch.full((M, N + 5), 9.0, device="cuda")
+    binding.gemm_trans(A, B, C, buf[:, 3:3 + N], trans_a=ta, trans_b=tb)  # D at an odd address
+    assert torch.equal(buf[:, 3:3 + N].cpu(), want)
+    assert (buf[:, :3] == 9.0).all() and (buf[:, 3 + N:] == 9.0).all()
+    a0 = torch.empty((0, M) if ta else (M, 0), dtype=F16, device="cuda")
+    b0 = torch.empty((0, N) if tb else (N, 0), dtype=F16, device="cuda")
+    D = binding.gemm_trans(a0, b0, C, trans_a=ta, trans_b=tb, beta=0.5)
+    assert torch.equal(D, 0.5 * C)
+    assert (binding.gemm_trans(a0, b0, trans_a=ta, trans_b=tb) == 0).all()
+
+
+def test_nan_stays_in_its_row():
+    A, B, _ = operands(5, 200, 130, 264, True, True, BF16, True)
+    clean = binding.gemm_trans(A, B, trans_a=True, trans_b=True)
+    A[9, 4] = float("nan")  # K row 9 of column 4: row 4 of D
+    D = binding.gemm_trans(A, B, trans_a=True, trans_b=True)
+    rows = torch.arange(200, device="cuda") != 4
+    assert torch.isnan(D[4]).all() and torch.equal(D[rows], clean[rows])
+
+
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+def test_timeout_reports_and_recovers(ta, tb):
+    A, B, _ = operands(6, 300, 300, 512, ta, tb, BF16, True)
+    good = binding.gemm_trans(A, B, trans_a=ta, trans_b=tb)
+    assert device_status() == binding.GEMM_OK
+    binding.gemm_set_wait_timeout(50_000_000)
+    binding.gemm_debug_inject(1)
+    try:
+        binding.gemm_trans(A, B, trans_a=ta, trans_b=tb)
+        assert device_status() == binding.GEMM_ERR_TIMEOUT
+    finally:
+        binding.gemm_debug_inject(0)
+        binding.gemm_set_wait_timeout(0)
+    assert torch.equal(binding.gemm_trans(A, B, trans_a=ta, trans_b=tb), good)
+
+
+def test_linear_layer_gradients_match_the_stored_transposes():
+    """dX = dY W and dW = dY^T X read in place equal the plain products of transposed copies."""
+    r = torch.Generator().manual_seed(1)
+    X, W, dY = (wide(m, n, BF16, r, exact=True) for m, n in ((200, 136), (264, 136), (200, 264)))
+    dX = binding.gemm_trans(dY, W, trans_b=True)
+    dW = binding.gemm_trans(dY, X, trans_a=True, trans_b=True)
+    assert torch.equal(dX, binding.gemm_bf16(dY, W.T.contiguous()))
+    assert torch.equal(dW, binding.gemm_bf16(dY.T.contiguous(), X.T.contiguous()))
+    assert np.isfinite(dW.cpu().numpy()).all()
