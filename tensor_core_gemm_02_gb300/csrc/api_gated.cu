@@ -504,7 +504,7 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
     p.kernel = 11;
     p.bm = 128;
     p.bn = bn;
-    p.stages = tcg::tile_mx_stages(1, bn, false);
+    p.stages = tcg::tile_gated_mx_stages(bn);
     p.tiles = ceil_div(M, 128) * ceil_div(N, bn / 2);
     p.splits = 1;
     p.grid = static_cast<int32_t>(p.tiles < sm_count ? p.tiles : sm_count);

@@ -79,11 +79,24 @@ __global__ void __launch_bounds__(256)
             *reinterpret_cast<uint4 *>(qg) = make_uint4(og[0], og[1], og[2], og[3]);
             *reinterpret_cast<uint4 *>(qu) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
         } else {
-            for (int i = 0; i < 8 && col + i < N; ++i) {
-                float dg, du;
-                slope_one<ACT>(widen<BF16>(pd[i]), widen<BF16>(pg[i]), widen<BF16>(pu[i]), dg, du);
-                qg[i] = BF16 ? f32_to_bf16_rn(dg) : f32_to_f16_rn(dg);
-                qu[i] = BF16 ? f32_to_bf16_rn(du) : f32_to_f16_rn(du);
+            // (all loads before the first store: one round trip, not one per element)
+            const int n = N - col < 8 ? static_cast<int>(N - col) : 8;
+            unsigned short d[8], g[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = i < n;
+                d[i] = in ? pd[i] : 0;
+                g[i] = in ? pg[i] : 0;
+                u[i] = in ? pu[i] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i < n) {
+                    float dg, du;
+                    slope_one<ACT>(widen<BF16>(d[i]), widen<BF16>(g[i]), widen<BF16>(u[i]), dg, du);
+                    qg[i] = BF16 ? f32_to_bf16_rn(dg) : f32_to_f16_rn(dg);
+                    qu[i] = BF16 ? f32_to_bf16_rn(du) : f32_to_f16_rn(du);
+                }
             }
         }
     }

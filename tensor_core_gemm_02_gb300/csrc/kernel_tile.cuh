@@ -53,9 +53,15 @@
 
 namespace tcg {
 
-template <int BN_, int STAGES_, bool PAIR_ = false, int NSUB_ = 1, int MC_ = 1, int MX_ = 0>
+template <int BN_, int STAGES_, bool PAIR_ = false, int NSUB_ = 1, int MC_ = 1, int MX_ = 0,
+          bool GATED_ = false>
 struct TileCfg {
     static constexpr bool PAIR = PAIR_;
+    // LAP (gated form, FP4 tiles 256 wide): two 256-column accumulators that
+    // overlap, so that the epilogue of one tile still runs beside the next tile's
+    // MMAs although the block scales need columns too (below).
+    static constexpr bool GATED = GATED_;
+    static constexpr bool LAP = GATED && MX_ != 0 && BN_ == 256;
     // MX: operand kind.  0 = f16/bf16 (tcgen05 kind::f16); 1 = FP4 E2M1 codes
     // packed two per byte (kind::mxf4); 2 = FP4 codes in the 16U4_ALIGN16B TMA
     // image, sixteen codes in the low 8 bytes of each 16-byte block
@@ -80,7 +86,7 @@ struct TileCfg {
     // Accumulators: two (the epilogue of one tile overlaps the next tile's
     // MMAs), except for two-half tiles and for FP4 tiles 256 wide, whose block
     // scales need TMEM columns beside the one 256-column accumulator.
-    static constexpr int NUM_ACC = (NSUB == 1 && !(MX != 0 && BN == 256)) ? 2 : 1;
+    static constexpr int NUM_ACC = (NSUB == 1 && (LAP || !(MX != 0 && BN == 256))) ? 2 : 1;
     static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // rows of B per half each CTA loads
     // K elements per stage: one 128-byte swizzle row of each operand row
     // (64 x 16-bit, 256 packed FP4 codes, or 128 codes in the 16U4 image)
@@ -117,8 +123,13 @@ struct TileCfg {
     static constexpr uint32_t OFF_B = STAGES * A_BYTES;
     static constexpr uint32_t OFF_SFS = STAGES * STAGE_BYTES;             // scales as loaded
     static constexpr uint32_t OFF_SFC = OFF_SFS + STAGES * SF_STAGE_BYTES;  // rearranged
-    static constexpr uint32_t OFF_EPI = OFF_SFC + STAGES * SF_CP_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_EPI + 8 * EPI_BUF;  // 4 warps x 2 buffers
+    // (gated: one rearranged image, its tiles being read out at once)
+    static constexpr int SFC_BUFS = GATED ? 1 : STAGES;
+    static constexpr uint32_t OFF_EPI = OFF_SFC + SFC_BUFS * SF_CP_BYTES;
+    // 4 warps x 2 buffers; LAP: 4 KB a warp (one float32 box or two 16-bit ones),
+    // which makes room for a fourth stage
+    static constexpr uint32_t EPI_BYTES = (LAP ? 4 : 8) * EPI_BUF;
+    static constexpr uint32_t OFF_BAR = OFF_EPI + EPI_BYTES;
     static constexpr uint32_t NUM_BARS = 2 * STAGES + 4 + 8 + (MX ? 2 * STAGES : 0);
     static constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
@@ -130,11 +141,21 @@ struct TileCfg {
     // that takes every other K block into an accumulator of its own; the
     // epilogue adds the two.  (Pairs and wider tiles are tensor-bound.)
     static constexpr int ISS = (!PAIR && MC == 1 && NSUB == 1 && BN <= 128 && MX == 0) ? 2 : 1;
-    static constexpr uint32_t ACC_COLS = NUM_ACC * TILE_N * ISS;  // fp32 accumulators
+    // LAP: the second accumulator starts ACC2_COL columns in and shares TILE_N -
+    // ACC2_COL of them with the first; the scales take two buffers of SF_COLS
+    // columns in turn (otherwise one per stage).  The MMAs of a tile start once
+    // the epilogue has read the shared columns of the tile before.
+    static constexpr uint32_t SF_BUFS = LAP ? 2u : static_cast<uint32_t>(STAGES);
+    static constexpr uint32_t ACC2_COL = LAP ? 512u - SF_BUFS * SF_COLS - TILE_N : TILE_N * ISS;
+    static constexpr uint32_t ACC_COLS = LAP ? ACC2_COL + TILE_N : NUM_ACC * TILE_N * ISS;  // fp32 accumulators
     static constexpr uint32_t SF_COL0 = ACC_COLS;                 // first scale column (FP4)
     static constexpr uint32_t TMEM_COLS = MX ? 512u : ACC_COLS;
     // warp 6: the second MMA issuer, or (FP4) the scale warp
-    static constexpr int THREADS = 192 + 32 * (ISS - 1) + (MX ? 32 : 0);
+    // (FP4) scale warps: one that rearranges a stage's scales for the MMA thread to
+    // copy; or (gated) four, one per quarter of TMEM lanes, that also store them
+    // into TMEM themselves
+    static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 4 : 1);
+    static constexpr int THREADS = 192 + 32 * (ISS - 1) + 32 * SCALE_WARPS;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "tile width");
     static_assert(NSUB == 1 || NSUB == 2, "one or two halves");
@@ -146,7 +167,9 @@ struct TileCfg {
                   "TMEM allocation must be a power of two in [32, 512]");
     static_assert(MX == 0 || (MC == 1 && NSUB == 1 && (BN == 256 || (BN == 128 && !PAIR))),
                   "FP4 operands: single CTAs with tiles 128 or 256 wide, or pairs with 256 x 256 tiles");
-    static_assert(MX == 0 || SF_COL0 + STAGES * SF_COLS <= 512, "TMEM for the block scales");
+    static_assert(MX == 0 || SF_COL0 + SF_BUFS * SF_COLS <= 512, "TMEM for the block scales");
+    static_assert(!LAP || (MX != 0 && BN == 256 && NSUB == 1 && ACC2_COL >= TILE_N - 64 && STAGES >= 3),
+                  "overlapping accumulators: FP4 tiles 256 wide, at most 64 columns shared");
 };
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled box image
@@ -158,6 +181,24 @@ __device__ __forceinline__ uint32_t swz_off(uint32_t row, uint32_t chunk, uint32
     const uint32_t mask = row_bytes / 16u - 1u;  // 7 or 3
     return lin ^ (((lin >> 7) & mask) << 4);
 }
+
+// Barrier 1 among the gated form's four scale warps, agreeing on whether any
+// thread found `p`.
+__device__ __forceinline__ bool scale_bar_any(bool p)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(p ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void scale_bar_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
 // Epilogue modes, a template parameter so that each kernel carries only its own:
 // the fma.rn epilogue with optional C, rows scattered through idx, reduce-add
@@ -182,8 +223,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                                const CUtensorMap &tmSFA, const CUtensorMap &tmSFB,
                                                const TileMapsTwo *two, const GemmArgs &args)
 {
-    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>;
     constexpr bool kGated = MODE == kModeGated;
+    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX, kGated>;
     constexpr bool kTwo = kGated || MAJ != 0;  // loads go through load_stage_two
     static_assert(!kTwo || MC == 1, "two-source forms: no A multicast");
     static_assert(!kGated || (NSUB == 1 && MAJ == 0), "gated form: one MMA half, K-major operands");
@@ -322,7 +363,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         if (MX)
             for (int st = 0; st < STAGES; ++st) {
                 mbar_init(sf_full_bar(st), 1);
-                mbar_init(sf_bar(st), PAIR ? 2 : 1);
+                mbar_init(sf_bar(st), kGated ? Cfg::SCALE_WARPS : (PAIR ? 2 : 1));
             }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -547,6 +588,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
             int ab = 0;
             uint32_t aph = 0;
             bool alive = true;
+            [[maybe_unused]] uint32_t tiles_begun = 0, blocks_begun = 0;  // (LAP)
             // K block kb of MMA half j on stage st into the accumulator at d_tmem
             // seeded accumulators (C written to TMEM by the epilogue) are
             // accumulated onto from the first K step on
@@ -562,13 +604,16 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 constexpr uint32_t kStepB = (MAJ & kMajB) != 0 ? 128u : 2u;
                 const uint32_t dj = d_tmem + static_cast<uint32_t>(j * BN);
                 if constexpr (MX != 0) {
-                    // the stage's scale tiles into its TMEM columns, then four
-                    // block-scaled MMAs of 32 bytes of K each; MMA k reads the
-                    // scales of its 128-element chunk, the byte(s) its scale ids pick
+                    // the stage's scale tiles into its TMEM columns (gated: the scale
+                    // warps have put them there), then four block-scaled MMAs of 32
+                    // bytes of K each; MMA k reads the scales of its 128-element
+                    // chunk, the byte(s) its scale ids pick
                     const uint32_t sfc = base + Cfg::OFF_SFC + st * Cfg::SF_CP_BYTES;
-                    const uint32_t sfcol = tmem_base + Cfg::SF_COL0 + st * Cfg::SF_COLS;
+                    const uint32_t sfcol =
+                        tmem_base + Cfg::SF_COL0 +
+                        (Cfg::LAP ? (blocks_begun & 1u) : static_cast<uint32_t>(st)) * Cfg::SF_COLS;
 #pragma unroll
-                    for (int ti = 0; ti < Cfg::SF_TILES; ++ti) {
+                    for (int ti = 0; ti < (kGated ? 0 : Cfg::SF_TILES); ++ti) {
                         if (PAIR)
                             tc_cp_32x128b_warpx4_pair(sfcol + 4u * ti, sdesc_rows16(sfc + 512u * ti));
                         else
@@ -644,6 +689,16 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 return true;
             };
             auto wait_acc_free = [&](int b) {
+                if constexpr (Cfg::LAP) {
+                    // the epilogue has read the columns that the tile before shares with
+                    // this one (and, working in order, all of the tile before that)
+                    const uint32_t n = tiles_begun++;
+                    if (n > 0 && !wait_bounded<true>(acce_bar(0), (n - 1u) & 1u, abort_flag, args.status,
+                                                     args.timeout_ns, kWhereMmaAccEmpty))
+                        return false;
+                    tc_fence_after_sync();
+                    return true;
+                }
                 // (seeded: the epilogue's first arrival is the seed, so the first
                 // use waits for it instead of passing on a fresh barrier)
                 if (!wait_bounded<true>(acce_bar(b), seeded ? aph : aph ^ 1u, abort_flag, args.status,
@@ -658,7 +713,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     if (!wait_acc_free(ab))
                         break;
                     const uint32_t d_tmem =
-                        tmem_base + static_cast<uint32_t>((ab * kIss + e) * TILE_N);
+                        tmem_base + (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
+                                              : static_cast<uint32_t>((ab * kIss + e) * TILE_N));
                     for (int32_t kb = 0; kb < nkb; ++kb) {
                         if (kIss > 1 && kb % kIss != e) {
                             if (++s == STAGES) {  // the other issuer's stage
@@ -674,6 +730,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         }
                         issue_half(st, kb, 0, d_tmem);
                         free_stage(st);  // frees the stage (in both CTAs of a pair)
+                        ++blocks_begun;
                     }
                     if (!alive)
                         break;
@@ -746,6 +803,101 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
             }
         }
         __syncwarp();
+    } else if (kGated && MX != 0 && warp >= 6) {
+        // ------------------------------------------------------------ scale warps (gated)
+        // As the one scale warp of the plain form below rearranges a stage's scales,
+        // four share the 512-byte tiles out; each then stores all of them into its
+        // quarter of the TMEM lanes (lane l takes the 16 bytes of rows l, l + 32, l +
+        // 64, l + 96 of a tile), where the MMA thread would have to copy them to.
+        // Those copies cost the tensor pipe about 110 of 600 ns a stage (8192 x 14336
+        // x 4096); stores from other warps run beside the MMAs.
+        if constexpr (kGated && MX != 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool good = true;  // no wait of this warp has given up
+            [[maybe_unused]] uint32_t blocks = 0;  // (LAP) K blocks begun
+            // rows 4 lane .. 4 lane + 3 of tile ti: load their four blocks' bytes, transpose
+            // them and store row r's word at 16 (r % 32) + 4 (r / 32)
+            auto arrange = [&](const uint8_t *src, uint8_t *dst, int ti) {
+                const uint8_t *rows = src;
+                uint32_t pitch = Cfg::BM;
+                int c = ti;  // 128-element chunk of the tile
+                uint32_t r = 4u * lane;
+                if (ti >= Cfg::SF_CHUNKS) {
+                    // Bg's image, then Bu's, each of half the tile's rows
+                    c = (ti - Cfg::SF_CHUNKS) / Cfg::SF_B_ROWTILES;
+                    r += 128u * ((ti - Cfg::SF_CHUNKS) % Cfg::SF_B_ROWTILES);
+                    pitch = Cfg::TILE_N / 2;
+                    rows += Cfg::SF_KB * Cfg::BM + (r / pitch) * Cfg::SF_KB * pitch;
+                }
+                rows += 4u * c * pitch + r % pitch;
+                uint32_t w[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    w[b] = *reinterpret_cast<const uint32_t *>(rows + b * pitch);
+                const uint32_t t0 = __byte_perm(w[0], w[1], 0x5140);
+                const uint32_t t1 = __byte_perm(w[0], w[1], 0x7362);
+                const uint32_t t2 = __byte_perm(w[2], w[3], 0x5140);
+                const uint32_t t3 = __byte_perm(w[2], w[3], 0x7362);
+                const uint32_t o[4] = {__byte_perm(t0, t2, 0x5410), __byte_perm(t0, t2, 0x7632),
+                                       __byte_perm(t1, t3, 0x5410), __byte_perm(t1, t3, 0x7632)};
+                uint8_t *tile = dst + 512u * ti + 4u * (lane / 8u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint32_t *>(tile + 16u * ((4u * lane + i) % 32u)) = o[i];
+            };
+            bool alive = true;
+            for (int32_t t = cta_set; t < args.num_tiles && alive; t += cta_sets) {
+                for (int32_t kb = 0; kb < args.num_k_blocks; ++kb) {
+                    good = good && warp_wait_bounded<true>(sf_full_bar(s), ph, abort_flag, args.status,
+                                                           args.timeout_ns, kWhereMmaFull);
+                    const uint8_t *src = gbase + Cfg::OFF_SFS + s * Cfg::SF_STAGE_BYTES;
+                    uint8_t *dst = gbase + Cfg::OFF_SFC;
+                    scale_bar_sync();  // every warp has read the stage before out of the image
+                    for (int ti = static_cast<int>(warp) - 6; good && ti < Cfg::SF_TILES; ti += Cfg::SCALE_WARPS)
+                        arrange(src, dst, ti);
+                    // the tiles are whole; and the four warps agree, so that all or none go on
+                    if (scale_bar_any(!good)) {
+                        alive = false;
+                        break;
+                    }
+                    uint32_t r[Cfg::SF_COLS];
+#pragma unroll
+                    for (int ti = 0; ti < Cfg::SF_TILES; ++ti)
+                        ld_shared_v4(smem_u32(dst) + 512u * ti + 16u * lane, r[4 * ti], r[4 * ti + 1],
+                                     r[4 * ti + 2], r[4 * ti + 3]);
+                    uint32_t buf = static_cast<uint32_t>(s);
+                    if constexpr (Cfg::LAP) {
+                        // two buffers: the MMAs of the block before the last are done with
+                        // this one (they have freed their stage)
+                        buf = blocks & 1u;
+                        const uint32_t i = blocks - 2u;
+                        if (blocks >= 2u)
+                            good = warp_wait_bounded<true>(empty_bar(static_cast<int>(i % STAGES)),
+                                                           (i / STAGES) & 1u, abort_flag, args.status,
+                                                           args.timeout_ns, kWhereProducerEmpty);
+                        ++blocks;
+                    }
+                    if (good) {
+                        tc_fence_after_sync();
+                        const uint32_t at =
+                            tmem_base + ((32u * (warp & 3u)) << 16) + Cfg::SF_COL0 + buf * Cfg::SF_COLS;
+#pragma unroll
+                        for (int i = 0; i < static_cast<int>(Cfg::SF_COLS) / 8; ++i)
+                            tc_st_32x32b_x8(at + 8u * i, r + 8 * i);
+                        tc_wait_st();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(sf_bar(s));
+                    }
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
     } else if (MX != 0 && warp == 6) {
         // ------------------------------------------------------------ scale warp
         // For every stage: wait for its loads, rearrange the scale rows as loaded
@@ -756,7 +908,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         // for its four blocks, transposes the 4 x 4 bytes so that each word
         // holds one row's four blocks, and stores row r's word at 16 (r % 32) +
         // 4 (r / 32).
-        if constexpr (MX != 0) {
+        if constexpr (MX != 0 && !kGated) {
             int s = 0;
             uint32_t ph = 0;
             bool alive = true;
@@ -775,17 +927,9 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         const bool a_tile = ti < Cfg::SF_CHUNKS;
                         const int c = a_tile ? ti : (ti - Cfg::SF_CHUNKS) / Cfg::SF_B_ROWTILES;
                         const int rt = a_tile ? 0 : (ti - Cfg::SF_CHUNKS) % Cfg::SF_B_ROWTILES;
-                        uint32_t pitch = a_tile ? Cfg::BM : Cfg::TILE_N;
-                        const uint8_t *rows = src + (a_tile ? 0u : Cfg::SF_KB * Cfg::BM);
-                        if (kGated && !a_tile) {
-                            // Bg's image, then Bu's, each of half the tile's rows: rows
-                            // 128 rt + 4 lane ... of the tile lie in one of the two
-                            pitch = Cfg::TILE_N / 2;
-                            const uint32_t r = 128u * rt + 4u * lane;
-                            rows += (r / pitch) * Cfg::SF_KB * pitch + 4u * c * pitch + r % pitch;
-                        } else {
-                            rows += 128u * rt + 4u * c * pitch + 4u * lane;
-                        }
+                        const uint32_t pitch = a_tile ? Cfg::BM : Cfg::TILE_N;
+                        const uint8_t *rows = src + (a_tile ? 0u : Cfg::SF_KB * Cfg::BM) + 128u * rt +
+                                              4u * c * pitch + 4u * lane;
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             w[ti][b] = *reinterpret_cast<const uint32_t *>(rows + b * pitch);
@@ -905,12 +1049,15 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         // Gated form: per 32 columns of D, G from the left half of the accumulator
         // and U from the right half (with two issuers, both partial sums of each),
         // kept copies of G and U if asked for, then D = act(G) * U.  Returns false
-        // when a wait gave up.
+        // when a wait gave up.  (Eight epilogue warps, each with half of the
+        // columns, measured no faster: 8192 x 14336 x 4096 FP4 481 against 471 us,
+        // 777 x 2743 x 1000 f16 19.0 against 19.4.)
         auto gated_epilogue = [&]() -> bool {
             constexpr int32_t kCols = TILE_N / 2;  // columns of D per tile
+            constexpr int32_t kChunks = kCols / 32;
             const int keep_kind = args.ab_bf16 != 0 ? kOutBF16 : kOutF16;
             const bool acc_none = args.num_k_blocks == 0;
-            int slot = 0;
+            uint32_t slot = 0;
             for (int32_t t = cta_set; t < args.num_tiles; t += cta_sets) {
                 int32_t mb, nb;
                 tile_coords(t, args, mb, nb);
@@ -918,7 +1065,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 const int32_t row0 = mb * Cfg::TILE_M + static_cast<int32_t>(role) * Cfg::BM +
                                      32 * static_cast<int32_t>(q);
                 const int32_t my_row = row0 + static_cast<int32_t>(lane);
-                const int32_t nchunks = min(kCols / 32, (args.N - n0 + 31) / 32);
+                const int32_t nchunks = min(kChunks, (args.N - n0 + 31) / 32);
                 // 32 columns from col0 of this warp's rows of one output matrix
                 auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, bool tail,
                                 void *ptr, int64_t ld, int kind, int32_t col0) {
@@ -938,10 +1085,18 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         }
                         return;
                     }
-                    const uint32_t buf = buf0 + static_cast<uint32_t>(slot) * Cfg::EPI_BUF;
-                    slot ^= 1;
-                    if (lane == 0)
-                        bulk_wait_group_read<1>();  // the store before the last has left this buffer
+                    // this warp's two buffers in turn, or (LAP) its one: two 16-bit boxes in
+                    // turn, or one of float32
+                    const uint32_t buf = Cfg::LAP ? base + Cfg::OFF_EPI + q * Cfg::EPI_BUF +
+                                                        (kind == kOutF32 ? 0u : slot * (Cfg::EPI_BUF / 2))
+                                                  : buf0 + slot * Cfg::EPI_BUF;
+                    slot ^= 1u;
+                    if (lane == 0) {  // the last store that used it has read it
+                        if (Cfg::LAP && kind == kOutF32)
+                            bulk_wait_group_read<0>();
+                        else
+                            bulk_wait_group_read<1>();
+                    }
                     __syncwarp();
                     if (kind == kOutF32) {
 #pragma unroll
@@ -967,41 +1122,10 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         bulk_commit_group();
                     }
                 };
-                if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status,
-                                             args.timeout_ns, kWhereEpiAccFull))
-                    return false;
-                tc_fence_after_sync();
-                for (int32_t c = 0; c < kCols / 32; ++c) {
-                    float g[32], u[32];
-                    if (c < nchunks) {
-                        const uint32_t col = tmem_base + ((32u * q) << 16) +
-                                             static_cast<uint32_t>(ab * kIss * TILE_N + 32 * c);
-                        uint32_t rg[32], ru[32];
-                        tc_ld_32x32b_x32(col, rg);
-                        tc_ld_32x32b_x32(col + kCols, ru);
-                        tc_wait_ld(rg);
-                        tc_wait_ld(ru);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            g[i] = acc_none ? 0.f : __uint_as_float(rg[i]);
-                            u[i] = acc_none ? 0.f : __uint_as_float(ru[i]);
-                        }
-                        if (kIss > 1 && args.num_k_blocks > 1) {
-                            tc_ld_32x32b_x32(col + TILE_N, rg);
-                            tc_ld_32x32b_x32(col + TILE_N + kCols, ru);
-                            tc_wait_ld(rg);
-                            tc_wait_ld(ru);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                g[i] = __fadd_rn(g[i], __uint_as_float(rg[i]));
-                                u[i] = __fadd_rn(u[i], __uint_as_float(ru[i]));
-                            }
-                        }
-                    }
-                    if (c == kCols / 32 - 1)
-                        release_unit(ab);
+                // chunk c: keep, activate, store
+                auto finish = [&](float(&g)[32], const float(&u)[32], int32_t c) {
                     if (c >= nchunks || row0 >= args.M)
-                        continue;
+                        return;
                     const int32_t col0 = n0 + 32 * c;
                     if (args.G != nullptr)
                         emit(g, &two->d2, args.keep_tma, args.keep_tail_direct, args.G, args.ldg,
@@ -1015,6 +1139,78 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             g[i] = act_value<decltype(tag)::value>(g[i]) * u[i];
                     });
                     emit(g, &tmD, args.d_tma, args.d_tail_direct, args.D, args.ldd, out_kind, col0);
+                };
+                // chunks [c0, c1) of the accumulator at TMEM address acc, handed back after
+                // the last if asked
+                auto load_finish = [&](uint32_t acc, int32_t c0, int32_t c1, bool hand_back) {
+#pragma unroll 1
+                    for (int32_t c = c0; c < c1; ++c) {
+                        float g[32], u[32];
+                        if (c < nchunks) {
+                            const uint32_t col = acc + static_cast<uint32_t>(32 * c);
+                            uint32_t rg[32], ru[32];
+                            tc_ld_32x32b_x32(col, rg);
+                            tc_ld_32x32b_x32(col + kCols, ru);
+                            tc_wait_ld(rg);
+                            tc_wait_ld(ru);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                g[i] = acc_none ? 0.f : __uint_as_float(rg[i]);
+                                u[i] = acc_none ? 0.f : __uint_as_float(ru[i]);
+                            }
+                            if (kIss > 1 && args.num_k_blocks > 1) {
+                                tc_ld_32x32b_x32(col + TILE_N, rg);
+                                tc_ld_32x32b_x32(col + TILE_N + kCols, ru);
+                                tc_wait_ld(rg);
+                                tc_wait_ld(ru);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    g[i] = __fadd_rn(g[i], __uint_as_float(rg[i]));
+                                    u[i] = __fadd_rn(u[i], __uint_as_float(ru[i]));
+                                }
+                            }
+                        }
+                        if (hand_back && c == c1 - 1)
+                            release_unit(ab);
+                        finish(g, u, c);
+                    }
+                };
+                if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status,
+                                             args.timeout_ns, kWhereEpiAccFull))
+                    return false;
+                tc_fence_after_sync();
+                const uint32_t acc0 = tmem_base + ((32u * q) << 16) +
+                                      (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
+                                                : static_cast<uint32_t>(ab * kIss * TILE_N));
+                if constexpr (Cfg::LAP) {
+                    // The accumulators share the first one's last columns (of U) and the
+                    // second one's first (of G): those 64 columns go into registers, and
+                    // the next tile's MMAs may start.
+                    uint32_t x[2][32];
+                    const uint32_t at = acc0 + (ab == 0 ? TILE_N - 64u : 0u);
+                    tc_ld_32x32b_x32(at, x[0]);
+                    tc_ld_32x32b_x32(at + 32u, x[1]);
+                    tc_wait_ld(x[0]);
+                    tc_wait_ld(x[1]);
+                    release_unit(0);
+                    const int32_t c_x = ab == 0 ? kChunks - 2 : 0;  // their chunks
+#pragma unroll
+                    for (int32_t j = 0; j < 2; ++j) {
+                        uint32_t y[32];
+                        tc_ld_32x32b_x32(acc0 + (ab == 0 ? 0u : kCols) + 32u * (c_x + j), y);
+                        tc_wait_ld(y);
+                        float g[32], u[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint32_t xi = j == 0 ? x[0][i] : x[1][i];
+                            g[i] = acc_none ? 0.f : __uint_as_float(ab == 0 ? y[i] : xi);
+                            u[i] = acc_none ? 0.f : __uint_as_float(ab == 0 ? xi : y[i]);
+                        }
+                        finish(g, u, c_x + j);
+                    }
+                    load_finish(acc0, 2 - c_x, 4 - c_x, false);
+                } else {
+                    load_finish(acc0, 0, kChunks, true);
                 }
                 if (++ab == Cfg::NUM_ACC) {
                     ab = 0;
@@ -1328,7 +1524,7 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
 // The gated form, and operands stored K x M / K x N (MAJ), with the second
 // source's descriptors.
 template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
-__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, 1, MX>::THREADS, 1)
+__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, MODE == kModeGated>::THREADS, 1)
     tile_gemm2_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmC,

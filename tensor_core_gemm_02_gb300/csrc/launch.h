@@ -66,6 +66,7 @@ cudaError_t launch_tile_mx(int mx, int bn, bool pair, const GemmMaps &maps, cons
 // two.sfb2: scales of A, Bg and Bu; single CTAs, bn 128 or 256).
 cudaError_t launch_tile_gated(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
                               const GemmArgs &args, int grid, cudaStream_t stream);
+int tile_gated_mx_stages(int bn);
 cudaError_t launch_tile_gated_mx(int bn, const GemmMaps &maps, const TileMapsTwo &two,
                                  const GemmArgs &args, int grid, cudaStream_t stream);
 

@@ -15,11 +15,11 @@
 namespace tcg {
 
 // attr must hold two entries
-template <int BN, int STAGES, bool PAIR, int NSUB, int MC, int MX = 0>
+template <int BN, int STAGES, bool PAIR, int NSUB, int MC, int MX = 0, bool GATED = false>
 inline void tile_fill_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid,
                              cudaStream_t stream)
 {
-    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>;
+    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX, GATED>;
     cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
@@ -61,7 +61,8 @@ template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
 cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, const GemmArgs &args,
                               int grid, cudaStream_t stream)
 {
-    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, 1, MX>;
+    constexpr bool kGated = MODE == kModeGated;
+    using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, kGated>;
     auto kfn = tile_gemm2_kernel<BN, STAGES, PAIR, NSUB, MODE, MX, MAJ>;
     cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Cfg::SMEM_ALLOC));
@@ -69,7 +70,7 @@ cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, cons
         return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    tile_fill_config<BN, STAGES, PAIR, NSUB, 1, MX>(cfg, attr, grid, stream);
+    tile_fill_config<BN, STAGES, PAIR, NSUB, 1, MX, kGated>(cfg, attr, grid, stream);
     return cudaLaunchKernelEx(&cfg, kfn, maps.a, maps.b, maps.c, maps.d, maps.sfa, maps.sfb, two, args);
 }
 
