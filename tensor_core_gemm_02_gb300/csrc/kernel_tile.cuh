@@ -156,6 +156,7 @@ struct TileCfg {
     // into TMEM themselves
     static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 4 : 1);
     static constexpr int THREADS = 192 + 32 * (ISS - 1) + 32 * SCALE_WARPS;
+    static_assert(STAGES % ISS == 0, "an issuer's stages are its own");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "tile width");
     static_assert(NSUB == 1 || NSUB == 2, "one or two halves");
@@ -578,7 +579,11 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         }
     } else if (warp == 1 || (Cfg::ISS == 2 && warp == 6)) {
         // ------------------------------------------------------------ MMA issuers
-        const int e = warp == 1 ? 0 : 1;  // issuer e takes the K blocks kb = e (mod kIss)
+        // issuer e takes the K blocks on the stages s = e (mod kIss): every other
+        // block, and each stage's phases always by the same issuer (one that came
+        // to a stage only every other time could take an earlier phase, which it
+        // did not wait for, for its own; the stages are even in number)
+        const int e = warp == 1 ? 0 : 1;
         if (lane == 0 && leader && e < kIss) {
             const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, Cfg::TILE_M, BN,
                                                     (MAJ & kMajA) != 0, (MAJ & kMajB) != 0);
@@ -715,8 +720,9 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     const uint32_t d_tmem =
                         tmem_base + (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
                                               : static_cast<uint32_t>((ab * kIss + e) * TILE_N));
+                    bool issued = false;  // this issuer has a block of the tile
                     for (int32_t kb = 0; kb < nkb; ++kb) {
-                        if (kIss > 1 && kb % kIss != e) {
+                        if (kIss > 1 && s % kIss != e) {
                             if (++s == STAGES) {  // the other issuer's stage
                                 s = 0;
                                 ph ^= 1u;
@@ -731,10 +737,11 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         issue_half(st, kb, 0, d_tmem);
                         free_stage(st);  // frees the stage (in both CTAs of a pair)
                         ++blocks_begun;
+                        issued = true;
                     }
                     if (!alive)
                         break;
-                    if (nkb <= e && !PAIR)
+                    if (!issued && !PAIR)
                         mbar_arrive(accf_bar(ab));  // nothing to multiply here
                     else
                         commit_to(accf_bar(ab));
@@ -1179,9 +1186,12 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                              args.timeout_ns, kWhereEpiAccFull))
                     return false;
                 tc_fence_after_sync();
-                const uint32_t acc0 = tmem_base + ((32u * q) << 16) +
-                                      (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
-                                                : static_cast<uint32_t>(ab * kIss * TILE_N));
+                // (two issuers and one K block: the sum is the one's whose stage it was on)
+                const uint32_t acc0 =
+                    tmem_base + ((32u * q) << 16) +
+                    (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
+                              : static_cast<uint32_t>(ab * kIss * TILE_N)) +
+                    (kIss > 1 && args.num_k_blocks == 1 && ((t - cta_set) / cta_sets) % kIss != 0 ? TILE_N : 0);
                 if constexpr (Cfg::LAP) {
                     // The accumulators share the first one's last columns (of U) and the
                     // second one's first (of G): those 64 columns go into registers, and
@@ -1323,6 +1333,10 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 zero_row = zero_row || v < 0 || v >= args.table_rows;
             }
 
+            // one K block, two issuers: the sum is the one's whose stage the block was on
+            const uint32_t acc_col0 =
+                static_cast<uint32_t>(ab * kIss * TILE_N) +
+                (kIss > 1 && args.num_k_blocks == 1 && ((t - cta_set) / cta_sets) % kIss != 0 ? TILE_N : 0);
             // the next tile on this accumulator (seeded mode)
             const int32_t t_next = t + Cfg::NUM_ACC * cta_sets;
             for (int32_t c = 0; c < TILE_N / 32; ++c) {
@@ -1338,7 +1352,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 const bool have = c < nchunks;
                 uint32_t acc[32];
                 if (have) {
-                    const uint32_t col = static_cast<uint32_t>(ab * kIss * TILE_N + 32 * c);
+                    const uint32_t col = acc_col0 + static_cast<uint32_t>(32 * c);
                     tc_ld_32x32b_x32(tmem_base + ((32u * q) << 16) + col, acc);
                     tc_wait_ld(acc);
                     if (kIss > 1 && args.num_k_blocks > 1) {
