@@ -22,13 +22,30 @@ constexpr float kGeluTanh3 = 0.07135481282720802f;  // 0.044715 of that
 constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
+// Phi(g), the normal distribution function, and e = exp(-g^2 / 2): the rational
+// approximation 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical
+// Functions, erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) with t = 1 / (1 + p x) for x
+// = |g| / sqrt(2), within 1.5e-7 (7.5e-8 of Phi).  One exponential, which the
+// slope needs anyway, and no branch; for g < 0 nothing cancels.
+__device__ __forceinline__ float normal_cdf(float g, float &e)
+{
+    const float x = fabsf(g) * kSqrtHalf;
+    const float t = __fdividef(1.f, 1.f + 0.3275911f * x);
+    e = __expf(-0.5f * g * g);
+    const float q = 0.5f * e * t *
+                    (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    return g < 0.f ? q : 1.f - q;  // (a NaN stays one)
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float g)
 {
     if (ACT == kActSilu)
         return __fdividef(g, 1.f + __expf(-g));
-    if (ACT == kActGelu)
-        return 0.5f * g * (1.f + erff(g * kSqrtHalf));
+    if (ACT == kActGelu) {
+        float e;
+        return g * normal_cdf(g, e);
+    }
     if (ACT == kActGeluTanh)
         return g * sigmoid_f32(g * (kGeluTanh1 + kGeluTanh3 * g * g));
     if (ACT == kActRelu)
@@ -45,9 +62,10 @@ __device__ __forceinline__ void act_value_slope(float g, float &a, float &s)
         a = g * p;
         s = p * (1.f + g * (1.f - p));
     } else if (ACT == kActGelu) {
-        const float c = 0.5f * (1.f + erff(g * kSqrtHalf));
+        float e;
+        const float c = normal_cdf(g, e);
         a = g * c;
-        s = c + g * kInvSqrt2Pi * __expf(-0.5f * g * g);
+        s = c + g * kInvSqrt2Pi * e;
     } else if (ACT == kActGeluTanh) {
         const float p = sigmoid_f32(g * (kGeluTanh1 + kGeluTanh3 * g * g));
         a = g * p;
