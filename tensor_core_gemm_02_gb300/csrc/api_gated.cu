@@ -335,6 +335,9 @@ struct TransProblem {
     int64_t ldb2 = 0;
     void *D2 = nullptr;
     int64_t ldd2 = 0;
+    // launched right behind a kernel that it does not depend on, but that waited
+    // for what it does depend on: it starts on the SMs that kernel leaves idle
+    bool co_tail = false;
 };
 
 // Launch (arguments already checked; M, N > 0).
@@ -400,6 +403,7 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
     a.d_tail_direct = (p.N * out_size(p.out)) % 16 != 0 ? 1 : 0;
     a.D2 = p.D2;
     a.ldd2 = p.ldd2;
+    a.co_tail = p.co_tail ? 1 : 0;
     if ((a.c_tma && !encode_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.C, p.N, p.M, p.ldc * 4, 32, 32,
                                CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd)) ||
@@ -707,8 +711,11 @@ gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf
             return st;
     }
     if (want_b) {
-        // [dBg; dBu] = [dG dU]^T A: both gradients' tiles in one launch
+        // [dBg; dBu] = [dG dU]^T A: both gradients' tiles in one launch, which fills the
+        // SMs as dA's tiles run out (both only need dG and dU: dA's kernel let this
+        // one start once it had passed its own wait for them)
         TransProblem p{};
+        p.co_tail = want_a;
         p.M = N;
         p.N = K;
         p.K = M;
