@@ -294,7 +294,9 @@ def _mat(name, t, rows, cols, dtype):
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), (ld if rows > 1 else max(ld, cols)) if cols else 0
+    if rows < 2 or not cols:  # (one row: its pitch says nothing; no columns: not used)
+        ld = max(ld, cols) if cols else 0
+    return t.data_ptr(), ld
 
 
 def _mat_or_null(name, t, rows, cols, dtype):

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 // Launch with programmatic dependent launch allowed (1) or not (0): a GEMM
@@ -18,6 +20,23 @@
 #endif
 
 namespace tcg {
+
+// Let `kfn` use `bytes` of dynamic shared memory, once per device (`done`: the
+// devices that have it, one bit each, kept by the caller per kernel).
+inline cudaError_t allow_smem(const void *kfn, uint32_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if ((done.load(std::memory_order_relaxed) & bit) != 0)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 struct GemmMaps {
     CUtensorMap a;    // A tiles, or the gather table (box of one row); FP4: A's codes

@@ -15,8 +15,8 @@ cudaError_t launch_skinny_gated_impl(const GemmMaps &maps, const TileMapsTwo &tw
 {
     using Cfg = SkinnyCfg<MP, 1, false, MX, true>;
     auto kfn = skinny_gated_kernel<MP, 1, MX>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Cfg::SMEM_ALLOC));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kfn), Cfg::SMEM_ALLOC, done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -64,8 +64,8 @@ cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, cons
     constexpr bool kGated = MODE == kModeGated;
     using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, kGated>;
     auto kfn = tile_gemm2_kernel<BN, STAGES, PAIR, NSUB, MODE, MX, MAJ>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Cfg::SMEM_ALLOC));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kfn), Cfg::SMEM_ALLOC, done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg;
