@@ -80,14 +80,21 @@ CUtensorMapDataType out_type(int out)
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
-// 32 x 32 boxes of an output matrix
+// 32 x 32 boxes of an output matrix, up to the last column whose row ends on whole 16
+// bytes (a store writes 16-byte pieces whole; the kernel stores the columns past it
+// one by one)
 bool encode_out(CUtensorMap *m, const void *p, int out, int64_t rows, int64_t cols, int64_t ld)
 {
+    const int64_t per16 = 16 / out_size(out);
+    cols = cols / per16 * per16;
     return encode_2d(m, out_type(out), p, cols, rows, ld * out_size(out), 32, 32,
                      out == GEMM_OUT_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-bool out_tma(const void *p, int64_t ld, int out) { return aligned16(p) && (ld * out_size(out)) % 16 == 0; }
+bool out_tma(const void *p, int64_t ld, int out, int64_t cols)
+{
+    return aligned16(p) && (ld * out_size(out)) % 16 == 0 && cols * out_size(out) >= 16;
+}
 
 // ---------------------------------------------------------------- gated form
 
@@ -173,15 +180,14 @@ void fill_gated(GemmArgs &a, const GatedProblem &p, const DeviceInfo *dev)
     a.splits = 1;
     a.k2_block = INT_MAX;
     a.m2_block = INT_MAX;
-    a.d_tma = out_tma(p.D, p.ldd, p.out) ? 1 : 0;
-    a.d_tail_direct = (p.N * out_size(p.out)) % 16 != 0 ? 1 : 0;
+    a.d_tma = out_tma(p.D, p.ldd, p.out, p.N) ? 1 : 0;
     a.G = p.G;
     a.ldg = p.ldg;
     a.U = p.U;
     a.ldu = p.ldu;
     const int kind = p.bf16 ? GEMM_OUT_BF16 : GEMM_OUT_F16;
-    a.keep_tma = (!p.G || out_tma(p.G, p.ldg, kind)) && (!p.U || out_tma(p.U, p.ldu, kind)) ? 1 : 0;
-    a.keep_tail_direct = (p.N * 2) % 16 != 0 ? 1 : 0;
+    a.keep_tma =
+        (!p.G || out_tma(p.G, p.ldg, kind, p.N)) && (!p.U || out_tma(p.U, p.ldu, kind, p.N)) ? 1 : 0;
 }
 
 gemm_status run_gated_skinny(const GatedProblem &p, const gemm_plan &plan, const DeviceInfo *dev)
@@ -399,8 +405,8 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
     a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
     a.splits = 1;
     a.c_tma = c_used && aligned16(p.C) && (p.ldc * 4) % 16 == 0 ? 1 : 0;
-    a.d_tma = out_tma(p.D, p.ldd, p.out) && (!more_m || out_tma(p.D2, p.ldd2, p.out)) ? 1 : 0;
-    a.d_tail_direct = (p.N * out_size(p.out)) % 16 != 0 ? 1 : 0;
+    a.d_tma =
+        out_tma(p.D, p.ldd, p.out, p.N) && (!more_m || out_tma(p.D2, p.ldd2, p.out, p.N)) ? 1 : 0;
     a.D2 = p.D2;
     a.ldd2 = p.ldd2;
     a.co_tail = p.co_tail ? 1 : 0;

@@ -61,7 +61,6 @@ struct GemmArgs {
     // gated form (D = act(G) * U from two weight matrices)
     int32_t act;            // gemm_act_t
     int32_t keep_tma;       // G and U boxes go out through TMA stores; else plain stores
-    int32_t keep_tail_direct;  // as d_tail_direct, for the 16-bit G and U
     void *G, *U;            // the two products, in the operand type; NULL: not kept
     int64_t ldg, ldu;
     // products with two sources: K blocks from k2_block on read the second pair

@@ -1074,15 +1074,16 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 const int32_t my_row = row0 + static_cast<int32_t>(lane);
                 const int32_t nchunks = min(kChunks, (args.N - n0 + 31) / 32);
                 // 32 columns from col0 of this warp's rows of one output matrix
-                auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, bool tail,
-                                void *ptr, int64_t ld, int kind, int32_t col0) {
-                    if (!tma || (tail && col0 + 32 > args.N)) {
-                        if (my_row >= args.M)
-                            return;
+                // (by TMA up to column n_tma, the last whole 16 bytes of a row, as the
+                // descriptor has it; plain stores for the rest)
+                auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, void *ptr,
+                                int64_t ld, int kind, int32_t col0) {
+                    const int32_t n_tma = tma ? args.N & ~(kind == kOutF32 ? 3 : 7) : 0;
+                    if (col0 + 32 > n_tma && n_tma < args.N && my_row < args.M) {
                         const int64_t o = static_cast<int64_t>(my_row) * ld + col0;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            if (col0 + i < args.N) {
+                            if (col0 + i >= n_tma && col0 + i < args.N) {
                                 if (kind == kOutF32)
                                     static_cast<float *>(ptr)[o + i] = v[i];
                                 else
@@ -1090,8 +1091,9 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                         kind == kOutBF16 ? f32_to_bf16_rn(v[i]) : f32_to_f16_rn(v[i]);
                             }
                         }
-                        return;
                     }
+                    if (col0 >= n_tma)
+                        return;
                     // this warp's two buffers in turn, or (LAP) its one: two 16-bit boxes in
                     // turn, or one of float32
                     const uint32_t buf = Cfg::LAP ? base + Cfg::OFF_EPI + q * Cfg::EPI_BUF +
@@ -1135,17 +1137,15 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         return;
                     const int32_t col0 = n0 + 32 * c;
                     if (args.G != nullptr)
-                        emit(g, &two->d2, args.keep_tma, args.keep_tail_direct, args.G, args.ldg,
-                             keep_kind, col0);
+                        emit(g, &two->d2, args.keep_tma, args.G, args.ldg, keep_kind, col0);
                     if (args.U != nullptr)
-                        emit(u, &two->d3, args.keep_tma, args.keep_tail_direct, args.U, args.ldu,
-                             keep_kind, col0);
+                        emit(u, &two->d3, args.keep_tma, args.U, args.ldu, keep_kind, col0);
                     with_act(args.act, [&](auto tag) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             g[i] = act_value<decltype(tag)::value>(g[i]) * u[i];
                     });
-                    emit(g, &tmD, args.d_tma, args.d_tail_direct, args.D, args.ldd, out_kind, col0);
+                    emit(g, &tmD, args.d_tma, args.D, args.ldd, out_kind, col0);
                 };
                 // chunks [c0, c1) of the accumulator at TMEM address acc, handed back after
                 // the last if asked
@@ -1300,14 +1300,14 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 }
             };
             // plain stores (reduce: float32 atomic adds) of this lane's row,
-            // column by column, nothing past column N
-            auto store_direct = [&](const float(&v)[32], int32_t col0) {
+            // column by column, from column `from`, nothing past column N
+            auto store_direct = [&](const float(&v)[32], int32_t col0, int32_t from) {
                 if (d_row < 0)
                     return;
                 const int64_t o = static_cast<int64_t>(d_row) * out_ld + col0;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    if (col0 + i < args.N) {
+                    if (col0 + i >= from && col0 + i < args.N) {
                         if (reduce)
                             atomicAdd(static_cast<float *>(out_d) + o + i, v[i]);
                         else if (out_kind == kOutF32)
@@ -1382,8 +1382,13 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 const int32_t col0 = n0 + 32 * c;
                 // plain stores: D not TMA-aligned, the 16-byte chunk that
                 // straddles column N, or (scattered rows) any partial chunk
+                // (operands stored K x M / K x N: D's descriptor ends with the last whole 16
+                // bytes of a row, and only the columns past it go by plain stores: 32 rows'
+                // worth of single elements cost a ragged last tile 2.4 us)
+                const int32_t n_tma = MAJ != 0 ? args.N & ~(out_kind == kOutF32 ? 3 : 7) : args.N;
                 const bool d_direct = !args.d_tma ||
-                                      ((args.d_tail_direct || scatter) && col0 + 32 > args.N);
+                                      (MAJ != 0 ? col0 >= n_tma
+                                                : (args.d_tail_direct || scatter) && col0 + 32 > args.N);
                 float v[32];
                 if (c_tma) {
                     if (!warp_wait_bounded<true>(c_bar(q, j), cph[j], abort_flag, args.status,
@@ -1415,8 +1420,10 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     for (int i = 0; i < 32; ++i)
                         v[i] = mul_rn(args.alpha, zero_row ? 0.f : __uint_as_float(acc[i]));
                 }
+                if (MAJ != 0 && !d_direct && n_tma < args.N && col0 + 32 > n_tma)
+                    store_direct(v, col0, n_tma);
                 if (d_direct) {
-                    store_direct(v, col0);
+                    store_direct(v, col0, col0);
                 } else {
                     if (!c_tma && bulk_lane)
                         bulk_wait_group_read<1>();  // the store two chunks back left buffer j
@@ -1464,7 +1471,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             bulk_commit_group();
                         }
                         if (!own_group_whole)
-                            store_direct(v, col0);
+                            store_direct(v, col0, col0);
                     }
                 }
                 if (c_tma && c + 2 < nchunks) {
