@@ -303,10 +303,22 @@ def _mat_or_null(name, t, rows, cols, dtype):
     return (None, 0) if t is None else _mat(name, t, rows, cols, dtype)
 
 
+# torch's allocation without its dispatcher (on the current device), where this torch has it:
+# between launches torch.empty costs a small call 3 us and more
+_empty_strided_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                              "_empty_strided_cuda", None)
+
+
+def _empty(rows, cols, pitch, dtype, device):
+    if _empty_strided_cuda is not None and device.type == "cuda" and device.index == torch._C._cuda_getDevice():
+        return _empty_strided_cuda((rows, cols), (pitch, 1), dtype)
+    return torch.empty_strided((rows, cols), (pitch, 1), dtype=dtype, device=device)
+
+
 def _padded(rows, cols, dtype, device):
     """An uninitialised matrix whose row pitch is a multiple of 16 bytes."""
     per = 16 // dtype.itemsize
-    return torch.empty_strided((rows, cols), ((cols + per - 1) // per * per, 1), dtype=dtype, device=device)
+    return _empty(rows, cols, (cols + per - 1) // per * per, dtype, device)
 
 
 def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, stream=None):
@@ -319,7 +331,7 @@ def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, 
     M, K = A.shape
     N = Bg.shape[0]
     if D is None:
-        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+        D = _empty(M, N, N, _DTYPE_OF_OUT[out], A.device)
     st = load_library().gemm_gated(
         M, N, K, bf16, *_mat("A", A, M, K, dt), *_mat("Bg", Bg, N, K, dt), *_mat("Bu", Bu, N, K, dt),
         *_mat_or_null("G", G, M, N, dt), *_mat_or_null("U", U, M, N, dt),
@@ -336,7 +348,7 @@ def gemm_gated_e2m1(Aq, As, Bgq, Bgs, Buq, Bus, D=None, *, act=ACT_SILU, out=OUT
     N = Bgq.shape[0]
     blocks, u8 = half // 16, torch.uint8
     if D is None:
-        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=Aq.device)
+        D = _empty(M, N, N, _DTYPE_OF_OUT[out], Aq.device)
     st = load_library().gemm_gated_e2m1(
         M, N, 2 * half, *_mat("Aq", Aq, M, half, u8), *_mat("As", As, blocks, M, u8),
         *_mat("Bgq", Bgq, N, half, u8), *_mat("Bgs", Bgs, blocks, N, u8), *_mat("Buq", Buq, N, half, u8),
@@ -364,14 +376,14 @@ def gemm_gated_backward(dD, G, U, A, Bg, Bu, *, dG=None, dU=None, dA=None, dBg=N
     a = bg = bu = pa = pbg = pbu = null
     if need_input:
         bg, bu = _mat("Bg", Bg, N, K, dt), _mat("Bu", Bu, N, K, dt)
-        dA = torch.empty((M, K), dtype=ot, device=dev) if dA is None else dA
+        dA = _empty(M, K, K, ot, dev) if dA is None else dA
         pa = _mat("dA", dA, M, K, ot)
     else:
         dA = None
     if need_weights:
         a = _mat("A", A, M, K, dt)
-        dBg = torch.empty((N, K), dtype=ot, device=dev) if dBg is None else dBg
-        dBu = torch.empty((N, K), dtype=ot, device=dev) if dBu is None else dBu
+        dBg = _empty(N, K, K, ot, dev) if dBg is None else dBg
+        dBu = _empty(N, K, K, ot, dev) if dBu is None else dBu
         pbg, pbu = _mat("dBg", dBg, N, K, ot), _mat("dBu", dBu, N, K, ot)
     else:
         dBg = dBu = None
@@ -398,7 +410,7 @@ def gemm_trans(A, B, C=None, D=None, *, trans_a=False, trans_b=False, alpha=1.0,
     if K != Kb:
         raise ValueError("A and B disagree on K")
     if D is None:
-        D = torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+        D = _empty(M, N, N, _DTYPE_OF_OUT[out], A.device)
     st = load_library().gemm_trans(
         M, N, K, bf16, 1 if trans_a else 0, *_mat("A", A, ra, ca, dt), 1 if trans_b else 0,
         *_mat("B", B, rb, cb, dt), *_mat_or_null("C", C, M, N, torch.float32),
@@ -420,7 +432,7 @@ def gemm_quantize_e2m1(X, Q=None, S=None, *, Y=None, stream=None):
     M, K = X.shape
     half, blocks = K // 2, K // 32
     if Q is None:
-        Q = torch.empty((M, half), dtype=u8, device=X.device)
+        Q = _empty(M, half, half, u8, X.device)
     if S is None:
         S = _padded(blocks, M, u8, X.device)
     st = load_library().gemm_quantize_e2m1(
