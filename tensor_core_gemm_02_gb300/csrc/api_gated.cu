@@ -80,15 +80,16 @@ CUtensorMapDataType out_type(int out)
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
-// 32 x 32 boxes of an output matrix, up to the last column whose row ends on whole 16
+// Boxes of 32 rows x box_cols columns of an output matrix, up to the last column whose row ends on whole 16
 // bytes (a store writes 16-byte pieces whole; the kernel stores the columns past it
 // one by one)
-bool encode_out(CUtensorMap *m, const void *p, int out, int64_t rows, int64_t cols, int64_t ld)
+bool encode_out(CUtensorMap *m, const void *p, int out, int64_t rows, int64_t cols, int64_t ld,
+                uint32_t box_cols = 32)
 {
     const int64_t per16 = 16 / out_size(out);
     cols = cols / per16 * per16;
-    return encode_2d(m, out_type(out), p, cols, rows, ld * out_size(out), 32, 32,
-                     out == GEMM_OUT_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    return encode_2d(m, out_type(out), p, cols, rows, ld * out_size(out), box_cols, 32,
+                     box_cols * out_size(out) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool out_tma(const void *p, int64_t ld, int out, int64_t cols)
@@ -410,10 +411,12 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
     a.D2 = p.D2;
     a.ldd2 = p.ldd2;
     a.co_tail = p.co_tail ? 1 : 0;
+    a.d_wide = a.d_tma && !c_used && p.out != GEMM_OUT_F32 ? 1 : 0;
+    const uint32_t d_cols = a.d_wide ? 64 : 32;
     if ((a.c_tma && !encode_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.C, p.N, p.M, p.ldc * 4, 32, 32,
                                CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        (a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd)) ||
-        (a.d_tma && more_m && !encode_out(&two.d2, p.D2, p.out, p.M, p.N, p.ldd2)))
+        (a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd, d_cols)) ||
+        (a.d_tma && more_m && !encode_out(&two.d2, p.D2, p.out, p.M, p.N, p.ldd2, d_cols)))
         return GEMM_ERR_CUDA;
     const int maj = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
     const cudaError_t e = tcg::launch_tile_major(maj, bn, pair, nsub, maps, two, a, grid, p.stream);

@@ -1051,6 +1051,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         int ab = 0;
         uint32_t aph = 0;
         uint32_t cph[2] = {0u, 0u};
+        [[maybe_unused]] uint32_t wide_slot = 0;  // (d_wide) the buffer of the next store
         bool alive = true;
 
         // Gated form: per 32 columns of D, G from the left half of the accumulator
@@ -1327,6 +1328,109 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 for (int j = 0; j < 2 && j < nchunks; ++j)
                     load_c(j, n0 + 32 * j);
             }
+            // 16-bit D without C (operands stored K x M / K x N): 64 columns at a time, one
+            // 128-byte row of D per thread, the next 64 on their way from TMEM meanwhile.
+            // Few K blocks a tile leave the epilogue to set the time, and the loads'
+            // latency, a fence and a store per 32 columns one after the other gave it
+            // 13 KB a microsecond (two 14336 x 4096 bf16 gradients of 16 rows: 118 us for
+            // 235 MB).
+            if (MAJ != 0 && args.d_wide) {
+                constexpr int kUnits = NSUB == 2 ? 2 : 1, kWide = kUnitChunks / 2;
+                const int32_t n_tma = args.N & ~7;
+                for (int h = 0; h < kUnits && alive; ++h) {
+                    const int unit = NSUB == 2 ? h : ab;
+                    if (!warp_wait_bounded<true>(accf_bar(unit), aph, abort_flag, args.status,
+                                                 args.timeout_ns, kWhereEpiAccFull)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    // (two issuers and one K block: the sum is the one's whose stage it was on)
+                    const bool both = kIss > 1 && args.num_k_blocks > 1;
+                    const uint32_t acc0 =
+                        tmem_base + ((32u * q) << 16) +
+                        static_cast<uint32_t>(ab * kIss * TILE_N + 64 * kWide * h) +
+                        (kIss > 1 && args.num_k_blocks == 1 && ((t - cta_set) / cta_sets) % kIss != 0 ? TILE_N : 0);
+                    const int32_t wide = min(kWide, (nchunks + 1) / 2 - kWide * h);  // with columns of D
+                    uint32_t lo[32], hi[32];
+                    if (wide > 0) {
+                        tc_ld_32x32b_x32(acc0, lo);
+                        tc_ld_32x32b_x32(acc0 + 32u, hi);
+                    }
+#pragma unroll 1
+                    for (int32_t w = 0; w < wide; ++w) {
+                        tc_wait_ld(lo);
+                        tc_wait_ld(hi);
+                        if (both) {
+                            uint32_t r[32];
+                            tc_ld_32x32b_x32(acc0 + 64u * w + TILE_N, r);
+                            tc_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                lo[i] = __float_as_uint(__fadd_rn(__uint_as_float(lo[i]), __uint_as_float(r[i])));
+                            tc_ld_32x32b_x32(acc0 + 64u * w + 32u + TILE_N, r);
+                            tc_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                hi[i] = __float_as_uint(__fadd_rn(__uint_as_float(hi[i]), __uint_as_float(r[i])));
+                        }
+                        uint32_t p[32];  // the 64 values, two per word
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a0 = acc_zero ? 0.f : mul_rn(args.alpha, __uint_as_float(lo[2 * i]));
+                            const float a1 = acc_zero ? 0.f : mul_rn(args.alpha, __uint_as_float(lo[2 * i + 1]));
+                            const float b0 = acc_zero ? 0.f : mul_rn(args.alpha, __uint_as_float(hi[2 * i]));
+                            const float b1 = acc_zero ? 0.f : mul_rn(args.alpha, __uint_as_float(hi[2 * i + 1]));
+                            p[i] = out_kind == kOutBF16 ? pack_bf16x2(a0, a1) : pack_f16x2(a0, a1);
+                            p[16 + i] = out_kind == kOutBF16 ? pack_bf16x2(b0, b1) : pack_f16x2(b0, b1);
+                        }
+                        if (w + 1 < wide) {
+                            tc_ld_32x32b_x32(acc0 + 64u * (w + 1), lo);
+                            tc_ld_32x32b_x32(acc0 + 64u * (w + 1) + 32u, hi);
+                        } else {
+                            release_unit(unit);
+                        }
+                        if (!rows_ok)
+                            continue;
+                        const int32_t col0 = n0 + 64 * (kWide * h + w);
+                        if (n_tma < args.N && col0 + 64 > n_tma && d_row >= 0) {
+                            unsigned short *drow = static_cast<unsigned short *>(out_d) +
+                                                   static_cast<int64_t>(d_row) * out_ld + col0;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (col0 + i >= n_tma && col0 + i < args.N)
+                                    drow[i] = static_cast<unsigned short>(p[i / 2] >> (16 * (i & 1)));
+                        }
+                        if (col0 >= n_tma)
+                            continue;
+                        const uint32_t buf = buf0 + wide_slot * Cfg::EPI_BUF;
+                        wide_slot ^= 1u;
+                        if (lane == 0)
+                            bulk_wait_group_read<1>();  // the store before the last has left this buffer
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(buf + swz_off(lane, i, 128u), p[4 * i], p[4 * i + 1], p[4 * i + 2],
+                                         p[4 * i + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d_hint(map_d, buf, col0, row0, epi_policy);
+                            bulk_commit_group();
+                        }
+                    }
+                    if (wide <= 0)
+                        release_unit(unit);
+                }
+                if (!alive)
+                    break;
+                if (++ab == Cfg::NUM_ACC) {
+                    ab = 0;
+                    aph ^= 1u;
+                }
+                continue;
+            }
+
             bool zero_row = acc_zero;
             if (args.gather && my_row < args.M) {
                 const int32_t v = args.idx[my_row];
