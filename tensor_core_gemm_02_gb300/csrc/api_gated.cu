@@ -347,11 +347,78 @@ struct TransProblem {
     bool co_tail = false;
 };
 
+void fill_trans(GemmArgs &a, const TransProblem &p, const DeviceInfo *dev)
+{
+    Problem q{};  // (the fields fill_common reads)
+    q.M = p.M;
+    q.N = p.N;
+    q.K = p.K;
+    q.bf16 = p.bf16;
+    q.C = p.C;
+    q.ldc = p.ldc;
+    q.D = p.D;
+    q.ldd = p.ldd;
+    q.out = p.out;
+    q.alpha = p.alpha;
+    q.beta = p.beta;
+    fill_common(a, q, dev);
+}
+
+// M <= 64 rows of A as stored, B stored K x N: the skinny kernel.
+gemm_status run_trans_skinny(const TransProblem &p, const gemm_plan &plan, const DeviceInfo *dev)
+{
+    GemmMaps maps;
+    TileMapsTwo two;
+    std::memset(&maps, 0, sizeof(maps));
+    std::memset(&two, 0, sizeof(two));
+    const CUtensorMapDataType t = ab_type(p.bf16);
+    const uint32_t mp = static_cast<uint32_t>(plan.bm);
+    auto map_a = [&](CUtensorMap *m, const void *A, int64_t lda) {
+        return encode_2d(m, t, A, p.K, p.M, lda * 2, 64, mp, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto map_b = [&](CUtensorMap *m, const void *B, int64_t ldb) {
+        return encode_2d(m, t, B, p.N, p.K, ldb * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    // (without a second source, its descriptors are the first's)
+    if (!map_a(&maps.a, p.A, p.lda) || !map_b(&maps.b, p.B, p.ldb) ||
+        !map_a(&two.a2, p.A2 ? p.A2 : p.A, p.A2 ? p.lda2 : p.lda) ||
+        !map_b(&two.b2, p.B2 ? p.B2 : p.B, p.B2 ? p.ldb2 : p.ldb))
+        return GEMM_ERR_CUDA;
+    GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    fill_trans(a, p, dev);
+    const int64_t k_blocks = ceil_div(p.K, tcg::skinny_kstage());
+    a.num_m_blocks = 1;
+    a.num_n_blocks = static_cast<int32_t>(plan.tiles);
+    a.num_k_blocks = static_cast<int32_t>(p.B2 ? 2 * k_blocks : k_blocks);
+    a.num_tiles = static_cast<int32_t>(plan.tiles);
+    a.sk_tiles = static_cast<int32_t>(plan.tiles);  // every tile shared block by block
+    a.group_m = 1;
+    a.splits = plan.splits;
+    a.k2_block = p.B2 ? static_cast<int32_t>(k_blocks) : INT_MAX;
+    if (plan.splits > 1) {
+        Workspace w;
+        const size_t bytes = static_cast<size_t>(plan.tiles) * plan.splits * 128 * mp * sizeof(float);
+        const gemm_status st =
+            get_workspace(dev->index, p.stream, bytes, static_cast<size_t>(plan.tiles), &w);
+        if (st != GEMM_OK)
+            return st;
+        a.workspace = w.partials;
+        a.counters = w.counters;
+    }
+    const cudaError_t e = tcg::launch_skinny_trans(plan.bm, maps, two, a, plan.grid, p.stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
 // Launch (arguments already checked; M, N > 0).
 gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
 {
     const bool c_used = p.C != nullptr && p.beta != 0.0f;
-    const gemm_plan plan = trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, c_used, dev->sm_count);
+    const int stored = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
+    const gemm_plan plan =
+        trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, p.B2 ? 2 : 1, stored, c_used, dev->sm_count);
+    if (plan.kernel == 2)
+        return run_trans_skinny(p, plan, dev);
     const bool pair = plan.kernel != 1;
     const int nsub = plan.kernel == 4 ? 2 : 1;
     const int bn = pair ? 256 : plan.bn;
@@ -380,21 +447,9 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
     if (p.K > 0 && (!map_a(&maps.a, p.A, p.lda) || !map_b(&maps.b, p.B, p.ldb) ||
                     (p.A2 && !map_a(&two.a2, p.A2, p.lda2)) || (p.B2 && !map_b(&two.b2, p.B2, p.ldb2))))
         return GEMM_ERR_CUDA;
-    Problem q{};  // (the fields fill_common reads)
-    q.M = p.M;
-    q.N = p.N;
-    q.K = p.K;
-    q.bf16 = p.bf16;
-    q.C = p.C;
-    q.ldc = p.ldc;
-    q.D = p.D;
-    q.ldd = p.ldd;
-    q.out = p.out;
-    q.alpha = p.alpha;
-    q.beta = p.beta;
     GemmArgs a;
     std::memset(&a, 0, sizeof(a));
-    fill_common(a, q, dev);
+    fill_trans(a, p, dev);
     const int64_t m_blocks = ceil_div(p.M, plan.bm), k_blocks = ceil_div(p.K, 64);
     const bool more_k = p.B2 != nullptr, more_m = p.D2 != nullptr;
     a.num_m_blocks = static_cast<int32_t>(more_m ? 2 * m_blocks : m_blocks);
@@ -418,8 +473,7 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
         (a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd, d_cols)) ||
         (a.d_tma && more_m && !encode_out(&two.d2, p.D2, p.out, p.M, p.N, p.ldd2, d_cols)))
         return GEMM_ERR_CUDA;
-    const int maj = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
-    const cudaError_t e = tcg::launch_tile_major(maj, bn, pair, nsub, maps, two, a, grid, p.stream);
+    const cudaError_t e = tcg::launch_tile_major(stored, bn, pair, nsub, maps, two, a, grid, p.stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -524,8 +578,10 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
     return p;
 }
 
-// Block rows of both stacked sources (sources = 2) count as one problem's.
-gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int sources, bool c_used, int sm_count)
+// m_sources, k_sources: sources stacked along M (their block rows count as one
+// problem's) and along K (one longer sum); stored: bit 0 A K x M, bit 1 B K x N.
+gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, bool c_used,
+                     int sm_count)
 {
     gemm_plan p;
     std::memset(&p, 0, sizeof(p));
@@ -533,12 +589,24 @@ gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int sources, bool c_used, 
         return p;
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
-    TileChoice c = choose_tile(sources * M, N, K, false, c_used, false, sm_count);
+    // few rows of A: the skinny kernel, where it shares a long sum over the SMs
+    const bool skinny_ok = M <= 64 && K > 0 && stored == 2 && m_sources == 1;
+    if (skinny_ok && (fk == 2 || (fk != 1 && fk != 3 && fk != 4 && skinny_wins(M, N, k_sources * K)))) {
+        set_skinny_plan(p, M, N, k_sources * ceil_div(K, tcg::skinny_kstage()) * tcg::skinny_kstage(),
+                        sm_count, false);
+        return p;
+    }
+    TileChoice c = choose_tile(m_sources * M, N, k_sources * K, false, c_used, false, sm_count);
+    // A short sum leaves the stores to set the time: single CTAs, which start and
+    // finish a tile without the pair's hand-overs (two sources stacked along M, 14336 x
+    // 4096 each, 16-bit: K = 16 24.8 against 34.0 us, 256 31.9 / 40.9, 1024 85.7 / 72.1)
+    if (c.kernel != 1 && k_sources * K < 512)
+        c = TileChoice{1, 256};
     if (fk == 1 || ((fk == 3 || fk == 4) && K > 0))
         c = TileChoice{fk, fbn};
     set_tile_plan(p, c.kernel, c.bn, M, N, sm_count);
-    if (sources > 1) {
-        p.tiles *= sources;
+    if (m_sources > 1) {
+        p.tiles *= m_sources;
         const int64_t cl = c.kernel == 1 ? 1 : 2, sets = sm_count / cl;
         p.grid = static_cast<int32_t>(cl * (p.tiles < sets ? p.tiles : sets));
     }

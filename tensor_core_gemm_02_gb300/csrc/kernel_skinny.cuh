@@ -49,6 +49,10 @@
 // of D.  They lie in different TMEM lanes: once a tile's sums are whole, thread n
 // < 64 (a column of G) and thread n + 64 (the same column of U) swap half of
 // their rows through shared memory, and each finishes half of the rows.
+//
+// B stored K x N (BT): a tile is 128 columns of B, loaded as two boxes of 64
+// columns x 64 K rows, which the MMA reads as an MN-major operand; with a second
+// source, the K blocks from args.k2_block on come from A2 and B2.
 #pragma once
 
 #include "act.cuh"
@@ -402,13 +406,15 @@ __device__ __forceinline__ void skinny_store_gated(const GemmArgs &a, float *swa
         skinny_store_rows<unsigned short>(a, nullptr, n, m, d, [](float x) { return f32_to_f16_rn(x); });
 }
 
-template <int MP, int KBOX, bool W4, bool MX, bool GATED>
+// tmB2, tmS2: Bu and its scales (gated form), or B2 and A2 (BT).
+template <int MP, int KBOX, bool W4, bool MX, bool GATED, bool BT>
 __device__ __forceinline__ void skinny_gemm_body(const CUtensorMap &tmA, const CUtensorMap &tmB,
                                                  const CUtensorMap &tmS, const CUtensorMap &tmSA,
                                                  const CUtensorMap *tmB2, const CUtensorMap *tmS2,
                                                  const GemmArgs &args)
 {
     using Cfg = SkinnyCfg<MP, KBOX, W4, MX, GATED>;
+    static_assert(!BT || (!W4 && !MX && !GATED), "B stored K x N: 16-bit operands");
     static_assert(!GATED || !W4, "gated form: 16-bit operands, or both FP4");
     constexpr int STAGES = Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -549,7 +555,16 @@ __device__ __forceinline__ void skinny_gemm_body(const CUtensorMap &tmA, const C
             for (int j = 0; j < KBOX; ++j) {
                 const int32_t k0 = kb * Cfg::KSTAGE + j * Cfg::BK;
                 const uint32_t sb = base + Cfg::OFF_B + st * Cfg::B_BYTES + j * Cfg::B_BOX;
-                if constexpr (GATED) {
+                if constexpr (BT) {
+                    const bool second = kb >= args.k2_block;
+                    const int32_t ks = second ? k0 - args.k2_block * Cfg::KSTAGE : k0;
+                    const CUtensorMap *mb = second ? tmB2 : &tmB;
+                    tma_load_2d(sb, mb, full_bar(st), t * Cfg::BN, ks);
+                    tma_load_2d(sb + Cfg::B_BOX / 2, mb, full_bar(st), t * Cfg::BN + 64, ks);
+                    tma_load_2d(base + Cfg::OFF_A + st * Cfg::A_BYTES + j * Cfg::A_BOX, second ? tmS2 : &tmA,
+                                full_bar(st), ks, 0);
+                    continue;
+                } else if constexpr (GATED) {
                     tma_load_2d(sb, &tmB, full_bar(st), k0, t * 64);
                     tma_load_2d(sb + Cfg::B_BOX / 2, tmB2, full_bar(st), k0, t * 64);
                 } else {
@@ -656,7 +671,7 @@ __device__ __forceinline__ void skinny_gemm_body(const CUtensorMap &tmA, const C
         // ------------------------------------------------------------ MMA issuers
         const int e = static_cast<int>(warp) - 1;  // this warp's share of each stage's blocks
         if (lane == 0) {
-            const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, Cfg::BN, MP);
+            const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, Cfg::BN, MP, BT, false);
             int s = 0;
             uint32_t ph = 0;
             int ab = 0;
@@ -731,14 +746,16 @@ __device__ __forceinline__ void skinny_gemm_body(const CUtensorMap &tmA, const C
                                 tc_mma_f16_tmem_a(d_tmem, bt + 8u * k, ad + 2u * k, idesc,
                                                   (st != i || j != e || k != 0) ? 1u : 0u);
                         } else {
-                            const uint64_t bd = sdesc_k_sw128(base + Cfg::OFF_B + s * Cfg::B_BYTES +
-                                                              j * Cfg::B_BOX);
+                            const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES + j * Cfg::B_BOX;
+                            const uint64_t bd = BT ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
+                            // descriptor step of a K step of 16: 32 bytes, or 16 rows of 128
+                            constexpr uint32_t kStepB = BT ? 128u : 2u;
                             // (several issuers: issuer e takes K steps e KPER .. of each box)
                             constexpr int KPER = (Cfg::BK / 16) / Cfg::ISSUERS;
 #pragma unroll
                             for (int kk = 0; kk < KPER; ++kk) {
                                 const int k = e * KPER + kk;
-                                tc_mma_f16(d_tmem, bd + 2u * k, ad + 2u * k, idesc,
+                                tc_mma_f16(d_tmem, bd + kStepB * k, ad + 2u * k, idesc,
                                            (st != i || j != 0 || kk != 0) ? 1u : 0u);
                             }
                         }
@@ -1184,7 +1201,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, W4, MX>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmS,
                        const __grid_constant__ CUtensorMap tmSA, const GemmArgs args)
 {
-    skinny_gemm_body<MP, KBOX, W4, MX, false>(tmA, tmB, tmS, tmSA, nullptr, nullptr, args);
+    skinny_gemm_body<MP, KBOX, W4, MX, false, false>(tmA, tmB, tmS, tmSA, nullptr, nullptr, args);
 }
 
 // The gated form: Bg and Bu (tmB, tmB2), (MX) their scales (tmS, tmS2).
@@ -1197,7 +1214,18 @@ __global__ void __launch_bounds__(SkinnyCfg<MP, KBOX, false, MX, true>::THREADS,
                         const __grid_constant__ CUtensorMap tmB2,
                         const __grid_constant__ CUtensorMap tmS2, const GemmArgs args)
 {
-    skinny_gemm_body<MP, KBOX, false, MX, true>(tmA, tmB, tmS, tmSA, &tmB2, &tmS2, args);
+    skinny_gemm_body<MP, KBOX, false, MX, true, false>(tmA, tmB, tmS, tmSA, &tmB2, &tmS2, args);
+}
+
+// B (and B2) stored K x N; A2: the second source's rows.
+template <int MP, int KBOX>
+__global__ void __launch_bounds__(SkinnyCfg<MP, KBOX>::THREADS, 1)
+    skinny_trans_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmB2,
+                        const __grid_constant__ CUtensorMap tmA2, const GemmArgs args)
+{
+    skinny_gemm_body<MP, KBOX, false, false, false, true>(tmA, tmB, tmB, tmA, &tmB2, &tmA2, args);
 }
 
 }  // namespace tcg

@@ -144,6 +144,10 @@ cudaError_t launch_skinny(int mp, const GemmMaps &maps, const GemmArgs &args, in
 // columns, maps.sfa: A's.  Tiles are 64 columns of D.
 cudaError_t launch_skinny_gated(int mp, bool mx, const GemmMaps &maps, const TileMapsTwo &two,
                                 const GemmArgs &args, int grid, cudaStream_t stream);
+// B stored K x N (boxes of 64 columns x 64 K rows); two.a2, two.b2: the second
+// source along K (args.k2_block), if any.
+cudaError_t launch_skinny_trans(int mp, const GemmMaps &maps, const TileMapsTwo &two, const GemmArgs &args,
+                                int grid, cudaStream_t stream);
 
 // Stream-K split of the skinny kernel: the CTA that owns linear k-block x
 // when W blocks are shared by G CTAs as [W g / G, W (g+1) / G).

@@ -300,6 +300,29 @@ def test_gradients_against_the_formula(act, M, N, K, dtype, out):
     check_products(x, dA, dBg, dBu, dG, dU, out, act)
 
 
+@pytest.mark.parametrize("M,N,K,dtype", [(1, 2048, 1032, BF16), (16, 1367, 1000, F16), (33, 3000, 520, BF16),
+                                         (64, 4096, 264, F16)])
+def test_gradients_of_few_tokens(M, N, K, dtype):
+    """dA's long sum on the swap-AB kernel, both sources in one list of K blocks."""
+    x = backward_inputs(M + K, M, N, K, dtype)
+    for form in ((0, 0), (2, 0)):
+        binding.gemm_debug_force_tile(*form)
+        check_products(x, *binding.gemm_gated_backward(**x, out=OUT_F32), OUT_F32, str(form))
+
+
+def test_fp4_long_output_under_repeats():
+    """A large float32 result keeps HBM busy with stores while loads are late: forty launches, each
+    equal to the first and without a wait that ran out."""
+    r = gen(12)
+    q = [x for n, s in ((2048, 1.0), (8192, 0.05), (8192, 0.05))
+         for x in binding.gemm_quantize_e2m1(torch.randn((n, 1024), generator=r).mul(s).cuda())]
+    first = binding.gemm_gated_e2m1(*q)
+    for _ in range(40):
+        D = torch.full_like(first, float("nan"))
+        assert torch.equal(binding.gemm_gated_e2m1(*q, D), first)
+    assert device_status() == binding.GEMM_OK
+
+
 @pytest.mark.parametrize("form", ["single64", "single128", "single256", "pair", "pair512"])
 def test_gradients_every_form(form):
     binding.gemm_debug_force_tile(*{"pair512": (4, 512)}.get(form, FORMS.get(form)))

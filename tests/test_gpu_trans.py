@@ -56,6 +56,22 @@ def test_exact_every_form(form, ta, tb):
             assert torch.equal(got.cpu(), s.float().to(ref.out_dtype(out))), (form, M, N, K, dtype, out)
 
 
+@pytest.mark.parametrize("form", ["auto", "skinny"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 130, 64), (3, 128, 1000), (16, 1030, 65), (17, 200, 2056),
+                                   (33, 520, 4100), (64, 257, 328), (48, 4096, 1024)])
+def test_exact_few_rows_of_a(form, M, N, K):
+    """The swap-AB kernel with B stored K x N: partial tiles, K shared out over CTAs, ragged sizes."""
+    binding.gemm_debug_force_tile(*((2, 0) if form == "skinny" else (0, 0)))
+    for dtype, out in ((BF16, OUT_F32), (F16, OUT_BF16), (BF16, OUT_F16)):
+        A, B, C = operands(M + N + K, M, N, K, False, True, dtype, True)
+        s, _ = product(A, B, False, True)
+        got = binding.gemm_trans(A, B, C, trans_b=True, alpha=0.5, beta=2.0, out=out)
+        want = (0.5 * s + 2.0 * C.cpu().double()).float().to(ref.out_dtype(out))
+        assert torch.equal(got.cpu(), want), (M, N, K, dtype, out)
+        got = binding.gemm_trans(A, B, trans_b=True, out=out)
+        assert torch.equal(got.cpu(), s.float().to(ref.out_dtype(out))), (M, N, K, dtype, out)
+
+
 @pytest.mark.parametrize("ta,tb", STORED)
 @pytest.mark.parametrize("M,N,K,dtype,out", [(1, 300, 4096, BF16, OUT_F32), (64, 4096, 1000, F16, OUT_F16),
                                              (500, 264, 4100, BF16, OUT_BF16)])
