@@ -345,7 +345,54 @@ struct TransProblem {
     // launched right behind a kernel that it does not depend on, but that waited
     // for what it does depend on: it starts on the SMs that kernel leaves idle
     bool co_tail = false;
+    int parts_use = kBufParts;  // buffer for the parts of a sum (its own for each product under way)
 };
+
+// How the sums of a product may be cut: `parts` of `k_part` K blocks each (1: not
+// cut), on single CTAs with 128 x bn tiles.
+struct Parts {
+    int parts;
+    int64_t k_part;
+    int bn;
+};
+
+// A product with few tiles and a long sum leaves most SMs idle: cut the sum, add
+// the parts' float32 results in a second kernel.  Time of a form, in ns: waves of
+// CTAs x K blocks x the time per K block (the operand bytes from L2 to an SM:
+// 190, 260 and 390 for 64, 128 and 256 columns, 280 for a pair's 256 x 256), and
+// for parts the second kernel, 2500 and its bytes.  At least 8 K blocks a part.
+Parts choose_parts(int64_t M, int64_t N, int64_t k_blocks, int m_sources, int sm_count)
+{
+    Parts best{1, k_blocks, 0};
+    if (k_blocks < 16 || M > (int64_t(1) << 20) || N > (int64_t(1) << 20))
+        return best;
+    const int widths[3] = {64, 128, 256};
+    const int64_t step[3] = {190, 260, 390};
+    const int64_t pair_tiles = m_sources * ceil_div(M, 256) * ceil_div(N, 256);
+    int64_t best_ns = ceil_div(pair_tiles, sm_count / 2 > 0 ? sm_count / 2 : 1) * k_blocks * 280;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = m_sources * ceil_div(M, 128) * ceil_div(N, widths[i]);
+        const int64_t whole = ceil_div(tiles, sm_count) * k_blocks * step[i];
+        if (whole < best_ns) {
+            best_ns = whole;
+            best = Parts{1, k_blocks, 0};
+        }
+        if (tiles > sm_count)
+            continue;
+        for (int64_t parts = 2; parts <= 16 && parts * tiles <= sm_count && k_blocks / parts >= 8; ++parts) {
+            const int64_t k_part = ceil_div(k_blocks, parts);
+            if ((parts - 1) * k_part >= k_blocks)
+                continue;  // (the last part would be empty)
+            // written and read once each, mostly in L2: 4 + 4 bytes at ~6 KB a ns
+            const int64_t ns = k_part * step[i] + 2500 + m_sources * M * N * 8 * parts / 6000;
+            if (ns < best_ns) {
+                best_ns = ns;
+                best = Parts{static_cast<int>(parts), k_part, widths[i]};
+            }
+        }
+    }
+    return best;
+}
 
 void fill_trans(GemmArgs &a, const TransProblem &p, const DeviceInfo *dev)
 {
@@ -410,15 +457,38 @@ gemm_status run_trans_skinny(const TransProblem &p, const gemm_plan &plan, const
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// Launch (arguments already checked; M, N > 0).
-gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
+// The second kernel of a product in parts (parts 0: there is none).
+struct AddParts {
+    const float *W = nullptr;
+    int64_t ldw = 0, part_rows = 0, second = 0;  // second: rows before the second stacked source's
+    int parts = 0;
+};
+
+// Add the parts of the product p.
+gemm_status add_parts(const TransProblem &p, const AddParts &add)
+{
+    if (add.parts == 0)
+        return GEMM_OK;
+    const bool c_used = p.C != nullptr && p.beta != 0.0f;
+    for (int i = 0; i < (p.D2 ? 2 : 1); ++i)
+        if (tcg::launch_add_parts(add.W + i * add.second * add.ldw, add.ldw, add.part_rows, add.parts,
+                                  c_used ? p.C : nullptr, p.ldc, i == 0 ? p.D : p.D2, i == 0 ? p.ldd : p.ldd2,
+                                  p.out, p.alpha, p.beta, static_cast<int32_t>(p.M),
+                                  static_cast<int32_t>(p.N), p.stream) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+    return GEMM_OK;
+}
+
+// Launch the product (arguments already checked; M, N > 0).  In parts, *add says
+// what add_parts has to add.
+gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev, AddParts *add)
 {
     const bool c_used = p.C != nullptr && p.beta != 0.0f;
     const int stored = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
-    const gemm_plan plan =
-        trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, p.B2 ? 2 : 1, stored, c_used, dev->sm_count);
+    gemm_plan plan = trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, p.B2 ? 2 : 1, stored, c_used, dev->sm_count);
     if (plan.kernel == 2)
         return run_trans_skinny(p, plan, dev);
+    const int parts = plan.splits;
     const bool pair = plan.kernel != 1;
     const int nsub = plan.kernel == 4 ? 2 : 1;
     const int bn = pair ? 256 : plan.bn;
@@ -452,6 +522,45 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev)
     fill_trans(a, p, dev);
     const int64_t m_blocks = ceil_div(p.M, plan.bm), k_blocks = ceil_div(p.K, 64);
     const bool more_k = p.B2 != nullptr, more_m = p.D2 != nullptr;
+    if (parts > 1) {
+        // every part's tiles, one part's block rows after the other, into a float32
+        // workspace of whole tiles' rows; C, alpha and D's type come with the adding
+        const int64_t part_m = more_m ? 2 * m_blocks : m_blocks;
+        const int64_t ldw = ceil_div(p.N, 4) * 4, rows = parts * part_m * plan.bm;
+        void *w = nullptr;
+        const gemm_status st = get_dequant_buffer(dev->index, p.stream, p.parts_use,
+                                                  static_cast<size_t>(rows) * ldw * sizeof(float), &w);
+        if (st != GEMM_OK)
+            return st;
+        a.M = static_cast<int32_t>(rows);
+        a.alpha = 1.0f;
+        a.has_c = 0;
+        a.D = w;
+        a.ldd = ldw;
+        a.out_kind = GEMM_OUT_F32;
+        a.part_m = static_cast<int32_t>(part_m);
+        a.num_m_blocks = static_cast<int32_t>(parts * part_m);
+        a.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, bn));
+        a.num_k_blocks = static_cast<int32_t>(ceil_div(more_k ? 2 * k_blocks : k_blocks, parts));
+        a.num_tiles = a.num_m_blocks * a.num_n_blocks;
+        a.k2_block = more_k ? static_cast<int32_t>(k_blocks) : INT_MAX;
+        a.m2_block = more_m ? static_cast<int32_t>(m_blocks) : INT_MAX;
+        a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
+        a.splits = 1;
+        a.d_tma = 1;
+        a.co_tail = p.co_tail ? 1 : 0;
+        // (the pitch is whole 16 bytes: a row's padding is written too)
+        if (!encode_out(&maps.d, w, GEMM_OUT_F32, rows, ldw, ldw))
+            return GEMM_ERR_CUDA;
+        a.N = static_cast<int32_t>(ldw);
+        add->W = static_cast<const float *>(w);
+        add->ldw = ldw;
+        add->part_rows = part_m * plan.bm;
+        add->second = m_blocks * plan.bm;
+        add->parts = parts;
+        const cudaError_t e = tcg::launch_tile_major(stored, bn, false, 1, maps, two, a, grid, p.stream);
+        return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    }
     a.num_m_blocks = static_cast<int32_t>(more_m ? 2 * m_blocks : m_blocks);
     a.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, bn * nsub));
     a.num_k_blocks = static_cast<int32_t>(more_k ? 2 * k_blocks : k_blocks);
@@ -596,6 +705,16 @@ gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sourc
                         sm_count, false);
         return p;
     }
+    const bool forced = fk == 1 || fk == 3 || fk == 4;
+    const Parts cut = forced ? Parts{1, 0, 0}
+                             : choose_parts(M, N, k_sources * ceil_div(K, 64), m_sources, sm_count);
+    if (cut.parts > 1) {
+        set_tile_plan(p, 1, cut.bn, M, N, sm_count);
+        p.splits = cut.parts;
+        p.tiles *= static_cast<int64_t>(m_sources) * cut.parts;
+        p.grid = static_cast<int32_t>(p.tiles < sm_count ? p.tiles : sm_count);
+        return p;
+    }
     TileChoice c = choose_tile(m_sources * M, N, k_sources * K, false, c_used, false, sm_count);
     // A short sum leaves the stores to set the time: single CTAs, which start and
     // finish a tile without the pair's hand-overs (two sources stacked along M, 14336 x
@@ -717,7 +836,10 @@ gemm_status gemm_trans(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, int t
     DeviceInfo *dev = nullptr;
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
-    return run_trans(p, dev);
+    AddParts add;
+    if ((st = run_trans(p, dev, &add)) != GEMM_OK)
+        return st;
+    return add_parts(p, add);
 }
 
 gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, const void *dD,
@@ -763,58 +885,62 @@ gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf
         tcg::launch_gated_slope(dD, lddd, G, ldg, U, ldu, dG, lddg, dU, lddu, static_cast<int32_t>(M),
                                 static_cast<int32_t>(N), bf16, act, cs) != cudaSuccess)
         return GEMM_ERR_CUDA;
+    TransProblem pa{}, pb{};
+    AddParts add_a, add_b;
     if (want_a) {
         // dA = [dG dU] [Bg; Bu]: one sum over 2 N, Bg and Bu read as stored (K columns contiguous)
-        TransProblem p{};
-        p.M = M;
-        p.N = K;
-        p.K = N;
-        p.bf16 = bf16;
-        p.tb = true;
-        p.A = dG;
-        p.lda = lddg;
-        p.B = Bg;
-        p.ldb = ldbg;
-        p.A2 = dU;
-        p.lda2 = lddu;
-        p.B2 = Bu;
-        p.ldb2 = ldbu;
-        p.D = dA;
-        p.ldd = ldda;
-        p.out = out;
-        p.alpha = 1.0f;
-        p.stream = cs;
-        if ((st = run_trans(p, dev)) != GEMM_OK)
+        pa.M = M;
+        pa.N = K;
+        pa.K = N;
+        pa.bf16 = bf16;
+        pa.tb = true;
+        pa.A = dG;
+        pa.lda = lddg;
+        pa.B = Bg;
+        pa.ldb = ldbg;
+        pa.A2 = dU;
+        pa.lda2 = lddu;
+        pa.B2 = Bu;
+        pa.ldb2 = ldbu;
+        pa.D = dA;
+        pa.ldd = ldda;
+        pa.out = out;
+        pa.alpha = 1.0f;
+        pa.stream = cs;
+        if ((st = run_trans(pa, dev, &add_a)) != GEMM_OK)
             return st;
     }
     if (want_b) {
         // [dBg; dBu] = [dG dU]^T A: both gradients' tiles in one launch, which fills the
         // SMs as dA's tiles run out (both only need dG and dU: dA's kernel let this
         // one start once it had passed its own wait for them)
-        TransProblem p{};
-        p.co_tail = want_a;
-        p.M = N;
-        p.N = K;
-        p.K = M;
-        p.bf16 = bf16;
-        p.ta = true;
-        p.tb = true;
-        p.A = dG;
-        p.lda = lddg;
-        p.A2 = dU;
-        p.lda2 = lddu;
-        p.B = A;
-        p.ldb = lda;
-        p.D = dBg;
-        p.ldd = lddbg;
-        p.D2 = dBu;
-        p.ldd2 = lddbu;
-        p.out = out;
-        p.alpha = 1.0f;
-        p.stream = cs;
-        if ((st = run_trans(p, dev)) != GEMM_OK)
+        pb.co_tail = want_a;
+        pb.parts_use = kBufParts + 1;
+        pb.M = N;
+        pb.N = K;
+        pb.K = M;
+        pb.bf16 = bf16;
+        pb.ta = true;
+        pb.tb = true;
+        pb.A = dG;
+        pb.lda = lddg;
+        pb.A2 = dU;
+        pb.lda2 = lddu;
+        pb.B = A;
+        pb.ldb = lda;
+        pb.D = dBg;
+        pb.ldd = lddbg;
+        pb.D2 = dBu;
+        pb.ldd2 = lddbu;
+        pb.out = out;
+        pb.alpha = 1.0f;
+        pb.stream = cs;
+        if ((st = run_trans(pb, dev, &add_b)) != GEMM_OK)
             return st;
     }
+    // (sums in parts are added last, so that the products run side by side)
+    if ((st = add_parts(pa, add_a)) != GEMM_OK || (st = add_parts(pb, add_b)) != GEMM_OK)
+        return st;
     return GEMM_OK;
 }
 

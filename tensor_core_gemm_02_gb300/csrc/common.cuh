@@ -66,6 +66,9 @@ struct GemmArgs {
     // products with two sources: K blocks from k2_block on read the second pair
     // of operands, block rows from m2_block on the second A and D
     int32_t k2_block, m2_block;
+    int32_t part_m;         // a sum in parts (0: whole): part p is the block rows from
+                            // p part_m on and the num_k_blocks K blocks from p num_k_blocks
+                            // on, and D the parts' float32 workspace
     int32_t d_wide;         // (operands stored K x M / K x N) 16-bit D without C: boxes of 64
                             // columns instead of 32
     void *D2;

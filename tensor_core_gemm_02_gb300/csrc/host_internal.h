@@ -97,9 +97,10 @@ void fill_common(GemmArgs &a, const Problem &p, const DeviceInfo *dev);
 gemm_status reset_static_scratch(int device);
 
 // Buffers the library keeps per (device, stream, use), grown geometrically:
-// bf16 weights converted from FP4, and block scales copied to a 16-byte row
-// pitch for TMA (B's for gemm_bf16_e2m1; A's and B's for gemm_e2m1).
-enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4 };
+// bf16 weights converted from FP4, block scales copied to a 16-byte row pitch
+// for TMA (B's for gemm_bf16_e2m1; A's and B's for gemm_e2m1, and Bu's for
+// gemm_gated_e2m1), and the parts of sums (kBufParts and the one after it).
+enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4, kBufParts = 5 };
 gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t bytes, void **out);
 
 // The form forced by gemm_debug_force_tile (kernel 0: none).

@@ -301,6 +301,11 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 else
                     tma_load_2d(dst, m, bar, x, y);
             };
+            // (a sum in parts: block row mb of part p starts at the part's K block)
+            if (MAJ != 0 && args.part_m > 0) {
+                kb += mb / args.part_m * args.num_k_blocks;
+                mb %= args.part_m;
+            }
             const bool second_k = MAJ != 0 && kb >= args.k2_block;
             const bool second_m = MAJ != 0 && mb >= args.m2_block;
             const CUtensorMap *ma = second_k || second_m ? &two->a2 : &tmA;
@@ -1238,8 +1243,9 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
             tile_coords(t, args, mb, nb);
             if (MC > 1)
                 nb = nb * MC + static_cast<int32_t>(share);
-            // (two sources stacked along M: the second has its own rows and D)
-            const bool second_m = MAJ != 0 && mb >= args.m2_block;
+            // (two sources stacked along M: the second has its own rows and D; a sum in
+            // parts: all of them go to the workspace as they are stacked)
+            const bool second_m = MAJ != 0 && args.part_m == 0 && mb >= args.m2_block;
             const CUtensorMap *const map_d = second_m ? &two->d2 : &tmD;
             void *const out_d = second_m ? args.D2 : args.D;
             const int64_t out_ld = second_m ? args.ldd2 : args.ldd;

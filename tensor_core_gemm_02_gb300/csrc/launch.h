@@ -96,6 +96,12 @@ cudaError_t launch_tile_major(int maj, int bn, bool pair, int nsub, const GemmMa
                               const TileMapsTwo &two, const GemmArgs &args, int grid,
                               cudaStream_t stream);
 
+// D[i][j] = fma.rn(alpha, sum_p W[p part_rows + i][j], beta C[i][j]) for i < M, j <
+// N, the parts p < parts added in order: W float32, ldw apart; D of type out.
+cudaError_t launch_add_parts(const float *W, int64_t ldw, int64_t part_rows, int32_t parts, const float *C,
+                             int64_t ldc, void *D, int64_t ldd, int out, float alpha, float beta, int32_t M,
+                             int32_t N, cudaStream_t stream);
+
 // dG = dD * U * act'(G), dU = dD * act(G) over M x N, 16-bit (bf16 or f16)
 // matrices; dG may be G and dU may be U.
 cudaError_t launch_gated_slope(const void *dD, int64_t lddd, const void *G, int64_t ldg,

@@ -310,6 +310,17 @@ def test_gradients_of_few_tokens(M, N, K, dtype):
         check_products(x, *binding.gemm_gated_backward(**x, out=OUT_F32), OUT_F32, str(form))
 
 
+@pytest.mark.parametrize("M,N,K,dtype", [(200, 3000, 136, BF16), (4100, 130, 72, F16), (2050, 300, 520, BF16)])
+def test_gradients_with_sums_in_parts(M, N, K, dtype):
+    """Long sums over few tiles (dA's over 2 N, the weight gradients' over M): both products in
+    parts, each in a buffer of its own, twice in a row."""
+    x = backward_inputs(M + N, M, N, K, dtype)
+    first = binding.gemm_gated_backward(**x, out=OUT_F32)
+    check_products(x, *first, OUT_F32, "in parts")
+    for a, b in zip(first, binding.gemm_gated_backward(**x, out=OUT_F32)):
+        assert torch.equal(a, b)
+
+
 def test_fp4_long_output_under_repeats():
     """A large float32 result keeps HBM busy with stores while loads are late: forty launches, each
     equal to the first and without a wait that ran out."""

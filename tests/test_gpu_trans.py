@@ -72,6 +72,29 @@ def test_exact_few_rows_of_a(form, M, N, K):
         assert torch.equal(got.cpu(), s.float().to(ref.out_dtype(out))), (M, N, K, dtype, out)
 
 
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+@pytest.mark.parametrize("M,N,K", [(100, 130, 2056), (128, 64, 4096), (300, 257, 4100), (257, 1001, 8200),
+                                   (66, 5, 3000)])
+def test_exact_long_sums_in_parts(ta, tb, M, N, K):
+    """Few tiles and many K blocks: the sum is cut into parts (the plan says how many), the parts
+    added in a second kernel, with C (in place too), every output type and odd addresses."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert binding.gemm_query_plan(M, N, K, trans=(ta, tb), sm_count=sms).splits > 1
+    for dtype, out in ((BF16, OUT_F32), (F16, OUT_BF16), (BF16, OUT_F16)):
+        A, B, C = operands(M + N + K, M, N, K, ta, tb, dtype, True)
+        s, _ = product(A, B, ta, tb)
+        got = binding.gemm_trans(A, B, C, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=out)
+        want = (0.5 * s + 2.0 * C.cpu().double()).float().to(ref.out_dtype(out))
+        assert torch.equal(got.cpu(), want), (dtype, out)
+        buf = torch.full((M, N + 5), 9.0, dtype=ref.out_dtype(out), device="cuda")
+        binding.gemm_trans(A, B, None, buf[:, 3:3 + N], trans_a=ta, trans_b=tb, out=out)
+        assert torch.equal(buf[:, 3:3 + N].cpu(), s.float().to(ref.out_dtype(out))), (dtype, out)
+        assert (buf[:, :3] == 9.0).all() and (buf[:, 3 + N:] == 9.0).all()
+    acc = C.clone()
+    binding.gemm_trans(A, B, acc, acc, trans_a=ta, trans_b=tb)
+    assert torch.equal(acc.cpu(), (s + C.cpu().double()).float())
+
+
 @pytest.mark.parametrize("ta,tb", STORED)
 @pytest.mark.parametrize("M,N,K,dtype,out", [(1, 300, 4096, BF16, OUT_F32), (64, 4096, 1000, F16, OUT_F16),
                                              (500, 264, 4100, BF16, OUT_BF16)])
