@@ -299,6 +299,14 @@ def _mat(name, t, rows, cols, dtype):
     return t.data_ptr(), ld
 
 
+def _on_device(*tensors):
+    """Every given tensor lies on the current CUDA device, where the call runs."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
 def _mat_or_null(name, t, rows, cols, dtype):
     return (None, 0) if t is None else _mat(name, t, rows, cols, dtype)
 
@@ -309,16 +317,11 @@ _empty_strided_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guard
                               "_empty_strided_cuda", None)
 
 
-def _empty(rows, cols, pitch, dtype, device):
+def _allocator(device):
+    """A function (size, stride, dtype) -> uninitialised tensor on the device."""
     if _empty_strided_cuda is not None and device.type == "cuda" and device.index == torch._C._cuda_getDevice():
-        return _empty_strided_cuda((rows, cols), (pitch, 1), dtype)
-    return torch.empty_strided((rows, cols), (pitch, 1), dtype=dtype, device=device)
-
-
-def _padded(rows, cols, dtype, device):
-    """An uninitialised matrix whose row pitch is a multiple of 16 bytes."""
-    per = 16 // dtype.itemsize
-    return _empty(rows, cols, (cols + per - 1) // per * per, dtype, device)
+        return _empty_strided_cuda
+    return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=device)
 
 
 def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, stream=None):
@@ -331,11 +334,12 @@ def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, 
     M, K = A.shape
     N = Bg.shape[0]
     if D is None:
-        D = _empty(M, N, N, _DTYPE_OF_OUT[out], A.device)
-    st = load_library().gemm_gated(
-        M, N, K, bf16, *_mat("A", A, M, K, dt), *_mat("Bg", Bg, N, K, dt), *_mat("Bu", Bu, N, K, dt),
-        *_mat_or_null("G", G, M, N, dt), *_mat_or_null("U", U, M, N, dt),
-        *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act), _stream_ptr(stream))
+        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+    args = (M, N, K, bf16, *_mat("A", A, M, K, dt), *_mat("Bg", Bg, N, K, dt), *_mat("Bu", Bu, N, K, dt),
+            *_mat_or_null("G", G, M, N, dt), *_mat_or_null("U", U, M, N, dt),
+            *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act))
+    _on_device(A, Bg, Bu, G, U, D)
+    st = load_library().gemm_gated(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated")
     return D
@@ -348,12 +352,12 @@ def gemm_gated_e2m1(Aq, As, Bgq, Bgs, Buq, Bus, D=None, *, act=ACT_SILU, out=OUT
     N = Bgq.shape[0]
     blocks, u8 = half // 16, torch.uint8
     if D is None:
-        D = _empty(M, N, N, _DTYPE_OF_OUT[out], Aq.device)
-    st = load_library().gemm_gated_e2m1(
-        M, N, 2 * half, *_mat("Aq", Aq, M, half, u8), *_mat("As", As, blocks, M, u8),
-        *_mat("Bgq", Bgq, N, half, u8), *_mat("Bgs", Bgs, blocks, N, u8), *_mat("Buq", Buq, N, half, u8),
-        *_mat("Bus", Bus, blocks, N, u8), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act),
-        _stream_ptr(stream))
+        D = _allocator(Aq.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+    args = (M, N, 2 * half, *_mat("Aq", Aq, M, half, u8), *_mat("As", As, blocks, M, u8),
+            *_mat("Bgq", Bgq, N, half, u8), *_mat("Bgs", Bgs, blocks, N, u8), *_mat("Buq", Buq, N, half, u8),
+            *_mat("Bus", Bus, blocks, N, u8), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act))
+    _on_device(Aq, As, Bgq, Bgs, Buq, Bus, D)
+    st = load_library().gemm_gated_e2m1(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated_e2m1")
     return D
@@ -366,31 +370,36 @@ def gemm_gated_backward(dD, G, U, A, Bg, Bu, *, dG=None, dU=None, dA=None, dBg=N
     dA = dG @ Bg + dU @ Bu, dBg = dG.T @ A and dBu = dU.T @ A in `out`'s type.
     dG may be G and dU may be U.  need_input / need_weights leave out dA / dBg
     and dBu (then None).  Returns (dA, dBg, dBu, dG, dU)."""
-    dt, dev, ot = dD.dtype, dD.device, _DTYPE_OF_OUT[out]
+    dt, new, ot = dD.dtype, _allocator(dD.device), _DTYPE_OF_OUT[out]
     bf16 = _bf16_flag("dD", dt)
     M, N = dD.shape
     K = A.shape[1] if need_weights else (Bg.shape[1] if need_input else 0)
     null = (None, 0)
-    dG = _padded(M, N, dt, dev) if dG is None else dG
-    dU = _padded(M, N, dt, dev) if dU is None else dU
+    pitch = (N + 7) // 8 * 8  # rows of whole 16 bytes
+    dG = new((M, N), (pitch, 1), dt) if dG is None else dG
+    dU = new((M, N), (pitch, 1), dt) if dU is None else dU
     a = bg = bu = pa = pbg = pbu = null
     if need_input:
         bg, bu = _mat("Bg", Bg, N, K, dt), _mat("Bu", Bu, N, K, dt)
-        dA = _empty(M, K, K, ot, dev) if dA is None else dA
+        dA = new((M, K), (K, 1), ot) if dA is None else dA
         pa = _mat("dA", dA, M, K, ot)
     else:
         dA = None
     if need_weights:
         a = _mat("A", A, M, K, dt)
-        dBg = _empty(N, K, K, ot, dev) if dBg is None else dBg
-        dBu = _empty(N, K, K, ot, dev) if dBu is None else dBu
+        dBg = new((N, K), (K, 1), ot) if dBg is None else dBg
+        dBu = new((N, K), (K, 1), ot) if dBu is None else dBu
         pbg, pbu = _mat("dBg", dBg, N, K, ot), _mat("dBu", dBu, N, K, ot)
     else:
         dBg = dBu = None
-    st = load_library().gemm_gated_backward(
-        M, N, K, bf16, *_mat("dD", dD, M, N, dt), *_mat("G", G, M, N, dt), *_mat("U", U, M, N, dt),
-        *a, *bg, *bu, *_mat("dG", dG, M, N, dt), *_mat("dU", dU, M, N, dt), *pa, *pbg, *pbu, out,
-        _act(act), _stream_ptr(stream))
+    args = (M, N, K, bf16, *_mat("dD", dD, M, N, dt), *_mat("G", G, M, N, dt), *_mat("U", U, M, N, dt),
+            *a, *bg, *bu, *_mat("dG", dG, M, N, dt), *_mat("dU", dU, M, N, dt), *pa, *pbg, *pbu, out, _act(act))
+    _on_device(dD, G, U, dG, dU, dA, dBg, dBu)
+    if need_input:
+        _on_device(Bg, Bu)
+    if need_weights:
+        _on_device(A)
+    st = load_library().gemm_gated_backward(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated_backward")
     return dA, dBg, dBu, dG, dU
@@ -410,11 +419,12 @@ def gemm_trans(A, B, C=None, D=None, *, trans_a=False, trans_b=False, alpha=1.0,
     if K != Kb:
         raise ValueError("A and B disagree on K")
     if D is None:
-        D = _empty(M, N, N, _DTYPE_OF_OUT[out], A.device)
-    st = load_library().gemm_trans(
-        M, N, K, bf16, 1 if trans_a else 0, *_mat("A", A, ra, ca, dt), 1 if trans_b else 0,
-        *_mat("B", B, rb, cb, dt), *_mat_or_null("C", C, M, N, torch.float32),
-        *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, alpha, beta, _stream_ptr(stream))
+        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+    args = (M, N, K, bf16, 1 if trans_a else 0, *_mat("A", A, ra, ca, dt), 1 if trans_b else 0,
+            *_mat("B", B, rb, cb, dt), *_mat_or_null("C", C, M, N, torch.float32),
+            *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, alpha, beta)
+    _on_device(A, B, C, D)
+    st = load_library().gemm_trans(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_trans")
     return D
@@ -431,13 +441,16 @@ def gemm_quantize_e2m1(X, Q=None, S=None, *, Y=None, stream=None):
         raise TypeError("X must be float32, bfloat16 or float16")
     M, K = X.shape
     half, blocks = K // 2, K // 32
-    if Q is None:
-        Q = _empty(M, half, half, u8, X.device)
-    if S is None:
-        S = _padded(blocks, M, u8, X.device)
-    st = load_library().gemm_quantize_e2m1(
-        M, K, kind, *_mat("X", X, M, K, dt), *_mat("Q", Q, M, half, u8), *_mat("S", S, blocks, M, u8),
-        *_mat_or_null("Y", Y, M, K, dt), _stream_ptr(stream))
+    if Q is None or S is None:
+        new = _allocator(X.device)
+        if Q is None:
+            Q = new((M, half), (half, 1), u8)
+        if S is None:  # (rows of whole 16 bytes, which the products read in place)
+            S = new((blocks, M), ((M + 15) // 16 * 16, 1), u8)
+    args = (M, K, kind, *_mat("X", X, M, K, dt), *_mat("Q", Q, M, half, u8), *_mat("S", S, blocks, M, u8),
+            *_mat_or_null("Y", Y, M, K, dt))
+    _on_device(X, Q, S, Y)
+    st = load_library().gemm_quantize_e2m1(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_quantize_e2m1")
     return Q, S

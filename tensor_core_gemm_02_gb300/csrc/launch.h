@@ -178,7 +178,7 @@ inline int64_t skinny_sk_tiles(int64_t T, int64_t G, bool w4)
 
 // Most CTAs that contribute to one shared tile (workspace slots per tile)
 // when `tiles` tiles of nkb K blocks are shared by G CTAs.
-inline int32_t skinny_max_parts(int64_t tiles, int64_t nkb, int64_t G)
+inline int32_t skinny_max_parts_of(int64_t tiles, int64_t nkb, int64_t G)
 {
     if (tiles == 0)
         return 1;
@@ -196,6 +196,21 @@ inline int32_t skinny_max_parts(int64_t tiles, int64_t nkb, int64_t G)
         most = parts > most ? parts : most;
     }
     return static_cast<int32_t>(most);
+}
+
+// The same, remembering the last few answers: two divisions a tile are microseconds of
+// a call whose kernel takes ten, and a model's calls come in a few sizes.
+inline int32_t skinny_max_parts(int64_t tiles, int64_t nkb, int64_t G)
+{
+    struct Answer {
+        int64_t tiles, nkb, G;
+        int32_t parts;
+    };
+    static thread_local Answer last[16] = {};
+    Answer &a = last[static_cast<uint64_t>(tiles * 31 + nkb * 7 + G) % 16];
+    if (a.parts == 0 || a.tiles != tiles || a.nkb != nkb || a.G != G)
+        a = Answer{tiles, nkb, G, skinny_max_parts_of(tiles, nkb, G)};
+    return a.parts;
 }
 
 }  // namespace tcg

@@ -124,6 +124,12 @@ def test_binding_refusals():
         binding.gemm_quantize_e2m1(torch.zeros((4, 32), dtype=torch.float64))
     with pytest.raises(ValueError):
         binding.gemm_quantize_e2m1(h(4, 32), Q=torch.zeros((4, 15), dtype=torch.uint8))
+    for call in (lambda: binding.gemm_gated(h(4, 8), h(4, 8), h(4, 8)),  # right, but not on a CUDA device
+                 lambda: binding.gemm_trans(h(4, 8), h(8, 16), trans_b=True),
+                 lambda: binding.gemm_gated_backward(h(4, 8), h(4, 8), h(4, 8), h(4, 16), h(8, 16), h(8, 16)),
+                 lambda: binding.gemm_quantize_e2m1(h(4, 32))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
     u = lambda r, c: torch.zeros((r, c), dtype=torch.uint8)  # noqa: E731
     with pytest.raises(ValueError):
         binding.gemm_gated_e2m1(u(4, 16), u(1, 4), u(8, 16), u(1, 8), u(8, 16), u(1, 7))

@@ -171,11 +171,13 @@ def test_other_stream_graph_and_repeats(M):
     assert torch.equal(D, binding.gemm_gated(A, Bg, Bu, out=OUT_BF16)) and not torch.equal(D, first)
 
 
-@pytest.mark.parametrize("form", ["single128", "pair", "skinny", "fp4"])
+@pytest.mark.parametrize("form", ["single128", "pair", "skinny", "fp4_skinny", "fp4_128", "fp4_256"])
 def test_timeout_reports_and_recovers(form):
-    M = 16 if form == "skinny" else 300
+    M = 16 if "skinny" in form else 300
     A, Bg, Bu = inputs(2, M, 512, 1024, BF16, exact=True)
-    if form == "fp4":
+    if form.startswith("fp4"):
+        if M > 64:
+            binding.gemm_debug_force_tile(11, int(form[4:]))
         q = [x for t in (A, Bg, Bu) for x in binding.gemm_quantize_e2m1(t)]
         call = lambda: binding.gemm_gated_e2m1(*q, act="relu")  # noqa: E731
     else:
