@@ -633,7 +633,10 @@ gemm_plan gated_plan(int64_t M, int64_t N, int64_t K, bool keep, int sm_count)
         return p;
     }
     // waves of CTAs (pairs) x accumulator width plus a fixed cost per tile, pairs
-    // at 0.9 (each SM moves 2/3 of the operand bytes), as choose_tile weighs them
+    // at 0.8 (each SM moves 2/3 of the operand bytes; 128 columns / pairs, 2973 x 1184 x
+    // 1073: 3 waves 22.9 us, 2 waves 19.4; 777 x 2743 x 1000: 2 waves 16.5, 2 18.8);
+    // short sums on single CTAs, whose tiles end without the pair's hand-over
+    // (single / pair, 4096 x 14336, bf16: K = 128 63 / 76 us, 512 85 / 90, 1024 150 / 132)
     int kernel = 1, bn = 256;
     double best = -1.0;
     for (int w : {256, 128, 64}) {
@@ -645,9 +648,9 @@ gemm_plan gated_plan(int64_t M, int64_t N, int64_t K, bool keep, int sm_count)
         }
     }
     const int pairs = sm_count / 2;
-    if (K > 0 && pairs > 0) {
+    if (K >= 768 && pairs > 0) {
         const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 128);
-        if (0.9 * static_cast<double>(ceil_div(tiles, pairs) * (256 + 32)) <= best) {
+        if (0.8 * static_cast<double>(ceil_div(tiles, pairs) * (256 + 32)) <= best) {
             kernel = 3;
             bn = 256;
         }
@@ -664,19 +667,21 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
         return p;
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
-    if (M <= 64 && K > 0 && fk != 11) {
+    // M <= 64: the skinny kernel, except for short sums, over one wave of tiles at that,
+    // where its join of the parts costs more than the sum (skinny / tile: 8 x 934 x 384
+    // 7.4 / 5.4 us, 2 x 3674 x 1760 8.8 / 7.2, 2 x 12529 x 64 7.9 / 6.7; 32 x 8192 x 1024
+    // 5.8 / 6.1, 16 x 2048 x 2048 6.8 / 7.1, 8 x 14336 x 512 6.1 / 7.5)
+    const bool one_wave = ceil_div(N, 64) <= sm_count;
+    if (M <= 64 && K > 256 && fk != 11 && !(one_wave && K < 2048)) {
         set_e2m1_skinny_plan(p, M, ceil_div(N, 64), K, sm_count);
         return p;
     }
-    int bn = 256;
-    if (fk == 11) {
-        bn = fbn;
-    } else {
-        const int64_t w256 = ceil_div(ceil_div(M, 128) * ceil_div(N, 128), sm_count);
-        const int64_t w128 = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
-        if (w128 * (128 + 32) < w256 * (256 + 32))
-            bn = 128;
-    }
+    // 256 columns halve what a tile reads of A, but leave one group of epilogue
+    // warps: worth it for long sums over several waves (128 / 256 columns: 2048 x 4096 x
+    // 4096 47 / 37 us, 1024 x 4096 x 2048 17.1 / 16.2; 4096 x 4096 x 1024 31 / 39, 4096 x
+    // 14336 x 512 79 / 117, and 3 waves of 128 columns, 200 x 14336 x 4096, 22.9 / 23.9)
+    const int64_t waves = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
+    const int bn = fk == 11 ? fbn : (K >= 2048 && waves >= 4 ? 256 : 128);
     p.kernel = 11;
     p.bm = 128;
     p.bn = bn;
@@ -718,9 +723,15 @@ gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sourc
     TileChoice c = choose_tile(m_sources * M, N, k_sources * K, false, c_used, false, sm_count);
     // A short sum leaves the stores to set the time: single CTAs, which start and
     // finish a tile without the pair's hand-overs (two sources stacked along M, 14336 x
-    // 4096 each, 16-bit: K = 16 24.8 against 34.0 us, 256 31.9 / 40.9, 1024 85.7 / 72.1)
-    if (c.kernel != 1 && k_sources * K < 512)
+    // 4096 each, 16-bit: K = 16 24.8 against 34.0 us, 256 31.9 / 40.9, 1024 85.7 / 72.1;
+    // both stored K x M, 2020 x 10164: K = 320 23.7 / 23.7, 384 26.5 / 24.7)
+    if (c.kernel != 1 && k_sources * K <= 320)
         c = TileChoice{1, 256};
+    // Up to 8 rows stored K x M are one 16-byte piece of each of K lines that every CTA
+    // reads: fewer, wider tiles (64 / 128 / 256 columns: 3 x 6279 x 1534 23.7 / 12.7 / 15.2
+    // us, 1 x 5894 x 387 11.4 / 6.0 / 6.9, 5 x 13769 x 2288 37.9 / 29.6 / 22.9)
+    if (M <= 8 && (stored & 1))
+        c = TileChoice{1, ceil_div(N, 128) <= 64 ? 128 : 256};
     if (fk == 1 || ((fk == 3 || fk == 4) && K > 0))
         c = TileChoice{fk, fbn};
     set_tile_plan(p, c.kernel, c.bn, M, N, sm_count);

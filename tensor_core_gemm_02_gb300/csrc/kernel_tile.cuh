@@ -155,7 +155,10 @@ struct TileCfg {
     // copy; or (gated) four, one per quarter of TMEM lanes, that also store them
     // into TMEM themselves
     static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 4 : 1);
-    static constexpr int THREADS = 192 + 32 * (ISS - 1) + 32 * SCALE_WARPS;
+    // Epilogue groups of four warps; the second one's come last.
+    static constexpr int EPI_GROUPS = GATED && BN >= 128 && !LAP ? 2 : 1;
+    static constexpr int EPI2_WARP0 = 6 + (ISS - 1) + SCALE_WARPS;
+    static constexpr int THREADS = 32 * (EPI2_WARP0 + 4 * (EPI_GROUPS - 1));
     static_assert(STAGES % ISS == 0, "an issuer's stages are its own");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN % 32 == 0 && BN >= 32 && BN <= 256, "tile width");
@@ -361,7 +364,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), kIss);  // each issuer's last MMAs of the tile
-            mbar_init(acce_bar(b), PAIR ? 8 : 4);  // one arrival per epilogue warp (of both CTAs)
+            // one arrival per epilogue warp (of both CTAs)
+            mbar_init(acce_bar(b), (PAIR ? 8 : 4) * Cfg::EPI_GROUPS);
         }
         for (int q = 0; q < 4; ++q)
             for (int j = 0; j < 2; ++j)
@@ -815,7 +819,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
             }
         }
         __syncwarp();
-    } else if (kGated && MX != 0 && warp >= 6) {
+    } else if (kGated && MX != 0 && warp >= 6 && warp < 6 + Cfg::SCALE_WARPS) {
         // ------------------------------------------------------------ scale warps (gated)
         // As the one scale warp of the plain form below rearranges a stage's scales,
         // four share the 512-byte tiles out; each then stores all of them into its
@@ -1062,23 +1066,23 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         // Gated form: per 32 columns of D, G from the left half of the accumulator
         // and U from the right half (with two issuers, both partial sums of each),
         // kept copies of G and U if asked for, then D = act(G) * U.  Returns false
-        // when a wait gave up.  (Eight epilogue warps, each with half of the
-        // columns, measured no faster: 8192 x 14336 x 4096 FP4 481 against 471 us,
-        // 777 x 2743 x 1000 f16 19.0 against 19.4.)
+        // when a wait gave up.
         auto gated_epilogue = [&]() -> bool {
             constexpr int32_t kCols = TILE_N / 2;  // columns of D per tile
-            constexpr int32_t kChunks = kCols / 32;
+            constexpr int32_t kChunks = kCols / 32 / Cfg::EPI_GROUPS;  // per group of warps
+            const int32_t group =
+                Cfg::EPI_GROUPS > 1 && warp >= static_cast<uint32_t>(Cfg::EPI2_WARP0) ? 1 : 0;
             const int keep_kind = args.ab_bf16 != 0 ? kOutBF16 : kOutF16;
             const bool acc_none = args.num_k_blocks == 0;
             uint32_t slot = 0;
             for (int32_t t = cta_set; t < args.num_tiles; t += cta_sets) {
                 int32_t mb, nb;
                 tile_coords(t, args, mb, nb);
-                const int32_t n0 = nb * kCols;
+                const int32_t n0 = nb * kCols + 32 * kChunks * group;
                 const int32_t row0 = mb * Cfg::TILE_M + static_cast<int32_t>(role) * Cfg::BM +
                                      32 * static_cast<int32_t>(q);
                 const int32_t my_row = row0 + static_cast<int32_t>(lane);
-                const int32_t nchunks = min(kChunks, (args.N - n0 + 31) / 32);
+                const int32_t nchunks = max(0, min(kChunks, (args.N - n0 + 31) / 32));
                 // 32 columns from col0 of this warp's rows of one output matrix
                 // (by TMA up to column n_tma, the last whole 16 bytes of a row, as the
                 // descriptor has it; plain stores for the rest)
@@ -1100,14 +1104,16 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     }
                     if (col0 >= n_tma)
                         return;
-                    // this warp's two buffers in turn, or (LAP) its one: two 16-bit boxes in
-                    // turn, or one of float32
-                    const uint32_t buf = Cfg::LAP ? base + Cfg::OFF_EPI + q * Cfg::EPI_BUF +
-                                                        (kind == kOutF32 ? 0u : slot * (Cfg::EPI_BUF / 2))
-                                                  : buf0 + slot * Cfg::EPI_BUF;
+                    // this warp's shared memory: two buffers of 4 KB in turn, or only one (LAP,
+                    // and two groups), for two 16-bit boxes in turn or one of float32
+                    constexpr bool kOne = Cfg::LAP || Cfg::EPI_GROUPS > 1;
+                    const uint32_t image = base + Cfg::OFF_EPI + (4u * group + q) * Cfg::EPI_BUF;
+                    const bool one_box = kOne && out_kind == kOutF32;  // (the larger kind sets the turn)
+                    const uint32_t buf = kOne ? image + (one_box ? 0u : slot * (Cfg::EPI_BUF / 2))
+                                              : buf0 + slot * Cfg::EPI_BUF;
                     slot ^= 1u;
                     if (lane == 0) {  // the last store that used it has read it
-                        if (Cfg::LAP && kind == kOutF32)
+                        if (one_box)
                             bulk_wait_group_read<0>();
                         else
                             bulk_wait_group_read<1>();
@@ -1194,7 +1200,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 tc_fence_after_sync();
                 // (two issuers and one K block: the sum is the one's whose stage it was on)
                 const uint32_t acc0 =
-                    tmem_base + ((32u * q) << 16) +
+                    tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(32 * kChunks * group) +
                     (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
                               : static_cast<uint32_t>(ab * kIss * TILE_N)) +
                     (kIss > 1 && args.num_k_blocks == 1 && ((t - cta_set) / cta_sets) % kIss != 0 ? TILE_N : 0);
