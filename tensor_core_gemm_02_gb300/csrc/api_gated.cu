@@ -303,7 +303,9 @@ gemm_status run_gated(const GatedProblem &p)
     std::memset(&a, 0, sizeof(a));
     fill_gated(a, p, dev);
     const int keep = p.bf16 ? GEMM_OUT_BF16 : GEMM_OUT_F16;
-    if ((a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd)) ||
+    // (the FP4 form stores 64 bytes of a row at a time)
+    const uint32_t d_cols = p.fp4 && p.out == GEMM_OUT_F32 ? 16 : 32;
+    if ((a.d_tma && !encode_out(&maps.d, p.D, p.out, p.M, p.N, p.ldd, d_cols)) ||
         (a.keep_tma && p.G && !encode_out(&two.d2, p.G, keep, p.M, p.N, p.ldg)) ||
         (a.keep_tma && p.U && !encode_out(&two.d3, p.U, keep, p.M, p.N, p.ldu)))
         return GEMM_ERR_CUDA;
@@ -669,19 +671,21 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
     forced_tile(&fk, &fbn);
     // M <= 64: the skinny kernel, except for short sums, over one wave of tiles at that,
     // where its join of the parts costs more than the sum (skinny / tile: 8 x 934 x 384
-    // 7.4 / 5.4 us, 2 x 3674 x 1760 8.8 / 7.2, 2 x 12529 x 64 7.9 / 6.7; 32 x 8192 x 1024
-    // 5.8 / 6.1, 16 x 2048 x 2048 6.8 / 7.1, 8 x 14336 x 512 6.1 / 7.5)
+    // 7.4 / 5.4 us, 2 x 3674 x 1760 8.8 / 7.2, 52 x 3012 x 3488 11.1 / 9.3, 2 x 12529 x 64
+    // 7.9 / 6.7; 32 x 8192 x 1024 5.8 / 6.1, 16 x 2048 x 2048 6.8 / 7.1, 8 x 14336 x 512
+    // 6.1 / 7.5)
     const bool one_wave = ceil_div(N, 64) <= sm_count;
-    if (M <= 64 && K > 256 && fk != 11 && !(one_wave && K < 2048)) {
+    if (M <= 64 && K > 256 && fk != 11 && !(one_wave && K < (M > 16 ? 4096 : 2048))) {
         set_e2m1_skinny_plan(p, M, ceil_div(N, 64), K, sm_count);
         return p;
     }
-    // 256 columns halve what a tile reads of A, but leave one group of epilogue
-    // warps: worth it for long sums over several waves (128 / 256 columns: 2048 x 4096 x
-    // 4096 47 / 37 us, 1024 x 4096 x 2048 17.1 / 16.2; 4096 x 4096 x 1024 31 / 39, 4096 x
-    // 14336 x 512 79 / 117, and 3 waves of 128 columns, 200 x 14336 x 4096, 22.9 / 23.9)
-    const int64_t waves = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
-    const int bn = fk == 11 ? fbn : (K >= 2048 && waves >= 4 ? 256 : 128);
+    // 256 columns: half as much of A is read, and a wave of tiles takes about 1.6 times
+    // as long (128 / 256 columns: 2048 x 4096 x 4096 7 / 4 waves 47 / 36 us, 1024 x 14336 x
+    // 1024 12 / 6 27 / 22, 4096 x 14336 x 512 48 / 24 78 / 70, 200 x 14336 x 4096 3 / 2 22.9 /
+    // 22.5, 512 x 4096 x 1024 2 / 1 7.6 / 7.6, 300 x 1000 x 4096 1 / 1 9.8 / 12.4)
+    const int64_t w128 = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
+    const int64_t w256 = ceil_div(ceil_div(M, 128) * ceil_div(N, 128), sm_count);
+    const int bn = fk == 11 ? fbn : (3 * w256 <= 2 * w128 ? 256 : 128);
     p.kernel = 11;
     p.bm = 128;
     p.bn = bn;

@@ -123,17 +123,20 @@ struct TileCfg {
     static constexpr uint32_t OFF_B = STAGES * A_BYTES;
     static constexpr uint32_t OFF_SFS = STAGES * STAGE_BYTES;             // scales as loaded
     static constexpr uint32_t OFF_SFC = OFF_SFS + STAGES * SF_STAGE_BYTES;  // rearranged
-    // (gated: one rearranged image, its tiles being read out at once)
-    static constexpr int SFC_BUFS = GATED ? 1 : STAGES;
+    // (gated: two rearranged images in turn, their tiles being read out at once)
+    static constexpr int SFC_BUFS = GATED ? 2 : STAGES;
     static constexpr uint32_t OFF_EPI = OFF_SFC + SFC_BUFS * SF_CP_BYTES;
-    // 4 warps x 2 buffers; LAP: 4 KB a warp (one float32 box or two 16-bit ones),
-    // which makes room for a fourth stage
+    // 4 warps x 2 buffers; (gated, two groups) 8 warps, a buffer each; LAP: half a
+    // buffer each, which makes room for a fourth stage
     static constexpr uint32_t EPI_BYTES = (LAP ? 4 : 8) * EPI_BUF;
     static constexpr uint32_t OFF_BAR = OFF_EPI + EPI_BYTES;
-    static constexpr uint32_t NUM_BARS = 2 * STAGES + 4 + 8 + (MX ? 2 * STAGES : 0);
-    static constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;
-    static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
-    static constexpr uint32_t SMEM_ALLOC = SMEM_BYTES + 1024;  // slack to align the base
+    static constexpr uint32_t NUM_BARS = 2 * STAGES + 4 + 8 + (MX ? 2 * STAGES : 0) + (MX && GATED ? 4 : 0);
+    static constexpr uint32_t SMEM_BYTES = OFF_BAR + NUM_BARS * 8 + 16;
+    // Slack to align the base.  LAP: the barriers lie in it, in front of the base or
+    // behind the data, whichever has room.
+    static constexpr uint32_t BAR_BYTES = NUM_BARS * 8 + 16;
+    static constexpr uint32_t SMEM_ALLOC = (LAP ? OFF_BAR : SMEM_BYTES) + 1024;
+    static_assert(BAR_BYTES <= 512, "room for the barriers on one side of the base");
     // MMA issuers.  One thread issues a tcgen05.mma about every 117 cycles
     // whatever its N, while a 128 x BN x 16 MMA takes the tensor pipe about
     // BN / 2 cycles: at BN <= 128 a lone issuer, not the tensor pipe, sets
@@ -152,11 +155,15 @@ struct TileCfg {
     static constexpr uint32_t TMEM_COLS = MX ? 512u : ACC_COLS;
     // warp 6: the second MMA issuer, or (FP4) the scale warp
     // (FP4) scale warps: one that rearranges a stage's scales for the MMA thread to
-    // copy; or (gated) four, one per quarter of TMEM lanes, that also store them
-    // into TMEM themselves
-    static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 4 : 1);
-    // Epilogue groups of four warps; the second one's come last.
-    static constexpr int EPI_GROUPS = GATED && BN >= 128 && !LAP ? 2 : 1;
+    // copy; or (gated) two that rearrange them and four, one per quarter of TMEM
+    // lanes, that store them into TMEM.  (Four that did both, meeting at a named
+    // barrier or two per stage, took longer than a stage's MMAs: 8192 x 14336 x 4096
+    // 372 us against 348, and 327 without any scale work.)
+    static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 6 : 1);
+    // Epilogue groups of four warps, the second one's last: two for the gated form,
+    // whose activation and stores take as long as the MMAs of a short sum (one / two:
+    // 4096 x 14336 x 512 FP4, 256-wide 115 / 70 us, 128-wide 99 / 72; bf16 x 128 76 / 63).
+    static constexpr int EPI_GROUPS = GATED && BN >= 128 ? 2 : 1;
     static constexpr int EPI2_WARP0 = 6 + (ISS - 1) + SCALE_WARPS;
     static constexpr int THREADS = 32 * (EPI2_WARP0 + 4 * (EPI_GROUPS - 1));
     static_assert(STAGES % ISS == 0, "an issuer's stages are its own");
@@ -185,24 +192,6 @@ __device__ __forceinline__ uint32_t swz_off(uint32_t row, uint32_t chunk, uint32
     const uint32_t mask = row_bytes / 16u - 1u;  // 7 or 3
     return lin ^ (((lin >> 7) & mask) << 4);
 }
-
-// Barrier 1 among the gated form's four scale warps, agreeing on whether any
-// thread found `p`.
-__device__ __forceinline__ bool scale_bar_any(bool p)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(p ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void scale_bar_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
 // Epilogue modes, a template parameter so that each kernel carries only its own:
 // the fma.rn epilogue with optional C, rows scattered through idx, reduce-add
@@ -247,7 +236,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
     const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x / 32u, 0);
     const uint32_t lane = threadIdx.x % 32u;
 
-    const uint32_t bar0 = base + Cfg::OFF_BAR;
+    const uint32_t bar0 = Cfg::LAP && base - raw >= Cfg::BAR_BYTES ? raw : base + Cfg::OFF_BAR;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
@@ -257,8 +246,11 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
     // for tcgen05.cp (in the leader: by the scale warps of both CTAs of a pair)
     auto sf_full_bar = [&](int st) { return bar0 + 8u * (2 * STAGES + 12 + st); };
     auto sf_bar = [&](int st) { return bar0 + 8u * (3 * STAGES + 12 + st); };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + Cfg::OFF_MISC);
-    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + Cfg::OFF_MISC + 4);
+    // (gated FP4) rearranged image i is whole / has been read
+    auto img_full_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 12 + i); };
+    auto img_free_bar = [&](uint32_t i) { return bar0 + 8u * (4 * STAGES + 14 + i); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 8 * Cfg::NUM_BARS);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
 
     // cluster bookkeeping: pairs (ranks 2p, 2p+1; the even rank leads), MC
     // CTAs or pairs sharing A, or one CTA
@@ -373,7 +365,12 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         if (MX)
             for (int st = 0; st < STAGES; ++st) {
                 mbar_init(sf_full_bar(st), 1);
-                mbar_init(sf_bar(st), kGated ? Cfg::SCALE_WARPS : (PAIR ? 2 : 1));
+                mbar_init(sf_bar(st), kGated ? 4 : (PAIR ? 2 : 1));
+            }
+        if (MX && kGated)
+            for (uint32_t i = 0; i < 2u; ++i) {
+                mbar_init(img_full_bar(i), 2);
+                mbar_init(img_free_bar(i), 4);
             }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -821,80 +818,95 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
         __syncwarp();
     } else if (kGated && MX != 0 && warp >= 6 && warp < 6 + Cfg::SCALE_WARPS) {
         // ------------------------------------------------------------ scale warps (gated)
-        // As the one scale warp of the plain form below rearranges a stage's scales,
-        // four share the 512-byte tiles out; each then stores all of them into its
-        // quarter of the TMEM lanes (lane l takes the 16 bytes of rows l, l + 32, l +
-        // 64, l + 96 of a tile), where the MMA thread would have to copy them to.
-        // Those copies cost the tensor pipe about 110 of 600 ns a stage (8192 x 14336
-        // x 4096); stores from other warps run beside the MMAs.
+        // The last two rearrange a stage's scales as the one scale warp of the plain form
+        // below does, into two images in turn.  The other four store each image into
+        // their quarter of the TMEM lanes (lane l takes the 16 bytes of rows l, l + 32, l +
+        // 64, l + 96 of a tile), where the MMA thread would have to copy it to.  Those
+        // copies cost the tensor pipe about 110 of 600 ns a stage (8192 x 14336 x 4096);
+        // stores from other warps run beside the MMAs.
         if constexpr (kGated && MX != 0) {
+            const bool arranges = warp >= 10u;
             int s = 0;
             uint32_t ph = 0;
-            bool good = true;  // no wait of this warp has given up
-            [[maybe_unused]] uint32_t blocks = 0;  // (LAP) K blocks begun
-            // rows 4 lane .. 4 lane + 3 of tile ti: load their four blocks' bytes, transpose
-            // them and store row r's word at 16 (r % 32) + 4 (r / 32)
-            auto arrange = [&](const uint8_t *src, uint8_t *dst, int ti) {
-                const uint8_t *rows = src;
-                uint32_t pitch = Cfg::BM;
-                int c = ti;  // 128-element chunk of the tile
-                uint32_t r = 4u * lane;
-                if (ti >= Cfg::SF_CHUNKS) {
-                    // Bg's image, then Bu's, each of half the tile's rows
-                    c = (ti - Cfg::SF_CHUNKS) / Cfg::SF_B_ROWTILES;
-                    r += 128u * ((ti - Cfg::SF_CHUNKS) % Cfg::SF_B_ROWTILES);
-                    pitch = Cfg::TILE_N / 2;
-                    rows += Cfg::SF_KB * Cfg::BM + (r / pitch) * Cfg::SF_KB * pitch;
-                }
-                rows += 4u * c * pitch + r % pitch;
-                uint32_t w[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    w[b] = *reinterpret_cast<const uint32_t *>(rows + b * pitch);
-                const uint32_t t0 = __byte_perm(w[0], w[1], 0x5140);
-                const uint32_t t1 = __byte_perm(w[0], w[1], 0x7362);
-                const uint32_t t2 = __byte_perm(w[2], w[3], 0x5140);
-                const uint32_t t3 = __byte_perm(w[2], w[3], 0x7362);
-                const uint32_t o[4] = {__byte_perm(t0, t2, 0x5410), __byte_perm(t0, t2, 0x7632),
-                                       __byte_perm(t1, t3, 0x5410), __byte_perm(t1, t3, 0x7632)};
-                uint8_t *tile = dst + 512u * ti + 4u * (lane / 8u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint32_t *>(tile + 16u * ((4u * lane + i) % 32u)) = o[i];
-            };
+            uint32_t blocks = 0;  // K blocks begun
             bool alive = true;
             for (int32_t t = cta_set; t < args.num_tiles && alive; t += cta_sets) {
                 for (int32_t kb = 0; kb < args.num_k_blocks; ++kb) {
-                    good = good && warp_wait_bounded<true>(sf_full_bar(s), ph, abort_flag, args.status,
-                                                           args.timeout_ns, kWhereMmaFull);
-                    const uint8_t *src = gbase + Cfg::OFF_SFS + s * Cfg::SF_STAGE_BYTES;
-                    uint8_t *dst = gbase + Cfg::OFF_SFC;
-                    scale_bar_sync();  // every warp has read the stage before out of the image
-                    for (int ti = static_cast<int>(warp) - 6; good && ti < Cfg::SF_TILES; ti += Cfg::SCALE_WARPS)
-                        arrange(src, dst, ti);
-                    // the tiles are whole; and the four warps agree, so that all or none go on
-                    if (scale_bar_any(!good)) {
-                        alive = false;
-                        break;
-                    }
-                    uint32_t r[Cfg::SF_COLS];
+                    const uint32_t img = blocks & 1u, use = blocks >> 1;
+                    const uint32_t at_img = base + Cfg::OFF_SFC + img * Cfg::SF_CP_BYTES;
+                    if (arranges) {
+                        if (!warp_wait_bounded<true>(sf_full_bar(s), ph, abort_flag, args.status,
+                                                     args.timeout_ns, kWhereMmaFull) ||
+                            (use > 0 && !warp_wait_bounded<true>(img_free_bar(img), (use - 1u) & 1u, abort_flag,
+                                                                 args.status, args.timeout_ns, kWhereMmaFull))) {
+                            alive = false;
+                            break;
+                        }
+                        // rows 4 lane .. 4 lane + 3 of tile ti: load their four blocks' bytes,
+                        // transpose them, store row r's word at 16 (r % 32) + 4 (r / 32)
+                        constexpr int kMine = Cfg::SF_TILES / 2;
+                        uint32_t w[kMine][4];
 #pragma unroll
-                    for (int ti = 0; ti < Cfg::SF_TILES; ++ti)
-                        ld_shared_v4(smem_u32(dst) + 512u * ti + 16u * lane, r[4 * ti], r[4 * ti + 1],
-                                     r[4 * ti + 2], r[4 * ti + 3]);
-                    uint32_t buf = static_cast<uint32_t>(s);
-                    if constexpr (Cfg::LAP) {
-                        // two buffers: the MMAs of the block before the last are done with
-                        // this one (they have freed their stage)
-                        buf = blocks & 1u;
-                        const uint32_t i = blocks - 2u;
-                        if (blocks >= 2u)
-                            good = warp_wait_bounded<true>(empty_bar(static_cast<int>(i % STAGES)),
-                                                           (i / STAGES) & 1u, abort_flag, args.status,
-                                                           args.timeout_ns, kWhereProducerEmpty);
-                        ++blocks;
-                    }
-                    if (good) {
+                        for (int j = 0; j < kMine; ++j) {
+                            const int ti = static_cast<int>(warp - 10u) + 2 * j;
+                            uint32_t rows = base + Cfg::OFF_SFS + s * Cfg::SF_STAGE_BYTES;
+                            uint32_t pitch = Cfg::BM;
+                            uint32_t c = ti;  // 128-element chunk of the tile
+                            uint32_t r = 4u * lane;
+                            if (ti >= Cfg::SF_CHUNKS) {
+                                // Bg's image, then Bu's, each of half the tile's rows
+                                c = (ti - Cfg::SF_CHUNKS) / Cfg::SF_B_ROWTILES;
+                                r += 128u * ((ti - Cfg::SF_CHUNKS) % Cfg::SF_B_ROWTILES);
+                                pitch = Cfg::TILE_N / 2;
+                                rows += Cfg::SF_KB * Cfg::BM + (r / pitch) * Cfg::SF_KB * pitch;
+                            }
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                w[j][b] = ld_shared_u32(rows + (4u * c + b) * pitch + r % pitch);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kMine; ++j) {
+                            const uint32_t t0 = __byte_perm(w[j][0], w[j][1], 0x5140);
+                            const uint32_t t1 = __byte_perm(w[j][0], w[j][1], 0x7362);
+                            const uint32_t t2 = __byte_perm(w[j][2], w[j][3], 0x5140);
+                            const uint32_t t3 = __byte_perm(w[j][2], w[j][3], 0x7362);
+                            const uint32_t o[4] = {__byte_perm(t0, t2, 0x5410), __byte_perm(t0, t2, 0x7632),
+                                                   __byte_perm(t1, t3, 0x5410), __byte_perm(t1, t3, 0x7632)};
+                            const uint32_t tile = at_img + 512u * (warp - 10u + 2u * j) + 4u * (lane / 8u);
+#pragma unroll
+                            for (uint32_t i = 0; i < 4u; ++i)
+                                st_shared_u32(tile + 16u * ((4u * lane + i) % 32u), o[i]);
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(img_full_bar(img));
+                    } else {
+                        if (!warp_wait_bounded<true>(img_full_bar(img), use & 1u, abort_flag, args.status,
+                                                     args.timeout_ns, kWhereMmaFull)) {
+                            alive = false;
+                            break;
+                        }
+                        uint32_t r[Cfg::SF_COLS];
+#pragma unroll
+                        for (int ti = 0; ti < Cfg::SF_TILES; ++ti)
+                            ld_shared_v4(at_img + 512u * ti + 16u * lane, r[4 * ti], r[4 * ti + 1],
+                                         r[4 * ti + 2], r[4 * ti + 3]);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(img_free_bar(img));
+                        uint32_t buf = static_cast<uint32_t>(s);
+                        if constexpr (Cfg::LAP) {
+                            // two buffers: the MMAs of the block before the last are done with
+                            // this one (they have freed their stage)
+                            buf = img;
+                            const uint32_t i = blocks - 2u;
+                            if (use > 0 && !warp_wait_bounded<true>(empty_bar(static_cast<int>(i % STAGES)),
+                                                                    (i / STAGES) & 1u, abort_flag, args.status,
+                                                                    args.timeout_ns, kWhereProducerEmpty)) {
+                                alive = false;
+                                break;
+                            }
+                        }
                         tc_fence_after_sync();
                         const uint32_t at =
                             tmem_base + ((32u * (warp & 3u)) << 16) + Cfg::SF_COL0 + buf * Cfg::SF_COLS;
@@ -907,6 +919,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         if (lane == 0)
                             mbar_arrive(sf_bar(s));
                     }
+                    ++blocks;
                     if (++s == STAGES) {
                         s = 0;
                         ph ^= 1u;
@@ -1072,6 +1085,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
             constexpr int32_t kChunks = kCols / 32 / Cfg::EPI_GROUPS;  // per group of warps
             const int32_t group =
                 Cfg::EPI_GROUPS > 1 && warp >= static_cast<uint32_t>(Cfg::EPI2_WARP0) ? 1 : 0;
+            static_assert(!Cfg::LAP || (kChunks == 2 && Cfg::ACC2_COL == TILE_N - 48u),
+                          "48 shared columns, of one group");
             const int keep_kind = args.ab_bf16 != 0 ? kOutBF16 : kOutF16;
             const bool acc_none = args.num_k_blocks == 0;
             uint32_t slot = 0;
@@ -1104,9 +1119,9 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     }
                     if (col0 >= n_tma)
                         return;
-                    // this warp's shared memory: two buffers of 4 KB in turn, or only one (LAP,
-                    // and two groups), for two 16-bit boxes in turn or one of float32
-                    constexpr bool kOne = Cfg::LAP || Cfg::EPI_GROUPS > 1;
+                    // this warp's shared memory: two buffers of 4 KB in turn, or (two groups) only
+                    // one, for two 16-bit boxes in turn or one of float32
+                    constexpr bool kOne = Cfg::EPI_GROUPS > 1;
                     const uint32_t image = base + Cfg::OFF_EPI + (4u * group + q) * Cfg::EPI_BUF;
                     const bool one_box = kOne && out_kind == kOutF32;  // (the larger kind sets the turn)
                     const uint32_t buf = kOne ? image + (one_box ? 0u : slot * (Cfg::EPI_BUF / 2))
@@ -1204,33 +1219,138 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     (Cfg::LAP ? static_cast<uint32_t>(ab) * Cfg::ACC2_COL
                               : static_cast<uint32_t>(ab * kIss * TILE_N)) +
                     (kIss > 1 && args.num_k_blocks == 1 && ((t - cta_set) / cta_sets) % kIss != 0 ? TILE_N : 0);
-                if constexpr (Cfg::LAP) {
-                    // The accumulators share the first one's last columns (of U) and the
-                    // second one's first (of G): those 64 columns go into registers, and
-                    // the next tile's MMAs may start.
-                    uint32_t x[2][32];
-                    const uint32_t at = acc0 + (ab == 0 ? TILE_N - 64u : 0u);
-                    tc_ld_32x32b_x32(at, x[0]);
-                    tc_ld_32x32b_x32(at + 32u, x[1]);
-                    tc_wait_ld(x[0]);
-                    tc_wait_ld(x[1]);
-                    release_unit(0);
-                    const int32_t c_x = ab == 0 ? kChunks - 2 : 0;  // their chunks
+                if constexpr (MX != 0) {
+                    // Columns 16 p .. 16 p + 15 of this group's: activate, and store 64 bytes
+                    // of each row at a time (16 columns of float32, 32 of 16 bits).
+                    // (Pieces of 32 would take more than the 128 registers that 16 warps have.)
+                    const bool f32 = out_kind == kOutF32;
+                    auto piece = [&](int32_t p, const uint32_t (&rg)[16], const uint32_t (&ru)[16]) {
+                        const int32_t col0 = n0 + 16 * p;
+                        if (col0 >= args.N || row0 >= args.M)
+                            return;
+                        float v[16];
+                        with_act(args.act, [&](auto tag) {
 #pragma unroll
-                    for (int32_t j = 0; j < 2; ++j) {
-                        uint32_t y[32];
-                        tc_ld_32x32b_x32(acc0 + (ab == 0 ? 0u : kCols) + 32u * (c_x + j), y);
-                        tc_wait_ld(y);
-                        float g[32], u[32];
+                            for (int i = 0; i < 16; ++i)
+                                v[i] = act_value<decltype(tag)::value>(acc_none ? 0.f : __uint_as_float(rg[i])) *
+                                       (acc_none ? 0.f : __uint_as_float(ru[i]));
+                        });
+                        const int32_t n_tma = args.d_tma ? args.N & ~(f32 ? 3 : 7) : 0;
+                        if (col0 + 16 > n_tma && n_tma < args.N && my_row < args.M) {
+                            const int64_t o = static_cast<int64_t>(my_row) * args.ldd + col0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint32_t xi = j == 0 ? x[0][i] : x[1][i];
-                            g[i] = acc_none ? 0.f : __uint_as_float(ab == 0 ? y[i] : xi);
-                            u[i] = acc_none ? 0.f : __uint_as_float(ab == 0 ? xi : y[i]);
+                            for (int i = 0; i < 16; ++i) {
+                                if (col0 + i >= n_tma && col0 + i < args.N) {
+                                    if (f32)
+                                        static_cast<float *>(args.D)[o + i] = v[i];
+                                    else
+                                        static_cast<unsigned short *>(args.D)[o + i] =
+                                            out_kind == kOutBF16 ? f32_to_bf16_rn(v[i]) : f32_to_f16_rn(v[i]);
+                                }
+                            }
                         }
-                        finish(g, u, c_x + j);
+                        // the box that this piece begins, or (16 bits, p odd) ends
+                        const int32_t box = f32 || (p & 1) == 0 ? col0 : col0 - 16;
+                        if (box >= n_tma)
+                            return;
+                        const uint32_t buf = base + Cfg::OFF_EPI + (4u * group + q) * (Cfg::EPI_BUF / 2);
+                        if (box == col0) {
+                            if (lane == 0)
+                                bulk_wait_group_read<0>();  // the last store has read it
+                            __syncwarp();
+                        }
+                        if (f32) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                st_shared_v4(buf + swz_off(lane, i, 64u), __float_as_uint(v[4 * i]),
+                                             __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                             __float_as_uint(v[4 * i + 3]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = out_kind == kOutBF16
+                                               ? pack_bf16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1])
+                                               : pack_f16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+                                st_shared_v4(buf + swz_off(lane, 2 * (p & 1) + i, 64u), w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        if (f32 || (p & 1) == 1 || col0 + 16 >= args.N) {  // (the box is complete)
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d_hint(&tmD, buf, box, row0, epi_policy);
+                                bulk_commit_group();
+                            }
+                        }
+                    };
+                    // The accumulators share the first one's last 48 columns (of U, group 1)
+                    // and the second one's first (of G, group 0).  Those go into the group's
+                    // registers, and the next tile's MMAs may start.
+                    const uint32_t own = acc0 + (ab == 0 ? 0u : kCols);   // of the other matrix
+                    const uint32_t sh = acc0 + (ab == 0 ? kCols : 0u);    // of the shared columns'
+                    if (Cfg::LAP && group == 1 - ab) {
+                        // pieces 1 .. 3 or 0 .. 2: x[0] holds the last or the first
+                        uint32_t x[3][16], y[16];
+                        tc_ld_32x32b_x16(sh + (ab == 0 ? 48u : 0u), x[0]);
+                        tc_ld_32x32b_x16(sh + 16u, x[1]);
+                        tc_ld_32x32b_x16(sh + 32u, x[2]);
+                        tc_wait_ld(x[0]);
+                        tc_wait_ld(x[1]);
+                        tc_wait_ld(x[2]);
+                        release_unit(0);
+                        auto both = [&](int32_t p, const uint32_t (&s)[16]) {
+                            uint32_t g[16], u[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                g[i] = ab == 0 ? y[i] : s[i];
+                                u[i] = ab == 0 ? s[i] : y[i];
+                            }
+                            piece(p, g, u);
+                        };
+                        {
+                            uint32_t s[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                s[i] = x[0][i];
+                            tc_ld_32x32b_x16(own, y);
+                            tc_wait_ld(y);
+                            if (ab == 0) {
+                                tc_ld_32x32b_x16(sh, s);
+                                tc_wait_ld(s);
+                            }
+                            both(0, s);
+                        }
+#pragma unroll
+                        for (int32_t p = 1; p < 3; ++p) {
+                            tc_ld_32x32b_x16(own + 16u * p, y);
+                            tc_wait_ld(y);
+                            both(p, x[p]);
+                        }
+                        tc_ld_32x32b_x16(own + 48u, y);
+                        tc_wait_ld(y);
+                        if (ab == 1) {
+                            tc_ld_32x32b_x16(sh + 48u, x[0]);
+                            tc_wait_ld(x[0]);
+                        }
+                        both(3, x[0]);
+                    } else {
+                        if (Cfg::LAP)
+                            release_unit(0);
+#pragma unroll 1
+                        for (int32_t p = 0; p < 2 * kChunks; ++p) {
+                            uint32_t g[16], u[16];
+                            tc_ld_32x32b_x16(acc0 + 16u * p, g);
+                            tc_ld_32x32b_x16(acc0 + kCols + 16u * p, u);
+                            tc_wait_ld(g);
+                            tc_wait_ld(u);
+                            if (!Cfg::LAP && p == 2 * kChunks - 1)
+                                release_unit(ab);
+                            piece(p, g, u);
+                        }
                     }
-                    load_finish(acc0, 2 - c_x, 4 - c_x, false);
                 } else {
                     load_finish(acc0, 0, kChunks, true);
                 }
