@@ -193,6 +193,63 @@ __device__ __forceinline__ uint32_t swz_off(uint32_t row, uint32_t chunk, uint32
     return lin ^ (((lin >> 7) & mask) << 4);
 }
 
+// A lane's row of a 32 x 32 box of D, converted, into the box's swizzled image.
+__device__ __forceinline__ void put_image(uint32_t buf, uint32_t lane, const float (&v)[32], int kind)
+{
+    if (kind == kOutF32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            st_shared_v4(buf + swz_off(lane, i, 128u), __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = kind == kOutBF16 ? pack_bf16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1])
+                                        : pack_f16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+            st_shared_v4(buf + swz_off(lane, i, 64u), w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// The image of a box of 32 rows and `cols` (16 or 32) columns to a D that TMA cannot
+// store to (rows not 16 bytes apart), lanes along the columns.  (Each lane its own row
+// of single elements, as accumulator lanes hold them, is 32 sectors a store: 4096 x
+// 4001 x 1024 gated, bf16 171 against 52 us.  It is kept for boxes of fewer rows,
+// where the copy's latency shows: 20 x 1003 x 512 5.1 against 7.1.)
+__device__ __forceinline__ void copy_image(uint32_t buf, uint32_t lane, uint32_t cols, int kind, void *ptr,
+                                           int64_t ld, int32_t row0, int32_t col0, const GemmArgs &args)
+{
+    __syncwarp();
+    const uint32_t size = kind == kOutF32 ? 4u : 2u;
+    const uint32_t x = lane % cols * size;
+    const int32_t col = col0 + static_cast<int32_t>(lane % cols);
+    if (col < args.N) {
+        // row lane / cols and every step-th from there, four loads in flight
+        const int32_t step = 32 / static_cast<int32_t>(cols);
+        for (int32_t r0 = static_cast<int32_t>(lane / cols); r0 < 32; r0 += 4 * step) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at =
+                    buf + swz_off(static_cast<uint32_t>(r0 + i * step), x / 16u, cols * size) + x % 16u;
+                w[i] = kind == kOutF32 ? ld_shared_u32(at) : ld_shared_u32(at & ~3u) >> (8u * (at & 2u));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t o = static_cast<int64_t>(row0 + r0 + i * step) * ld + col;
+                if (kind == kOutF32)
+                    static_cast<float *>(ptr)[o] = __uint_as_float(w[i]);
+                else
+                    static_cast<unsigned short *>(ptr)[o] = static_cast<unsigned short>(w[i]);
+            }
+        }
+    }
+    __syncwarp();
+}
+
 // Epilogue modes, a template parameter so that each kernel carries only its own:
 // the fma.rn epilogue with optional C, rows scattered through idx, reduce-add
 // into D, accumulators seeded with C, and the gated form.
@@ -1098,12 +1155,13 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                      32 * static_cast<int32_t>(q);
                 const int32_t my_row = row0 + static_cast<int32_t>(lane);
                 const int32_t nchunks = max(0, min(kChunks, (args.N - n0 + 31) / 32));
+                const bool whole_rows = row0 + 32 <= args.M;
                 // 32 columns from col0 of this warp's rows of one output matrix
                 // (by TMA up to column n_tma, the last whole 16 bytes of a row, as the
                 // descriptor has it; plain stores for the rest)
                 auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, void *ptr,
                                 int64_t ld, int kind, int32_t col0) {
-                    const int32_t n_tma = tma ? args.N & ~(kind == kOutF32 ? 3 : 7) : 0;
+                    const int32_t n_tma = tma ? args.N & ~(kind == kOutF32 ? 3 : 7) : (whole_rows ? args.N : 0);
                     if (col0 + 32 > n_tma && n_tma < args.N && my_row < args.M) {
                         const int64_t o = static_cast<int64_t>(my_row) * ld + col0;
 #pragma unroll
@@ -1134,22 +1192,10 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             bulk_wait_group_read<1>();
                     }
                     __syncwarp();
-                    if (kind == kOutF32) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            st_shared_v4(buf + swz_off(lane, i, 128u), __float_as_uint(v[4 * i]),
-                                         __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                         __float_as_uint(v[4 * i + 3]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = kind == kOutBF16 ? pack_bf16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1])
-                                                        : pack_f16x2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
-                            st_shared_v4(buf + swz_off(lane, i, 64u), w[0], w[1], w[2], w[3]);
-                        }
+                    put_image(buf, lane, v, kind);
+                    if (!tma) {
+                        copy_image(buf, lane, 32u, kind, ptr, ld, row0, col0, args);
+                        return;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -1235,7 +1281,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                 v[i] = act_value<decltype(tag)::value>(acc_none ? 0.f : __uint_as_float(rg[i])) *
                                        (acc_none ? 0.f : __uint_as_float(ru[i]));
                         });
-                        const int32_t n_tma = args.d_tma ? args.N & ~(f32 ? 3 : 7) : 0;
+                        const int32_t n_tma =
+                            args.d_tma ? args.N & ~(f32 ? 3 : 7) : (whole_rows ? args.N : 0);
                         if (col0 + 16 > n_tma && n_tma < args.N && my_row < args.M) {
                             const int64_t o = static_cast<int64_t>(my_row) * args.ldd + col0;
 #pragma unroll
@@ -1278,6 +1325,10 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             }
                         }
                         if (f32 || (p & 1) == 1 || col0 + 16 >= args.N) {  // (the box is complete)
+                            if (!args.d_tma) {
+                                copy_image(buf, lane, f32 ? 16u : 32u, out_kind, args.D, args.ldd, row0, box, args);
+                                return;
+                            }
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) {
@@ -1658,7 +1709,13 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 }
                 if (MAJ != 0 && !d_direct && n_tma < args.N && col0 + 32 > n_tma)
                     store_direct(v, col0, n_tma);
-                if (d_direct) {
+                if (MAJ != 0 && !args.d_tma && row0 + 32 <= args.M) {
+                    __syncwarp();  // (all of C read)
+                    put_image(buf, lane, v, out_kind);
+                    copy_image(buf, lane, 32u, out_kind, out_d, out_ld, row0, col0, args);
+                    if (c_tma)
+                        fence_proxy_async_smem();  // (the buffer is a TMA load's next)
+                } else if (d_direct) {
                     store_direct(v, col0, col0);
                 } else {
                     if (!c_tma && bulk_lane)

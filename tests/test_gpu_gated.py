@@ -419,3 +419,37 @@ def test_gradients_unaligned_inputs_and_nan_rows():
     assert torch.isnan(dA[4]).all() and torch.equal(dA[rows.cuda()], want[0][rows.cuda()])
     for got, ok in ((dBg, want[1]), (dBu, want[2])):
         assert torch.isnan(got[6]).all() and torch.equal(got[cols.cuda()], ok[cols.cuda()])
+
+
+def odd_rows(M, N, out):
+    """An M x N output whose rows are not 16 bytes apart, in a buffer of NaNs, and that buffer."""
+    dtype = {OUT_F32: torch.float32, OUT_BF16: BF16, OUT_F16: F16}[out]
+    b = torch.full((M + 1, N + 9 - N % 8), float("nan"), dtype=dtype, device="cuda")
+    return b[:M, 1:1 + N], b
+
+
+@pytest.mark.parametrize("out", [OUT_F32, OUT_BF16, OUT_F16])
+@pytest.mark.parametrize("M,N,K", [(32, 33, 64), (191, 300, 128), (300, 129, 320)])
+def test_output_rows_not_16_bytes_apart(out, M, N, K):
+    """D (and kept G) written without TMA, on every tile form: the same bits as an aligned D,
+    nothing beside it."""
+    A, Bg, Bu = inputs(M, M, N, K, F16)
+    fp4 = [t for m in (A, Bg, Bu) for t in binding.gemm_quantize_e2m1(m)]
+    calls = [(FORMS[f], lambda D, **kw: binding.gemm_gated(A, Bg, Bu, D, act="gelu", out=out, **kw))
+             for f in ("single64", "single128", "single256", "pair")]
+    calls += [((11, bn), lambda D: binding.gemm_gated_e2m1(*fp4, D, act="gelu", out=out)) for bn in (128, 256)]
+    for form, call in calls:
+        binding.gemm_debug_force_tile(*form)
+        want = call(None) if N % 8 == 0 else call(torch.empty((M, N + 8 - N % 8), dtype=odd_rows(1, N, out)[0].dtype,
+                                                              device="cuda")[:, :N])
+        for keep in ((False, True) if form[0] != 11 else (False,)):
+            D, buf = odd_rows(M, N, out)
+            G, gbuf = odd_rows(M, N, OUT_F16)
+            call(D, G=G) if keep else call(D)
+            assert np.array_equal(bits(D), bits(want)), (form, keep)
+            assert int(torch.isnan(buf).sum()) == buf.numel() - M * N
+            if keep:
+                K_aligned = torch.empty((M, N + 8 - N % 8), dtype=F16, device="cuda")[:, :N]
+                call(D, G=K_aligned)
+                assert np.array_equal(bits(G), bits(K_aligned)), form
+                assert int(torch.isnan(gbuf).sum()) == gbuf.numel() - M * N

@@ -161,3 +161,23 @@ def test_linear_layer_gradients_match_the_stored_transposes():
     assert torch.equal(dX, binding.gemm_bf16(dY, W.T.contiguous()))
     assert torch.equal(dW, binding.gemm_bf16(dY.T.contiguous(), X.T.contiguous()))
     assert np.isfinite(dW.cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("out", [OUT_F32, OUT_BF16, OUT_F16])
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+def test_output_rows_not_16_bytes_apart(ta, tb, out):
+    """D written without TMA, with and without C, on every form: the same bits as an aligned D,
+    nothing beside it."""
+    M, N, K = 300, 205, 200
+    dtype = {OUT_F32: torch.float32, OUT_BF16: BF16, OUT_F16: F16}[out]
+    A, B, C = operands(3, M, N, K, ta, tb, BF16, False)
+    for name, form in FORMS.items():
+        for c in (None, C):
+            binding.gemm_debug_force_tile(*form)
+            aligned = torch.empty((M, 208), dtype=dtype, device="cuda")[:, :N]
+            binding.gemm_trans(A, B, c, aligned, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=out)
+            buf = torch.full((M + 1, 211), float("nan"), dtype=dtype, device="cuda")
+            D = buf[:M, 3:3 + N]
+            binding.gemm_trans(A, B, c, D, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=out)
+            assert torch.equal(D, aligned), (name, c is not None)
+            assert int(torch.isnan(buf).sum()) == buf.numel() - M * N
