@@ -1113,7 +1113,7 @@ gemm_status gemm_query_plan(int64_t M, int64_t N, int64_t K, int form, int has_c
         return GEMM_OK;
     }
     if (form >= 18) {
-        *plan = trans_plan(M, N, K, 1, 1, form - 17, has_c != 0, sm_count);
+        *plan = trans_plan(M, N, K, 1, 1, form - 17, sm_count);
         return GEMM_OK;
     }
     if (form == 5) {

@@ -350,50 +350,86 @@ struct TransProblem {
     int parts_use = kBufParts;  // buffer for the parts of a sum (its own for each product under way)
 };
 
-// How the sums of a product may be cut: `parts` of `k_part` K blocks each (1: not
-// cut), on single CTAs with 128 x bn tiles.
-struct Parts {
-    int parts;
-    int64_t k_part;
-    int bn;
+// One way to run a product: the tile kernel's form, and how its sums are cut
+// (parts of k_part K blocks; 1: not cut).  Time: waves of tiles (of every source and
+// part) x tile_ns + extra_ns.
+struct Form {
+    int kernel, bn, parts;
+    int64_t k_part, tiles, tile_ns, extra_ns;
 };
 
-// A product with few tiles and a long sum leaves most SMs idle: cut the sum, add
-// the parts' float32 results in a second kernel.  Time of a form, in ns: waves of
-// CTAs x K blocks x the time per K block (the operand bytes from L2 to an SM:
-// 190, 260 and 390 for 64, 128 and 256 columns, 280 for a pair's 256 x 256), and
-// for parts the second kernel, 2500 and its bytes.  At least 8 K blocks a part.
-Parts choose_parts(int64_t M, int64_t N, int64_t k_blocks, int m_sources, int sm_count)
+constexpr int kMaxForms = 8;
+
+int64_t form_ns(const Form &f, int64_t sms)
 {
-    Parts best{1, k_blocks, 0};
-    if (k_blocks < 16 || M > (int64_t(1) << 20) || N > (int64_t(1) << 20))
-        return best;
-    const int widths[3] = {64, 128, 256};
-    const int64_t step[3] = {190, 260, 390};
-    const int64_t pair_tiles = m_sources * ceil_div(M, 256) * ceil_div(N, 256);
-    int64_t best_ns = ceil_div(pair_tiles, sm_count / 2 > 0 ? sm_count / 2 : 1) * k_blocks * 280;
-    for (int i = 0; i < 3; ++i) {
-        const int64_t tiles = m_sources * ceil_div(M, 128) * ceil_div(N, widths[i]);
-        const int64_t whole = ceil_div(tiles, sm_count) * k_blocks * step[i];
-        if (whole < best_ns) {
-            best_ns = whole;
-            best = Parts{1, k_blocks, 0};
-        }
-        if (tiles > sm_count)
+    const int64_t sets = f.kernel == 1 ? sms : sms / 2;
+    return sets > 0 ? ceil_div(f.tiles, sets) * f.tile_ns + f.extra_ns : INT64_MAX / 4;
+}
+
+// The forms of a product, with their times in ns.  A tile takes its K blocks x the
+// time of one (the operand bytes from L2 to an SM: 190, 260 and 390 for 64, 128 and 256
+// columns, 280 and 532 for a pair's 256 x 256 and 256 x 512) and a fixed part, its
+// epilogue as far as the next tile's MMAs do not hide it.  A product with few tiles
+// and a long sum leaves most SMs idle: it may be cut, in at least 8 K blocks a part,
+// and the parts' float32 results added in a second kernel (2500 and its bytes).
+// Against measurements (64 / 128 / 256 columns / pairs / 512-wide pairs, us): two
+// sources stacked along M, 2816 x 1024 x 2048 47 / 34 / 30 / 26 / 25; 911 x 6867 x 606
+// 19.3 / 14.3 / 15.4 / 13.2 / 13.7; 460 x 6030 x 397 9.8 / 8.3 / 6.9 / 7.5 / 11.1.
+int trans_forms(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, int sm_count,
+                Form (&out)[kMaxForms])
+{
+    struct Step {
+        int kernel, bn;
+        int64_t block_ns, fixed_ns;
+    };
+    constexpr Step steps[5] = {{1, 64, 190, 300}, {1, 128, 260, 500}, {1, 256, 390, 600}, {3, 256, 280, 1500},
+                               {4, 512, 532, 3000}};
+    const int64_t kb = k_sources * ceil_div(K, 64);
+    int n = 0;
+    for (const Step &s : steps) {
+        // A short sum leaves the stores to set the time: single CTAs, which start and
+        // finish a tile without the pair's hand-overs (two sources stacked along M, 14336
+        // x 4096 each, 16-bit: K = 16 24.8 against 34.0 us, 256 31.9 / 40.9, 1024 85.7 /
+        // 72.1; both stored K x M, 2020 x 10164: K = 320 23.7 / 23.7, 384 26.5 / 24.7)
+        if (s.kernel != 1 && (k_sources * K <= 320 || (s.kernel == 4 && N <= 256)))
             continue;
-        for (int64_t parts = 2; parts <= 16 && parts * tiles <= sm_count && k_blocks / parts >= 8; ++parts) {
-            const int64_t k_part = ceil_div(k_blocks, parts);
-            if ((parts - 1) * k_part >= k_blocks)
+        // Up to 8 rows stored K x M are one 16-byte piece of each of K lines that every
+        // CTA reads: fewer, wider tiles (64 / 128 / 256 columns: 3 x 6279 x 1534 23.7 / 12.7
+        // / 15.2 us, 1 x 5894 x 387 11.4 / 6.0 / 6.9, 5 x 13769 x 2288 37.9 / 29.6 / 22.9)
+        if (M <= 8 && (stored & 1) && (s.kernel != 1 || s.bn != (ceil_div(N, 128) <= 64 ? 128 : 256)))
+            continue;
+        Form f{s.kernel, s.bn, 1, kb, 0, kb * s.block_ns + s.fixed_ns, 0};
+        f.tiles = m_sources * ceil_div(M, s.kernel == 1 ? 128 : 256) * ceil_div(N, s.bn);
+        out[n++] = f;
+        if (s.kernel != 1 || kb < 16 || f.tiles > sm_count || (M <= 8 && (stored & 1)))
+            continue;
+        Form cut = f;
+        int64_t cut_ns = INT64_MAX;
+        for (int64_t parts = 2; parts <= 16 && parts * f.tiles <= sm_count && kb / parts >= 8; ++parts) {
+            const int64_t k_part = ceil_div(kb, parts);
+            if ((parts - 1) * k_part >= kb)
                 continue;  // (the last part would be empty)
             // written and read once each, mostly in L2: 4 + 4 bytes at ~6 KB a ns
-            const int64_t ns = k_part * step[i] + 2500 + m_sources * M * N * 8 * parts / 6000;
-            if (ns < best_ns) {
-                best_ns = ns;
-                best = Parts{static_cast<int>(parts), k_part, widths[i]};
+            const Form c{1,           s.bn, static_cast<int>(parts), k_part, parts * f.tiles, k_part * s.block_ns + s.fixed_ns,
+                         2500 + m_sources * M * N * 8 * parts / 6000};
+            if (form_ns(c, sm_count) < cut_ns) {
+                cut_ns = form_ns(c, sm_count);
+                cut = c;
             }
         }
+        if (cut.parts > 1)
+            out[n++] = cut;
     }
-    return best;
+    return n;
+}
+
+void set_form_plan(gemm_plan &p, const Form &f, int64_t M, int64_t N, int64_t sms)
+{
+    set_tile_plan(p, f.kernel, f.bn, M, N, static_cast<int>(sms));
+    p.splits = f.parts;
+    p.tiles = f.tiles;
+    const int64_t cl = f.kernel == 1 ? 1 : 2, sets = sms / cl;
+    p.grid = static_cast<int32_t>(cl * (p.tiles < sets ? p.tiles : sets));
 }
 
 void fill_trans(GemmArgs &a, const TransProblem &p, const DeviceInfo *dev)
@@ -483,11 +519,10 @@ gemm_status add_parts(const TransProblem &p, const AddParts &add)
 
 // Launch the product (arguments already checked; M, N > 0).  In parts, *add says
 // what add_parts has to add.
-gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev, AddParts *add)
+gemm_status run_trans(const TransProblem &p, gemm_plan plan, const DeviceInfo *dev, AddParts *add)
 {
     const bool c_used = p.C != nullptr && p.beta != 0.0f;
     const int stored = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
-    gemm_plan plan = trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, p.B2 ? 2 : 1, stored, c_used, dev->sm_count);
     if (plan.kernel == 2)
         return run_trans_skinny(p, plan, dev);
     const int parts = plan.splits;
@@ -499,7 +534,7 @@ gemm_status run_trans(const TransProblem &p, const DeviceInfo *dev, AddParts *ad
         const int resident = tcg::tile_max_clusters(256, true, nsub, 1);
         if (resident <= 0)
             return GEMM_ERR_CUDA;
-        grid = static_cast<int>(2 * (plan.tiles < resident ? plan.tiles : resident));
+        grid = grid < 2 * resident ? grid : 2 * resident;
     }
     GemmMaps maps;
     TileMapsTwo two;
@@ -698,8 +733,7 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
 
 // m_sources, k_sources: sources stacked along M (their block rows count as one
 // problem's) and along K (one longer sum); stored: bit 0 A K x M, bit 1 B K x N.
-gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, bool c_used,
-                     int sm_count)
+gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, int sm_count)
 {
     gemm_plan p;
     std::memset(&p, 0, sizeof(p));
@@ -714,37 +748,64 @@ gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sourc
                         sm_count, false);
         return p;
     }
-    const bool forced = fk == 1 || fk == 3 || fk == 4;
-    const Parts cut = forced ? Parts{1, 0, 0}
-                             : choose_parts(M, N, k_sources * ceil_div(K, 64), m_sources, sm_count);
-    if (cut.parts > 1) {
-        set_tile_plan(p, 1, cut.bn, M, N, sm_count);
-        p.splits = cut.parts;
-        p.tiles *= static_cast<int64_t>(m_sources) * cut.parts;
-        p.grid = static_cast<int32_t>(p.tiles < sm_count ? p.tiles : sm_count);
-        return p;
+    Form forms[kMaxForms];
+    const int n = trans_forms(M, N, K, m_sources, k_sources, stored, sm_count, forms);
+    Form best = forms[0];
+    for (int i = 1; i < n; ++i)
+        if (form_ns(forms[i], sm_count) <= form_ns(best, sm_count))
+            best = forms[i];
+    if (fk == 1 || ((fk == 3 || fk == 4) && K > 0)) {
+        best = Form{fk, fbn, 1, 0, 0, 0, 0};
+        best.tiles = m_sources * ceil_div(M, fk == 1 ? 128 : 256) * ceil_div(N, fbn);
     }
-    TileChoice c = choose_tile(m_sources * M, N, k_sources * K, false, c_used, false, sm_count);
-    // A short sum leaves the stores to set the time: single CTAs, which start and
-    // finish a tile without the pair's hand-overs (two sources stacked along M, 14336 x
-    // 4096 each, 16-bit: K = 16 24.8 against 34.0 us, 256 31.9 / 40.9, 1024 85.7 / 72.1;
-    // both stored K x M, 2020 x 10164: K = 320 23.7 / 23.7, 384 26.5 / 24.7)
-    if (c.kernel != 1 && k_sources * K <= 320)
-        c = TileChoice{1, 256};
-    // Up to 8 rows stored K x M are one 16-byte piece of each of K lines that every CTA
-    // reads: fewer, wider tiles (64 / 128 / 256 columns: 3 x 6279 x 1534 23.7 / 12.7 / 15.2
-    // us, 1 x 5894 x 387 11.4 / 6.0 / 6.9, 5 x 13769 x 2288 37.9 / 29.6 / 22.9)
-    if (M <= 8 && (stored & 1))
-        c = TileChoice{1, ceil_div(N, 128) <= 64 ? 128 : 256};
-    if (fk == 1 || ((fk == 3 || fk == 4) && K > 0))
-        c = TileChoice{fk, fbn};
-    set_tile_plan(p, c.kernel, c.bn, M, N, sm_count);
-    if (m_sources > 1) {
-        p.tiles *= m_sources;
-        const int64_t cl = c.kernel == 1 ? 1 : 2, sets = sm_count / cl;
-        p.grid = static_cast<int32_t>(cl * (p.tiles < sets ? p.tiles : sets));
-    }
+    set_form_plan(p, best, M, N, sm_count);
     return p;
+}
+
+namespace {
+
+// The plans of a product and of one that starts on the SMs it leaves (both tile
+// kernels with static schedules): either the second also takes the first one's SMs, and
+// its last CTAs start once those are done, or it keeps to the rest.  (All gradients,
+// bf16, the second product spread over every SM by its own best form / planned together:
+// 1000 x 1367 x 1000 30.9 / 26.0 us, 2048 x 2816 x 1024 71.6 / 41.7, 3000 x 700 x 700
+// 30.9 / 25.3, 8192 x 5632 x 2048 512 / 525.)
+void plan_side_by_side(const TransProblem &a, const TransProblem &b, int sm_count, gemm_plan *plan_a,
+                       gemm_plan *plan_b)
+{
+    Form fa[kMaxForms], fb[kMaxForms];
+    const int na = trans_forms(a.M, a.N, a.K, 1, 2, 2, sm_count, fa);
+    const int nb = trans_forms(b.M, b.N, b.K, 2, 1, 3, sm_count, fb);
+    int64_t best = INT64_MAX;
+    int best_a = 0, best_b = 0;
+    int64_t best_sms = sm_count;
+    for (int i = 0; i < na; ++i) {
+        const int64_t ns = form_ns(fa[i], sm_count), cl = fa[i].kernel == 1 ? 1 : 2;
+        const int64_t used = cl * fa[i].tiles < sm_count ? cl * fa[i].tiles : sm_count;
+        for (int j = 0; j < nb; ++j) {
+            const int64_t after = ns + form_ns(fb[j], sm_count);
+            const int64_t beside = form_ns(fb[j], sm_count - used);
+            const int64_t both = beside > ns ? beside : ns;
+            if (both < best || after < best) {
+                best = both <= after ? both : after;
+                best_a = i;
+                best_b = j;
+                best_sms = both <= after ? sm_count - used : sm_count;
+            }
+        }
+    }
+    std::memset(plan_a, 0, sizeof(*plan_a));
+    std::memset(plan_b, 0, sizeof(*plan_b));
+    set_form_plan(*plan_a, fa[best_a], a.M, a.N, sm_count);
+    set_form_plan(*plan_b, fb[best_b], b.M, b.N, best_sms);
+}
+
+}  // namespace
+
+gemm_plan plan_of_trans(const TransProblem &p, const DeviceInfo *dev)
+{
+    const int stored = (p.ta ? 1 : 0) | (p.tb ? 2 : 0);
+    return trans_plan(p.M, p.N, p.K, p.D2 ? 2 : 1, p.B2 ? 2 : 1, stored, dev->sm_count);
 }
 
 }  // namespace host
@@ -852,7 +913,7 @@ gemm_status gemm_trans(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, int t
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
     AddParts add;
-    if ((st = run_trans(p, dev, &add)) != GEMM_OK)
+    if ((st = run_trans(p, plan_of_trans(p, dev), dev, &add)) != GEMM_OK)
         return st;
     return add_parts(p, add);
 }
@@ -922,8 +983,6 @@ gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf
         pa.out = out;
         pa.alpha = 1.0f;
         pa.stream = cs;
-        if ((st = run_trans(pa, dev, &add_a)) != GEMM_OK)
-            return st;
     }
     if (want_b) {
         // [dBg; dBu] = [dG dU]^T A: both gradients' tiles in one launch, which fills the
@@ -950,9 +1009,19 @@ gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf
         pb.out = out;
         pb.alpha = 1.0f;
         pb.stream = cs;
-        if ((st = run_trans(pb, dev, &add_b)) != GEMM_OK)
-            return st;
     }
+    gemm_plan plan_a{}, plan_b{};
+    if (want_a)
+        plan_a = plan_of_trans(pa, dev);
+    if (want_b)
+        plan_b = plan_of_trans(pb, dev);
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    if (want_a && want_b && plan_a.kernel != 2 && M > 0 && N > 0 && fk == 0)
+        plan_side_by_side(pa, pb, dev->sm_count, &plan_a, &plan_b);
+    if ((want_a && (st = run_trans(pa, plan_a, dev, &add_a)) != GEMM_OK) ||
+        (want_b && (st = run_trans(pb, plan_b, dev, &add_b)) != GEMM_OK))
+        return st;
     // (sums in parts are added last, so that the products run side by side)
     if ((st = add_parts(pa, add_a)) != GEMM_OK || (st = add_parts(pb, add_b)) != GEMM_OK)
         return st;

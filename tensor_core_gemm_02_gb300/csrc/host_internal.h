@@ -139,8 +139,7 @@ void set_e2m1_skinny_plan(gemm_plan &p, int64_t M, int64_t tiles, int64_t K, int
 // form applied.
 gemm_plan gated_plan(int64_t M, int64_t N, int64_t K, bool keep, int sm_count);
 gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count);
-gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, bool c_used,
-                     int sm_count);
+gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, int stored, int sm_count);
 
 // Plan of gemm_e2m1 (kernel 11: packed codes, kind::mxf4; 12: the 16U4 image,
 // kind::mxf8f6f4), with a forced form applied.
