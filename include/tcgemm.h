@@ -32,15 +32,17 @@
  * memory beyond the asynchronous execution of the call.  It holds, per
  * device, a small status word in its own device globals and a host-side cache
  * of TMA descriptors; per device and stream, the skinny (M <= 64) path keeps
- * a workspace for split tiles, and the FP4 path buffers for converted weights
- * or re-pitched scales, each allocated once and grown on demand (so calls on
- * different streams never share them).
+ * a workspace for split tiles, the FP4 paths buffers for converted weights
+ * or re-pitched scales, and gemm_trans and gemm_gated_backward one or two for
+ * the float32 parts of long sums over few tiles (splits > 1), each allocated
+ * once and grown on demand (so calls on different streams never share them).
  *
  * Execution: calls are asynchronous on `stream` (a cudaStream_t; NULL means
  * the legacy default stream) on the current device.  A call may launch more
  * than one kernel on that stream (a large gathered call runs whole waves of
  * clustered CTAs and, beside them, single CTAs on the SMs no cluster fits;
- * FP4 weights with M > 128 are first converted to bf16); work issued later
+ * FP4 weights with M > 128 are first converted to bf16; a sum in parts is
+ * added by a second kernel, in a fixed order); work issued later
  * on the stream still starts only after all of them, and every form can be
  * captured into a CUDA graph.
  *
@@ -436,7 +438,7 @@ gemm_status gemm_gated_e2m1(int64_t M, int64_t N, int64_t K,
  *  dBg, dBu       N x K of type `out`, both or neither NULL (not wanted).
  *  M == 0: dBg = dBu = 0.  N == 0: dA = 0.  K == 0: only dG and dU.
  *  Outputs must not overlap inputs or one another otherwise (GEMM_ERR_ALIAS).
- *  relu'(0) is 0.  Other errors and execution as gemm_f16 (up to three kernels).
+ *  relu'(0) is 0.  Other errors and execution as gemm_f16 (up to six kernels).
  */
 gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf16,
                                 const void *dD, int64_t lddd,
@@ -550,7 +552,8 @@ const char *gemm_status_string(int status);
  *           operands (M <= 64, K > 0; block-scaled MMA kind::mxf4)
  *  bm, bn   output tile; for the skinny kernel bm is the padded M and bn 128
  *  stages   shared-memory ring depth
- *  tiles    output tiles; splits = K slices per tile (skinny kernel)
+ *  tiles    output tiles (gemm_trans: of every part of the sum); splits = K
+ *           slices per tile (skinny kernel), parts of each sum (gemm_trans)
  *  grid     CTAs launched for `sm_count` SMs (pairs: at most sm_count / 2
  *           pairs; on a device, at most the pairs that can be resident)
  */

@@ -410,8 +410,12 @@ int trans_forms(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, i
             if ((parts - 1) * k_part >= kb)
                 continue;  // (the last part would be empty)
             // written and read once each, mostly in L2: 4 + 4 bytes at ~6 KB a ns
-            const Form c{1,           s.bn, static_cast<int>(parts), k_part, parts * f.tiles, k_part * s.block_ns + s.fixed_ns,
-                         2500 + m_sources * M * N * 8 * parts / 6000};
+            Form c = f;
+            c.parts = static_cast<int>(parts);
+            c.k_part = k_part;
+            c.tiles = parts * f.tiles;
+            c.tile_ns = k_part * s.block_ns + s.fixed_ns;
+            c.extra_ns = 2500 + m_sources * M * N * 8 * parts / 6000;
             if (form_ns(c, sm_count) < cut_ns) {
                 cut_ns = form_ns(c, sm_count);
                 cut = c;

@@ -16,6 +16,8 @@
 // maximum).  The scales are stored one row per 32-element block, so a thread
 // block covers 32 rows: their scale bytes meet in shared memory and leave as
 // 32-byte runs, whole sectors.  All loads of a warp's rows go out first.
+// Measured: 8192 x 14336 bf16 with the values 86 us (6.2 TB/s), without them 57 (5.2
+// TB/s); float32 145 us (6.9 TB/s) and 82; 16 x 4096 2 us.  (One element a lane: 129.)
 #include <cuda_runtime.h>
 
 #include "common.cuh"
