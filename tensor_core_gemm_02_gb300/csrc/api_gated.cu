@@ -314,8 +314,9 @@ gemm_status run_gated(const GatedProblem &p)
     a.num_k_blocks = static_cast<int32_t>(ceil_div(p.K, kstage));
     a.num_tiles = static_cast<int32_t>(plan.tiles);
     a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
-    const cudaError_t e = p.fp4 ? tcg::launch_tile_gated_mx(bn, maps, two, a, grid, p.stream)
-                                : tcg::launch_tile_gated(bn, pair, maps, two, a, grid, p.stream);
+    const bool rows = !a.d_tma || !a.keep_tma;
+    const cudaError_t e = p.fp4 ? tcg::launch_tile_gated_mx(bn, rows, maps, two, a, grid, p.stream)
+                                : tcg::launch_tile_gated(bn, pair, rows, maps, two, a, grid, p.stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

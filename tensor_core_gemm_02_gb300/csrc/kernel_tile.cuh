@@ -268,7 +268,20 @@ __device__ __forceinline__ void copy_image(uint32_t buf, uint32_t lane, uint32_t
 // for short ones (4096 x 14336 x 512: bf16 85 us, FP4 70).  FP4 with parts left out: no
 // scale work 327 of then 372 us, no activation or stores 356, neither 292, nor two
 // thirds of the loads 259.
-enum : int { kModePlain = 0, kModeScatter = 1, kModeReduce = 2, kModeSeed = 3, kModeGated = 4 };
+//
+// kModeGatedRows: the gated form for outputs (D, or kept G or U) whose rows are not
+// whole 16 bytes apart.  A kernel of its own: its stores beside the others cost every
+// call time (4096 x 14336 x 512 FP4 74 -> 89 us).
+enum : int {
+    kModePlain = 0,
+    kModeScatter = 1,
+    kModeReduce = 2,
+    kModeSeed = 3,
+    kModeGated = 4,
+    kModeGatedRows = 5
+};
+template <int MODE>
+constexpr bool kIsGated = MODE == kModeGated || MODE == kModeGatedRows;
 
 // Storage of the 16-bit operands: A stored K x M, B stored K x N (bits); the
 // boxes are then 64 columns x 64 K rows and the MMA reads them as MN-major, at the
@@ -281,7 +294,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                                const CUtensorMap &tmSFA, const CUtensorMap &tmSFB,
                                                const TileMapsTwo *two, const GemmArgs &args)
 {
-    constexpr bool kGated = MODE == kModeGated;
+    constexpr bool kGated = kIsGated<MODE>;
+    constexpr bool kRows = MODE == kModeGatedRows;
     using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, MC, MX, kGated>;
     constexpr bool kTwo = kGated || MAJ != 0;  // loads go through load_stage_two
     static_assert(!kTwo || MC == 1, "two-source forms: no A multicast");
@@ -1169,7 +1183,8 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                 // descriptor has it; plain stores for the rest)
                 auto emit = [&](const float(&v)[32], const CUtensorMap *map, bool tma, void *ptr,
                                 int64_t ld, int kind, int32_t col0) {
-                    const int32_t n_tma = tma ? args.N & ~(kind == kOutF32 ? 3 : 7) : (whole_rows ? args.N : 0);
+                    const int32_t n_tma =
+                        !kRows || tma ? args.N & ~(kind == kOutF32 ? 3 : 7) : (whole_rows ? args.N : 0);
                     if (col0 + 32 > n_tma && n_tma < args.N && my_row < args.M) {
                         const int64_t o = static_cast<int64_t>(my_row) * ld + col0;
 #pragma unroll
@@ -1201,7 +1216,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     }
                     __syncwarp();
                     put_image(buf, lane, v, kind);
-                    if (!tma) {
+                    if (kRows && !tma) {
                         copy_image(buf, lane, 32u, kind, ptr, ld, row0, col0, args);
                         return;
                     }
@@ -1290,7 +1305,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                                        (acc_none ? 0.f : __uint_as_float(ru[i]));
                         });
                         const int32_t n_tma =
-                            args.d_tma ? args.N & ~(f32 ? 3 : 7) : (whole_rows ? args.N : 0);
+                            !kRows || args.d_tma ? args.N & ~(f32 ? 3 : 7) : (whole_rows ? args.N : 0);
                         if (col0 + 16 > n_tma && n_tma < args.N && my_row < args.M) {
                             const int64_t o = static_cast<int64_t>(my_row) * args.ldd + col0;
 #pragma unroll
@@ -1333,7 +1348,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             }
                         }
                         if (f32 || (p & 1) == 1 || col0 + 16 >= args.N) {  // (the box is complete)
-                            if (!args.d_tma) {
+                            if (kRows && !args.d_tma) {
                                 copy_image(buf, lane, f32 ? 16u : 32u, out_kind, args.D, args.ldd, row0, box, args);
                                 return;
                             }
@@ -1846,7 +1861,7 @@ __global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, MC, MX>::THREA
 // The gated form, and operands stored K x M / K x N (MAJ), with the second
 // source's descriptors.
 template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
-__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, MODE == kModeGated>::THREADS, 1)
+__global__ void __launch_bounds__(TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, kIsGated<MODE>>::THREADS, 1)
     tile_gemm2_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmC,

@@ -82,11 +82,14 @@ cudaError_t launch_tile_mx(int mx, int bn, bool pair, const GemmMaps &maps, cons
 // tiles (bn 64, 128, 256), or CTA pairs with 256 x 256 ones; D tiles are bn / 2
 // wide.  maps.b / two.b2: Bg / Bu in boxes of bn / 2 rows; maps.d, two.d2,
 // two.d3: D, G, U.  The mx form takes packed FP4 codes (maps.sfa, maps.sfb,
-// two.sfb2: scales of A, Bg and Bu; single CTAs, bn 128 or 256).
-cudaError_t launch_tile_gated(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
+// two.sfb2: scales of A, Bg and Bu; single CTAs, bn 128 or 256).  rows: D, or
+// a kept G or U, has no descriptor (rows not whole 16 bytes apart).
+cudaError_t launch_tile_gated(int bn, bool pair, bool rows, const GemmMaps &maps, const TileMapsTwo &two,
                               const GemmArgs &args, int grid, cudaStream_t stream);
 int tile_gated_mx_stages(int bn);
-cudaError_t launch_tile_gated_mx(int bn, const GemmMaps &maps, const TileMapsTwo &two,
+cudaError_t launch_tile_gated_rows(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
+                                   const GemmArgs &args, int grid, cudaStream_t stream);
+cudaError_t launch_tile_gated_mx(int bn, bool rows, const GemmMaps &maps, const TileMapsTwo &two,
                                  const GemmArgs &args, int grid, cudaStream_t stream);
 
 // Operands stored K x M (maj bit 0) or K x N (bit 1), boxes of 64 columns x 64 K

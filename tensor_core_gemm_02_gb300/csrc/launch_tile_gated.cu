@@ -1,21 +1,14 @@
 // launch_tile_gated.cu -- the tile kernel's gated-form instantiations for 16-bit
-// operands (ring depths as the plain forms of the same tiles).
+// operands.
 #include "launch_tile_impl.cuh"
 
 namespace tcg {
 
-cudaError_t launch_tile_gated(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
+cudaError_t launch_tile_gated(int bn, bool pair, bool rows, const GemmMaps &maps, const TileMapsTwo &two,
                               const GemmArgs &args, int grid, cudaStream_t stream)
 {
-    if (pair)
-        return bn == 256 ? tile_launch2_impl<256, 6, true, 1, kModeGated, 0, 0>(maps, two, args, grid, stream)
-                         : cudaErrorInvalidValue;
-    switch (bn) {
-    case 256: return tile_launch2_impl<256, 4, false, 1, kModeGated, 0, 0>(maps, two, args, grid, stream);
-    case 128: return tile_launch2_impl<128, 6, false, 1, kModeGated, 0, 0>(maps, two, args, grid, stream);
-    case 64: return tile_launch2_impl<64, 8, false, 1, kModeGated, 0, 0>(maps, two, args, grid, stream);
-    default: return cudaErrorInvalidValue;
-    }
+    return rows ? launch_tile_gated_rows(bn, pair, maps, two, args, grid, stream)
+                : launch_tile_gated_impl<kModeGated>(bn, pair, maps, two, args, grid, stream);
 }
 
 }  // namespace tcg

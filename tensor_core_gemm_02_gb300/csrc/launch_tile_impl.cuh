@@ -61,7 +61,7 @@ template <int BN, int STAGES, bool PAIR, int NSUB, int MODE, int MX, int MAJ>
 cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, const GemmArgs &args,
                               int grid, cudaStream_t stream)
 {
-    constexpr bool kGated = MODE == kModeGated;
+    constexpr bool kGated = kIsGated<MODE>;
     using Cfg = TileCfg<BN, STAGES, PAIR, NSUB, 1, MX, kGated>;
     auto kfn = tile_gemm2_kernel<BN, STAGES, PAIR, NSUB, MODE, MX, MAJ>;
     static std::atomic<uint64_t> done{0};
@@ -72,6 +72,34 @@ cudaError_t tile_launch2_impl(const GemmMaps &maps, const TileMapsTwo &two, cons
     cudaLaunchAttribute attr[2];
     tile_fill_config<BN, STAGES, PAIR, NSUB, 1, MX, kGated>(cfg, attr, grid, stream);
     return cudaLaunchKernelEx(&cfg, kfn, maps.a, maps.b, maps.c, maps.d, maps.sfa, maps.sfb, two, args);
+}
+
+// The gated form in mode MODE: 16-bit operands (ring depths as the plain forms of the
+// same tiles), and packed FP4 ones (single CTAs; as deep as shared memory allows).
+template <int MODE>
+cudaError_t launch_tile_gated_impl(int bn, bool pair, const GemmMaps &maps, const TileMapsTwo &two,
+                                   const GemmArgs &args, int grid, cudaStream_t stream)
+{
+    if (pair)
+        return bn == 256 ? tile_launch2_impl<256, 6, true, 1, MODE, 0, 0>(maps, two, args, grid, stream)
+                         : cudaErrorInvalidValue;
+    switch (bn) {
+    case 256: return tile_launch2_impl<256, 4, false, 1, MODE, 0, 0>(maps, two, args, grid, stream);
+    case 128: return tile_launch2_impl<128, 6, false, 1, MODE, 0, 0>(maps, two, args, grid, stream);
+    case 64: return tile_launch2_impl<64, 8, false, 1, MODE, 0, 0>(maps, two, args, grid, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int MODE>
+cudaError_t launch_tile_gated_mx_impl(int bn, const GemmMaps &maps, const TileMapsTwo &two,
+                                      const GemmArgs &args, int grid, cudaStream_t stream)
+{
+    switch (bn) {
+    case 256: return tile_launch2_impl<256, 4, false, 1, MODE, 1, 0>(maps, two, args, grid, stream);
+    case 128: return tile_launch2_impl<128, 5, false, 1, MODE, 1, 0>(maps, two, args, grid, stream);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 template <int MAJ>
