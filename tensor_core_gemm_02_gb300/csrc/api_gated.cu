@@ -19,6 +19,15 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int kGroupM = 16;  // block rows per tile-order group, as the plain forms
+// FP4: rows of A are a quarter as long, and each group reads all of B's: groups of up to
+// 64 block rows that hold 16 MB of A (8192 x 14336 x 4096, 8 / 16 / 32 / 64 block rows with
+// the quantiser 379 / 365 / 356 / 351 us; 8192 x 4096 x 14336, 16 / 64 alone 341 / 348;
+// bf16 8192 x 14336 x 4096 1018 / 1008 / 1090 / 1085)
+int32_t fp4_group_m(int64_t K)
+{
+    const int64_t rows = (int64_t(1) << 24) / (64 * (K > 0 ? K : 1));  // 128 rows of K / 2 bytes
+    return static_cast<int32_t>(rows < kGroupM ? kGroupM : (rows > 64 ? 64 : rows));
+}
 
 struct Span {
     const void *p;
@@ -313,7 +322,8 @@ gemm_status run_gated(const GatedProblem &p)
     a.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, bn / 2));
     a.num_k_blocks = static_cast<int32_t>(ceil_div(p.K, kstage));
     a.num_tiles = static_cast<int32_t>(plan.tiles);
-    a.group_m = a.num_m_blocks < kGroupM ? a.num_m_blocks : kGroupM;
+    const int32_t group_m = p.fp4 ? fp4_group_m(p.K) : kGroupM;
+    a.group_m = a.num_m_blocks < group_m ? a.num_m_blocks : group_m;
     const bool rows = !a.d_tma || !a.keep_tma;
     const cudaError_t e = p.fp4 ? tcg::launch_tile_gated_mx(bn, rows, maps, two, a, grid, p.stream)
                                 : tcg::launch_tile_gated(bn, pair, rows, maps, two, a, grid, p.stream);

@@ -159,7 +159,7 @@ struct TileCfg {
     // copy; or (gated) two that rearrange them and four, one per quarter of TMEM
     // lanes, that store them into TMEM.  (Four that did both, meeting at a named
     // barrier or two per stage, took longer than a stage's MMAs: 8192 x 14336 x 4096
-    // 372 us against 348, and 327 without any scale work.)
+    // 372 us against 348.)
     static constexpr int SCALE_WARPS = MX == 0 ? 0 : (GATED ? 6 : 1);
     // Epilogue groups of four warps, the second one's last: two for the gated form,
     // whose activation and stores take as long as the MMAs of a short sum (one / two:
@@ -264,10 +264,10 @@ __device__ __forceinline__ void copy_image(uint32_t buf, uint32_t lane, uint32_t
 // lane.  The output tile is BN / 2 columns wide.
 //
 // Bound by the tensor cores for long sums (8192 x 14336 x 4096 bf16 with G and U kept 1020
-// to 1050 us, 1.85 PFLOP/s; FP4 348 us, 5.5 PFLOP/s) and by the epilogue's instructions
-// for short ones (4096 x 14336 x 512: bf16 85 us, FP4 70).  FP4 with parts left out: no
-// scale work 327 of then 372 us, no activation or stores 356, neither 292, nor two
-// thirds of the loads 259.
+// to 1050 us, 1.85 PFLOP/s; FP4 335 us, 5.7 PFLOP/s) and by the epilogue's instructions
+// for short ones (4096 x 14336 x 512: bf16 85 us, FP4 72).  FP4 with parts left out: no
+// scale work 338 of then 353 us, no activation or stores 320, two thirds of the loads
+// 334, none of these 282.
 //
 // kModeGatedRows: the gated form for outputs (D, or kept G or U) whose rows are not
 // whole 16 bytes apart.  A kernel of its own: its stores beside the others cost every
