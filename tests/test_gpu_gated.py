@@ -453,3 +453,13 @@ def test_output_rows_not_16_bytes_apart(out, M, N, K):
                 call(D, G=K_aligned)
                 assert np.array_equal(bits(G), bits(K_aligned)), form
                 assert int(torch.isnan(gbuf).sum()) == gbuf.numel() - M * N
+
+
+@pytest.mark.parametrize("bn", [128, 256])
+def test_fp4_more_block_rows_than_a_group(bn):
+    """M past 64 block rows (a full group of the tile order and a part of one), bit for bit."""
+    M, N, K = 8450, 130, 96
+    (aq, as_, a), (gq, gs, bg), (uq, us, bu) = fp4_inputs(5, M, N, K)
+    want, _, _ = exact_relu(a, bg, bu, BF16)
+    binding.gemm_debug_force_tile(11, bn)
+    assert np.array_equal(bits(binding.gemm_gated_e2m1(aq, as_, gq, gs, uq, us, act="relu", out=OUT_BF16)), want)
