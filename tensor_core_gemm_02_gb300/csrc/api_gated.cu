@@ -382,7 +382,7 @@ int64_t form_ns(const Form &f, int64_t sms)
 // columns, 280 and 532 for a pair's 256 x 256 and 256 x 512) and a fixed part, its
 // epilogue as far as the next tile's MMAs do not hide it.  A product with few tiles
 // and a long sum leaves most SMs idle: it may be cut, in at least 8 K blocks a part,
-// and the parts' float32 results added in a second kernel (2500 and its bytes).
+// and the parts' float32 results added in a second kernel (4000 and its bytes).
 // Against measurements (64 / 128 / 256 columns / pairs / 512-wide pairs, us): two
 // sources stacked along M, 2816 x 1024 x 2048 47 / 34 / 30 / 26 / 25; 911 x 6867 x 606
 // 19.3 / 14.3 / 15.4 / 13.2 / 13.7; 460 x 6030 x 397 9.8 / 8.3 / 6.9 / 7.5 / 11.1.
@@ -426,7 +426,7 @@ int trans_forms(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, i
             c.k_part = k_part;
             c.tiles = parts * f.tiles;
             c.tile_ns = k_part * s.block_ns + s.fixed_ns;
-            c.extra_ns = 2500 + m_sources * M * N * 8 * parts / 6000;
+            c.extra_ns = 4000 + m_sources * M * N * 8 * parts / 6000;
             if (form_ns(c, sm_count) < cut_ns) {
                 cut_ns = form_ns(c, sm_count);
                 cut = c;
@@ -721,21 +721,22 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
     forced_tile(&fk, &fbn);
     // M <= 64: the skinny kernel, except for short sums, over one wave of tiles at that,
     // where its join of the parts costs more than the sum (skinny / tile: 8 x 934 x 384
-    // 7.4 / 5.4 us, 2 x 3674 x 1760 8.8 / 7.2, 52 x 3012 x 3488 11.1 / 9.3, 2 x 12529 x 64
+    // 7.4 / 5.4 us, 16 x 5632 x 2048 9.7 / 6.8, 52 x 3012 x 3488 11.1 / 9.3, 2 x 12529 x 64
     // 7.9 / 6.7; 32 x 8192 x 1024 5.8 / 6.1, 16 x 2048 x 2048 6.8 / 7.1, 8 x 14336 x 512
     // 6.1 / 7.5)
     const bool one_wave = ceil_div(N, 64) <= sm_count;
-    if (M <= 64 && K > 256 && fk != 11 && !(one_wave && K < (M > 16 ? 4096 : 2048))) {
+    if (M <= 64 && K > 256 && fk != 11 && !(one_wave && K < (M > 16 || N >= 4096 ? 4096 : 2048))) {
         set_e2m1_skinny_plan(p, M, ceil_div(N, 64), K, sm_count);
         return p;
     }
     // 256 columns: half as much of A is read, and a wave of tiles takes about 1.6 times
-    // as long (128 / 256 columns: 2048 x 4096 x 4096 7 / 4 waves 47 / 36 us, 1024 x 14336 x
-    // 1024 12 / 6 27 / 22, 4096 x 14336 x 512 48 / 24 78 / 70, 200 x 14336 x 4096 3 / 2 22.9 /
-    // 22.5, 512 x 4096 x 1024 2 / 1 7.6 / 7.6, 300 x 1000 x 4096 1 / 1 9.8 / 12.4)
+    // as long (128 / 256 columns: 2048 x 4096 x 4096 7 / 4 waves 47 / 33 us, 1024 x 14336 x
+    // 1024 12 / 6 26 / 23, 200 x 14336 x 4096 3 / 2 22.9 / 22.5, 512 x 4096 x 1024 2 / 1 7.6 /
+    // 7.6, 300 x 1000 x 4096 1 / 1 9.8 / 12.4), but for the shortest sums (4096 x 14336 x 512
+    // 48 / 24 69 / 72, 1763 x 7578 x 288 11 / 6 18.7 / 21.3)
     const int64_t w128 = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
     const int64_t w256 = ceil_div(ceil_div(M, 128) * ceil_div(N, 128), sm_count);
-    const int bn = fk == 11 ? fbn : (3 * w256 <= 2 * w128 ? 256 : 128);
+    const int bn = fk == 11 ? fbn : (K > 512 && 3 * w256 <= 2 * w128 ? 256 : 128);
     p.kernel = 11;
     p.bm = 128;
     p.bn = bn;
@@ -756,9 +757,14 @@ gemm_plan trans_plan(int64_t M, int64_t N, int64_t K, int m_sources, int k_sourc
         return p;
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
-    // few rows of A: the skinny kernel, where it shares a long sum over the SMs
+    // few rows of A: the skinny kernel, where it shares a long sum over the SMs and B
+    // is long enough to stream; a sum in parts has less to join (skinny / parts, 16 and 64
+    // rows, bf16: 2816 x 1024 9.3 / 8.7 and 11.6 / 8.5 us, 16384 x 512 17.1 / 11.6 and 23.3 /
+    // 11.8, 5632 x 2048 12.1 / 11.8 and 14.9 / 12.0; 4096 x 4096 11.9 / 14.7 and 14.1 / 13.3,
+    // 14336 x 4096 24.0 / 29.4 and 27.2 / 30.8)
     const bool skinny_ok = M <= 64 && K > 0 && stored == 2 && m_sources == 1;
-    if (skinny_ok && (fk == 2 || (fk != 1 && fk != 3 && fk != 4 && skinny_wins(M, N, k_sources * K)))) {
+    const bool streams = k_sources * K <= INT64_MAX / N && k_sources * K * N > 12 << 20;
+    if (skinny_ok && (fk == 2 || (fk != 1 && fk != 3 && fk != 4 && streams && skinny_wins(M, N, k_sources * K)))) {
         set_skinny_plan(p, M, N, k_sources * ceil_div(K, tcg::skinny_kstage()) * tcg::skinny_kstage(),
                         sm_count, false);
         return p;
