@@ -369,7 +369,7 @@ struct Form {
     int64_t k_part, tiles, tile_ns, extra_ns;
 };
 
-constexpr int kMaxForms = 8;
+constexpr int kMaxForms = 9;
 
 int64_t form_ns(const Form &f, int64_t sms)
 {
@@ -382,7 +382,9 @@ int64_t form_ns(const Form &f, int64_t sms)
 // columns, 280 and 532 for a pair's 256 x 256 and 256 x 512) and a fixed part, its
 // epilogue as far as the next tile's MMAs do not hide it.  A product with few tiles
 // and a long sum leaves most SMs idle: it may be cut, in at least 8 K blocks a part,
-// and the parts' float32 results added in a second kernel (4000 and its bytes).
+// and the parts' float32 results added in a second kernel (4000 and its bytes).  (Whole /
+// in parts, or parts on single CTAs / on pairs: 512 x 512 x 8192 36 / 14 us, 512 x 4096 x
+// 14336 60 / 53, 256 x 4096 x 14336 38 / 35.)
 // Against measurements (64 / 128 / 256 columns / pairs / 512-wide pairs, us): two
 // sources stacked along M, 2816 x 1024 x 2048 47 / 34 / 30 / 26 / 25; 911 x 6867 x 606
 // 19.3 / 14.3 / 15.4 / 13.2 / 13.7; 460 x 6030 x 397 9.8 / 8.3 / 6.9 / 7.5 / 11.1.
@@ -412,11 +414,12 @@ int trans_forms(int64_t M, int64_t N, int64_t K, int m_sources, int k_sources, i
         Form f{s.kernel, s.bn, 1, kb, 0, kb * s.block_ns + s.fixed_ns, 0};
         f.tiles = m_sources * ceil_div(M, s.kernel == 1 ? 128 : 256) * ceil_div(N, s.bn);
         out[n++] = f;
-        if (s.kernel != 1 || kb < 16 || f.tiles > sm_count || (M <= 8 && (stored & 1)))
+        const int64_t sets = s.kernel == 1 ? sm_count : sm_count / 2;
+        if (s.kernel == 4 || kb < 16 || f.tiles > sets || (M <= 8 && (stored & 1)))
             continue;
         Form cut = f;
         int64_t cut_ns = INT64_MAX;
-        for (int64_t parts = 2; parts <= 16 && parts * f.tiles <= sm_count && kb / parts >= 8; ++parts) {
+        for (int64_t parts = 2; parts <= 16 && parts * f.tiles <= sets && kb / parts >= 8; ++parts) {
             const int64_t k_part = ceil_div(kb, parts);
             if ((parts - 1) * k_part >= kb)
                 continue;  // (the last part would be empty)
@@ -610,7 +613,7 @@ gemm_status run_trans(const TransProblem &p, gemm_plan plan, const DeviceInfo *d
         add->part_rows = part_m * plan.bm;
         add->second = m_blocks * plan.bm;
         add->parts = parts;
-        const cudaError_t e = tcg::launch_tile_major(stored, bn, false, 1, maps, two, a, grid, p.stream);
+        const cudaError_t e = tcg::launch_tile_major(stored, bn, pair, 1, maps, two, a, grid, p.stream);
         return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
     }
     a.num_m_blocks = static_cast<int32_t>(more_m ? 2 * m_blocks : m_blocks);

@@ -463,3 +463,10 @@ def test_fp4_more_block_rows_than_a_group(bn):
     want, _, _ = exact_relu(a, bg, bu, BF16)
     binding.gemm_debug_force_tile(11, bn)
     assert np.array_equal(bits(binding.gemm_gated_e2m1(aq, as_, gq, gs, uq, us, act="relu", out=OUT_BF16)), want)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(1000, 1367, 1000, F16), (512, 2000, 800, BF16), (1500, 700, 700, BF16)])
+def test_gradients_planned_side_by_side(M, N, K, dtype):
+    """Both products of a size where the weights' one keeps to the SMs that the input's leaves."""
+    x = backward_inputs(M, M, N, K, dtype)
+    check_products(x, *binding.gemm_gated_backward(**x), OUT_F32, (M, N, K))

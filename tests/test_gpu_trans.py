@@ -181,3 +181,20 @@ def test_output_rows_not_16_bytes_apart(ta, tb, out):
             binding.gemm_trans(A, B, c, D, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=out)
             assert torch.equal(D, aligned), (name, c is not None)
             assert int(torch.isnan(buf).sum()) == buf.numel() - M * N
+
+
+@pytest.mark.parametrize("ta,tb", STORED[:3])
+def test_exact_sums_in_parts_on_pairs(ta, tb):
+    """More rows than one block and a long sum: parts on CTA pairs, with C and at an odd address."""
+    M, N, K = 500, 1000, 8200
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    plan = binding.gemm_query_plan(M, N, K, trans=(ta, tb), sm_count=sms)
+    assert plan.splits > 1 and (sms != 152 or plan.kernel == 3)
+    A, B, C = operands(11, M, N, K, ta, tb, BF16, True)
+    s, _ = product(A, B, ta, tb)
+    got = binding.gemm_trans(A, B, C, trans_a=ta, trans_b=tb, alpha=0.5, beta=2.0, out=OUT_F16)
+    assert torch.equal(got.cpu(), (0.5 * s + 2.0 * C.cpu().double()).float().half())
+    buf = torch.full((M, N + 5), 9.0, device="cuda")
+    binding.gemm_trans(A, B, None, buf[:, 3:3 + N], trans_a=ta, trans_b=tb)
+    assert torch.equal(buf[:, 3:3 + N].cpu(), s.float())
+    assert (buf[:, :3] == 9.0).all() and (buf[:, 3 + N:] == 9.0).all()
