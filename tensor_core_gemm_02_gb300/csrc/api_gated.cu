@@ -736,7 +736,7 @@ gemm_plan gated_e2m1_plan(int64_t M, int64_t N, int64_t K, int sm_count)
     // as long (128 / 256 columns: 2048 x 4096 x 4096 7 / 4 waves 47 / 33 us, 1024 x 14336 x
     // 1024 12 / 6 26 / 23, 200 x 14336 x 4096 3 / 2 22.9 / 22.5, 512 x 4096 x 1024 2 / 1 7.6 /
     // 7.6, 300 x 1000 x 4096 1 / 1 9.8 / 12.4), but for the shortest sums (4096 x 14336 x 512
-    // 48 / 24 69 / 72, 1763 x 7578 x 288 11 / 6 18.7 / 21.3)
+    // 48 / 24 67 / 72, 1763 x 7578 x 288 11 / 6 18.7 / 21.3)
     const int64_t w128 = ceil_div(ceil_div(M, 128) * ceil_div(N, 64), sm_count);
     const int64_t w256 = ceil_div(ceil_div(M, 128) * ceil_div(N, 128), sm_count);
     const int bn = fk == 11 ? fbn : (K > 512 && 3 * w256 <= 2 * w128 ? 256 : 128);

@@ -1323,10 +1323,14 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         const int32_t box = f32 || (p & 1) == 0 ? col0 : col0 - 16;
                         if (box >= n_tma)
                             return;
-                        const uint32_t buf = base + Cfg::OFF_EPI + (4u * group + q) * (Cfg::EPI_BUF / 2);
+                        // this warp's shared memory: two boxes in turn, or (LAP) one
+                        const uint32_t buf =
+                            base + Cfg::OFF_EPI +
+                            (Cfg::LAP ? (4u * group + q) * (Cfg::EPI_BUF / 2)
+                                      : (4u * group + q) * Cfg::EPI_BUF + slot * (Cfg::EPI_BUF / 2));
                         if (box == col0) {
-                            if (lane == 0)
-                                bulk_wait_group_read<0>();  // the last store has read it
+                            if (lane == 0)  // the store that used it last has read it
+                                bulk_wait_group_read<Cfg::LAP ? 0 : 1>();
                             __syncwarp();
                         }
                         if (f32) {
@@ -1348,6 +1352,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                             }
                         }
                         if (f32 || (p & 1) == 1 || col0 + 16 >= args.N) {  // (the box is complete)
+                            slot ^= 1u;
                             if (kRows && !args.d_tma) {
                                 copy_image(buf, lane, f32 ? 16u : 32u, out_kind, args.D, args.ldd, row0, box, args);
                                 return;
@@ -1423,7 +1428,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                         }
                     } else {
                         // The second piece's loads go out before the first one's arithmetic
-                        // (4096 x 14336 x 512 72 -> 69 us; above, one more copy of the body
+                        // (4096 x 14336 x 512 70 -> 67 us; above, one more copy of the body
                         // costs more than the wait: 74 -> 81).
                         static_assert(!kGated || Cfg::LAP || kChunks == 1, "two pieces");
                         uint32_t g[2][16], u[2][16];
