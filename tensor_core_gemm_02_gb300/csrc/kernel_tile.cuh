@@ -1208,7 +1208,7 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     const uint32_t buf = kOne ? image + (one_box ? 0u : slot * (Cfg::EPI_BUF / 2))
                                               : buf0 + slot * Cfg::EPI_BUF;
                     slot ^= 1u;
-                    if (lane == 0) {  // the last store that used it has read it
+                    if (lane == 0) {  // the last store that used it, two uses back, has read it
                         if (one_box)
                             bulk_wait_group_read<0>();
                         else
@@ -1217,7 +1217,13 @@ __device__ __forceinline__ void tile_gemm_body(const CUtensorMap &tmA, const CUt
                     __syncwarp();
                     put_image(buf, lane, v, kind);
                     if (kRows && !tma) {
+                        // (an empty group: the wait above counts groups, and every use of a
+                        // buffer has to be one, or with G and U going out by TMA and D this
+                        // way, or the reverse, it would pass while the store that used the
+                        // buffer last still reads it)
                         copy_image(buf, lane, 32u, kind, ptr, ld, row0, col0, args);
+                        if (lane == 0)
+                            bulk_commit_group();
                         return;
                     }
                     fence_proxy_async_smem();

@@ -470,3 +470,32 @@ def test_gradients_planned_side_by_side(M, N, K, dtype):
     """Both products of a size where the weights' one keeps to the SMs that the input's leaves."""
     x = backward_inputs(M, M, N, K, dtype)
     check_products(x, *binding.gemm_gated_backward(**x), OUT_F32, (M, N, K))
+
+
+MIXES = {"GU|d": ("GU", "D"), "G|d": ("G", "D"), "U|d": ("U", "D"), "D|gu": ("D", "GU"), "D|g": ("D", "G"),
+         "D|u": ("D", "U")}
+
+
+@pytest.mark.parametrize("out", [OUT_F32, OUT_BF16, OUT_F16])
+@pytest.mark.parametrize("form", ["single64", "single128", "single256", "pair"])
+def test_outputs_of_mixed_alignment(form, out):
+    """D, G and U of one call, some with rows 16 bytes apart (stored by TMA) and some not (copied), over
+    several chunks and tiles per CTA: every one bit for bit, nothing beside it."""
+    M, N, K = 1300, 4001, 64
+    A, Bg, Bu = inputs(7, M, N, K, BF16, exact=True)
+    d, g, u = exact_relu(A, Bg, Bu, ref.out_dtype(out))
+    want = {"D": d, "G": g.bfloat16().float().numpy(), "U": u.bfloat16().float().numpy()}
+    binding.gemm_debug_force_tile(*FORMS[form])
+    for name, (aligned, odd) in MIXES.items():
+        for _ in range(3):
+            x, bufs = {}, {}
+            for k in aligned:
+                dtype = ref.out_dtype(out) if k == "D" else BF16
+                bufs[k] = torch.full((M, (N + 7) // 8 * 8), float("nan"), dtype=dtype, device="cuda")
+                x[k] = bufs[k][:, :N]
+            for k in odd:
+                x[k], bufs[k] = odd_rows(M, N, out if k == "D" else OUT_BF16)
+            binding.gemm_gated(A, Bg, Bu, act="relu", out=out, **x)
+            for k in x:
+                assert np.array_equal(bits(x[k]), want[k]), (name, k)
+                assert int(torch.isnan(bufs[k]).sum()) == bufs[k].numel() - M * N, (name, k)
