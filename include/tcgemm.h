@@ -34,8 +34,11 @@
  * of TMA descriptors; per device and stream, the skinny (M <= 64) path keeps
  * a workspace for split tiles, the FP4 paths buffers for converted weights
  * or re-pitched scales, and gemm_trans and gemm_gated_backward one or two for
- * the float32 parts of long sums over few tiles (splits > 1), each allocated
- * once and grown on demand (so calls on different streams never share them).
+ * the float32 parts of long sums over few tiles (splits > 1).  Each is allocated
+ * by the first call that needs it; a call that needs more gets a new one of at
+ * least twice the size, and the old one stays until the process ends (together
+ * the old ones are no larger than the newest), since a captured graph may hold
+ * its address.  Calls on different streams never share them.
  *
  * Execution: calls are asynchronous on `stream` (a cudaStream_t; NULL means
  * the legacy default stream) on the current device.  A call may launch more
@@ -43,8 +46,11 @@
  * clustered CTAs and, beside them, single CTAs on the SMs no cluster fits;
  * FP4 weights with M > 128 are first converted to bf16; a sum in parts is
  * added by a second kernel, in a fixed order); work issued later
- * on the stream still starts only after all of them, and every form can be
- * captured into a CUDA graph.
+ * on the stream still starts only after all of them.  Every form can be captured
+ * into a CUDA graph, its first call too.  A captured call keeps the buffers of
+ * the stream it was captured on, wherever the graph runs: a graph does not run at
+ * the same time as another one captured on that stream, as calls on it, or as
+ * itself.
  *
  * Per-device state (the status word's address, the workspaces, the address of
  * the allocation-free entry point's array) is set up by the first call on a

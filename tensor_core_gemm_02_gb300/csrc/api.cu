@@ -93,47 +93,82 @@ gemm_status device_info(DeviceInfo **out)
     return GEMM_OK;
 }
 
+namespace {
+
+// Device memory that stays allocated until the process ends, zeroed if asked.  Works at
+// any time, also while this or another stream is being captured into a graph: an
+// allocation is no stream operation, but a capturing thread has to say (relaxed mode)
+// that it does not mean it to be one, and the zeros are written on a stream that takes
+// no part.
+gemm_status new_buffer(size_t bytes, bool zeroed, void **out)
+{
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    void *p = nullptr;
+    cudaError_t e = cudaMalloc(&p, bytes > 0 ? bytes : 256);
+    if (e == cudaSuccess && zeroed) {
+        cudaStream_t s = nullptr;
+        e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+        if (e == cudaSuccess) {
+            e = cudaMemsetAsync(p, 0, bytes, s);
+            const cudaError_t done = cudaStreamSynchronize(s);
+            e = e == cudaSuccess ? done : e;
+            cudaStreamDestroy(s);
+        }
+        if (e != cudaSuccess)
+            cudaFree(p);
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    *out = p;
+    return GEMM_OK;
+}
+
+}  // namespace
+
 // Workspace of (device, stream) with room for `bytes` of partials and `count`
-// counters; grows geometrically.  New counters start at zero; the kernel
-// returns every counter it uses to zero.
+// counters.  New counters start at zero; the kernel returns every counter it uses to
+// zero.  Partials or counters that are too few get a new buffer of at least twice the
+// size; the old one stays, for calls under way and for graphs that hold its address
+// (together the old ones are no larger than the newest), and in g_ws, whose counters
+// are cleared after an error.
 gemm_status get_workspace(int device, cudaStream_t stream, size_t bytes, size_t count,
                           Workspace *out)
 {
     std::lock_guard<std::mutex> lock(g_ws_mu);
-    Workspace *w = nullptr;
-    for (Workspace &x : g_ws)
+    Workspace w;  // the newest of this device and stream
+    w.device = device;
+    w.stream = stream;
+    for (const Workspace &x : g_ws)
         if (x.device == device && x.stream == stream)
-            w = &x;
-    if (!w) {
-        g_ws.push_back(Workspace{});
-        w = &g_ws.back();
-        w->device = device;
-        w->stream = stream;
+            w = x;
+    const bool more_partials = !w.partials || w.partial_bytes < bytes;
+    const bool more_counters = !w.counters || w.counter_count < count;
+    gemm_status st;
+    if (more_partials) {
+        const size_t nb = bytes > 2 * w.partial_bytes ? bytes : 2 * w.partial_bytes;
+        void *p = nullptr;
+        if ((st = new_buffer(nb, false, &p)) != GEMM_OK)
+            return st;
+        w.partials = static_cast<float *>(p);
+        w.partial_bytes = nb;
     }
-    if (w->partial_bytes < bytes || w->counter_count < count) {
-        if (w->partials || w->counters) {
-            // earlier kernels on this stream may still use the old buffers
-            if (cudaStreamSynchronize(stream) != cudaSuccess)
-                return GEMM_ERR_CUDA;
-            cudaFree(w->partials);
-            cudaFree(w->counters);
-            w->partials = nullptr;
-            w->counters = nullptr;
+    if (more_counters) {
+        const size_t nc = count > 2 * w.counter_count ? count : 2 * w.counter_count;
+        void *p = nullptr;
+        if ((st = new_buffer(nc * sizeof(uint32_t), true, &p)) != GEMM_OK) {
+            if (more_partials)
+                cudaFree(w.partials);
+            return st;
         }
-        const size_t nb = bytes > 2 * w->partial_bytes ? bytes : 2 * w->partial_bytes;
-        const size_t nc = count > 2 * w->counter_count ? count : 2 * w->counter_count;
-        w->partial_bytes = 0;
-        w->counter_count = 0;
-        if (cudaMalloc(&w->partials, nb > 0 ? nb : 256) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-        if (cudaMalloc(&w->counters, nc * sizeof(uint32_t)) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-        if (cudaMemsetAsync(w->counters, 0, nc * sizeof(uint32_t), stream) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-        w->partial_bytes = nb;
-        w->counter_count = nc;
+        w.counters = static_cast<uint32_t *>(p);
+        w.counter_count = nc;
     }
-    *out = *w;
+    if (more_partials || more_counters)
+        g_ws.push_back(w);
+    *out = w;
     return GEMM_OK;
 }
 
@@ -591,8 +626,8 @@ void fill_common(GemmArgs &a, const Problem &p, const DeviceInfo *dev)
     a.timeout_ns = g_timeout_ns.load();
 }
 
-// Buffers of the FP4 paths, one per (device, stream, use), grown
-// geometrically: kBufWeights holds the bf16 copy of the weights for M > 64,
+// Buffers, one per (device, stream, use), grown as the workspaces are (an outgrown one
+// stays allocated): kBufWeights holds the bf16 copy of the weights for M > 64,
 // kBufScales a copy of the scales with a 16-byte row pitch for the TMA loads
 // of the M <= 64 path when the caller's pitch or base is not 16-byte aligned
 // (kBufScalesA / kBufScalesB: the same for gemm_e2m1's two operands).
@@ -610,31 +645,22 @@ gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t 
                                void **out)
 {
     std::lock_guard<std::mutex> lock(g_dq_mu);
-    DequantBuffer *b = nullptr;
-    for (DequantBuffer &x : g_dq)
+    DequantBuffer b;  // the newest of this device, stream and use
+    b.device = device;
+    b.stream = stream;
+    b.use = use;
+    for (const DequantBuffer &x : g_dq)
         if (x.device == device && x.stream == stream && x.use == use)
-            b = &x;
-    if (!b) {
-        g_dq.push_back(DequantBuffer{});
-        b = &g_dq.back();
-        b->device = device;
-        b->stream = stream;
-        b->use = use;
+            b = x;
+    if (!b.ptr || b.bytes < bytes) {
+        const size_t nb = bytes > 2 * b.bytes ? bytes : 2 * b.bytes;
+        const gemm_status st = new_buffer(nb, false, &b.ptr);
+        if (st != GEMM_OK)
+            return st;
+        b.bytes = nb;
+        g_dq.push_back(b);
     }
-    if (b->bytes < bytes) {
-        if (b->ptr) {
-            if (cudaStreamSynchronize(stream) != cudaSuccess)  // earlier calls may still read it
-                return GEMM_ERR_CUDA;
-            cudaFree(b->ptr);
-            b->ptr = nullptr;
-        }
-        const size_t nb = bytes > 2 * b->bytes ? bytes : 2 * b->bytes;
-        b->bytes = 0;
-        if (cudaMalloc(&b->ptr, nb) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-        b->bytes = nb;
-    }
-    *out = b->ptr;
+    *out = b.ptr;
     return GEMM_OK;
 }
 

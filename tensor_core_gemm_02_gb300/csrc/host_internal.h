@@ -61,7 +61,8 @@ struct Workspace {
 };
 
 // Workspace of (device, stream) with room for `bytes` of partials and `count`
-// counters (allocated on first use, grown geometrically; counters start at zero).
+// counters (allocated on first use, grown geometrically, outgrown ones kept; counters
+// start at zero).
 gemm_status get_workspace(int device, cudaStream_t stream, size_t bytes, size_t count,
                           Workspace *out);
 
@@ -96,7 +97,8 @@ void fill_common(GemmArgs &a, const Problem &p, const DeviceInfo *dev);
 // device-side error; noalloc.cu).
 gemm_status reset_static_scratch(int device);
 
-// Buffers the library keeps per (device, stream, use), grown geometrically:
+// Buffers the library keeps per (device, stream, use), grown geometrically (outgrown
+// ones stay allocated, for graphs that hold their address):
 // bf16 weights converted from FP4, block scales copied to a 16-byte row pitch
 // for TMA (B's for gemm_bf16_e2m1; A's and B's for gemm_e2m1, and Bu's for
 // gemm_gated_e2m1), and the parts of sums (kBufParts and the one after it).
