@@ -62,6 +62,14 @@ gemm_status device_info(DeviceInfo **out)
         return GEMM_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices)
         return GEMM_ERR_UNSUPPORTED;
+    // The driver's descriptor encoding needs the device's context to be current on this
+    // thread, which on a new thread it is not until a call like this one.
+    static thread_local int current = -1;
+    if (current != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        current = dev;
+    }
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceInfo &d = g_dev[dev];
     if (!d.ready) {
