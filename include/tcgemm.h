@@ -52,6 +52,9 @@
  * the same time as another one captured on that stream, as calls on it, or as
  * itself.
  *
+ * Any host threads may call at the same time, also on one stream: a call's
+ * launches that hand on data through a kept buffer are not mixed with another's.
+ *
  * Per-device state (the status word's address, the workspaces, the address of
  * the allocation-free entry point's array) is set up by the first call on a
  * device and kept for the life of the process; it does not survive

@@ -672,6 +672,13 @@ gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t 
     return GEMM_OK;
 }
 
+std::mutex &buffer_mutex(int device, cudaStream_t stream)
+{
+    static std::mutex m[64];
+    const uint64_t h = reinterpret_cast<uint64_t>(stream);
+    return m[(h ^ (h >> 4) ^ (h >> 10) ^ static_cast<uint64_t>(device)) % 64];
+}
+
 gemm_status run_skinny(const Problem &p, const gemm_plan &plan, const DeviceInfo *dev)
 {
     const int mp = plan.bm;
@@ -680,6 +687,7 @@ gemm_status run_skinny(const Problem &p, const gemm_plan &plan, const DeviceInfo
     if (!encode_2d(&maps.a, ab_type(p.bf16), p.A, p.K, p.M, p.lda * 2, 64,
                    static_cast<uint32_t>(mp), CU_TENSOR_MAP_SWIZZLE_128B))
         return GEMM_ERR_CUDA;
+    std::unique_lock<std::mutex> hold;  // (a copy of the scales)
     if (p.w4) {
         // codes: 32-byte boxes (64 elements) of 128 rows; scales: the block's
         // two rows of 128 columns (rows 16-byte aligned for TMA: copy them if
@@ -689,6 +697,7 @@ gemm_status run_skinny(const Problem &p, const gemm_plan &plan, const DeviceInfo
         if (!aligned16(scales) || lds % 16) {
             const int64_t pitch = (p.N + 15) / 16 * 16;
             void *buf = nullptr;
+            hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, p.stream));
             gemm_status st = get_dequant_buffer(dev->index, p.stream, kBufScales,
                                                 static_cast<size_t>(pitch) * (p.K / 32), &buf);
             if (st != GEMM_OK)
@@ -955,6 +964,7 @@ gemm_status run(const Problem &p)
         // many rows: turn the weights into bf16 once (exact: every code times a
         // power of two fits bf16 unless it leaves its range) and run the bf16 GEMM
         void *wb = nullptr;
+        std::lock_guard<std::mutex> hold(buffer_mutex(dev->index, p.stream));
         if ((st = get_dequant_buffer(dev->index, p.stream, kBufWeights,
                                      static_cast<size_t>(p.N) * p.K * 2, &wb)) != GEMM_OK)
             return st;

@@ -179,6 +179,7 @@ gemm_status run_e2m1(const E2m1Problem &p)
     DeviceInfo *dev = nullptr;
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
+    std::lock_guard<std::mutex> hold(buffer_mutex(dev->index, p.stream));  // (copies of the scales)
     const gemm_plan plan = e2m1_plan(p.M, p.N, p.K, p.image, dev->sm_count);
     if (plan.kernel == 15)
         return run_e2m1_skinny(p, plan, dev);

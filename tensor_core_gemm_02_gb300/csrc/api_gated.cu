@@ -265,6 +265,9 @@ gemm_status run_gated(const GatedProblem &p)
     DeviceInfo *dev = nullptr;
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
+    std::unique_lock<std::mutex> hold;
+    if (p.fp4)  // (copies of the scales)
+        hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, p.stream));
     const gemm_plan plan = p.fp4 ? gated_e2m1_plan(p.M, p.N, p.K, dev->sm_count)
                                  : gated_plan(p.M, p.N, p.K, p.G || p.U, dev->sm_count);
     if (plan.kernel == 2 || plan.kernel == 15)
@@ -519,6 +522,9 @@ struct AddParts {
     int64_t ldw = 0, part_rows = 0, second = 0;  // second: rows before the second stacked source's
     int parts = 0;
 };
+
+// Whether the product of this plan goes through a buffer of parts.
+bool in_parts(const gemm_plan &plan) { return plan.kernel != 2 && plan.splits > 1; }
 
 // Add the parts of the product p.
 gemm_status add_parts(const TransProblem &p, const AddParts &add)
@@ -936,8 +942,12 @@ gemm_status gemm_trans(int64_t M, int64_t N, int64_t K, int dtype_is_bf16, int t
     DeviceInfo *dev = nullptr;
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
+    const gemm_plan plan = plan_of_trans(p, dev);
+    std::unique_lock<std::mutex> hold;
+    if (in_parts(plan))
+        hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, p.stream));
     AddParts add;
-    if ((st = run_trans(p, plan_of_trans(p, dev), dev, &add)) != GEMM_OK)
+    if ((st = run_trans(p, plan, dev, &add)) != GEMM_OK)
         return st;
     return add_parts(p, add);
 }
@@ -1043,6 +1053,9 @@ gemm_status gemm_gated_backward(int64_t M, int64_t N, int64_t K, int dtype_is_bf
     forced_tile(&fk, &fbn);
     if (want_a && want_b && plan_a.kernel != 2 && M > 0 && N > 0 && fk == 0)
         plan_side_by_side(pa, pb, dev->sm_count, &plan_a, &plan_b);
+    std::unique_lock<std::mutex> hold;
+    if (in_parts(plan_a) || in_parts(plan_b))
+        hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, cs));
     if ((want_a && (st = run_trans(pa, plan_a, dev, &add_a)) != GEMM_OK) ||
         (want_b && (st = run_trans(pb, plan_b, dev, &add_b)) != GEMM_OK))
         return st;

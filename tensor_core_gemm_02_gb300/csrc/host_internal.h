@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "launch.h"
 #include "tcgemm.h"
@@ -104,6 +105,12 @@ gemm_status reset_static_scratch(int device);
 // gemm_gated_e2m1), and the parts of sums (kBufParts and the one after it).
 enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4, kBufParts = 5 };
 gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t bytes, void **out);
+
+// To be held from get_dequant_buffer to the last launch that reads the buffer, where a
+// call writes it in one launch and reads it in another: otherwise another thread's
+// call on the stream may come between the two and fill the buffer anew.  (One mutex
+// for some streams: holding it is a few launches' time.)  Never taken twice at once.
+std::mutex &buffer_mutex(int device, cudaStream_t stream);
 
 // The form forced by gemm_debug_force_tile (kernel 0: none).
 void forced_tile(int *kernel, int *bn);

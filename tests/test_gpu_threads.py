@@ -80,3 +80,137 @@ def test_threads_on_own_streams_match_single_threaded():
     assert not any(t.is_alive() for t in threads)
     assert not failures, failures[:5]
     assert device_status() == binding.GEMM_OK
+
+
+def _quarters(seed, rows, cols):
+    r = torch.Generator().manual_seed(seed)
+    return (torch.randint(-4, 5, (rows, cols), generator=r).float() / 4).to(torch.bfloat16).to(DEV)
+
+
+def _trans_parts(i):
+    """gemm_trans in parts, another shape per thread."""
+    M, N, K = 128 + 32 * i, 64 + 8 * i, 4096
+    A, B = _quarters(60 + i, K, M), _quarters(70 + i, K, N)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert binding.gemm_query_plan(M, N, K, trans=(True, True), sm_count=sms).splits > 1
+    return lambda s: binding.gemm_trans(A, B, trans_a=True, trans_b=True, stream=s)
+
+
+def test_bare_calls_from_threads_on_one_stream():
+    """As below for gemm_trans in parts, through the C entry with its arguments in hand: the calls'
+    two launches are as close to one another's as they get."""
+    s, lib = torch.cuda.Stream(device=DEV), binding.load_library()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    operands, want, outs, calls = [], [], [], []
+    for i in range(4):
+        M, N, K = 128 + 32 * i, 64 + 8 * i, 4096
+        A, B = _quarters(60 + i, K, M), _quarters(70 + i, K, N)
+        assert binding.gemm_query_plan(M, N, K, trans=(True, True), sm_count=sms).splits > 1
+        operands.append((A, B))
+        want.append((A.double().T @ B.double()).float())
+        outs.append(torch.zeros((200, M, N), device=DEV))
+        calls.append([(M, N, K, 1, 1, A.data_ptr(), M, 1, B.data_ptr(), N, None, 0, D.data_ptr(), N, OUT_F32,
+                       1.0, 0.0, s.cuda_stream) for D in outs[i]])
+    torch.cuda.synchronize()
+    go, status = threading.Barrier(len(calls)), []
+
+    def worker(i):
+        binding.gemm_check_device_status(s)
+        for _ in range(10):
+            go.wait(timeout=60)
+            status.extend({lib.gemm_trans(*args) for args in calls[i]})
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=600)
+    assert not any(t.is_alive() for t in threads) and set(status) == {binding.GEMM_OK}
+    s.synchronize()
+    for i, D in enumerate(outs):
+        wrong = [j for j in range(len(D)) if not torch.equal(D[j], want[i])]
+        assert not wrong, (i, wrong[:8], len(wrong))
+    assert device_status() == binding.GEMM_OK
+
+
+def _gradients_in_parts(i):
+    M, N, K = 4096, 64 + 16 * i, 72 + 8 * i
+    dD, G, U, A = (_quarters(80 + 10 * i + j, M, n) for j, n in enumerate((N, N, N, K)))
+    Bg, Bu = _quarters(84 + 10 * i, N, K), _quarters(85 + 10 * i, N, K)
+    return lambda s: torch.cat([t.flatten() for t in binding.gemm_gated_backward(
+        dD, G, U, A, Bg, Bu, act="relu", stream=s)[:3]])
+
+
+def _weights_to_bf16(i):
+    """FP4 weights and many rows: the weights are converted into a buffer first."""
+    p = _fp4(90 + i, 200, 256 + 32 * i, 512)
+    A, B, Bs = p.A.to(DEV), p.B.to(DEV), p.Bs.to(DEV)
+    return lambda s: binding.gemm_bf16_e2m1(A, B, Bs, stream=s)
+
+
+def _copied_scales(i, few=False):
+    """Both operands FP4, scale rows not 16 bytes apart (copied into buffers first)."""
+    M, N, K = 16 if few else 200, 256 + 32 * i, 512
+    r = torch.Generator().manual_seed(100 + i)
+    x = []
+    for rows in (M, N, N):
+        x.append(torch.randint(0, 256, (rows, K // 2), generator=r, dtype=torch.uint8).to(DEV))
+        x.append(torch.randint(126, 129, (K // 32, rows + 1), generator=r, dtype=torch.uint8).to(DEV)[:, 1:])
+    return lambda s: binding.gemm_gated_e2m1(*x, act="relu", stream=s)
+
+
+def _copied_scales_few(i):
+    return _copied_scales(i, few=True)
+
+
+def _weight_scales(i):
+    """FP4 weights and few rows, the same of their scales."""
+    p = _fp4(110 + i, 16, 2048 + 64 * i, 512)
+    A, B = p.A.to(DEV), p.B.to(DEV)
+    Bs = torch.cat((p.Bs[:, :1], p.Bs), dim=1).to(DEV)[:, 1:]
+    return lambda s: binding.gemm_bf16_e2m1(A, B, Bs, stream=s)
+
+
+def _plain_e2m1(i):
+    M, N, K = 200, 256 + 32 * i, 512
+    r = torch.Generator().manual_seed(120 + i)
+    x = []
+    for rows in (M, N):
+        x.append(torch.randint(0, 256, (rows, K // 2), generator=r, dtype=torch.uint8).to(DEV))
+        x.append(torch.randint(126, 129, (K // 32, rows + 1), generator=r, dtype=torch.uint8).to(DEV)[:, 1:])
+    return lambda s: binding.gemm_e2m1(*x, stream=s)
+
+
+@pytest.mark.parametrize("make", [_trans_parts, _gradients_in_parts, _weights_to_bf16, _copied_scales,
+                                  _copied_scales_few, _weight_scales, _plain_e2m1])
+def test_threads_on_one_stream(make):
+    """Calls of several launches that pass data on through a kept buffer, from threads that share one
+    stream: each result as alone, bit for bit (exact sums)."""
+    s = torch.cuda.Stream(device=DEV)
+    calls = [make(i) for i in range(3)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        want = [call(s).clone() for call in calls]
+    s.synchronize()
+    go, failures = threading.Barrier(len(calls)), []
+
+    def worker(i):
+        try:
+            with torch.cuda.stream(s):
+                for it in range(6):
+                    go.wait(timeout=60)
+                    outs = [calls[i](s) for _ in range(50)]
+                    s.synchronize()
+                    failures.extend((i, it, j) for j, o in enumerate(outs) if not torch.equal(o, want[i]))
+        except Exception as e:  # noqa: BLE001 -- reported below
+            failures.append((i, repr(e)))
+            go.abort()
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=600)
+    assert not any(t.is_alive() for t in threads)
+    assert not failures, failures[:5]
+    assert device_status() == binding.GEMM_OK
