@@ -529,14 +529,14 @@ def gemm_query_plan(M, N, K, gather=False, has_c=False, sm_count=148, scatter=Fa
                     seeded=False, fp4=False, noalloc=False, e2m1=None, gated=None, trans=None) -> Plan:
     """e2m1: None, or FP4_PACKED / FP4_ALIGN16B for gemm_e2m1's plan; gated: "16" or "e2m1"
     for gemm_gated's (has_c: a product is kept) or gemm_gated_e2m1's; trans: (trans_a,
-    trans_b), not both False, for gemm_trans's."""
+    trans_b) for gemm_trans's (both False: the plain form's, which then runs)."""
     p = Plan()
     form = 1 if gather else (2 if scatter else (3 if seeded else (4 if fp4 else (5 if noalloc else 0))))
     if e2m1 is not None:
         form = 6 + int(e2m1)
     if gated is not None:
         form = {"16": 16, "e2m1": 17}[gated]
-    if trans is not None:
+    if trans is not None and (trans[0] or trans[1]):
         form = 17 + int(bool(trans[0])) + 2 * int(bool(trans[1]))
     _check(load_library().gemm_query_plan(M, N, K, form, int(bool(has_c)),
                                           sm_count, ctypes.byref(p)), "gemm_query_plan")

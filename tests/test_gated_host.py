@@ -176,3 +176,13 @@ def test_reference_forms_agree_with_torch():
             s = 2.0 ** (int(scales[i, j // 32]) - 127)
             assert abs(values[i, j] - x[i, j]) <= min(abs(np.sign(x[i, j]) * v * s - x[i, j]) for v in ref.LEVELS) + 1e-12
     assert (scales == np.floor(np.log2(np.abs(x).reshape(4, 2, 32).max(2))) + 125).all()
+
+
+@pytest.mark.parametrize("has_c", [False, True])
+@pytest.mark.parametrize("M,N,K", [(16, 4096, 4096), (512, 512, 8192), (8192, 8192, 512), (3, 5, 7)])
+def test_plan_of_untransposed_operands_is_the_plain_one(lib, M, N, K, has_c):
+    """gemm_trans with neither operand transposed runs gemm_f16 / gemm_bf16, and its plan says so."""
+    fields = [name for name, _ in binding.Plan._fields_]
+    plain = binding.gemm_query_plan(M, N, K, has_c=has_c, sm_count=152)
+    got = binding.gemm_query_plan(M, N, K, has_c=has_c, sm_count=152, trans=(False, False))
+    assert [getattr(got, f) for f in fields] == [getattr(plain, f) for f in fields]
