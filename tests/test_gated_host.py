@@ -1,5 +1,10 @@
 """Host-side checks of the gated entry points that need no GPU: refusals before any CUDA call,
 the binding's own checks, and plans."""
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -186,3 +191,21 @@ def test_plan_of_untransposed_operands_is_the_plain_one(lib, M, N, K, has_c):
     plain = binding.gemm_query_plan(M, N, K, has_c=has_c, sm_count=152)
     got = binding.gemm_query_plan(M, N, K, has_c=has_c, sm_count=152, trans=(False, False))
     assert [getattr(got, f) for f in fields] == [getattr(plain, f) for f in fields]
+
+
+def test_binding_without_torchs_private_calls():
+    """The current device and stream come from torch's public calls where it lacks the private ones."""
+    code = textwrap.dedent("""
+        import types, torch
+        for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+            if hasattr(torch._C, name):
+                delattr(torch._C, name)
+        torch.cuda.current_device = lambda: 1
+        torch.cuda.current_stream = lambda device=None: types.SimpleNamespace(cuda_stream=100 + device)
+        from tensor_core_gemm_02_gb300 import binding
+        assert binding._stream_ptr(None) == 101 and binding._stream_ptr(7) == 7
+        print("right")
+        """)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "right", r.stdout + r.stderr
