@@ -392,7 +392,9 @@ gemm_status gemm_skinny_noalloc(int64_t M, int64_t N, int64_t K, int dtype_is_bf
  *  Other errors, alignment and execution as gemm_f16.
  *
  * Activations: SILU g sigmoid(g); GELU g Phi(g) (with erf); GELU_TANH its tanh
- * form; RELU max(g, 0); SIGMOID sigmoid(g).
+ * form; RELU max(g, 0); SIGMOID sigmoid(g).  In float32, each within a few units of
+ * its own last place, and about one more for every unit of the exponential's argument
+ * (g, g^2 / 2 for GELU); exponentials and sigmoids below 2^-126 count as 0.
  */
 typedef enum {
     GEMM_ACT_SILU = 0,

@@ -8,7 +8,8 @@
 // eight columns of one row (three 16-byte loads, two 16-byte stores), blocks
 // are wide along the columns; rows whose base or pitch is not 16-byte aligned,
 // and the columns past the last multiple of eight, go element by element.
-// Measured: 8192 x 14336 171 us (6.9 TB/s, the rate of a plain copy).
+// Measured: 8192 x 14336 171 us (6.9 TB/s, the rate of a plain copy); gelu, with the
+// longest arithmetic, 195.
 #include <cuda_runtime.h>
 
 #include "act.cuh"

@@ -49,8 +49,8 @@
 // of D.  They lie in different TMEM lanes: once a tile's sums are whole, thread n
 // < 64 (a column of G) and thread n + 64 (the same column of U) swap half of
 // their rows through shared memory, and each finishes half of the rows.  Bound by
-// streaming the weights: 16 x 14336 x 4096 bf16 40.2 us (5.9 TB/s), FP4 17.7 us (3.6 TB/s;
-// 8.3 us of it the stream, the rest its start and the last pieces' epilogues).
+// streaming the weights: 16 x 14336 x 4096 bf16 40.4 us (5.8 TB/s), FP4 15.8 us (4.0 TB/s;
+// the rest is the stream's start and the last pieces' epilogues).
 //
 // B stored K x N (BT): a tile is 128 columns of B, loaded as two boxes of 64
 // columns x 64 K rows, which the MMA reads as an MN-major operand; with a second

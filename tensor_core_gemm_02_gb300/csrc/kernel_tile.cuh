@@ -263,11 +263,13 @@ __device__ __forceinline__ void copy_image(uint32_t buf, uint32_t lane, uint32_t
 // plain tile, and an epilogue thread finds G and U of its row in its own TMEM
 // lane.  The output tile is BN / 2 columns wide.
 //
-// Bound by the tensor cores for long sums (8192 x 14336 x 4096 bf16 with G and U kept 1020
-// to 1050 us, 1.85 PFLOP/s; FP4 335 us, 5.7 PFLOP/s) and by the epilogue's instructions
-// for short ones (4096 x 14336 x 512: bf16 85 us, FP4 72).  FP4 with parts left out: no
-// scale work 338 of then 353 us, no activation or stores 320, two thirds of the loads
-// 334, none of these 282.
+// 16-bit operands: bound by the tensor cores for long sums (8192 x 14336 x 4096 bf16 with G
+// and U kept 1.02 to 1.10 ms with the power cap's clocks, 1.75 to 1.88 PFLOP/s) and by
+// the epilogue's instructions for short ones (4096 x 14336 x 512: 84 to 87 us, with gelu
+// 100 to 104).  FP4: the MMA thread waits between stages, for the scales and its turn of
+// the loads (8192 x 14336 x 4096 334 us, 5.8 PFLOP/s), or for the epilogue (4096 x 14336 x
+// 512 67 us; with gelu, whose polynomial is the longest, 87 to 90, and 374 to 382 of the
+// long one).
 //
 // kModeGatedRows: the gated form for outputs (D, or kept G or U) whose rows are not
 // whole 16 bytes apart.  A kernel of its own: its stores beside the others cost every
