@@ -510,6 +510,101 @@ gemm_status gemm_quantize_e2m1(int64_t M, int64_t K, int type,
                                void *Y, int64_t ldy, void *stream);
 
 /*
+ * The rows of each group, from their group ids: a stable counting sort.
+ *     offsets[g] = number of i with 0 <= ids[i] < g          (0 <= g <= groups)
+ *     order      = 0 .. M - 1 by ids[i], equal ids in their order; positions whose id is
+ *                  outside [0, groups) come last, behind offsets[groups], in their order
+ *     rows[i]    = order[i] / choices
+ * For a router that gives each of M / choices tokens `choices` experts, ids is its tokens x
+ * choices matrix of experts, and rows the token of each row, as gemm_grouped's idx takes it.
+ *
+ *  M, groups   in [0, 2^31) and [0, 1024] (GEMM_ERR_UNSUPPORTED above); choices >= 1.
+ *  ids         M int32; offsets groups + 1, order M, rows M (or NULL) int32: device memory,
+ *              4-byte aligned, not overlapping (GEMM_ERR_ALIAS).  M == 0: offsets are zeros.
+ */
+gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const int32_t *ids,
+                            int32_t *offsets, int32_t *order, int32_t *rows, void *stream);
+
+/*
+ * Rows grouped by weights: for every group g and its rows offsets[g] <= i < offsets[g + 1],
+ *     D[i][:] = alpha * A[idx ? idx[i] : i][:] * op(B_g)
+ * with B_g N x K and op its transpose (as gemm_f16), or B_g stored K x N (trans_b = 1, as
+ * gemm_trans: the gradient of the input).  Rows of D before offsets[0] and from
+ * offsets[groups] on keep what they hold.  The offsets are read on the device: the host
+ * need not know them, and a captured call follows them.
+ *
+ *  groups            in [0, 1024] (GEMM_ERR_UNSUPPORTED above); 0: nothing is done.
+ *  offsets           groups + 1 int32, not falling, in [0, M].  Where they are not, nothing
+ *                    is computed and GEMM_ERR_INDEX is recorded in the device status word.
+ *  M                 rows of D (and of A without idx; entries of idx).
+ *  A, lda            M x K, or with idx a table of a_rows >= 1 rows (gemm_gather_rows): 16-byte
+ *                    aligned, lda a multiple of 8.  a_rows is not read without idx.
+ *  idx               NULL, or M int32 rows of A, read for rows of a group only; they may
+ *                    repeat.  An index outside [0, a_rows) makes its row zero and records
+ *                    GEMM_ERR_INDEX.
+ *  B, ldb, stride_b  `groups` matrices, ldb a multiple of 8, the starts of consecutive ones
+ *                    stride_b elements apart (a multiple of 8, no less than a matrix).
+ *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.
+ *  K == 0            the groups' rows are 0.
+ *  Sums are float32, multiplied by alpha (mul.rn) and rounded once; the same bits every time.
+ *  Other errors and execution as gemm_f16.
+ */
+gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16,
+                         const void *A, int64_t a_rows, int64_t lda,
+                         const int32_t *idx, const int32_t *offsets,
+                         int trans_b, const void *B, int64_t ldb, int64_t stride_b,
+                         void *D, int64_t ldd,
+                         int out, float alpha, void *stream);
+
+/*
+ * The gradients of the groups' weights: for every group
+ *     dB_g = alpha * sum over its rows i of dD[i][:]^T * A[i][:]       (N x K)
+ * with dD M x N and A M x K as they lie in memory; a group without rows gets zeros.  Rows
+ * outside every group are not used, whatever they hold.
+ *
+ *  dD, lddd; A, lda      16-byte aligned, pitches multiples of 8.
+ *  offsets, groups       as gemm_grouped; offsets that are not valid make every dB_g zero.
+ *  dB, lddb, stride_db   `groups` matrices of type `out`, stride_db elements apart (no less
+ *                        than a matrix); must not overlap dD, A or offsets.
+ *  Other errors and execution as gemm_grouped.
+ */
+gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16,
+                                 const void *dD, int64_t lddd,
+                                 const void *A, int64_t lda,
+                                 const int32_t *offsets,
+                                 void *dB, int64_t lddb, int64_t stride_db,
+                                 int out, float alpha, void *stream);
+
+/*
+ * Newton-Schulz steps on each matrix of a stack: X_0 = X / (|X| + eps) with |X| the square
+ * root of the sum of X's squares, then `steps` times
+ *     X <- a X + (b P + c P^2) X  with  P = X X^T
+ * (on the smaller side: X (b P + c P^2) with P = X^T X where M > N), and Y = X.  With
+ * suitable a, b, c this moves every singular value of X towards 1, as optimisers do with the
+ * update of a weight matrix.
+ *
+ *  count             matrices; X and Y M x N, their starts stride_x and stride_y elements
+ *                    apart (no less than a matrix), aligned to their element sizes.
+ *  type, out         gemm_out_t of X and of Y.
+ *  steps             1 to 100; a, b, c finite; eps >= 0.
+ *  Y                 may be X exactly (same pointer, type, pitch and stride); any other
+ *                    overlap is GEMM_ERR_ALIAS.
+ *  Rounding: the norm and every sum are float32.  The products' operands -- X, P and b P + c
+ *  P^2 -- are held in float16 between them, scaled by 2^12 (so that elements down to 2^-26
+ *  keep 11 bits); the iterates' elements have to stay below 16, and P's and b P + c P^2's
+ *  below 16, as they do where the singular values stay below 2.  The last step is rounded
+ *  once, to Y's type.
+ *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.
+ *  Workspace: per device and stream, up to 1 GiB or one matrix's (4 M N + 4 min(M, N)^2
+ *  bytes) if that is more, kept as the other workspaces are.
+ *  Other errors and execution as gemm_f16 (2 + 3 steps kernels, more for a large stack).
+ */
+gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, int type,
+                               const void *X, int64_t ldx, int64_t stride_x, int out,
+                               void *Y, int64_t ldy, int64_t stride_y,
+                               int steps, float a, float b, float c, float eps, void *stream);
+
+/*
  * Synchronises `stream`, then returns and clears the first error the device
  * recorded since the last call on the current device (GEMM_OK if none).
  * Returns GEMM_ERR_CUDA if the synchronisation itself failed.  After a

@@ -69,6 +69,12 @@ def load_library(path: str = LIB_PATH):
     lib.gemm_trans.argtypes = [i64, i64, i64, i32, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, f32,
                                f32, vp]
     lib.gemm_quantize_e2m1.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_group_rows.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.gemm_grouped.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i32, vp, i64, i64, vp, i64, i32,
+                                 f32, vp]
+    lib.gemm_grouped_weights.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp, i64, i64, i32, f32, vp]
+    lib.gemm_orthogonalize.argtypes = [i64, i64, i64, i32, vp, i64, i64, i32, vp, i64, i64, i32, f32, f32, f32,
+                                       f32, vp]
     lib.gemm_seeded.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp]
     lib.gemm_accumulate.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, f32, vp]
     lib.gemm_scatter_rows.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64,
@@ -85,7 +91,8 @@ def load_library(path: str = LIB_PATH):
     for name in ("gemm_f16", "gemm_bf16", "gemm_gather_rows", "gemm_scatter_rows", "gemm_accumulate",
                  "gemm_seeded", "gemm_bf16_e2m1", "gemm_e2m1",
                  "gemm_gated", "gemm_gated_e2m1", "gemm_gated_backward", "gemm_trans",
-                 "gemm_quantize_e2m1", "gemm_skinny_noalloc",
+                 "gemm_quantize_e2m1", "gemm_group_rows", "gemm_grouped", "gemm_grouped_weights",
+                 "gemm_orthogonalize", "gemm_skinny_noalloc",
                  "gemm_check_device_status",
                  "gemm_query_plan", "gemm_set_wait_timeout", "gemm_debug_inject",
                  "gemm_debug_force_tile"):
@@ -459,6 +466,126 @@ def gemm_quantize_e2m1(X, Q=None, S=None, *, Y=None, stream=None):
     if st != GEMM_OK:
         raise GemmError(st, "gemm_quantize_e2m1")
     return Q, S
+
+
+def _stack(name, t, depth, rows, cols, dtype):
+    """(pointer, leading dimension, stride) of a depth x rows x cols argument of that dtype."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (depth, rows, cols):
+        raise ValueError(f"{name} must be {depth} x {rows} x {cols}")
+    stride, ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows < 2 or not cols:  # (one row: its pitch says nothing; no columns: not used)
+        ld = (max(ld, cols) + 7) // 8 * 8 if depth < 2 or not cols else max(stride, ld, cols)
+    return t.data_ptr(), ld, stride
+
+
+def _ints(name, t, shape):
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def gemm_group_rows(ids, groups, offsets=None, order=None, rows=None, *, stream=None):
+    """The rows of each group: ids (int32, 1-D, or tokens x choices) are group numbers, those
+    outside [0, groups) of no group.  Returns (offsets, order, rows): offsets (groups + 1
+    int32) where each group's rows begin, order the positions in ids.flatten() by group, equal
+    ones in their order, those of no group last, and rows = order // choices (choices 1 for
+    1-D ids), which gemm_grouped takes as its idx."""
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be 1-D or tokens x choices")
+    choices = max(1, ids.shape[1]) if ids.dim() == 2 else 1
+    M, new, i32 = ids.numel(), _allocator(ids.device), torch.int32
+    offsets = new((groups + 1,), (1,), i32) if offsets is None else offsets
+    order = new((M,), (1,), i32) if order is None else order
+    rows = new((M,), (1,), i32) if rows is None else rows
+    args = (M, groups, choices, _ints("ids", ids, ids.shape), _ints("offsets", offsets, (groups + 1,)),
+            _ints("order", order, (M,)), _ints("rows", rows, (M,)))
+    _on_device(ids, offsets, order, rows)
+    st = load_library().gemm_group_rows(*args, _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_group_rows")
+    return offsets, order, rows
+
+
+def gemm_grouped(A, B, offsets, D=None, *, idx=None, trans_b=False, alpha=1.0, out=OUT_F32, stream=None):
+    """D[i] = alpha * A[i] @ B[g].T for the rows offsets[g] <= i < offsets[g + 1] of every group g;
+    f16 or bf16 A (M x K) and B (groups x N x K, or groups x K x N with trans_b: A[i] @ B[g]).
+    idx (M int32): row i is A[idx[i]] of a table A.  Rows of D outside every group keep what
+    they hold (a new D is zero there).  offsets (groups + 1 int32) are read on the device."""
+    dt = A.dtype
+    bf16 = _bf16_flag("A", dt)
+    table, K = A.shape
+    M = table if idx is None else idx.shape[0]
+    groups, rb, cb = B.shape
+    N = cb if trans_b else rb
+    if (rb if trans_b else cb) != K:
+        raise ValueError("A and B disagree on K")
+    if D is None:
+        D = torch.zeros((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+    a, lda = _mat("A", A, table, K, dt)
+    args = (M, N, K, groups, bf16, a, table, lda,
+            None if idx is None else _ints("idx", idx, (M,)), _ints("offsets", offsets, (groups + 1,)),
+            1 if trans_b else 0, *_stack("B", B, groups, rb, cb, dt), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]),
+            out, alpha)
+    _on_device(A, B, offsets, idx, D)
+    st = load_library().gemm_grouped(*args, _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped")
+    return D
+
+
+def gemm_grouped_weights(dD, A, offsets, dB=None, *, alpha=1.0, out=OUT_F32, stream=None):
+    """The gradients of gemm_grouped's weights: dB[g] = alpha * dD[rows of g].T @ A[rows of g] (groups x N
+    x K), zero for a group without rows; dD M x N and A M x K, f16 or bf16, rows grouped by
+    offsets."""
+    dt = dD.dtype
+    bf16 = _bf16_flag("dD", dt)
+    M, N = dD.shape
+    K = A.shape[1]
+    groups = offsets.shape[0] - 1
+    if dB is None:
+        dB = _allocator(dD.device)((groups, N, K), (N * K, K, 1), _DTYPE_OF_OUT[out])
+    args = (M, N, K, groups, bf16, *_mat("dD", dD, M, N, dt), *_mat("A", A, M, K, dt),
+            _ints("offsets", offsets, (groups + 1,)), *_stack("dB", dB, groups, N, K, _DTYPE_OF_OUT[out]), out, alpha)
+    _on_device(dD, A, offsets, dB)
+    st = load_library().gemm_grouped_weights(*args, _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped_weights")
+    return dB
+
+
+def gemm_orthogonalize(X, Y=None, *, steps=5, coefs=(3.4445, -4.7750, 2.0315), eps=1e-7, stream=None):
+    """Newton-Schulz steps on X (M x N, or a stack count x M x N; float32, bf16 or f16): X / (|X| + eps),
+    then `steps` times X <- a X + (b P + c P @ P) X with P = X @ X.T and (a, b, c) = coefs,
+    which move the singular values towards 1.  Y has X's shape and, unless given, its dtype;
+    Y may be X.  Returns Y."""
+    kind = _OUT_OF_DTYPE.get(X.dtype)
+    if kind is None:
+        raise TypeError("X must be float32, bfloat16 or float16")
+    if X.dim() not in (2, 3):
+        raise ValueError("X must be M x N or count x M x N")
+    if Y is None:
+        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    out = _OUT_OF_DTYPE.get(Y.dtype)
+    if out is None:
+        raise TypeError("Y must be float32, bfloat16 or float16")
+    if Y.shape != X.shape:
+        raise ValueError("Y must have X's shape")
+    x, y = (X, Y) if X.dim() == 3 else (X[None], Y[None])
+    count, M, N = x.shape
+    a, b, c = coefs
+    args = (count, M, N, kind, *_stack("X", x, count, M, N, X.dtype), out, *_stack("Y", y, count, M, N, Y.dtype),
+            steps, a, b, c, eps)
+    _on_device(X, Y)
+    st = load_library().gemm_orthogonalize(*args, _stream_ptr(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_orthogonalize")
+    return Y
 
 
 def gemm_seeded(A, B, C, D=None, *, out=OUT_F32, stream=None):

@@ -40,7 +40,6 @@ namespace tcg {
 namespace host {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 
 
@@ -194,7 +193,7 @@ gemm_status reset_workspaces(int device)
 // ------------------------------------------------------------- descriptors
 
 struct MapKey {
-    uint64_t ptr, inner, outer, stride;
+    uint64_t ptr, inner, outer, stride, depth, stride2;
     uint32_t box_inner, box_outer, dtype, swizzle;
     bool operator==(const MapKey &o) const { return std::memcmp(this, &o, sizeof(*this)) == 0; }
 };
@@ -223,11 +222,12 @@ uint64_t hash_key(const MapKey &k)
     return h;
 }
 
-// A 2-D row-major tensor: `inner` contiguous elements per row, `outer` rows
-// `stride_bytes` apart, copied in boxes of box_inner x box_outer.
-bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint64_t inner,
-               uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swizzle)
+// `depth` row-major matrices `stride2_bytes` apart (depth 0: one, as a 2-D tensor): `inner`
+// contiguous elements per row, `outer` rows `stride_bytes` apart, copied in boxes of box_inner x
+// box_outer.
+bool encode_3d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint64_t inner, uint64_t outer,
+               uint64_t stride_bytes, uint64_t depth, uint64_t stride2_bytes, uint32_t box_inner,
+               uint32_t box_outer, CUtensorMapSwizzle swizzle)
 {
     MapKey key;
     std::memset(&key, 0, sizeof(key));
@@ -235,6 +235,8 @@ bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint6
     key.inner = inner;
     key.outer = outer;
     key.stride = stride_bytes;
+    key.depth = depth;
+    key.stride2 = stride2_bytes;
     key.box_inner = box_inner;
     key.box_outer = box_outer;
     key.dtype = static_cast<uint32_t>(dtype);
@@ -247,11 +249,11 @@ bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint6
             return true;
         }
     }
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {stride_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(m, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+    cuuint64_t dims[3] = {inner, outer, depth};
+    cuuint64_t strides[2] = {stride_bytes, stride2_bytes};
+    cuuint32_t box[3] = {box_inner, box_outer, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, dtype, depth > 0 ? 3 : 2, const_cast<void *>(ptr), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -261,6 +263,14 @@ bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint6
     g_cache[slot].key = key;
     g_cache[slot].map = *m;
     return true;
+}
+
+// A 2-D row-major tensor.
+bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint64_t inner,
+               uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+               CUtensorMapSwizzle swizzle)
+{
+    return encode_3d(m, dtype, ptr, inner, outer, stride_bytes, 0, 0, box_inner, box_outer, swizzle);
 }
 
 // ------------------------------------------------------------- validation

@@ -8,7 +8,6 @@
 
 #include <climits>
 #include <cstring>
-#include <initializer_list>
 
 #include "host_internal.h"
 
@@ -17,7 +16,6 @@ namespace host {
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int kGroupM = 16;  // block rows per tile-order group, as the plain forms
 // FP4: rows of A are a quarter as long, and each group reads all of B's: groups of up to
 // 64 block rows that hold 16 MB of A (8192 x 14336 x 4096, 8 / 16 / 32 / 64 block rows with
@@ -27,66 +25,6 @@ int32_t fp4_group_m(int64_t K)
 {
     const int64_t rows = (int64_t(1) << 24) / (64 * (K > 0 ? K : 1));  // 128 rows of K / 2 bytes
     return static_cast<int32_t>(rows < kGroupM ? kGroupM : (rows > 64 ? 64 : rows));
-}
-
-struct Span {
-    const void *p;
-    uint64_t bytes;
-};
-
-// Whether any of the outputs overlaps an input or another output.
-bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
-{
-    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Span &i : ins)
-            if (overlap(o->p, o->bytes, i.p, i.bytes))
-                return true;
-        for (const Span *q = o + 1; q != outs.end(); ++q)
-            if (overlap(o->p, o->bytes, q->p, q->bytes))
-                return true;
-    }
-    return false;
-}
-
-bool out_ok(int out) { return out == GEMM_OUT_F32 || out == GEMM_OUT_BF16 || out == GEMM_OUT_F16; }
-bool act_ok(int act) { return act >= GEMM_ACT_SILU && act <= GEMM_ACT_SIGMOID; }
-bool elem_aligned(const void *p, int size)
-{
-    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(size - 1)) == 0;
-}
-
-// A matrix argument: pointer, leading dimension, rows and columns of `esize`-byte
-// elements; `mma`: it is a TMA operand (16-byte base and pitch).
-struct Mat {
-    const void *p;
-    int64_t ld;
-    int64_t rows, cols;
-    int esize;
-    bool mma;
-};
-
-gemm_status check_mats(std::initializer_list<Mat> mats)
-{
-    for (const Mat &m : mats)
-        if (m.rows > 0 && m.cols > 0 && (!m.p || m.ld < m.cols))
-            return GEMM_ERR_INVALID_ARG;
-    for (const Mat &m : mats)
-        if (m.ld > kMaxDim)
-            return GEMM_ERR_UNSUPPORTED;
-    for (const Mat &m : mats)
-        if (m.rows > 0 && m.cols > 0 &&
-            (m.mma ? !aligned16(m.p) || (m.ld * m.esize) % 16 != 0 : !elem_aligned(m.p, m.esize)))
-            return GEMM_ERR_ALIGNMENT;
-    return GEMM_OK;
-}
-
-Span span_of(const Mat &m) { return Span{m.p, span_bytes(m.rows, m.cols, m.ld, m.esize)}; }
-
-CUtensorMapDataType out_type(int out)
-{
-    return out == GEMM_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                               : (out == GEMM_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
 // Boxes of 32 rows x box_cols columns of an output matrix, up to the last column whose row ends on whole 16
@@ -99,11 +37,6 @@ bool encode_out(CUtensorMap *m, const void *p, int out, int64_t rows, int64_t co
     cols = cols / per16 * per16;
     return encode_2d(m, out_type(out), p, cols, rows, ld * out_size(out), box_cols, 32,
                      box_cols * out_size(out) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
-bool out_tma(const void *p, int64_t ld, int out, int64_t cols)
-{
-    return aligned16(p) && (ld * out_size(out)) % 16 == 0 && cols * out_size(out) >= 16;
 }
 
 // ---------------------------------------------------------------- gated form

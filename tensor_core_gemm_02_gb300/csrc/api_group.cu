@@ -1,0 +1,500 @@
+// api_group.cu -- the entry points for layers of experts: gemm_group_rows, gemm_grouped,
+// gemm_grouped_weights (products over groups of rows) and gemm_orthogonalize (Newton-Schulz
+// steps on a stack of matrices).  include/tcgemm.h has the contracts.  Checks run before any
+// CUDA call, as everywhere.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "host_internal.h"
+#include "launch_group.h"
+
+namespace tcg {
+namespace host {
+
+namespace {
+
+constexpr int64_t kMaxGroups = 1024;  // (a warp keeps 32 groups a lane)
+constexpr int kGroupM = 16;           // block rows per tile-order group, as the plain forms
+
+// A form of the group kernel, with the time of a tile's K block and of its fixed part in ns
+// (operand bytes from L2 to an SM set the first, the epilogue and the hand-overs the second).
+struct GForm {
+    int bn;
+    bool pair;
+    int64_t block_ns, fixed_ns;
+};
+constexpr GForm kForms[4] = {{64, false, 300, 300}, {128, false, 300, 500}, {256, false, 390, 600}, {256, true, 280, 1500}};
+
+// The form of the least waves x time of a tile.  tiles(tile_m, bn): tiles of the problem
+// (0: the form does not apply).
+template <class F>
+GForm choose_form(int64_t k_blocks, int sm_count, F tiles)
+{
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    const GForm *best = nullptr;
+    int64_t best_ns = 0;
+    for (const GForm &f : kForms) {
+        const int64_t n = tiles(f.pair ? 256 : 128, f.bn), sets = f.pair ? sm_count / 2 : sm_count;
+        if (n <= 0 || sets <= 0)
+            continue;
+        if ((fk == 1 && !f.pair && f.bn == fbn) || (fk == 3 && f.pair))
+            return f;
+        const int64_t ns = ceil_div(n, sets) * (k_blocks * f.block_ns + f.fixed_ns);
+        if (!best || ns < best_ns) {
+            best = &f;
+            best_ns = ns;
+        }
+    }
+    return best ? *best : kForms[1];
+}
+
+// CTAs of a launch over at most `tiles` tiles.
+gemm_status group_grid(const GForm &f, int64_t tiles, const DeviceInfo *dev, int *grid)
+{
+    int64_t sets = dev->sm_count;
+    if (f.pair) {
+        sets = tcg::tile_max_clusters(256, true, 1, 1);  // (the same shared memory)
+        if (sets <= 0)
+            return GEMM_ERR_CUDA;
+    }
+    *grid = static_cast<int>((f.pair ? 2 : 1) * (tiles < sets ? tiles : sets));
+    return GEMM_OK;
+}
+
+void fill_group(GroupArgs &a, bool bf16, int out, const DeviceInfo *dev)
+{
+    std::memset(&a, 0, sizeof(a));
+    GemmArgs g;
+    std::memset(&g, 0, sizeof(g));
+    Problem q{};
+    fill_common(g, q, dev);
+    a.out_kind = out;
+    a.ab_bf16 = bf16 ? 1 : 0;
+    a.extra_tx = g.extra_tx;
+    a.status = g.status;
+    a.timeout_ns = g.timeout_ns;
+    a.beta = 0.0f;
+}
+
+// D of a launch: `depth` matrices of rows x cols; false if the descriptor was refused.
+bool set_out(GroupArgs &a, GroupMaps &maps, void *D, int out, int64_t rows, int64_t cols, int64_t ld,
+             int64_t depth, int64_t stride)
+{
+    const int64_t es = out_size(out), per16 = 16 / es;
+    a.D = D;
+    a.ldd = ld;
+    a.stride_d = stride;
+    a.n_out = static_cast<int32_t>(cols);
+    a.d_vec = aligned16(D) && ld * es % 16 == 0 && (depth == 1 || stride * es % 16 == 0) ? 1 : 0;
+    a.d_tma = a.d_vec && cols >= per16 ? 1 : 0;
+    return !a.d_tma || encode_3d(&maps.d, out_type(out), D, cols / per16 * per16, rows, ld * es, depth,
+                                 depth == 1 ? rows * ld * es : stride * es, static_cast<uint32_t>(128 / es), 32,
+                                 CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// A stack of `depth` matrices of rows x cols 16-bit elements as an operand: boxes of 64
+// columns and box_rows rows.
+bool set_operand(CUtensorMap *m, bool bf16, const void *p, int64_t cols, int64_t rows, int64_t ld, int64_t depth,
+                 int64_t stride, int box_rows)
+{
+    return encode_3d(m, ab_type(bf16), p, cols, rows, ld * 2, depth, depth == 1 ? rows * ld * 2 : stride * 2, 64,
+                     static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// A stack of matrices among the arguments: checked as check_mats checks one, and the
+// distance from one to the next, which may not be less than a matrix.
+struct Stack {
+    Mat m;
+    int64_t depth, stride;
+};
+gemm_status check_stack(const Stack &s)
+{
+    if (s.depth == 0 || s.m.rows == 0 || s.m.cols == 0)
+        return GEMM_OK;
+    const gemm_status st = check_mats({s.m});
+    if (st != GEMM_OK || s.depth == 1)
+        return st;
+    if (s.stride < (s.m.rows - 1) * s.m.ld + s.m.cols)
+        return GEMM_ERR_INVALID_ARG;
+    if (s.stride > INT64_MAX / 8 / s.depth)
+        return GEMM_ERR_UNSUPPORTED;
+    return s.m.mma && s.stride * s.m.esize % 16 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+Span span_of(const Stack &s)
+{
+    if (s.depth == 0 || s.m.rows == 0 || s.m.cols == 0)
+        return Span{nullptr, 0};
+    const Span one = span_of(s.m);
+    return Span{one.p, one.bytes + static_cast<uint64_t>(s.depth - 1) * s.stride * s.m.esize};
+}
+
+bool bad_flag(int f) { return f != 0 && f != 1; }
+
+}  // namespace
+
+}  // namespace host
+}  // namespace tcg
+
+using namespace tcg::host;
+using tcg::GroupArgs;
+using tcg::GroupMaps;
+
+extern "C" {
+
+gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const int32_t *ids, int32_t *offsets,
+                            int32_t *order, int32_t *rows, void *stream)
+{
+    if (M < 0 || groups < 0 || choices < 1 || !offsets || (M > 0 && (!ids || !order)))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || choices > kMaxDim || groups > kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (!elem_aligned(offsets, 4) || (M > 0 && (!elem_aligned(ids, 4) || !elem_aligned(order, 4) || !elem_aligned(rows, 4))))
+        return GEMM_ERR_ALIGNMENT;
+    const uint64_t b = static_cast<uint64_t>(M) * 4;
+    if (any_overlap({Span{offsets, static_cast<uint64_t>(groups + 1) * 4}, Span{order, b}, Span{rows, rows ? b : 0}},
+                    {Span{ids, b}}))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status st = device_info(&dev);
+    if (st != GEMM_OK)
+        return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    int64_t chunks = 1;
+    void *counts = nullptr;
+    std::unique_lock<std::mutex> hold;
+    if (M > tcg::kGroupRowsOne) {
+        chunks = ceil_div(M, tcg::kGroupRowsChunk);
+        chunks = chunks < dev->sm_count ? chunks : dev->sm_count;
+        hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, cs));
+        if ((st = get_dequant_buffer(dev->index, cs, kBufGroupRows,
+                                     static_cast<size_t>(chunks * (groups + 1)) * sizeof(int32_t), &counts)) != GEMM_OK)
+            return st;
+    }
+    const cudaError_t e = tcg::launch_group_rows_sort(ids, M, static_cast<int32_t>(groups),
+                                                      static_cast<int32_t>(choices), offsets, order, rows,
+                                                      static_cast<int32_t *>(counts), static_cast<int32_t>(chunks), cs);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16, const void *A,
+                         int64_t a_rows, int64_t lda, const int32_t *idx, const int32_t *offsets, int trans_b,
+                         const void *B, int64_t ldb, int64_t stride_b, void *D, int64_t ldd, int out, float alpha,
+                         void *stream)
+{
+    if (bad_flag(dtype_is_bf16) || bad_flag(trans_b) || M < 0 || N < 0 || K < 0 || groups < 0 || !out_ok(out) ||
+        (idx && a_rows < 1))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || (idx && a_rows > kMaxDim) || groups > kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0 || groups == 0)
+        return GEMM_OK;
+    auto most = [&](int tm, int bn) { return (M / tm + groups) * ceil_div(N, bn); };
+    if (most(128, 64) > kMaxDim)
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t rows = idx ? a_rows : M;
+    const Mat a{A, lda, K > 0 ? rows : 0, K, 2, true}, d{D, ldd, M, N, out_size(out), false};
+    const Stack b{Mat{B, ldb, trans_b ? K : N, trans_b ? N : K, 2, true}, groups, stride_b};
+    if (!offsets)
+        return GEMM_ERR_INVALID_ARG;
+    gemm_status st = check_mats({a, d});
+    if (st != GEMM_OK || (st = check_stack(b)) != GEMM_OK)
+        return st;
+    if (!elem_aligned(offsets, 4) || !elem_aligned(idx, 4))
+        return GEMM_ERR_ALIGNMENT;
+    if (any_overlap({span_of(d)}, {span_of(a), span_of(b), Span{offsets, static_cast<uint64_t>(groups + 1) * 4},
+                                   Span{idx, idx ? static_cast<uint64_t>(M) * 4 : 0}}))
+        return GEMM_ERR_ALIAS;
+    // a group of r rows has ceil(r / tile) block rows: on average half a tile more than its rows
+    auto tiles = [&](int tm, int bn) {
+        const int64_t blocks = M / tm + (groups < M ? groups : M) / 2 + 1;
+        return (blocks < M ? blocks : M) * ceil_div(N, bn);
+    };
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const bool bf16 = dtype_is_bf16 == 1;
+    const tcg::host::GForm f = choose_form(ceil_div(K, 64), dev->sm_count, tiles);
+    int grid = 0;
+    if ((st = group_grid(f, most(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK)
+        return st;
+    GroupMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    GroupArgs g;
+    fill_group(g, bf16, out, dev);
+    const bool a_ok = K == 0 || (idx ? encode_2d(&maps.a, ab_type(bf16), A, K, rows, lda * 2, 64, 1,
+                                                 CU_TENSOR_MAP_SWIZZLE_128B)
+                                     : set_operand(&maps.a, bf16, A, K, M, lda, 1, 0, 128));
+    const bool b_ok = K == 0 || (trans_b ? set_operand(&maps.b, bf16, B, N, K, ldb, groups, stride_b, 64)
+                                         : set_operand(&maps.b, bf16, B, K, N, ldb, groups, stride_b,
+                                                       f.pair ? f.bn / 2 : f.bn));
+    if (!a_ok || !b_ok || !set_out(g, maps, D, out, M, N, ldd, 1, 0))
+        return GEMM_ERR_CUDA;
+    g.groups = static_cast<int32_t>(groups);
+    g.offsets = offsets;
+    g.rows = static_cast<int32_t>(M);
+    g.N = static_cast<int32_t>(N);
+    g.K = static_cast<int32_t>(K);
+    g.num_n_blocks = static_cast<int32_t>(ceil_div(N, f.bn));
+    g.group_m = kGroupM;
+    g.alpha = alpha;
+    g.idx = idx;
+    g.table_rows = static_cast<int32_t>(rows);
+    g.loads = K > 0 ? 1 : 0;
+    const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, maps, g, grid, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16, const void *dD,
+                                 int64_t lddd, const void *A, int64_t lda, const int32_t *offsets, void *dB,
+                                 int64_t lddb, int64_t stride_db, int out, float alpha, void *stream)
+{
+    if (bad_flag(dtype_is_bf16) || M < 0 || N < 0 || K < 0 || groups < 0 || !out_ok(out))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > kMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (N == 0 || K == 0 || groups == 0)
+        return GEMM_OK;
+    if (ceil_div(N, 128) > kMaxDim / ceil_div(K, 64) / groups)
+        return GEMM_ERR_UNSUPPORTED;
+    const Mat dd{dD, lddd, M, N, 2, true}, a{A, lda, M, K, 2, true};
+    const Stack db{Mat{dB, lddb, N, K, out_size(out), false}, groups, stride_db};
+    if (!offsets)
+        return GEMM_ERR_INVALID_ARG;
+    gemm_status st = check_mats({dd, a});
+    if (st != GEMM_OK || (st = check_stack(db)) != GEMM_OK)
+        return st;
+    if (!elem_aligned(offsets, 4))
+        return GEMM_ERR_ALIGNMENT;
+    if (any_overlap({span_of(db)}, {span_of(dd), span_of(a), Span{offsets, static_cast<uint64_t>(groups + 1) * 4}}))
+        return GEMM_ERR_ALIAS;
+    auto tiles = [&](int tm, int bn) { return groups * ceil_div(N, tm) * ceil_div(K, bn); };
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const bool bf16 = dtype_is_bf16 == 1;
+    const tcg::host::GForm f = choose_form(ceil_div(ceil_div(M, groups), 64), dev->sm_count, tiles);
+    int grid = 0;
+    if ((st = group_grid(f, tiles(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK)
+        return st;
+    GroupMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    GroupArgs g;
+    fill_group(g, bf16, out, dev);
+    if ((M > 0 && (!set_operand(&maps.a, bf16, dD, N, M, lddd, 1, 0, 64) ||
+                   !set_operand(&maps.b, bf16, A, K, M, lda, 1, 0, 64))) ||
+        !set_out(g, maps, dB, out, N, K, lddb, groups, stride_db))
+        return GEMM_ERR_CUDA;
+    g.groups = static_cast<int32_t>(groups);
+    g.offsets = offsets;
+    g.rows = static_cast<int32_t>(M);
+    g.M = static_cast<int32_t>(N);
+    g.N = static_cast<int32_t>(K);
+    g.num_m_blocks = static_cast<int32_t>(ceil_div(N, f.pair ? 256 : 128));
+    g.num_n_blocks = static_cast<int32_t>(ceil_div(K, f.bn));
+    g.group_m = kGroupM;
+    g.alpha = alpha;
+    g.loads = M > 0 ? 1 : 0;
+    const cudaError_t e = tcg::launch_group_sum(f.bn, f.pair, maps, g, grid, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace tcg {
+namespace host {
+namespace {
+
+// A product of the Newton-Schulz steps over a stack of `count` matrices: D = alpha op(A) op(B)
+// + beta C, M x N, the sum over K; operands float16.
+struct BatchProduct {
+    int64_t count, M, N, K;
+    int maj;  // bit 0: A stored K x M, bit 1: B stored K x N
+    bool sym;
+    const uint16_t *A;
+    int64_t lda, stride_a;
+    const uint16_t *B;
+    int64_t ldb, stride_b;
+    const uint16_t *C;
+    int64_t ldc, stride_c;
+    void *D;
+    int64_t ldd, stride_d;
+    int out;
+    bool padded;  // D is a workspace: its rows' padding is written too
+    float alpha, beta;
+};
+
+gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t stream)
+{
+    auto tiles = [&](int tm, int bn) -> int64_t {
+        const int64_t mb = ceil_div(p.M, tm);
+        if (p.sym)
+            return tm < bn ? 0 : p.count * (tm / bn) * (mb * (mb + 1) / 2);
+        return p.count * mb * ceil_div(p.N, bn);
+    };
+    const GForm f = choose_form(ceil_div(p.K, 64), dev->sm_count, tiles);
+    const int tm = f.pair ? 256 : 128, b_rows = f.pair ? f.bn / 2 : f.bn;
+    int grid = 0;
+    gemm_status st = group_grid(f, tiles(tm, f.bn), dev, &grid);
+    if (st != GEMM_OK)
+        return st;
+    GroupMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    GroupArgs g;
+    fill_group(g, false, p.out, dev);
+    const bool a_ok = (p.maj & 1) ? set_operand(&maps.a, false, p.A, p.M, p.K, p.lda, p.count, p.stride_a, 64)
+                                  : set_operand(&maps.a, false, p.A, p.K, p.M, p.lda, p.count, p.stride_a, 128);
+    const bool b_ok = (p.maj & 2) ? set_operand(&maps.b, false, p.B, p.N, p.K, p.ldb, p.count, p.stride_b, 64)
+                                  : set_operand(&maps.b, false, p.B, p.K, p.N, p.ldb, p.count, p.stride_b, b_rows);
+    if (!a_ok || !b_ok || !set_out(g, maps, p.D, p.out, p.M, p.padded ? p.ldd : p.N, p.ldd, p.count, p.stride_d))
+        return GEMM_ERR_CUDA;
+    g.groups = static_cast<int32_t>(p.count);
+    g.M = static_cast<int32_t>(p.M);
+    g.N = static_cast<int32_t>(p.N);
+    g.K = static_cast<int32_t>(p.K);
+    g.num_m_blocks = static_cast<int32_t>(ceil_div(p.M, tm));
+    g.num_n_blocks = static_cast<int32_t>(ceil_div(p.N, f.bn));
+    g.group_m = kGroupM;
+    g.alpha = p.alpha;
+    g.beta = p.beta;
+    g.C = p.C;
+    g.ldc = p.ldc;
+    g.stride_c = p.stride_c;
+    g.loads = 1;
+    const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, maps, g, grid, stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Powers of two that keep the float16 iterates (elements up to 1 and a little) and their
+// products with themselves (as small as the product of two of their elements) away from
+// float16's subnormal numbers.
+constexpr float kIterateScale = 4096.0f, kProductScale = 4096.0f;
+// Workspace of a call: matrices are taken so many at a time that theirs fit, one at least.
+constexpr int64_t kOrthogonalizeBytes = int64_t(1) << 30;
+
+}  // namespace
+}  // namespace host
+}  // namespace tcg
+
+extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, int type, const void *X, int64_t ldx,
+                                          int64_t stride_x, int out, void *Y, int64_t ldy, int64_t stride_y,
+                                          int steps, float a, float b, float c, float eps, void *stream)
+{
+    if (count < 0 || M < 0 || N < 0 || !out_ok(type) || !out_ok(out) || steps < 1 || steps > 100 ||
+        !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !(eps >= 0.0f))
+        return GEMM_ERR_INVALID_ARG;
+    if (count > kMaxDim || M > kMaxDim || N > kMaxDim)
+        return GEMM_ERR_UNSUPPORTED;
+    if (count == 0 || M == 0 || N == 0)
+        return GEMM_OK;
+    if (ceil_div(M, 128) > kMaxDim / ceil_div(N, 64) || M > (int64_t(1) << 40) / N)
+        return GEMM_ERR_UNSUPPORTED;
+    const Stack x{Mat{X, ldx, M, N, out_size(type), false}, count, stride_x};
+    const Stack y{Mat{Y, ldy, M, N, out_size(out), false}, count, stride_y};
+    gemm_status st = check_stack(x);
+    if (st != GEMM_OK || (st = check_stack(y)) != GEMM_OK)
+        return st;
+    const bool in_place = X == Y && type == out && ldx == ldy && (count == 1 || stride_x == stride_y);
+    if (!in_place && any_overlap({span_of(y)}, {span_of(x)}))
+        return GEMM_ERR_ALIAS;
+    const bool wide = M <= N;
+    const int64_t s = wide ? M : N, l = wide ? N : M;
+    DeviceInfo *dev = nullptr;
+    if ((st = device_info(&dev)) != GEMM_OK)
+        return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // workspace of a matrix: two iterates, the product of one with itself, and the polynomial of that
+    const int64_t ldi = ceil_div(N, 8) * 8, ldp = ceil_div(s, 8) * 8;
+    const int64_t size_i = ceil_div(M * ldi, 64) * 64, size_p = ceil_div(s * ldp, 64) * 64;
+    const int parts = tcg::orthogonalize_parts(M, N);
+    const int64_t each = 2 * (2 * size_i + 2 * size_p) + 4 * static_cast<int64_t>(parts);
+    int64_t at_once = kOrthogonalizeBytes / each;
+    const int64_t tiles_one = ceil_div(M, 128) * ceil_div(N, 64);
+    at_once = at_once < count ? at_once : count;
+    at_once = at_once < 65535 ? at_once : 65535;  // (a grid's second dimension)
+    at_once = at_once < kMaxDim / tiles_one ? at_once : kMaxDim / tiles_one;
+    at_once = at_once > 1 ? at_once : 1;
+    std::unique_lock<std::mutex> hold(buffer_mutex(dev->index, cs));
+    void *w = nullptr;
+    if ((st = get_dequant_buffer(dev->index, cs, kBufOrthogonalize, static_cast<size_t>(at_once * each), &w)) != GEMM_OK)
+        return st;
+    uint16_t *iter[2] = {static_cast<uint16_t *>(w), static_cast<uint16_t *>(w) + at_once * size_i};
+    uint16_t *prod = iter[1] + at_once * size_i, *poly = prod + at_once * size_p;
+    float *partial = reinterpret_cast<float *>(poly + at_once * size_p);
+    for (int64_t first = 0; first < count; first += at_once) {
+        const int64_t n = count - first < at_once ? count - first : at_once;
+        const void *xf = static_cast<const uint8_t *>(X) + first * stride_x * out_size(type);
+        void *yf = static_cast<uint8_t *>(Y) + first * stride_y * out_size(out);
+        if (tcg::launch_square_sums(xf, ldx, stride_x, type, static_cast<int32_t>(M), static_cast<int32_t>(N),
+                                    static_cast<int32_t>(n), partial, parts, cs) != cudaSuccess ||
+            tcg::launch_normalize(xf, ldx, stride_x, type, static_cast<int32_t>(M), static_cast<int32_t>(N),
+                                  static_cast<int32_t>(n), partial, parts, kIterateScale, eps, iter[0], ldi, size_i,
+                                  cs) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        for (int i = 0; i < steps; ++i) {
+            const uint16_t *xi = iter[i % 2];
+            const bool last = i == steps - 1;
+            // P = kProductScale X X^T (or X^T X), on the smaller side
+            BatchProduct p{};
+            p.count = n;
+            p.M = p.N = s;
+            p.K = l;
+            p.maj = wide ? 0 : 3;
+            p.sym = true;
+            p.A = p.B = xi;
+            p.lda = p.ldb = ldi;
+            p.stride_a = p.stride_b = size_i;
+            p.D = prod;
+            p.ldd = ldp;
+            p.stride_d = size_p;
+            p.out = GEMM_OUT_F16;
+            p.padded = true;
+            p.alpha = kProductScale / (kIterateScale * kIterateScale);
+            if ((st = run_batch(p, dev, cs)) != GEMM_OK)
+                return st;
+            // Q = kProductScale (b P + c P^2)
+            p.K = s;
+            p.maj = 0;
+            p.A = p.B = prod;
+            p.lda = p.ldb = ldp;
+            p.stride_a = p.stride_b = size_p;
+            p.C = prod;
+            p.ldc = ldp;
+            p.stride_c = size_p;
+            p.D = poly;
+            p.alpha = c / kProductScale;
+            p.beta = b;
+            if ((st = run_batch(p, dev, cs)) != GEMM_OK)
+                return st;
+            // X <- a X + Q X (or X Q; Q is symmetric)
+            BatchProduct u{};
+            u.count = n;
+            u.M = M;
+            u.N = N;
+            u.K = s;
+            u.maj = wide ? 2 : 0;
+            u.A = wide ? poly : xi;
+            u.lda = wide ? ldp : ldi;
+            u.stride_a = wide ? size_p : size_i;
+            u.B = wide ? xi : poly;
+            u.ldb = wide ? ldi : ldp;
+            u.stride_b = wide ? size_i : size_p;
+            u.C = xi;
+            u.ldc = ldi;
+            u.stride_c = size_i;
+            u.D = last ? yf : iter[1 - i % 2];
+            u.ldd = last ? ldy : ldi;
+            u.stride_d = last ? stride_y : size_i;
+            u.out = last ? out : GEMM_OUT_F16;
+            u.padded = !last;
+            u.alpha = last ? 1.0f / (kIterateScale * kProductScale) : 1.0f / kProductScale;
+            u.beta = last ? a / kIterateScale : a;
+            if ((st = run_batch(u, dev, cs)) != GEMM_OK)
+                return st;
+        }
+    }
+    return GEMM_OK;
+}

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "launch.h"
@@ -13,6 +14,9 @@
 
 namespace tcg {
 namespace host {
+
+// Most elements of a dimension or pitch.
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 struct DeviceInfo {
     bool ready = false;
@@ -78,6 +82,11 @@ bool encode_2d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint6
                uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapSwizzle swizzle);
 
+// The same for `depth` matrices `stride2_bytes` apart (boxes of one matrix).
+bool encode_3d(CUtensorMap *m, CUtensorMapDataType dtype, const void *ptr, uint64_t inner, uint64_t outer,
+               uint64_t stride_bytes, uint64_t depth, uint64_t stride2_bytes, uint32_t box_inner,
+               uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
 CUtensorMapDataType ab_type(bool bf16);
 int64_t ceil_div(int64_t a, int64_t b);
 gemm_plan make_plan(int64_t M, int64_t N, int64_t K, bool gather, bool c_used, int sm_count,
@@ -102,8 +111,10 @@ gemm_status reset_static_scratch(int device);
 // ones stay allocated, for graphs that hold their address):
 // bf16 weights converted from FP4, block scales copied to a 16-byte row pitch
 // for TMA (B's for gemm_bf16_e2m1; A's and B's for gemm_e2m1, and Bu's for
-// gemm_gated_e2m1), and the parts of sums (kBufParts and the one after it).
-enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4, kBufParts = 5 };
+// gemm_gated_e2m1), the parts of sums (kBufParts and the one after it), gemm_orthogonalize's
+// iterates and gemm_group_rows' counts.
+enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4, kBufParts = 5,
+       kBufOrthogonalize = 7, kBufGroupRows = 8 };
 gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t bytes, void **out);
 
 // To be held from get_dequant_buffer to the last launch that reads the buffer, where a
@@ -119,6 +130,73 @@ bool aligned16(const void *p);
 uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esize);
 bool overlap(const void *a, uint64_t an, const void *b, uint64_t bn);
 int out_size(int out);
+
+// ---- checks of the entry points in api_gated.cu and api_group.cu
+
+struct Span {
+    const void *p;
+    uint64_t bytes;
+};
+
+// Whether any of the outputs overlaps an input or another output.
+inline bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (overlap(o->p, o->bytes, i.p, i.bytes))
+                return true;
+        for (const Span *q = o + 1; q != outs.end(); ++q)
+            if (overlap(o->p, o->bytes, q->p, q->bytes))
+                return true;
+    }
+    return false;
+}
+
+inline bool out_ok(int out) { return out == GEMM_OUT_F32 || out == GEMM_OUT_BF16 || out == GEMM_OUT_F16; }
+inline bool act_ok(int act) { return act >= GEMM_ACT_SILU && act <= GEMM_ACT_SIGMOID; }
+inline bool elem_aligned(const void *p, int size)
+{
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(size - 1)) == 0;
+}
+
+// A matrix argument: pointer, leading dimension, rows and columns of `esize`-byte
+// elements; `mma`: it is a TMA operand (16-byte base and pitch).
+struct Mat {
+    const void *p;
+    int64_t ld;
+    int64_t rows, cols;
+    int esize;
+    bool mma;
+};
+
+inline gemm_status check_mats(std::initializer_list<Mat> mats)
+{
+    for (const Mat &m : mats)
+        if (m.rows > 0 && m.cols > 0 && (!m.p || m.ld < m.cols))
+            return GEMM_ERR_INVALID_ARG;
+    for (const Mat &m : mats)
+        if (m.ld > kMaxDim)
+            return GEMM_ERR_UNSUPPORTED;
+    for (const Mat &m : mats)
+        if (m.rows > 0 && m.cols > 0 &&
+            (m.mma ? !aligned16(m.p) || (m.ld * m.esize) % 16 != 0 : !elem_aligned(m.p, m.esize)))
+            return GEMM_ERR_ALIGNMENT;
+    return GEMM_OK;
+}
+
+inline Span span_of(const Mat &m) { return Span{m.p, span_bytes(m.rows, m.cols, m.ld, m.esize)}; }
+
+inline CUtensorMapDataType out_type(int out)
+{
+    return out == GEMM_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                               : (out == GEMM_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+}
+
+inline bool out_tma(const void *p, int64_t ld, int out, int64_t cols)
+{
+    return aligned16(p) && (ld * out_size(out)) % 16 == 0 && cols * out_size(out) >= 16;
+}
 
 // Any problem of the A * B^T entry points: validate, choose a kernel, launch.
 gemm_status run(const Problem &p);

@@ -1,0 +1,757 @@
+// kernel_group.cuh -- persistent warp-specialised tcgen05 products over groups.
+//
+//   KIND_ROWS   D[i] = alpha A[i] B_g^T for the rows i of group g: the rows of A and D
+//               are grouped by offsets that only the device knows, B is a stack.
+//               Tiles are cut group by group: a group of r rows has ceil(r / TILE_M)
+//               block rows, so a tile never mixes groups.  Its boxes of A may reach
+//               into the next group's rows (loaded, multiplied, never stored).
+//   KIND_SUM    D_g = alpha A_g^T B_g over the rows of group g (both operands stored
+//               with the sum's index outermost): every group has the same tiles, and
+//               its own number of K blocks.  The last block of a group ends inside a
+//               box, whose other rows belong to the next group and may hold anything
+//               (also NaN): a warp of its own zeroes them in shared memory before the
+//               MMAs read the stage.
+//   KIND_BATCH  D_g = alpha A_g B_g^T + beta C_g for a stack of equal sizes, in either
+//               storage, C in 16 bits.  SYM: D_g is known to be symmetric (A A^T, or
+//               the square of a symmetric matrix): only the tiles that reach the
+//               diagonal or lie below it are computed, and each is stored twice.
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), warps 2-5
+// epilogue, (KIND_SUM) warp 6 zeroes.  Two TMEM accumulators: the epilogue of one tile
+// runs beside the next tile's MMAs.  PAIR: the roles on a CTA pair and one 256 x 256 tile
+// (tcgen05 cta_group::2), each CTA loading its 128 rows of A and its half of B.  The
+// protocol is the tile kernel's (kernel_tile.cuh).  Every wait is bounded.
+//
+// Why tiles from device offsets and not from a list: a list is a second kernel before
+// every call.  Each warp that needs coordinates reads the offsets (at most 1024 groups,
+// 4 KB) once, keeps a prefix sum of block rows in its lanes, and finds a tile's group with
+// two ballots where it is not the last one's.
+#pragma once
+
+#include "common.cuh"
+
+namespace tcg {
+
+enum : int { kKindRows = 0, kKindSum = 1, kKindBatch = 2 };
+
+struct GroupMaps {
+    CUtensorMap a, b, d;  // 3-D (inner, rows, group); a is 2-D rows of a table when gathered
+};
+
+struct GroupArgs {
+    int32_t groups;
+    const int32_t *offsets;  // groups + 1 row numbers (KIND_ROWS, KIND_SUM)
+    int32_t rows;            // rows the offsets may name (of A and D, or the sum's)
+    int32_t M, N, K;         // of one group's product (KIND_ROWS: M unused; KIND_SUM: K unused)
+    int32_t num_m_blocks, num_n_blocks;
+    int32_t group_m;         // tile order: block rows visited side by side
+    float alpha, beta;
+    int32_t out_kind, ab_bf16;
+    const int32_t *idx;      // KIND_ROWS: row i of A is row idx[i] of a table (NULL: row i)
+    int32_t table_rows;
+    int32_t d_tma;           // D goes out through TMA where a box is whole
+    int32_t d_vec;           // D's rows are whole 16 bytes apart, its base 16-byte aligned
+    void *D;
+    int64_t ldd, stride_d;   // elements between rows, and between groups
+    int32_t n_out;           // columns of D that may be written (N, or a workspace's padding too)
+    const uint16_t *C;       // KIND_BATCH: f16, 16-byte aligned rows (NULL: none)
+    int64_t ldc, stride_c;
+    int32_t loads;           // there is something to multiply (K > 0; KIND_SUM: rows > 0)
+    uint32_t extra_tx;
+    uint32_t *status;
+    uint64_t timeout_ns;
+};
+
+template <int BN_, int STAGES_, bool PAIR_, int KIND_>
+struct GroupCfg {
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_;
+    static constexpr int TILE_M = PAIR ? 256 : 128;
+    static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;
+    static constexpr uint32_t A_BYTES = BM * 128u, B_BYTES = BN_LOCAL * 128u;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr uint32_t OFF_A = 0, OFF_B = STAGES * A_BYTES;
+    static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes, two a warp
+    static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_EPI + 8 * EPI_BUF;
+    static constexpr uint32_t NUM_BARS = 3 * STAGES + 4;
+    static constexpr uint32_t SMEM_ALLOC = OFF_BAR + NUM_BARS * 8 + 16 + 1024;
+    static constexpr int THREADS = 32 * (KIND_ == kKindSum ? 7 : 6);
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+    static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
+    static_assert(!PAIR || BN == 256, "pairs: 256 x 256");
+};
+
+// The groups' rows, as one warp knows them.  Lane l keeps the block rows of groups l per
+// .. l per + per - 1.
+template <int TILE_M>
+struct GroupRows {
+    const int32_t *off;
+    int32_t groups, rows, per;
+    int32_t first, mine;  // block rows before this lane's groups, and of them
+    int32_t total;        // block rows of all groups (0 where the offsets are not valid)
+    bool ok;
+    // the group found last: its rows, its first block row and their number
+    int32_t g_last, lo_last, hi_last, base_last, blocks_last;
+
+    // (L2: the offsets may be the work of the kernel before, beside which this one began)
+    __device__ __forceinline__ int32_t at(int32_t g) const { return __ldcg(off + g); }
+
+    // (whole warp; offsets that fall, or leave [0, rows], make every group empty)
+    __device__ __forceinline__ void init(const int32_t *offsets, int32_t n, int32_t limit, uint32_t lane)
+    {
+        off = offsets;
+        groups = n;
+        rows = limit;
+        per = (n + 31) / 32;
+        mine = 0;
+        bool good = true;
+        const int32_t g0 = static_cast<int32_t>(lane) * per;
+        for (int32_t g = g0; g < min(g0 + per, n); ++g) {
+            const int32_t lo = at(g), hi = at(g + 1);
+            good = good && lo >= 0 && lo <= hi && hi <= limit;
+            mine += good ? (hi - lo + TILE_M - 1) / TILE_M : 0;
+        }
+        ok = __all_sync(0xffffffffu, good);
+        int32_t sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, sum, d);
+            if (static_cast<int>(lane) >= d)
+                sum += x;
+        }
+        first = sum - mine;
+        total = ok ? __shfl_sync(0xffffffffu, sum, 31) : 0;
+        base_last = blocks_last = 0;
+        g_last = -1;
+    }
+
+    // rows [lo_last, hi_last) of group g
+    __device__ __forceinline__ void load(int32_t g)
+    {
+        if (g == g_last)
+            return;
+        g_last = g;
+        lo_last = ok ? at(g) : 0;
+        hi_last = ok ? at(g + 1) : 0;
+    }
+
+    // (whole warp) the group of block row q < total
+    __device__ __forceinline__ void find(int32_t q, uint32_t lane)
+    {
+        if (q >= base_last && q < base_last + blocks_last)
+            return;
+        const int chunk = __ffs(__ballot_sync(0xffffffffu, q >= first && q < first + mine)) - 1;
+        const int32_t g = chunk * per + static_cast<int32_t>(lane);
+        int32_t l = 0, h = 0;
+        if (static_cast<int32_t>(lane) < per && g < groups) {
+            l = at(g);
+            h = at(g + 1);
+        }
+        const int32_t blocks = (h - l + TILE_M - 1) / TILE_M;
+        int32_t sum = blocks;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, sum, d);
+            if (static_cast<int>(lane) >= d)
+                sum += x;
+        }
+        const int32_t start = __shfl_sync(0xffffffffu, first, chunk) + sum - blocks;
+        const int who = __ffs(__ballot_sync(0xffffffffu, q >= start && q < start + blocks)) - 1;
+        g_last = chunk * per + who;
+        lo_last = __shfl_sync(0xffffffffu, l, who);
+        hi_last = __shfl_sync(0xffffffffu, h, who);
+        base_last = __shfl_sync(0xffffffffu, start, who);
+        blocks_last = __shfl_sync(0xffffffffu, blocks, who);
+    }
+};
+
+// One tile's place.
+struct GroupTile {
+    int32_t g;          // group
+    int32_t row0, end;  // its first row (PAIR: of the pair's tile) and the end of the rows it may store
+    int32_t n0;         // first column
+    int32_t k0;         // KIND_SUM: first row of the sum
+    bool mirror;        // SYM: below the diagonal, stored a second time
+};
+
+__device__ __forceinline__ int32_t swz128(uint32_t row, uint32_t chunk)
+{
+    return static_cast<int32_t>(row * 128u + ((chunk ^ (row & 7u)) << 4));
+}
+
+// Rows [0, nrows) of a 32 x 128-byte image to D at (row0, col0), columns below N: pieces of 16
+// bytes (four rows by eight pieces a pass, each row's 128 bytes together) where D has
+// them, single elements otherwise.
+__device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, int32_t nrows, uint32_t esize,
+                                                 void *D, int64_t ldd, int32_t row0, int32_t col0, int32_t N,
+                                                 bool vec)
+{
+    const uint32_t chunk = lane % 8u;
+    const int32_t per = static_cast<int32_t>(16u / esize);
+    const int32_t col = col0 + static_cast<int32_t>(chunk) * per;
+    for (int32_t r = static_cast<int32_t>(lane / 8u); r < nrows; r += 4) {
+        uint32_t w[4];
+        ld_shared_v4(buf + swz128(r, chunk), w[0], w[1], w[2], w[3]);
+        uint8_t *p = static_cast<uint8_t *>(D) + ((static_cast<int64_t>(row0) + r) * ldd + col) * esize;
+        if (vec && col + per <= N) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (esize == 4u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < N)
+                    reinterpret_cast<uint32_t *>(p)[i] = w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < N)
+                    reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM>
+__global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
+    group_gemm_kernel(const __grid_constant__ GroupMaps maps, const GroupArgs args)
+{
+    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND>;
+    constexpr bool kRows = KIND == kKindRows, kSum = KIND == kKindSum, kBatch = KIND == kKindBatch;
+    constexpr bool kMnA = (MAJ & 1) != 0, kMnB = (MAJ & 2) != 0;
+    constexpr int TM = Cfg::TILE_M;
+    static_assert(!SYM || kBatch, "symmetric results: equal sizes");
+    static_assert(!kSum || MAJ == 3, "a sum over rows: both operands stored with them outermost");
+    static_assert(!kRows || !kMnA, "grouped rows are stored row by row");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+
+    const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x / 32u, 0);
+    const uint32_t lane = threadIdx.x % 32u;
+
+    const uint32_t bar0 = base + Cfg::OFF_BAR;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    // (KIND_SUM) the boxes of a group's last, partial block have landed in this CTA
+    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 8 * Cfg::NUM_BARS);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+
+    const uint32_t role = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = role == 0u;
+    const int32_t cta_set = static_cast<int32_t>(blockIdx.x) / (PAIR ? 2 : 1);
+    const int32_t cta_sets = static_cast<int32_t>(gridDim.x) / (PAIR ? 2 : 1);
+    auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0u) : bar; };
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            // (KIND_SUM on pairs: two arrivals, since a partial block is handed over by both
+            // CTAs' zeroing warps; the leader's producer arrives twice for a whole one)
+            mbar_init(full_bar(s), kSum && PAIR ? 2 : 1);
+            mbar_init(empty_bar(s), 1);
+            mbar_init(tail_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), PAIR ? 8 : 4);
+        }
+        *abort_flag = 0u;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        if (args.loads) {
+            tma_prefetch_desc(&maps.a);
+            tma_prefetch_desc(&maps.b);
+        }
+        if (args.d_tma)
+            tma_prefetch_desc(&maps.d);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    grid_dependency_wait();
+    tc_fence_before_sync();
+    if (PAIR)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    if (threadIdx.x == 0)
+        grid_launch_dependents();
+
+    // ---- the tiles, as each warp finds them
+    GroupRows<TM> gr;
+    int32_t num_tiles;
+    if constexpr (kBatch) {
+        const int32_t per = SYM ? (TM / BN) * (args.num_m_blocks * (args.num_m_blocks + 1) / 2)
+                                : args.num_m_blocks * args.num_n_blocks;
+        num_tiles = args.groups * per;
+    } else {
+        gr.init(args.offsets, args.groups, args.rows, lane);
+        if (!gr.ok && blockIdx.x == 0 && threadIdx.x == 0)
+            record_error(args.status, kStatusIndex, 0);
+        if constexpr (kRows)
+            num_tiles = gr.total * args.num_n_blocks;
+        else
+            num_tiles = args.groups * args.num_m_blocks * args.num_n_blocks;
+    }
+    // (KIND_ROWS: by the whole warp)
+    auto locate = [&](int32_t t) {
+        GroupTile p{};
+        int32_t blocks = args.num_m_blocks, r = t;
+        if constexpr (kRows) {
+            gr.find(t / args.num_n_blocks, lane);
+            p.g = gr.g_last;
+            blocks = gr.blocks_last;
+            r = t - gr.base_last * args.num_n_blocks;
+            p.row0 = gr.lo_last;
+            p.end = gr.hi_last;
+        } else if constexpr (SYM) {
+            // block row mb of a matrix has the TM / BN (mb + 1) tiles up to the diagonal
+            constexpr int32_t q = TM / BN;
+            const int32_t per = q * (blocks * (blocks + 1) / 2);
+            p.g = t / per;
+            r = t - p.g * per;
+            const int32_t u = r / q;
+            int32_t mb = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(u) + 1.0f) - 1.0f) * 0.5f);
+            while (mb * (mb + 1) / 2 > u)
+                --mb;
+            while ((mb + 1) * (mb + 2) / 2 <= u)
+                ++mb;
+            const int32_t nb = r - q * (mb * (mb + 1) / 2);
+            p.row0 = mb * TM;
+            p.n0 = nb * BN;
+            p.end = args.M;
+            p.mirror = nb / q != mb;
+            return p;
+        } else {
+            const int32_t per = blocks * args.num_n_blocks;
+            p.g = t / per;
+            r = t - p.g * per;
+            p.end = args.M;
+            if constexpr (kSum) {
+                gr.load(p.g);
+                p.k0 = gr.lo_last;
+            }
+        }
+        const int32_t per_super = args.group_m * args.num_n_blocks;
+        const int32_t first_m = r / per_super * args.group_m;
+        const int32_t rows = min(blocks - first_m, args.group_m);
+        const int32_t rr = r % per_super;
+        p.row0 += (first_m + rr % rows) * TM;
+        p.n0 = rr / rows * BN;
+        return p;
+    };
+    const int32_t k_blocks = (args.K + Cfg::BK - 1) / Cfg::BK;
+    // K blocks of tile t (KIND_SUM: of its group)
+    auto blocks_of = [&](int32_t t, int32_t &rem) -> int32_t {
+        rem = 0;
+        if constexpr (kSum) {
+            gr.load(t / (args.num_m_blocks * args.num_n_blocks));
+            const int32_t n = gr.hi_last - gr.lo_last;
+            rem = n % Cfg::BK;
+            return (n + Cfg::BK - 1) / Cfg::BK;
+        }
+        return k_blocks;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        int s = 0;
+        uint32_t ph = 0;
+        int pending = 0;
+        [[maybe_unused]] uint32_t tails = 0, tail_ph = 0;  // (bit per stage) last use partial; parity of tail_bar
+        bool first = true, alive = true;
+        for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
+            const GroupTile p = locate(t);
+            int32_t rem;
+            const int32_t nkb = blocks_of(t, rem);
+            const int32_t m0 = p.row0 + static_cast<int32_t>(role) * Cfg::BM;
+            const int32_t n0 = p.n0 + static_cast<int32_t>(role) * Cfg::BN_LOCAL;
+            const int32_t ga = kBatch ? p.g : 0, gb = kSum ? 0 : p.g;
+            int32_t rows[4] = {0, 0, 0, 0};
+            if (kRows && args.idx) {
+                // lane l fetches rows 4 l .. 4 l + 3, four per gather4; rows past the group's,
+                // and those whose index is not a row of the table, fetch row 0
+                for (int r = 0; r < 4; ++r) {
+                    const int32_t m = m0 + 4 * static_cast<int32_t>(lane) + r;
+                    const int32_t v = m < p.end ? __ldcg(args.idx + m) : 0;
+                    if (v < 0 || v >= args.table_rows)
+                        record_error(args.status, kStatusIndex, 0);
+                    else
+                        rows[r] = v;
+                }
+            }
+            for (int32_t kb = 0; kb < nkb; ++kb) {
+                if (!warp_wait_bounded<true>(empty_bar(s), ph ^ 1u, abort_flag, args.status, args.timeout_ns,
+                                             kWhereProducerEmpty)) {
+                    alive = false;
+                    break;
+                }
+                const bool part = kSum && rem != 0 && kb == nkb - 1;
+                const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES;
+                const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES;
+                const int32_t k = p.k0 + kb * Cfg::BK;
+                if (lane == 0) {
+                    const uint32_t extra = first ? args.extra_tx : 0u;
+                    if (part) {
+                        mbar_arrive_expect_tx(tail_bar(s), Cfg::STAGE_BYTES + extra);
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(full_bar(s), (PAIR ? 2u : 1u) * Cfg::STAGE_BYTES + extra);
+                        if (kSum && PAIR)
+                            mbar_arrive(full_bar(s));
+                    }
+                }
+                first = false;
+                __syncwarp();
+                // (a partial block is counted in this CTA, whose zeroing warp waits for it)
+                const uint32_t bar = part ? tail_bar(s) : lead(full_bar(s));
+                auto load = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
+                    if (PAIR && !part)
+                        tma_load_3d_pair(dst, m, bar, x, y, z);
+                    else
+                        tma_load_3d(dst, m, bar, x, y, z);
+                };
+                if (kRows && args.idx) {
+                    if (PAIR)
+                        tma_gather4_pair(sa + lane * 512u, &maps.a, bar, k, rows[0], rows[1], rows[2], rows[3]);
+                    else
+                        tma_gather4(sa + lane * 512u, &maps.a, bar, k, rows[0], rows[1], rows[2], rows[3]);
+                } else if (lane == 0) {
+                    if constexpr (kMnA) {
+                        for (int j = 0; j < Cfg::BM / 64; ++j)
+                            load(sa + j * 8192u, &maps.a, m0 + 64 * j, k, ga);
+                    } else {
+                        load(sa, &maps.a, k, m0, ga);
+                    }
+                }
+                if (lane == 0) {
+                    if constexpr (kMnB) {
+                        for (int j = 0; j < Cfg::BN_LOCAL / 64; ++j)
+                            load(sb + j * 8192u, &maps.b, n0 + 64 * j, k, gb);
+                    } else {
+                        load(sb, &maps.b, k, n0, gb);
+                    }
+                }
+                if constexpr (kSum)
+                    tails = part ? tails | (1u << s) : tails & ~(1u << s);
+                if (part)
+                    tail_ph ^= 1u << s;
+                pending = min(pending + 1, STAGES);
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!alive) {
+            // every copy issued lands before the shared memory is released (bounded; the
+            // leader's barriers count both CTAs' bytes)
+            int ds = s;
+            uint32_t dph = ph;
+            for (int i = 0; i < pending; ++i) {
+                if (--ds < 0) {
+                    ds = STAGES - 1;
+                    dph ^= 1u;
+                }
+                if ((tails >> ds) & 1u)
+                    wait_drain(tail_bar(ds), ((tail_ph >> ds) & 1u) ^ 1u, 10000000ull);
+                else if (leader)
+                    wait_drain(full_bar(ds), dph, 10000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && leader) {
+            const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, TM, BN, kMnA, kMnB);
+            int s = 0, ab = 0;
+            uint32_t ph = 0, aph = 0;
+            bool alive = true;
+            auto commit_to = [&](uint32_t bar) {
+                if (PAIR)
+                    tc_commit_pair_multicast(bar, 3);
+                else
+                    tc_commit(bar);
+            };
+            for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
+                int32_t rem;
+                const int32_t nkb = blocks_of(t, rem);
+                if (!wait_bounded<true>(acce_bar(ab), aph ^ 1u, abort_flag, args.status, args.timeout_ns,
+                                        kWhereMmaAccEmpty))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
+                for (int32_t kb = 0; kb < nkb; ++kb) {
+                    const bool part = kSum && rem != 0 && kb == nkb - 1;
+                    // (the peer's zeros: an acquire at cluster scope)
+                    const bool got =
+                        PAIR && part
+                            ? wait_bounded_cluster(full_bar(s), ph, abort_flag, args.status, args.timeout_ns,
+                                                   kWhereMmaFull)
+                            : wait_bounded<true>(full_bar(s), ph, abort_flag, args.status, args.timeout_ns,
+                                                 kWhereMmaFull);
+                    if (!got) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES;
+                    const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES;
+                    const uint64_t ad = kMnA ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+                    const uint64_t bd = kMnB ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
+                    constexpr uint32_t kStepA = kMnA ? 128u : 2u, kStepB = kMnB ? 128u : 2u;
+                    // (of a partial block only the K steps that hold rows of the group)
+                    const int steps = part ? (rem + 15) / 16 : 4;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k < steps) {
+                            const uint32_t acc = (kb | k) != 0 ? 1u : 0u;
+                            if (PAIR)
+                                tc_mma_f16_pair(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
+                            else
+                                tc_mma_f16(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
+                        }
+                    }
+                    commit_to(empty_bar(s));
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!alive)
+                    break;
+                commit_to(accf_bar(ab));
+                if (++ab == 2) {
+                    ab = 0;
+                    aph ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (kSum && warp == 6) {
+        // ------------------------------------------------------------ zeroing warp
+        if constexpr (kSum) {
+            int s = 0;
+            uint32_t tail_ph = 0;
+            for (int32_t t = cta_set; t < num_tiles; t += cta_sets) {
+                int32_t rem;
+                const int32_t nkb = blocks_of(t, rem);
+                if (rem != 0) {
+                    const int at = (s + nkb - 1) % STAGES;
+                    if (!warp_wait_bounded(tail_bar(at), (tail_ph >> at) & 1u, abort_flag, args.status,
+                                           args.timeout_ns, kWhereMmaFull))
+                        break;
+                    tail_ph ^= 1u << at;
+                    // rows [rem, next multiple of 16) of every box: 64 columns are one row's 128
+                    // bytes, so the swizzle does not matter
+                    const uint32_t sa = base + Cfg::OFF_A + at * Cfg::A_BYTES;
+                    const uint32_t sb = base + Cfg::OFF_B + at * Cfg::B_BYTES;
+                    const int32_t more = (rem + 15) / 16 * 16 - rem;
+                    constexpr int32_t kBoxesA = Cfg::BM / 64, kBoxes = kBoxesA + Cfg::BN_LOCAL / 64;
+                    for (int32_t i = static_cast<int32_t>(lane); i < more * 8; i += 32) {
+                        const uint32_t o = static_cast<uint32_t>(rem * 128 + i * 16);
+#pragma unroll
+                        for (int j = 0; j < kBoxes; ++j)
+                            st_shared_v4((j < kBoxesA ? sa + 8192u * j : sb + 8192u * (j - kBoxesA)) + o, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR)
+                            mbar_arrive_cluster(lead(full_bar(at)));
+                        else
+                            mbar_arrive(full_bar(at));
+                    }
+                }
+                s = (s + nkb) % STAGES;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const uint32_t q = warp & 3u;
+        const uint32_t buf0 = base + Cfg::OFF_EPI + q * 2u * Cfg::EPI_BUF;
+        const bool f32 = args.out_kind == kOutF32;
+        const uint32_t esize = f32 ? 4u : 2u;
+        const int32_t wide = f32 ? 32 : 64;  // columns of a 128-byte row
+        // TMA stores whole 16 bytes of a row: D's descriptor ends with the last whole ones
+        const int32_t n_tma = args.n_out & ~(f32 ? 3 : 7);
+        const uint64_t policy = l2_policy_evict_first();
+        int ab = 0;
+        uint32_t aph = 0, slot = 0;
+        for (int32_t t = cta_set; t < num_tiles; t += cta_sets) {
+            const GroupTile p = locate(t);
+            int32_t rem;
+            const int32_t nkb = blocks_of(t, rem);
+            const int32_t row0 = p.row0 + static_cast<int32_t>(role) * Cfg::BM + 32 * static_cast<int32_t>(q);
+            const int32_t nrows = min(32, p.end - row0);
+            const int32_t my_row = row0 + static_cast<int32_t>(lane);
+            bool zero = nkb == 0;
+            if (kRows && args.idx && my_row < p.end) {
+                const int32_t v = __ldcg(args.idx + my_row);
+                zero = zero || v < 0 || v >= args.table_rows;
+            }
+            // (SYM: the second half of a matrix's last diagonal block may lie past its end)
+            const int32_t chunks = max(1, min(BN / wide, (args.N - p.n0 + wide - 1) / wide));
+            uint8_t *d_g = static_cast<uint8_t *>(args.D) + (kRows ? 0 : p.g * args.stride_d * esize);
+            const uint16_t *c_row = nullptr;
+            if (kBatch && args.C && my_row < p.end)
+                c_row = args.C + p.g * args.stride_c + static_cast<int64_t>(my_row) * args.ldc + p.n0;
+            if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                         kWhereEpiAccFull))
+                break;
+            tc_fence_after_sync();
+            const uint32_t acc0 = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN);
+            // 32 columns from col of this lane's row: alpha acc + beta C
+            auto take = [&](int32_t col, float(&v)[32]) {
+                uint32_t r[32];
+                tc_ld_32x32b_x32(acc0 + static_cast<uint32_t>(col), r);
+                if (kBatch && args.C) {
+                    uint4 c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = c_row && p.n0 + col + 8 * i < args.N
+                                   ? *reinterpret_cast<const uint4 *>(c_row + col + 8 * i)
+                                   : make_uint4(0, 0, 0, 0);
+                    tc_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t w = reinterpret_cast<const uint32_t *>(c)[i / 2];
+                        const float x = cvt_f16_f32(static_cast<uint16_t>(w >> (16 * (i & 1))));
+                        v[i] = fma_rn(args.alpha, __uint_as_float(r[i]), mul_rn(args.beta, x));
+                    }
+                } else {
+                    tc_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = zero ? 0.f : mul_rn(args.alpha, __uint_as_float(r[i]));
+                }
+            };
+            auto pack2 = [&](float a, float b) {
+                return args.out_kind == kOutBF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+            };
+            // columns col .. col + 31 of the tile, a second time: D[column][row], two columns of
+            // D's row from a lane and its neighbour, two rows of D per pair of columns
+            auto mirror = [&](int32_t col, const float(&v)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const bool odd = (lane & 1u) != 0u;
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                    const uint32_t w = odd ? pack2(other, v[i + 1]) : pack2(v[i], other);
+                    const int32_t r = p.n0 + col + i + (odd ? 1 : 0);
+                    const int32_t c = my_row & ~1;
+                    // (an odd size: the last pair's second element goes into the row's padding)
+                    if (r < args.N && c < p.end)
+                        *reinterpret_cast<uint32_t *>(d_g + (static_cast<int64_t>(r) * args.ldd + c) * 2) = w;
+                }
+            };
+            for (int32_t c = 0; c < chunks; ++c) {
+                const int32_t col = c * wide;
+                uint32_t w[32];
+                {
+                    float v[32];
+                    take(col, v);
+                    if (SYM && p.mirror)
+                        mirror(col, v);
+                    if (f32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = __float_as_uint(v[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    }
+                }
+                if (!f32) {
+                    float v[32];
+                    take(col + 32, v);
+                    if (SYM && p.mirror)
+                        mirror(col + 32, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[16 + i] = pack2(v[2 * i], v[2 * i + 1]);
+                }
+                if (c == chunks - 1) {
+                    // the accumulator is read: hand it back
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR && !leader)
+                            mbar_arrive_cluster(lead(acce_bar(ab)));
+                        else
+                            mbar_arrive(acce_bar(ab));
+                    }
+                }
+                const int32_t col0 = p.n0 + col;
+                if (nrows <= 0 || col0 >= args.N)
+                    continue;
+                const uint32_t buf = buf0 + slot * Cfg::EPI_BUF;
+                slot ^= 1u;
+                if (lane == 0)
+                    bulk_wait_group_read<1>();  // the store before the last has left this buffer
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_shared_v4(buf + swz128(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                // a whole box by TMA; rows that end with the group (KIND_ROWS; the others' boxes
+                // end with their matrix), or columns past the last whole 16 bytes, by plain stores
+                const bool tma = args.d_tma && (!kRows || nrows == 32) && (col0 + wide <= n_tma || n_tma == args.n_out);
+                if (tma) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kBatch)  // (read by the next product)
+                            tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                        else
+                            tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.g, policy);
+                    }
+                } else {
+                    __syncwarp();
+                    store_image_rows(buf, lane, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
+                    __syncwarp();
+                }
+                if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
+                    bulk_commit_group();
+            }
+            if (++ab == 2) {
+                ab = 0;
+                aph ^= 1u;
+            }
+        }
+        if (lane == 0)
+            bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    tc_fence_before_sync();
+    if (PAIR) {
+        if (threadIdx.x == 0 && *abort_flag)
+            st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(abort_flag)), role ^ 1u), 1u);
+        if (*abort_flag && !leader) {
+            // copies that report to the leader's barriers get time to land here too
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 100000ull) {
+            }
+        }
+        cluster_sync_all();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace tcg

@@ -1,0 +1,39 @@
+// launch_group.h -- host-side interface between the entry points for groups
+// (api_group.cu) and their kernels' launchers.
+#pragma once
+
+#include "kernel_group.cuh"
+#include "launch.h"
+
+namespace tcg {
+
+// A form of the group kernel: single CTAs with 128 x bn tiles (bn 64, 128, 256), or
+// (pair) CTA pairs with 256 x 256 ones.  maj: bit 0 A stored with K outermost, bit 1 B.
+// grid counts CTAs.
+cudaError_t launch_group_rows(int bn, bool pair, bool b_major, const GroupMaps &maps, const GroupArgs &args,
+                              int grid, cudaStream_t stream);
+cudaError_t launch_group_sum(int bn, bool pair, const GroupMaps &maps, const GroupArgs &args, int grid,
+                             cudaStream_t stream);
+// (symmetric results: maj 0 or 3, bn 128 or pairs; others: maj 0 or 2)
+cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, const GroupMaps &maps,
+                               const GroupArgs &args, int grid, cudaStream_t stream);
+
+// The stable order of M ids by value: offsets (groups + 1), order and rows (each M; rows
+// may be NULL: order[i] / choices).  counts: `chunks` x (groups + 1) int32 (unused for one
+// chunk).
+constexpr int64_t kGroupRowsChunk = 16384;  // ids a thread block sorts, where there are several
+constexpr int64_t kGroupRowsOne = 65536;    // up to this many, one does
+cudaError_t launch_group_rows_sort(const int32_t *ids, int64_t M, int32_t groups, int32_t choices,
+                                   int32_t *offsets, int32_t *order, int32_t *rows, int32_t *counts,
+                                   int32_t chunks, cudaStream_t stream);
+
+// Sums of squares of `count` matrices X (M x N of type kOut...), in `parts` parts each, to
+// partial; and Xs = f16(X scale / (sqrt(the parts' sum) + eps)).
+int orthogonalize_parts(int64_t M, int64_t N);
+cudaError_t launch_square_sums(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
+                               int32_t count, float *partial, int parts, cudaStream_t stream);
+cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
+                             int32_t count, const float *partial, int parts, float scale, float eps,
+                             uint16_t *Xs, int64_t lds, int64_t stride_s, cudaStream_t stream);
+
+}  // namespace tcg

@@ -1,0 +1,204 @@
+// orthogonalize.cu -- the elementwise ends of gemm_orthogonalize: the matrices' norms, and
+// the normalised matrices in float16.
+//
+// Both are bound by memory: the first reads X, the second reads it again (mostly from L2
+// where the stack is small) and writes 2 bytes an element.  A thread block takes a part of a
+// matrix's rows; its sum of squares is float32 (each thread's over its own elements, then
+// the block's by shuffles), the parts of a matrix are added in order by every block of the
+// second kernel: no atomics, the same bits every time.
+//
+// The normalised matrix is scaled by a power of two before it is rounded to float16: X / |X|
+// has elements down to 1 / |X|, and float16 keeps its 11 bits only above 2^-14.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch_group.h"
+
+namespace tcg {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxParts = 256;
+
+// Eight elements of a row from column c (those below N), as float32.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void *X, int64_t at, int32_t n, bool vec, float (&v)[8])
+{
+    if (TYPE == kOutF32) {
+        const float *p = static_cast<const float *>(X) + at;
+        if (vec && n >= 8) {
+            const float4 a = __ldcg(reinterpret_cast<const float4 *>(p));
+            const float4 b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = i < n ? __ldcg(p + i) : 0.f;
+        }
+    } else {
+        const unsigned short *p = static_cast<const unsigned short *>(X) + at;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (vec && n >= 8) {
+            const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(p));
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    w[i / 2] |= static_cast<uint32_t>(__ldcg(p + i)) << (16 * (i & 1));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned short h = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
+            v[i] = TYPE == kOutBF16 ? cvt_bf16_f32(h) : cvt_f16_f32(h);
+        }
+    }
+}
+
+__device__ __forceinline__ float block_sum(float x)
+{
+    __shared__ float part[kThreads / 32];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2)
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+    if (threadIdx.x % 32 == 0)
+        part[threadIdx.x / 32] = x;
+    __syncthreads();
+    float s = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i)
+        s += part[i];
+    return s;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads)
+    square_sums_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, bool vec,
+                       float *partial)
+{
+    const int32_t parts = static_cast<int32_t>(gridDim.x), g = static_cast<int32_t>(blockIdx.y);
+    const int64_t per_row = (N + 7) / 8, pieces = per_row * M;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t step = static_cast<int64_t>(parts) * kThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < pieces; i += 4 * step) {
+        float v[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t p = i + j * step;
+            const int64_t r = p / per_row;
+            const int32_t c = static_cast<int32_t>(p - r * per_row) * 8;
+            load8<TYPE>(X, g * stride_x + r * ldx + c, p < pieces ? N - c : 0, vec, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[j] = fmaf(v[j][e], v[j][e], sum[j]);
+    }
+    const float s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (threadIdx.x == 0)
+        partial[static_cast<int64_t>(g) * parts + blockIdx.x] = s;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads)
+    normalize_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, bool vec,
+                     const float *partial, int32_t parts, float scale, float eps, uint16_t *Xs, int64_t lds,
+                     int64_t stride_s)
+{
+    const int32_t g = static_cast<int32_t>(blockIdx.y);
+    const int64_t per_row = (N + 7) / 8, pieces = per_row * M;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float sum = 0.f;
+    for (int32_t i = static_cast<int32_t>(threadIdx.x); i < parts; i += kThreads)
+        sum += __ldcg(partial + static_cast<int64_t>(g) * parts + i);
+    const float f = scale / (sqrtf(block_sum(sum)) + eps);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < pieces; i += 4 * step) {
+        float v[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t p = i + j * step;
+            const int64_t r = p / per_row;
+            const int32_t c = static_cast<int32_t>(p - r * per_row) * 8;
+            load8<TYPE>(X, g * stride_x + r * ldx + c, p < pieces ? N - c : 0, vec, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t p = i + j * step;
+            if (p >= pieces)
+                break;
+            const int64_t r = p / per_row;
+            const int64_t c = (p - r * per_row) * 8;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16x2(v[j][2 * e] * f, v[j][2 * e + 1] * f);
+            // (rows of Xs are whole 16 bytes: the last piece fills the padding)
+            *reinterpret_cast<uint4 *>(Xs + g * stride_s + r * lds + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+bool vec_ok(const void *X, int64_t ldx, int64_t stride_x, int type)
+{
+    const int64_t es = type == kOutF32 ? 4 : 2;
+    return reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * es % 16 == 0 && stride_x * es % 16 == 0;
+}
+
+template <class... P, class... A>
+cudaError_t launch(void (*kfn)(P...), dim3 grid, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = TCG_PDL;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kfn, static_cast<P>(args)...);
+}
+
+unsigned blocks_for(int64_t M, int64_t N, int64_t per_thread)
+{
+    const int64_t pieces = (N + 7) / 8 * M;
+    const int64_t b = (pieces + kThreads * per_thread - 1) / (kThreads * per_thread);
+    return static_cast<unsigned>(b < 1 ? 1 : (b > 2048 ? 2048 : b));
+}
+
+}  // namespace
+
+int orthogonalize_parts(int64_t M, int64_t N)
+{
+    const unsigned b = blocks_for(M, N, 4);
+    return static_cast<int>(b < kMaxParts ? b : kMaxParts);
+}
+
+cudaError_t launch_square_sums(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
+                               int32_t count, float *partial, int parts, cudaStream_t stream)
+{
+    auto k = type == kOutF32    ? square_sums_kernel<kOutF32>
+             : type == kOutBF16 ? square_sums_kernel<kOutBF16>
+                                : square_sums_kernel<kOutF16>;
+    return launch(k, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(count)), stream, X, ldx, stride_x,
+                  M, N, vec_ok(X, ldx, stride_x, type), partial);
+}
+
+cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
+                             int32_t count, const float *partial, int parts, float scale, float eps,
+                             uint16_t *Xs, int64_t lds, int64_t stride_s, cudaStream_t stream)
+{
+    auto k = type == kOutF32    ? normalize_kernel<kOutF32>
+             : type == kOutBF16 ? normalize_kernel<kOutBF16>
+                                : normalize_kernel<kOutF16>;
+    return launch(k, dim3(blocks_for(M, N, 4), static_cast<unsigned>(count)), stream, X, ldx, stride_x, M, N,
+                  vec_ok(X, ldx, stride_x, type), partial, parts, scale, eps, Xs, lds, stride_s);
+}
+
+}  // namespace tcg

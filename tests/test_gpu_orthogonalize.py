@@ -1,0 +1,183 @@
+"""gemm_orthogonalize on the GPU (needs a GB300) against the recurrence in 64 bits.
+
+Bound, in the Frobenius norm |.| (|.|2: the largest singular value): a step from X, with P = X X^T
+over l and Q = b P + c P^2 over s, makes these errors, each f16 rounding at most 2^-11 of its matrix
+(and half a unit of the subnormal range, 2^-25, an element before the scaling by 2^12):
+    eP = (2^-11 + sum(l)) |X|^2 + 2^-23 |P| + s 2^-37
+    eQ = (|b| + 2 |c| (|P|2 + eP)) eP + sum(s) |c| (|P| + eP)^2 + 2^-22 (|b| |P| + |c| |P|2 |P|) + 2^-11 |Q| + s 2^-37
+    eX = eQ |X|2 + sum(s) (|Q| + eQ) |X| + 2^-22 (|a| |X| + |Q| |X|2) + 2^-11 |X'| + sqrt(m n) 2^-37
+and passes an error e of X on as L e, L the largest slope of a x + b x^3 + c x^5 up to the largest
+singular value (and e itself): the divided differences of a function are at most its largest slope.
+sum(K) is gated_ref's bound of a tensor-core sum.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_ref as ref
+from gpu_helpers import device_status
+from tensor_core_gemm_02_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+FORMS = {"auto": (0, 0), "single64": (1, 64), "single128": (1, 128), "pair256": (3, 256)}
+MUON = (3.4445, -4.7750, 2.0315)
+QUINTIC = (1.875, -1.25, 0.375)  # slope at most 1.875: errors stay small over many steps
+EPS = 1e-7
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    binding.gemm_debug_force_tile(0, 0)
+    assert device_status() == binding.GEMM_OK
+    yield
+    binding.gemm_debug_force_tile(0, 0)
+    assert device_status() == binding.GEMM_OK
+
+
+def recurrence(x, coefs, steps, eps, out):
+    """(Y, bound of |error|) of one matrix in 64 bits."""
+    a, b, c = coefs
+    x = x.double().cpu()
+    x = x / (x.norm() + eps)
+    if x.shape[0] > x.shape[1]:
+        x = x.T
+        flip = True
+    else:
+        flip = False
+    s, l = x.shape
+    two = lambda m: torch.linalg.matrix_norm(m, 2).item()  # noqa: E731
+    # the norm: float32 sums of N squares (2^-24 each, pairwise in part: at most the chain of a
+    # thread), the root, the division and a product; then the rounding to f16
+    e = (2.0 ** -11 + 2.0 ** -16) * x.norm().item() + (s * l) ** 0.5 * 2.0 ** -37
+    for i in range(steps):
+        p = x @ x.T
+        q = b * p + c * (p @ p)
+        y = a * x + q @ x
+        X, P, Q, Y = (m.norm().item() for m in (x, p, q, y))
+        X2, P2 = two(x) + e, two(p)
+        grid = np.linspace(0.0, X2, 2001)
+        L = np.abs(a + 3 * b * grid ** 2 + 5 * c * grid ** 4).max() + 1e-3 * (abs(a) + abs(b) + abs(c))
+        eP = (2.0 ** -11 + ref.sum_bound(l)) * X * X + 2.0 ** -23 * P + s * 2.0 ** -37
+        eQ = ((abs(b) + 2 * abs(c) * (P2 + eP)) * eP + ref.sum_bound(s) * abs(c) * (P + eP) ** 2
+              + 2.0 ** -22 * (abs(b) * P + abs(c) * P2 * P) + 2.0 ** -11 * Q + s * 2.0 ** -37)
+        last = HALF[out] if i == steps - 1 else 2.0 ** -11
+        eX = (eQ * X2 + ref.sum_bound(s) * (Q + eQ) * X + 2.0 ** -22 * (abs(a) * X + Q * X2) + last * Y
+              + (s * l) ** 0.5 * (2.0 ** -25 if out == torch.float16 and i == steps - 1 else 2.0 ** -37))
+        e = L * e + eX
+        x = y
+    return (x.T if flip else x), e
+
+
+def stack(count, m, n, dtype, seed, scale=1.0, pad=3):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn((count, m, n), generator=gen) + 3 * torch.randn((count, m, 1), generator=gen) * torch.randn((count, 1, n), generator=gen)
+    buf = torch.full((count, m + 1, n + pad), float("nan"))
+    buf[:, :m, :n] = x * scale
+    return buf.to(dtype).cuda()[:, :m, :n]
+
+
+def check(X, coefs, steps, out=None, eps=EPS, Y=None):
+    out = X.dtype if out is None else out
+    if Y is None:
+        Y = torch.empty(X.shape, dtype=out, device="cuda")
+    inputs = X.clone()
+    binding.gemm_orthogonalize(X, Y, steps=steps, coefs=coefs, eps=eps)
+    for i in range(X.shape[0]):
+        want, bound = recurrence(inputs[i], coefs, steps, eps, out)
+        err = (Y[i].cpu().double() - want).norm().item()
+        assert err <= bound, (tuple(X.shape), X.dtype, out, coefs, steps, i, err, bound)
+    return Y
+
+
+SIZES = [(1, 1, 1), (1, 1, 40), (2, 40, 1), (3, 64, 64), (2, 65, 130), (2, 130, 63), (1, 129, 257), (1, 300, 200),
+         (2, 200, 520), (1, 513, 515)]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("count,m,n", SIZES)
+def test_one_step(form, count, m, n):
+    binding.gemm_debug_force_tile(*FORMS[form])
+    for dtype, out in ((torch.float32, torch.float32), (torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)):
+        check(stack(count, m, n, dtype, m + n), MUON, 1, out)
+
+
+@pytest.mark.parametrize("count,m,n", [(2, 64, 200), (1, 200, 64), (2, 130, 257), (1, 600, 520), (1, 1000, 1367)])
+def test_five_steps(count, m, n):
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        check(stack(count, m, n, dtype, m), QUINTIC, 5)
+        check(stack(count, m, n, dtype, m), MUON, 2)
+    check(stack(count, m, n, torch.float32, m), MUON, 5)
+
+
+def test_singular_values_reach_one():
+    """Ten steps of the convergent polynomial on a matrix of singular values between 0.1 and 1 leave
+    an orthogonal matrix: every step moves s towards 1, and 10 of them past 1 - 2^-11."""
+    gen = torch.Generator().manual_seed(0)
+    u, _ = torch.linalg.qr(torch.randn(96, 96, generator=gen, dtype=torch.float64))
+    v, _ = torch.linalg.qr(torch.randn(200, 96, generator=gen, dtype=torch.float64))
+    x = (u * torch.linspace(0.1, 1.0, 96, dtype=torch.float64)) @ v.T
+    y = binding.gemm_orthogonalize(x.float().cuda(), steps=14, coefs=QUINTIC).cpu().double()
+    exact = x.float().double()
+    exact = exact / (exact.norm() + EPS)
+    for _ in range(14):
+        p = exact @ exact.T
+        exact = QUINTIC[0] * exact + (QUINTIC[1] * p + QUINTIC[2] * (p @ p)) @ exact
+    assert (torch.linalg.svdvals(exact) - 1).abs().max() < 2.0 ** -11
+    # the steps' own errors are of the order of f16's rounding, and the polynomial's slope at 1 is 0
+    assert (torch.linalg.svdvals(y) - 1).abs().max() < 16 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("scale", [1e-12, 1e-3, 1.0, 1e6])
+def test_scales(scale):
+    """The norm is divided out: small and large matrices alike."""
+    check(stack(2, 70, 150, torch.float32, 1, scale), MUON, 1, eps=0.0)
+    check(stack(2, 150, 70, torch.bfloat16, 1, scale), QUINTIC, 2, eps=0.0)
+
+
+def test_in_place_and_strided():
+    X = stack(3, 90, 70, torch.bfloat16, 4)
+    want = binding.gemm_orthogonalize(X, steps=3)
+    Y = stack(3, 90, 70, torch.bfloat16, 5, pad=11)
+    binding.gemm_orthogonalize(X, Y, steps=3)
+    assert torch.equal(Y, want)
+    binding.gemm_orthogonalize(X, X, steps=3)
+    assert torch.equal(X, want)
+    assert torch.equal(binding.gemm_orthogonalize(stack(3, 90, 70, torch.bfloat16, 4)[1], steps=3), want[1])
+
+
+def test_padding_is_left_alone():
+    X = stack(2, 60, 45, torch.float32, 4)
+    buf = torch.full((2, 61, 51), 7.0, device="cuda")
+    binding.gemm_orthogonalize(X, buf[:, :60, :45])
+    assert (buf[:, 60:] == 7).all() and (buf[:, :, 45:] == 7).all()
+    assert torch.isfinite(buf[:, :60, :45]).all()
+
+
+def test_zeros_and_what_is_not_finite():
+    X = stack(4, 50, 80, torch.float32, 6)
+    good = binding.gemm_orthogonalize(X)
+    X[0] = 0
+    X[2, 3, 3] = float("inf")
+    X[3, 49, 79] = float("nan")
+    Y = binding.gemm_orthogonalize(X)
+    assert (Y[0] == 0).all()
+    assert torch.equal(Y[1], good[1])
+    assert torch.isnan(Y[2]).all() and torch.isnan(Y[3]).all()
+    assert torch.isnan(binding.gemm_orthogonalize(torch.zeros(4, 4, device="cuda"), eps=0.0)).all()
+
+
+def test_same_bits_every_time():
+    X = stack(5, 300, 200, torch.bfloat16, 8)
+    a = binding.gemm_orthogonalize(X)
+    for _ in range(3):
+        assert torch.equal(binding.gemm_orthogonalize(X), a)
+
+
+def test_a_stack_larger_than_the_workspace():
+    """Taken in parts: each matrix as if alone."""
+    X = torch.randn((20000, 96, 100), device="cuda").bfloat16()
+    Y = binding.gemm_orthogonalize(X, steps=2)
+    for i in (0, 1, 9999, 13000, 19999):
+        assert torch.equal(Y[i], binding.gemm_orthogonalize(X[i], steps=2)), i
