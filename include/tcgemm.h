@@ -547,6 +547,8 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.
  *  K == 0            the groups' rows are 0.
  *  Sums are float32, multiplied by alpha (mul.rn) and rounded once; the same bits every time.
+ *  (Of float32 results the sums are added up in registers, rounded to nearest, every 256 of
+ *  K; of the others in the tensor cores' accumulators throughout.)
  *  Other errors and execution as gemm_f16.
  */
 gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16,
@@ -589,13 +591,15 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *  steps             1 to 100; a, b, c finite; eps >= 0.
  *  Y                 may be X exactly (same pointer, type, pitch and stride); any other
  *                    overlap is GEMM_ERR_ALIAS.
- *  Rounding: the norm and every sum are float32.  The products' operands -- X, P and b P + c
- *  P^2 -- are held in float16 between them, scaled by 2^12 (so that elements down to 2^-26
- *  keep 11 bits); the iterates' elements have to stay below 16, and P's and b P + c P^2's
- *  below 16, as they do where the singular values stay below 2.  The last step is rounded
- *  once, to Y's type.
+ *  Rounding: the norm and every sum are float32.  Between the products the iterate X is held
+ *  as two float16 matrices, a high part and the rest (22 bits), P and b P + c P^2 in float16.
+ *  The products take the high part of X; all of their operands in two parts in the last step
+ *  of a float16 Y and in every step of a float32 Y (three products for one), so that the
+ *  steps' error stays below the rounding of Y.  All are scaled by 2^12: the elements of the
+ *  iterates, of P and of b P + c P^2 have to stay below 16, as they do where the singular
+ *  values stay below 2.  The last step is rounded once, to Y's type.
  *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.
- *  Workspace: per device and stream, up to 1 GiB or one matrix's (4 M N + 4 min(M, N)^2
+ *  Workspace: per device and stream, up to 1 GiB or one matrix's (8 M N + 8 min(M, N)^2
  *  bytes) if that is more, kept as the other workspaces are.
  *  Other errors and execution as gemm_f16 (2 + 3 steps kernels, more for a large stack).
  */

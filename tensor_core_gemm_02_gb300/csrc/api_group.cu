@@ -26,12 +26,13 @@ struct GForm {
     bool pair;
     int64_t block_ns, fixed_ns;
 };
+// (float32 results, and operands in two parts: single CTAs of 64 or 128 columns)
 constexpr GForm kForms[4] = {{64, false, 300, 300}, {128, false, 300, 500}, {256, false, 390, 600}, {256, true, 280, 1500}};
 
 // The form of the least waves x time of a tile.  tiles(tile_m, bn): tiles of the problem
 // (0: the form does not apply).
 template <class F>
-GForm choose_form(int64_t k_blocks, int sm_count, F tiles)
+GForm choose_form(int64_t k_blocks, int prec, int sm_count, F tiles)
 {
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
@@ -39,7 +40,7 @@ GForm choose_form(int64_t k_blocks, int sm_count, F tiles)
     int64_t best_ns = 0;
     for (const GForm &f : kForms) {
         const int64_t n = tiles(f.pair ? 256 : 128, f.bn), sets = f.pair ? sm_count / 2 : sm_count;
-        if (n <= 0 || sets <= 0)
+        if (n <= 0 || sets <= 0 || (prec != kPrecAcc && f.bn > 128))
             continue;
         if ((fk == 1 && !f.pair && f.bn == fbn) || (fk == 3 && f.pair))
             return f;
@@ -217,7 +218,8 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
     const bool bf16 = dtype_is_bf16 == 1;
-    const tcg::host::GForm f = choose_form(ceil_div(K, 64), dev->sm_count, tiles);
+    const int prec = out == GEMM_OUT_F32 ? tcg::kPrecSums : tcg::kPrecAcc;
+    const tcg::host::GForm f = choose_form(ceil_div(K, 64), prec, dev->sm_count, tiles);
     int grid = 0;
     if ((st = group_grid(f, most(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK)
         return st;
@@ -244,7 +246,7 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     g.idx = idx;
     g.table_rows = static_cast<int32_t>(rows);
     g.loads = K > 0 ? 1 : 0;
-    const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, maps, g, grid, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, prec, maps, g, grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -276,7 +278,8 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
     const bool bf16 = dtype_is_bf16 == 1;
-    const tcg::host::GForm f = choose_form(ceil_div(ceil_div(M, groups), 64), dev->sm_count, tiles);
+    const int prec = out == GEMM_OUT_F32 ? tcg::kPrecSums : tcg::kPrecAcc;
+    const tcg::host::GForm f = choose_form(ceil_div(ceil_div(M, groups), 64), prec, dev->sm_count, tiles);
     int grid = 0;
     if ((st = group_grid(f, tiles(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK)
         return st;
@@ -298,7 +301,7 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
     g.group_m = kGroupM;
     g.alpha = alpha;
     g.loads = M > 0 ? 1 : 0;
-    const cudaError_t e = tcg::launch_group_sum(f.bn, f.pair, maps, g, grid, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = tcg::launch_group_sum(f.bn, f.pair, prec, maps, g, grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -325,6 +328,10 @@ struct BatchProduct {
     int out;
     bool padded;  // D is a workspace: its rows' padding is written too
     float alpha, beta;
+    // elements from each matrix to its low part: of A and B operands too where `split`, of C
+    // and D where not 0
+    bool split;
+    int64_t a_lo, b_lo, c_lo, d_lo;
 };
 
 gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t stream)
@@ -335,7 +342,8 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
             return tm < bn ? 0 : p.count * (tm / bn) * (mb * (mb + 1) / 2);
         return p.count * mb * ceil_div(p.N, bn);
     };
-    const GForm f = choose_form(ceil_div(p.K, 64), dev->sm_count, tiles);
+    const int prec = p.split ? tcg::kPrecSplit : tcg::kPrecAcc;
+    const GForm f = choose_form(ceil_div(p.K, 64), prec, dev->sm_count, tiles);
     const int tm = f.pair ? 256 : 128, b_rows = f.pair ? f.bn / 2 : f.bn;
     int grid = 0;
     gemm_status st = group_grid(f, tiles(tm, f.bn), dev, &grid);
@@ -345,12 +353,27 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     std::memset(&maps, 0, sizeof(maps));
     GroupArgs g;
     fill_group(g, false, p.out, dev);
-    const bool a_ok = (p.maj & 1) ? set_operand(&maps.a, false, p.A, p.M, p.K, p.lda, p.count, p.stride_a, 64)
-                                  : set_operand(&maps.a, false, p.A, p.K, p.M, p.lda, p.count, p.stride_a, 128);
-    const bool b_ok = (p.maj & 2) ? set_operand(&maps.b, false, p.B, p.N, p.K, p.ldb, p.count, p.stride_b, 64)
-                                  : set_operand(&maps.b, false, p.B, p.K, p.N, p.ldb, p.count, p.stride_b, b_rows);
-    if (!a_ok || !b_ok || !set_out(g, maps, p.D, p.out, p.M, p.padded ? p.ldd : p.N, p.ldd, p.count, p.stride_d))
+    auto map_a = [&](CUtensorMap *m, const uint16_t *x) {
+        return (p.maj & 1) ? set_operand(m, false, x, p.M, p.K, p.lda, p.count, p.stride_a, 64)
+                           : set_operand(m, false, x, p.K, p.M, p.lda, p.count, p.stride_a, 128);
+    };
+    auto map_b = [&](CUtensorMap *m, const uint16_t *x) {
+        return (p.maj & 2) ? set_operand(m, false, x, p.N, p.K, p.ldb, p.count, p.stride_b, 64)
+                           : set_operand(m, false, x, p.K, p.N, p.ldb, p.count, p.stride_b, b_rows);
+    };
+    if (!map_a(&maps.a, p.A) || !map_b(&maps.b, p.B) ||
+        (p.split && (!map_a(&maps.a_lo, p.A + p.a_lo) || !map_b(&maps.b_lo, p.B + p.b_lo))))
         return GEMM_ERR_CUDA;
+    const int64_t cols = p.padded ? p.ldd : p.N;
+    if (p.d_lo != 0) {  // (a workspace: both parts alike)
+        if (!set_out(g, maps, static_cast<uint16_t *>(p.D) + p.d_lo, p.out, p.M, cols, p.ldd, p.count, p.stride_d))
+            return GEMM_ERR_CUDA;
+        maps.d_lo = maps.d;
+    }
+    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d))
+        return GEMM_ERR_CUDA;
+    g.c_lo = p.c_lo;
+    g.d_lo = p.d_lo;
     g.groups = static_cast<int32_t>(p.count);
     g.M = static_cast<int32_t>(p.M);
     g.N = static_cast<int32_t>(p.N);
@@ -364,7 +387,7 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     g.ldc = p.ldc;
     g.stride_c = p.stride_c;
     g.loads = 1;
-    const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, maps, g, grid, stream);
+    const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, prec, maps, g, grid, stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -406,11 +429,17 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // The iterate is held in two float16 parts, since what its rounding loses in one step the
+    // next ones multiply.  The products take the high parts, or, in the last `exact` steps, both:
+    // as many steps as it takes for their error to stay below the rounding of Y's type
+    // (1000 x 1367, relative to 64 bits, without Y's rounding: no step 2.7e-4, the last 1.2e-4,
+    // all 1e-6; one float16 part of X, 3.1e-3).
+    const int exact = out == GEMM_OUT_F32 ? steps : (out == GEMM_OUT_F16 ? 1 : 0);
     // workspace of a matrix: two iterates, the product of one with itself, and the polynomial of that
     const int64_t ldi = ceil_div(N, 8) * 8, ldp = ceil_div(s, 8) * 8;
     const int64_t size_i = ceil_div(M * ldi, 64) * 64, size_p = ceil_div(s * ldp, 64) * 64;
     const int parts = tcg::orthogonalize_parts(M, N);
-    const int64_t each = 2 * (2 * size_i + 2 * size_p) + 4 * static_cast<int64_t>(parts);
+    const int64_t each = 2 * (4 * size_i + 4 * size_p) + 4 * static_cast<int64_t>(parts);
     int64_t at_once = kOrthogonalizeBytes / each;
     const int64_t tiles_one = ceil_div(M, 128) * ceil_div(N, 64);
     at_once = at_once < count ? at_once : count;
@@ -421,9 +450,10 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     void *w = nullptr;
     if ((st = get_dequant_buffer(dev->index, cs, kBufOrthogonalize, static_cast<size_t>(at_once * each), &w)) != GEMM_OK)
         return st;
-    uint16_t *iter[2] = {static_cast<uint16_t *>(w), static_cast<uint16_t *>(w) + at_once * size_i};
-    uint16_t *prod = iter[1] + at_once * size_i, *poly = prod + at_once * size_p;
-    float *partial = reinterpret_cast<float *>(poly + at_once * size_p);
+    const int64_t lo_i = at_once * size_i, lo_p = at_once * size_p;  // to the low parts
+    uint16_t *iter[2] = {static_cast<uint16_t *>(w), static_cast<uint16_t *>(w) + 2 * lo_i};
+    uint16_t *prod = iter[1] + 2 * lo_i, *poly = prod + 2 * lo_p;
+    float *partial = reinterpret_cast<float *>(poly + 2 * lo_p);
     for (int64_t first = 0; first < count; first += at_once) {
         const int64_t n = count - first < at_once ? count - first : at_once;
         const void *xf = static_cast<const uint8_t *>(X) + first * stride_x * out_size(type);
@@ -432,11 +462,11 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
                                     static_cast<int32_t>(n), partial, parts, cs) != cudaSuccess ||
             tcg::launch_normalize(xf, ldx, stride_x, type, static_cast<int32_t>(M), static_cast<int32_t>(N),
                                   static_cast<int32_t>(n), partial, parts, kIterateScale, eps, iter[0], ldi, size_i,
-                                  cs) != cudaSuccess)
+                                  lo_i, cs) != cudaSuccess)
             return GEMM_ERR_CUDA;
         for (int i = 0; i < steps; ++i) {
             const uint16_t *xi = iter[i % 2];
-            const bool last = i == steps - 1;
+            const bool last = i == steps - 1, both = i >= steps - exact;
             // P = kProductScale X X^T (or X^T X), on the smaller side
             BatchProduct p{};
             p.count = n;
@@ -453,6 +483,9 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
             p.out = GEMM_OUT_F16;
             p.padded = true;
             p.alpha = kProductScale / (kIterateScale * kIterateScale);
+            p.split = both;
+            p.a_lo = p.b_lo = lo_i;
+            p.d_lo = both ? lo_p : 0;
             if ((st = run_batch(p, dev, cs)) != GEMM_OK)
                 return st;
             // Q = kProductScale (b P + c P^2)
@@ -467,6 +500,8 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
             p.D = poly;
             p.alpha = c / kProductScale;
             p.beta = b;
+            p.a_lo = p.b_lo = lo_p;
+            p.c_lo = both ? lo_p : 0;
             if ((st = run_batch(p, dev, cs)) != GEMM_OK)
                 return st;
             // X <- a X + Q X (or X Q; Q is symmetric)
@@ -490,6 +525,11 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
             u.stride_d = last ? stride_y : size_i;
             u.out = last ? out : GEMM_OUT_F16;
             u.padded = !last;
+            u.split = both;
+            u.a_lo = wide ? lo_p : lo_i;
+            u.b_lo = wide ? lo_i : lo_p;
+            u.c_lo = lo_i;
+            u.d_lo = last ? 0 : lo_i;
             u.alpha = last ? 1.0f / (kIterateScale * kProductScale) : 1.0f / kProductScale;
             u.beta = last ? a / kIterateScale : a;
             if ((st = run_batch(u, dev, cs)) != GEMM_OK)

@@ -16,6 +16,15 @@
 //               the square of a symmetric matrix): only the tiles that reach the
 //               diagonal or lie below it are computed, and each is stored twice.
 //
+// Sums.  The tensor cores add each K step of 16 to a float32 accumulator and drop what
+// does not fit, so the error of a long sum grows with its steps.  How much of that is let
+// stand is a template parameter:
+//   PREC_ACC    one accumulator for the whole sum (results of 16 bits).
+//   PREC_SUMS   the accumulator is emptied every four K blocks into float32 registers, which
+//               round to nearest (float32 results: 1000 x 1367 summed over 1000 1.2e-6 -> 3e-7).
+//   PREC_SPLIT  as PREC_SUMS, and both operands are pairs of float16 matrices, a high part and
+//               the rest: high x high + high x low + low x high, 22 bits of each operand.
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), warps 2-5
 // epilogue, (KIND_SUM) warp 6 zeroes.  Two TMEM accumulators: the epilogue of one tile
 // runs beside the next tile's MMAs.  PAIR: the roles on a CTA pair and one 256 x 256 tile
@@ -33,9 +42,11 @@
 namespace tcg {
 
 enum : int { kKindRows = 0, kKindSum = 1, kKindBatch = 2 };
+enum : int { kPrecAcc = 0, kPrecSums = 1, kPrecSplit = 2 };
 
 struct GroupMaps {
-    CUtensorMap a, b, d;  // 3-D (inner, rows, group); a is 2-D rows of a table when gathered
+    CUtensorMap a, b, d;           // 3-D (inner, rows, group); a is 2-D rows of a table when gathered
+    CUtensorMap a_lo, b_lo, d_lo;  // the low parts (PREC_SPLIT; d_lo where D is written in two parts)
 };
 
 struct GroupArgs {
@@ -56,21 +67,24 @@ struct GroupArgs {
     int32_t n_out;           // columns of D that may be written (N, or a workspace's padding too)
     const uint16_t *C;       // KIND_BATCH: f16, 16-byte aligned rows (NULL: none)
     int64_t ldc, stride_c;
+    int64_t c_lo, d_lo;      // KIND_BATCH: elements from C, D to their low parts (0: none)
     int32_t loads;           // there is something to multiply (K > 0; KIND_SUM: rows > 0)
     uint32_t extra_tx;
     uint32_t *status;
     uint64_t timeout_ns;
 };
 
-template <int BN_, int STAGES_, bool PAIR_, int KIND_>
+template <int BN_, int STAGES_, bool PAIR_, int KIND_, int PREC_>
 struct GroupCfg {
+    static constexpr int PARTS = PREC_ == kPrecSplit ? 2 : 1;  // boxes of an operand in a stage
+    static constexpr int CHUNK = PREC_ == kPrecAcc ? 0 : 4;    // K blocks an accumulator takes (0: all)
     static constexpr bool PAIR = PAIR_;
     static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_;
     static constexpr int TILE_M = PAIR ? 256 : 128;
     static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;
     static constexpr uint32_t A_BYTES = BM * 128u, B_BYTES = BN_LOCAL * 128u;
-    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr uint32_t OFF_A = 0, OFF_B = STAGES * A_BYTES;
+    static constexpr uint32_t STAGE_BYTES = PARTS * (A_BYTES + B_BYTES);
+    static constexpr uint32_t OFF_A = 0, OFF_B = STAGES * PARTS * A_BYTES;
     static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes, two a warp
     static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_EPI + 8 * EPI_BUF;
@@ -81,6 +95,7 @@ struct GroupCfg {
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
     static_assert(!PAIR || BN == 256, "pairs: 256 x 256");
+    static_assert(PREC_ == kPrecAcc || (BN <= 128 && !PAIR), "a row's sums in a thread's registers");
 };
 
 // The groups' rows, as one warp knows them.  Lane l keeps the block rows of groups l per
@@ -211,15 +226,17 @@ __device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, in
     }
 }
 
-template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM>
-__global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
+template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC>
+__global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREADS, 1)
     group_gemm_kernel(const __grid_constant__ GroupMaps maps, const GroupArgs args)
 {
-    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND>;
+    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC>;
+    constexpr bool kSums = PREC != kPrecAcc, kSplit = PREC == kPrecSplit;
     constexpr bool kRows = KIND == kKindRows, kSum = KIND == kKindSum, kBatch = KIND == kKindBatch;
     constexpr bool kMnA = (MAJ & 1) != 0, kMnB = (MAJ & 2) != 0;
     constexpr int TM = Cfg::TILE_M;
     static_assert(!SYM || kBatch, "symmetric results: equal sizes");
+    static_assert(!kSplit || kBatch, "operands in two parts: equal sizes");
     static_assert(!kSum || MAJ == 3, "a sum over rows: both operands stored with them outermost");
     static_assert(!kRows || !kMnA, "grouped rows are stored row by row");
     extern __shared__ uint8_t smem_raw[];
@@ -397,8 +414,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                     break;
                 }
                 const bool part = kSum && rem != 0 && kb == nkb - 1;
-                const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES;
-                const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES;
+                const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
+                const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
                 const int32_t k = p.k0 + kb * Cfg::BK;
                 if (lane == 0) {
                     const uint32_t extra = first ? args.extra_tx : 0u;
@@ -426,19 +443,29 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                     else
                         tma_gather4(sa + lane * 512u, &maps.a, bar, k, rows[0], rows[1], rows[2], rows[3]);
                 } else if (lane == 0) {
-                    if constexpr (kMnA) {
-                        for (int j = 0; j < Cfg::BM / 64; ++j)
-                            load(sa + j * 8192u, &maps.a, m0 + 64 * j, k, ga);
-                    } else {
-                        load(sa, &maps.a, k, m0, ga);
+#pragma unroll
+                    for (int part2 = 0; part2 < Cfg::PARTS; ++part2) {
+                        const CUtensorMap *m = part2 == 0 ? &maps.a : &maps.a_lo;
+                        const uint32_t to = sa + part2 * Cfg::A_BYTES;
+                        if constexpr (kMnA) {
+                            for (int j = 0; j < Cfg::BM / 64; ++j)
+                                load(to + j * 8192u, m, m0 + 64 * j, k, ga);
+                        } else {
+                            load(to, m, k, m0, ga);
+                        }
                     }
                 }
                 if (lane == 0) {
-                    if constexpr (kMnB) {
-                        for (int j = 0; j < Cfg::BN_LOCAL / 64; ++j)
-                            load(sb + j * 8192u, &maps.b, n0 + 64 * j, k, gb);
-                    } else {
-                        load(sb, &maps.b, k, n0, gb);
+#pragma unroll
+                    for (int part2 = 0; part2 < Cfg::PARTS; ++part2) {
+                        const CUtensorMap *m = part2 == 0 ? &maps.b : &maps.b_lo;
+                        const uint32_t to = sb + part2 * Cfg::B_BYTES;
+                        if constexpr (kMnB) {
+                            for (int j = 0; j < Cfg::BN_LOCAL / 64; ++j)
+                                load(to + j * 8192u, m, n0 + 64 * j, k, gb);
+                        } else {
+                            load(to, m, k, n0, gb);
+                        }
                     }
                 }
                 if constexpr (kSum)
@@ -484,12 +511,32 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
             for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
                 int32_t rem;
                 const int32_t nkb = blocks_of(t, rem);
-                if (!wait_bounded<true>(acce_bar(ab), aph ^ 1u, abort_flag, args.status, args.timeout_ns,
-                                        kWhereMmaAccEmpty))
+                auto wait_acc = [&]() {
+                    const bool got = wait_bounded<true>(acce_bar(ab), aph ^ 1u, abort_flag, args.status,
+                                                        args.timeout_ns, kWhereMmaAccEmpty);
+                    tc_fence_after_sync();
+                    return got;
+                };
+                auto next_acc = [&]() {
+                    commit_to(accf_bar(ab));
+                    if (++ab == 2) {
+                        ab = 0;
+                        aph ^= 1u;
+                    }
+                };
+                if (!wait_acc())
                     break;
-                tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
                 for (int32_t kb = 0; kb < nkb; ++kb) {
+                    // (a chunk's sum goes to the epilogue, the next chunk starts from zero)
+                    const bool begins = kSums ? kb % Cfg::CHUNK == 0 : kb == 0;
+                    if (kSums && begins && kb > 0) {
+                        next_acc();
+                        if (!wait_acc()) {
+                            alive = false;
+                            break;
+                        }
+                    }
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
                     const bool part = kSum && rem != 0 && kb == nkb - 1;
                     // (the peer's zeros: an acquire at cluster scope)
                     const bool got =
@@ -503,21 +550,27 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES;
-                    const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES;
-                    const uint64_t ad = kMnA ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
-                    const uint64_t bd = kMnB ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
+                    const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
+                    const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
                     constexpr uint32_t kStepA = kMnA ? 128u : 2u, kStepB = kMnB ? 128u : 2u;
                     // (of a partial block only the K steps that hold rows of the group)
                     const int steps = part ? (rem + 15) / 16 : 4;
+                    // low x high and high x low first, while the sum is small
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < steps) {
-                            const uint32_t acc = (kb | k) != 0 ? 1u : 0u;
-                            if (PAIR)
-                                tc_mma_f16_pair(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
-                            else
-                                tc_mma_f16(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
+                    for (int pr = kSplit ? 0 : 2; pr < 3; ++pr) {
+                        const uint32_t pa = sa + (pr == 0 ? Cfg::A_BYTES : 0u);
+                        const uint32_t pb = sb + (pr == 1 ? Cfg::B_BYTES : 0u);
+                        const uint64_t ad = kMnA ? sdesc_mn_sw128(pa) : sdesc_k_sw128(pa);
+                        const uint64_t bd = kMnB ? sdesc_mn_sw128(pb) : sdesc_k_sw128(pb);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k < steps) {
+                                const uint32_t acc = !begins || k > 0 || pr > (kSplit ? 0 : 2) ? 1u : 0u;
+                                if (PAIR)
+                                    tc_mma_f16_pair(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
+                                else
+                                    tc_mma_f16(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
+                            }
                         }
                     }
                     commit_to(empty_bar(s));
@@ -528,11 +581,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                 }
                 if (!alive)
                     break;
-                commit_to(accf_bar(ab));
-                if (++ab == 2) {
-                    ab = 0;
-                    aph ^= 1u;
-                }
+                next_acc();
             }
         }
         __syncwarp();
@@ -552,7 +601,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                     tail_ph ^= 1u << at;
                     // rows [rem, next multiple of 16) of every box: 64 columns are one row's 128
                     // bytes, so the swizzle does not matter
-                    const uint32_t sa = base + Cfg::OFF_A + at * Cfg::A_BYTES;
+                    const uint32_t sa = base + Cfg::OFF_A + at * Cfg::A_BYTES;  // (one part a stage)
                     const uint32_t sb = base + Cfg::OFF_B + at * Cfg::B_BYTES;
                     const int32_t more = (rem + 15) / 16 * 16 - rem;
                     constexpr int32_t kBoxesA = Cfg::BM / 64, kBoxes = kBoxesA + Cfg::BN_LOCAL / 64;
@@ -604,95 +653,107 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
             const uint16_t *c_row = nullptr;
             if (kBatch && args.C && my_row < p.end)
                 c_row = args.C + p.g * args.stride_c + static_cast<int64_t>(my_row) * args.ldc + p.n0;
-            if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
-                                         kWhereEpiAccFull))
-                break;
-            tc_fence_after_sync();
-            const uint32_t acc0 = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN);
-            // 32 columns from col of this lane's row: alpha acc + beta C
-            auto take = [&](int32_t col, float(&v)[32]) {
-                uint32_t r[32];
-                tc_ld_32x32b_x32(acc0 + static_cast<uint32_t>(col), r);
-                if (kBatch && args.C) {
-                    uint4 c[4];
+            // accumulators as they fill: the last (only) one's address, or (PREC_SUMS) all added up
+            // in registers and handed back
+            float sums[kSums ? BN : 1];
+            uint32_t acc0 = 0;
+            auto hand_back = [&]() {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR && !leader)
+                        mbar_arrive_cluster(lead(acce_bar(ab)));
+                    else
+                        mbar_arrive(acce_bar(ab));
+                }
+                if (++ab == 2) {
+                    ab = 0;
+                    aph ^= 1u;
+                }
+            };
+            bool alive = true;
+            const int32_t fills = kSums ? max(1, (nkb + Cfg::CHUNK - 1) / max(1, Cfg::CHUNK)) : 1;
+            for (int32_t f = 0; f < fills; ++f) {
+                if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                             kWhereEpiAccFull)) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                acc0 = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN);
+                if constexpr (kSums) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        c[i] = c_row && p.n0 + col + 8 * i < args.N
-                                   ? *reinterpret_cast<const uint4 *>(c_row + col + 8 * i)
-                                   : make_uint4(0, 0, 0, 0);
-                    tc_wait_ld(r);
+                    for (int c = 0; c < BN / 32; ++c) {
+                        uint32_t r[32];
+                        tc_ld_32x32b_x32(acc0 + 32u * c, r);
+                        tc_wait_ld(r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sums[32 * c + i] = f == 0 ? __uint_as_float(r[i])
+                                                      : __fadd_rn(sums[32 * c + i], __uint_as_float(r[i]));
+                    }
+                    hand_back();
+                }
+            }
+            if (!alive)
+                break;
+            // 32 columns from col of this lane's row, in v: alpha sum + beta C
+            auto finish = [&](int32_t col, float(&v)[32]) {
+                if (kBatch && args.C) {
+                    uint4 c[4], cl[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool there = c_row && p.n0 + col + 8 * i < args.N;
+                        c[i] = there ? *reinterpret_cast<const uint4 *>(c_row + col + 8 * i) : make_uint4(0, 0, 0, 0);
+                        cl[i] = there && args.c_lo
+                                    ? *reinterpret_cast<const uint4 *>(c_row + args.c_lo + col + 8 * i)
+                                    : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
+                        const int sh = 16 * (i & 1);
                         const uint32_t w = reinterpret_cast<const uint32_t *>(c)[i / 2];
-                        const float x = cvt_f16_f32(static_cast<uint16_t>(w >> (16 * (i & 1))));
-                        v[i] = fma_rn(args.alpha, __uint_as_float(r[i]), mul_rn(args.beta, x));
+                        const uint32_t wl = reinterpret_cast<const uint32_t *>(cl)[i / 2];
+                        const float x = cvt_f16_f32(static_cast<uint16_t>(w >> sh)) +
+                                        cvt_f16_f32(static_cast<uint16_t>(wl >> sh));
+                        v[i] = fma_rn(args.alpha, v[i], mul_rn(args.beta, x));
                     }
                 } else {
-                    tc_wait_ld(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        v[i] = zero ? 0.f : mul_rn(args.alpha, __uint_as_float(r[i]));
+                        v[i] = zero ? 0.f : mul_rn(args.alpha, v[i]);
                 }
             };
             auto pack2 = [&](float a, float b) {
                 return args.out_kind == kOutBF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
             };
+            // what rounding to float16 leaves of the values
+            auto rest = [&](float(&v)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] -= cvt_f16_f32(f32_to_f16_rn(v[i]));
+            };
             // columns col .. col + 31 of the tile, a second time: D[column][row], two columns of
             // D's row from a lane and its neighbour, two rows of D per pair of columns
-            auto mirror = [&](int32_t col, const float(&v)[32]) {
+            auto mirror = [&](int32_t col, const float(&v)[32], int64_t part) {
+                const int32_t c = my_row & ~1;
+                const bool odd = (lane & 1u) != 0u;
+                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + c;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const bool odd = (lane & 1u) != 0u;
                     const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
                     const uint32_t w = odd ? pack2(other, v[i + 1]) : pack2(v[i], other);
                     const int32_t r = p.n0 + col + i + (odd ? 1 : 0);
-                    const int32_t c = my_row & ~1;
                     // (an odd size: the last pair's second element goes into the row's padding)
                     if (r < args.N && c < p.end)
-                        *reinterpret_cast<uint32_t *>(d_g + (static_cast<int64_t>(r) * args.ldd + c) * 2) = w;
+                        *reinterpret_cast<uint32_t *>(d + static_cast<int64_t>(r) * args.ldd) = w;
                 }
             };
-            for (int32_t c = 0; c < chunks; ++c) {
-                const int32_t col = c * wide;
-                uint32_t w[32];
-                {
-                    float v[32];
-                    take(col, v);
-                    if (SYM && p.mirror)
-                        mirror(col, v);
-                    if (f32) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            w[i] = __float_as_uint(v[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = pack2(v[2 * i], v[2 * i + 1]);
-                    }
-                }
-                if (!f32) {
-                    float v[32];
-                    take(col + 32, v);
-                    if (SYM && p.mirror)
-                        mirror(col + 32, v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[16 + i] = pack2(v[2 * i], v[2 * i + 1]);
-                }
-                if (c == chunks - 1) {
-                    // the accumulator is read: hand it back
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR && !leader)
-                            mbar_arrive_cluster(lead(acce_bar(ab)));
-                        else
-                            mbar_arrive(acce_bar(ab));
-                    }
-                }
+            // a 128-byte row a lane, from column col of the tile, to D (part 0) or its low part
+            auto put = [&](int32_t col, const uint32_t(&w)[32], bool low) {
                 const int32_t col0 = p.n0 + col;
                 if (nrows <= 0 || col0 >= args.N)
-                    continue;
+                    return;
                 const uint32_t buf = buf0 + slot * Cfg::EPI_BUF;
                 slot ^= 1u;
                 if (lane == 0)
@@ -709,21 +770,93 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) {
                         if (kBatch)  // (read by the next product)
-                            tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                            tma_store_3d(low ? &maps.d_lo : &maps.d, buf, col0, row0, p.g);
                         else
                             tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.g, policy);
                     }
                 } else {
                     __syncwarp();
-                    store_image_rows(buf, lane, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
+                    store_image_rows(buf, lane, nrows, esize, d_g + (low ? args.d_lo * 2 : 0), args.ldd, row0, col0,
+                                     args.n_out, args.d_vec != 0);
                     __syncwarp();
                 }
                 if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
                     bulk_commit_group();
-            }
-            if (++ab == 2) {
-                ab = 0;
-                aph ^= 1u;
+            };
+            // 32 columns: from registers, or from the accumulator
+            auto take = [&](int c32, float(&v)[32]) {
+                if constexpr (kSums) {
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c)  // (selects: registers have no addresses)
+                        if (c == c32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = sums[32 * c + i];
+                        }
+                } else {
+                    uint32_t r[32];
+                    tc_ld_32x32b_x32(acc0 + 32u * static_cast<uint32_t>(c32), r);
+                    tc_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(r[i]);
+                }
+                finish(32 * c32, v);
+            };
+            const int per = wide / 32;
+            auto piece = [&](int c, bool last) {
+                const int32_t col = c * wide;
+                uint32_t w[32], wl[32];
+                const bool two = kBatch && args.d_lo != 0;
+                float v[32];
+                take(c * per, v);
+                if (SYM && p.mirror)
+                    mirror(col, v, 0);
+                if (f32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        w[i] = __float_as_uint(v[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    if (two) {
+                        rest(v);
+                        if (SYM && p.mirror)
+                            mirror(col, v, args.d_lo);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            wl[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+                    }
+                    take(c * per + 1, v);
+                    if (SYM && p.mirror)
+                        mirror(col + 32, v, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[16 + i] = pack2(v[2 * i], v[2 * i + 1]);
+                    if (two) {
+                        rest(v);
+                        if (SYM && p.mirror)
+                            mirror(col + 32, v, args.d_lo);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            wl[16 + i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+                    }
+                }
+                if (!kSums && last)
+                    hand_back();
+                put(col, w, false);
+                if (two)
+                    put(col, wl, true);
+            };
+            if constexpr (kSums) {
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c)
+                    if (c < chunks)
+                        piece(c, false);
+            } else {
+                for (int32_t c = 0; c < chunks; ++c)
+                    piece(c, c == chunks - 1);
             }
         }
         if (lane == 0)

@@ -9,13 +9,13 @@ namespace tcg {
 
 // A form of the group kernel: single CTAs with 128 x bn tiles (bn 64, 128, 256), or
 // (pair) CTA pairs with 256 x 256 ones.  maj: bit 0 A stored with K outermost, bit 1 B.
-// grid counts CTAs.
-cudaError_t launch_group_rows(int bn, bool pair, bool b_major, const GroupMaps &maps, const GroupArgs &args,
+// grid counts CTAs.  prec: kPrecAcc, or (bn 64 or 128) sums kept in registers.
+cudaError_t launch_group_rows(int bn, bool pair, bool b_major, int prec, const GroupMaps &maps, const GroupArgs &args,
                               int grid, cudaStream_t stream);
-cudaError_t launch_group_sum(int bn, bool pair, const GroupMaps &maps, const GroupArgs &args, int grid,
-                             cudaStream_t stream);
-// (symmetric results: maj 0 or 3, bn 128 or pairs; others: maj 0 or 2)
-cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, const GroupMaps &maps,
+cudaError_t launch_group_sum(int bn, bool pair, int prec, const GroupMaps &maps, const GroupArgs &args,
+                             int grid, cudaStream_t stream);
+// (symmetric results: maj 0 or 3; others: maj 0 or 2; prec: kPrecAcc or kPrecSplit)
+cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, int prec, const GroupMaps &maps,
                                const GroupArgs &args, int grid, cudaStream_t stream);
 
 // The stable order of M ids by value: offsets (groups + 1), order and rows (each M; rows
@@ -28,12 +28,12 @@ cudaError_t launch_group_rows_sort(const int32_t *ids, int64_t M, int32_t groups
                                    int32_t chunks, cudaStream_t stream);
 
 // Sums of squares of `count` matrices X (M x N of type kOut...), in `parts` parts each, to
-// partial; and Xs = f16(X scale / (sqrt(the parts' sum) + eps)).
+// partial; and X scale / (sqrt(the parts' sum) + eps) as float16 Xs and, lo elements behind it, the rest.
 int orthogonalize_parts(int64_t M, int64_t N);
 cudaError_t launch_square_sums(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
                                int32_t count, float *partial, int parts, cudaStream_t stream);
 cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
                              int32_t count, const float *partial, int parts, float scale, float eps,
-                             uint16_t *Xs, int64_t lds, int64_t stride_s, cudaStream_t stream);
+                             uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo, cudaStream_t stream);
 
 }  // namespace tcg

@@ -5,11 +5,11 @@
 
 namespace tcg {
 
-template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM>
+template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC>
 cudaError_t group_launch_impl(const GroupMaps &maps, const GroupArgs &args, int grid, cudaStream_t stream)
 {
-    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND>;
-    auto kfn = group_gemm_kernel<BN, STAGES, PAIR, KIND, MAJ, SYM>;
+    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC>;
+    auto kfn = group_gemm_kernel<BN, STAGES, PAIR, KIND, MAJ, SYM, PREC>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kfn), Cfg::SMEM_ALLOC, done);
     if (e != cudaSuccess)
@@ -40,16 +40,28 @@ cudaError_t group_launch_forms(int bn, bool pair, const GroupMaps &maps, const G
                                cudaStream_t stream)
 {
     if (pair)
-        return bn == 256 ? group_launch_impl<256, 6, true, KIND, MAJ, SYM>(maps, args, grid, stream)
+        return bn == 256 ? group_launch_impl<256, 6, true, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream)
                          : cudaErrorInvalidValue;
     if (bn == 128)
-        return group_launch_impl<128, 6, false, KIND, MAJ, SYM>(maps, args, grid, stream);
+        return group_launch_impl<128, 6, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     if (bn == 64)
-        return group_launch_impl<64, 8, false, KIND, MAJ, SYM>(maps, args, grid, stream);
+        return group_launch_impl<64, 8, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     if constexpr (!SYM) {
         if (bn == 256)
-            return group_launch_impl<256, 4, false, KIND, MAJ, SYM>(maps, args, grid, stream);
+            return group_launch_impl<256, 4, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     }
+    return cudaErrorInvalidValue;
+}
+
+// The forms that keep float32 sums in registers.
+template <int KIND, int MAJ, bool SYM, int PREC>
+cudaError_t group_launch_sums(int bn, const GroupMaps &maps, const GroupArgs &args, int grid, cudaStream_t stream)
+{
+    constexpr int kDeep = PREC == kPrecSplit ? 2 : 1;
+    if (bn == 128)
+        return group_launch_impl<128, 6 / kDeep, false, KIND, MAJ, SYM, PREC>(maps, args, grid, stream);
+    if (bn == 64)
+        return group_launch_impl<64, 8 / kDeep, false, KIND, MAJ, SYM, PREC>(maps, args, grid, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -3,10 +3,11 @@
 
 namespace tcg {
 
-cudaError_t launch_group_sum(int bn, bool pair, const GroupMaps &maps, const GroupArgs &args, int grid,
-                             cudaStream_t stream)
+cudaError_t launch_group_sum(int bn, bool pair, int prec, const GroupMaps &maps, const GroupArgs &args,
+                             int grid, cudaStream_t stream)
 {
-    return group_launch_forms<kKindSum, 3, false>(bn, pair, maps, args, grid, stream);
+    return prec == kPrecSums ? group_launch_sums<kKindSum, 3, false, kPrecSums>(bn, maps, args, grid, stream)
+                             : group_launch_forms<kKindSum, 3, false>(bn, pair, maps, args, grid, stream);
 }
 
 }  // namespace tcg

@@ -107,7 +107,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
     normalize_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, bool vec,
                      const float *partial, int32_t parts, float scale, float eps, uint16_t *Xs, int64_t lds,
-                     int64_t stride_s)
+                     int64_t stride_s, int64_t lo)
 {
     const int32_t g = static_cast<int32_t>(blockIdx.y);
     const int64_t per_row = (N + 7) / 8, pieces = per_row * M;
@@ -134,12 +134,18 @@ __global__ void __launch_bounds__(kThreads)
                 break;
             const int64_t r = p / per_row;
             const int64_t c = (p - r * per_row) * 8;
-            uint32_t w[4];
+            uint32_t w[4], wl[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = pack_f16x2(v[j][2 * e] * f, v[j][2 * e + 1] * f);
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = v[j][2 * e] * f, x1 = v[j][2 * e + 1] * f;
+                w[e] = pack_f16x2(x0, x1);
+                wl[e] = pack_f16x2(x0 - cvt_f16_f32(static_cast<unsigned short>(w[e])),
+                                   x1 - cvt_f16_f32(static_cast<unsigned short>(w[e] >> 16)));
+            }
             // (rows of Xs are whole 16 bytes: the last piece fills the padding)
-            *reinterpret_cast<uint4 *>(Xs + g * stride_s + r * lds + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            uint16_t *to = Xs + g * stride_s + r * lds + c;
+            *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(to + lo) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
         }
     }
 }
@@ -192,13 +198,13 @@ cudaError_t launch_square_sums(const void *X, int64_t ldx, int64_t stride_x, int
 
 cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
                              int32_t count, const float *partial, int parts, float scale, float eps,
-                             uint16_t *Xs, int64_t lds, int64_t stride_s, cudaStream_t stream)
+                             uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo, cudaStream_t stream)
 {
     auto k = type == kOutF32    ? normalize_kernel<kOutF32>
              : type == kOutBF16 ? normalize_kernel<kOutBF16>
                                 : normalize_kernel<kOutF16>;
     return launch(k, dim3(blocks_for(M, N, 4), static_cast<unsigned>(count)), stream, X, ldx, stride_x, M, N,
-                  vec_ok(X, ldx, stride_x, type), partial, parts, scale, eps, Xs, lds, stride_s);
+                  vec_ok(X, ldx, stride_x, type), partial, parts, scale, eps, Xs, lds, stride_s, lo);
 }
 
 }  // namespace tcg

@@ -36,6 +36,11 @@ def _clean():
     assert device_status() == binding.GEMM_OK
 
 
+def sum_bound(K, out):
+    """As gated_ref's; float32 results are added up in registers every 256 of K, each time one rounding."""
+    return ref.sum_bound(K) if out != OUT_F32 else ref.sum_bound(min(K, 256)) + K / 256 * 2.0 ** -24
+
+
 def offsets_of(counts, front):
     return torch.tensor(np.cumsum([front] + list(counts)), dtype=torch.int32, device="cuda")
 
@@ -93,7 +98,7 @@ def check_grouped(counts, front, behind, N, K, trans_b, dtype, out, exact, seed=
     if exact:
         assert torch.equal(D.cpu()[inside], want.float().to(ref.out_dtype(out))), what
     else:
-        b = alpha * ref.sum_bound(K) * t[inside] + 2.0 ** -23 * want.abs()
+        b = alpha * sum_bound(K, out) * t[inside] + 2.0 ** -23 * want.abs()
         assert_close(D.cpu()[inside], want, b + ref.rounding(want.abs() + b, out), what)
 
 
@@ -227,7 +232,7 @@ def check_weights(counts, front, behind, N, K, dtype, out, exact, pad=8):
             assert torch.equal(dB[g].cpu(), want.float().to(ref.out_dtype(out))), (g, what)
         else:
             t = d[lo:hi].abs().T @ a[lo:hi].abs()
-            b = 2.0 * ref.sum_bound(hi - lo) * t + 2.0 ** -23 * want.abs()
+            b = 2.0 * sum_bound(hi - lo, out) * t + 2.0 ** -23 * want.abs()
             assert_close(dB[g], want, b + ref.rounding(want.abs() + b, out), (g, what))
 
 

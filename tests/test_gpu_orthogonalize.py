@@ -1,14 +1,16 @@
 """gemm_orthogonalize on the GPU (needs a GB300) against the recurrence in 64 bits.
 
 Bound, in the Frobenius norm |.| (|.|2: the largest singular value): a step from X, with P = X X^T
-over l and Q = b P + c P^2 over s, makes these errors, each f16 rounding at most 2^-11 of its matrix
-(and half a unit of the subnormal range, 2^-25, an element before the scaling by 2^12):
-    eP = (2^-11 + sum(l)) |X|^2 + 2^-23 |P| + s 2^-37
-    eQ = (|b| + 2 |c| (|P|2 + eP)) eP + sum(s) |c| (|P| + eP)^2 + 2^-22 (|b| |P| + |c| |P|2 |P|) + 2^-11 |Q| + s 2^-37
-    eX = eQ |X|2 + sum(s) (|Q| + eQ) |X| + 2^-22 (|a| |X| + |Q| |X|2) + 2^-11 |X'| + sqrt(m n) 2^-37
-and passes an error e of X on as L e, L the largest slope of a x + b x^3 + c x^5 up to the largest
-singular value (and e itself): the divided differences of a function are at most its largest slope.
-sum(K) is gated_ref's bound of a tensor-core sum.
+over l and Q = b P + c P^2 over s, whose operands are rounded by at most h of themselves (2^-11, one
+float16; 2^-22, two; half a unit of the subnormal range, 2^-25, an element before the scaling by
+2^12), makes these errors:
+    eP = (2 h + h^2 + sum(l)) |X|^2 + (2^-23 + h) |P| + s 2^-37
+    eQ = (|b| + 2 |c| (|P|2 + eP)) eP + sum(s) |c| (|P| + eP)^2 + 2^-22 (|b| |P| + |c| |P|2 |P|) + h |Q| + s 2^-37
+    eX = eQ |X|2 (1 + h) + (|Q|2 h + sum(s) (|Q| + eQ)) |X| + 2^-22 (|a| |X| + |Q| |X|2) + r |X'| + sqrt(m n) 2^-37
+(r: 2^-22, the iterate's two parts, or in the last step the rounding to Y) and passes an error e of
+X on as L e, L the largest slope of a x + b x^3 + c x^5 up to the largest singular value (and e
+itself): the divided differences of a function are at most its largest slope.  sum(K) is gated_ref's
+bound of a tensor-core sum.
 """
 import numpy as np
 import pytest
@@ -49,21 +51,24 @@ def recurrence(x, coefs, steps, eps, out):
     s, l = x.shape
     two = lambda m: torch.linalg.matrix_norm(m, 2).item()  # noqa: E731
     # the norm: float32 sums of N squares (2^-24 each, pairwise in part: at most the chain of a
-    # thread), the root, the division and a product; then the rounding to f16
-    e = (2.0 ** -11 + 2.0 ** -16) * x.norm().item() + (s * l) ** 0.5 * 2.0 ** -37
+    # thread), the root, the division and a product; then the iterate's two parts
+    e = 2.0 ** -16 * x.norm().item() + (s * l) ** 0.5 * 2.0 ** -37
+    exact = {torch.float32: steps, torch.float16: 1, torch.bfloat16: 0}[out]
     for i in range(steps):
+        h = 2.0 ** -22 if i >= steps - exact else 2.0 ** -11
         p = x @ x.T
         q = b * p + c * (p @ p)
         y = a * x + q @ x
         X, P, Q, Y = (m.norm().item() for m in (x, p, q, y))
-        X2, P2 = two(x) + e, two(p)
+        X2, P2, Q2 = two(x) + e, two(p), two(q)
         grid = np.linspace(0.0, X2, 2001)
         L = np.abs(a + 3 * b * grid ** 2 + 5 * c * grid ** 4).max() + 1e-3 * (abs(a) + abs(b) + abs(c))
-        eP = (2.0 ** -11 + ref.sum_bound(l)) * X * X + 2.0 ** -23 * P + s * 2.0 ** -37
+        eP = (2 * h + h * h + ref.sum_bound(l)) * X * X + (2.0 ** -23 + h) * P + s * 2.0 ** -37
         eQ = ((abs(b) + 2 * abs(c) * (P2 + eP)) * eP + ref.sum_bound(s) * abs(c) * (P + eP) ** 2
-              + 2.0 ** -22 * (abs(b) * P + abs(c) * P2 * P) + 2.0 ** -11 * Q + s * 2.0 ** -37)
-        last = HALF[out] if i == steps - 1 else 2.0 ** -11
-        eX = (eQ * X2 + ref.sum_bound(s) * (Q + eQ) * X + 2.0 ** -22 * (abs(a) * X + Q * X2) + last * Y
+              + 2.0 ** -22 * (abs(b) * P + abs(c) * P2 * P) + h * Q + s * 2.0 ** -37)
+        last = HALF[out] if i == steps - 1 else 2.0 ** -22
+        eX = (eQ * X2 * (1 + h) + (Q2 * h + ref.sum_bound(s) * (Q + eQ)) * X
+              + 2.0 ** -22 * (abs(a) * X + Q * X2) + last * Y
               + (s * l) ** 0.5 * (2.0 ** -25 if out == torch.float16 and i == steps - 1 else 2.0 ** -37))
         e = L * e + eX
         x = y
