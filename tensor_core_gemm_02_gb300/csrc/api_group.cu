@@ -229,7 +229,8 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     fill_group(g, bf16, out, dev);
     const bool a_ok = K == 0 || (idx ? encode_2d(&maps.a, ab_type(bf16), A, K, rows, lda * 2, 64, 1,
                                                  CU_TENSOR_MAP_SWIZZLE_128B)
-                                     : set_operand(&maps.a, bf16, A, K, M, lda, 1, 0, 128));
+                                     : encode_2d(&maps.a, ab_type(bf16), A, K, M, lda * 2, 64, 128,
+                                                 CU_TENSOR_MAP_SWIZZLE_128B));
     const bool b_ok = K == 0 || (trans_b ? set_operand(&maps.b, bf16, B, N, K, ldb, groups, stride_b, 64)
                                          : set_operand(&maps.b, bf16, B, K, N, ldb, groups, stride_b,
                                                        f.pair ? f.bn / 2 : f.bn));
@@ -287,8 +288,8 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
     std::memset(&maps, 0, sizeof(maps));
     GroupArgs g;
     fill_group(g, bf16, out, dev);
-    if ((M > 0 && (!set_operand(&maps.a, bf16, dD, N, M, lddd, 1, 0, 64) ||
-                   !set_operand(&maps.b, bf16, A, K, M, lda, 1, 0, 64))) ||
+    if ((M > 0 && (!encode_2d(&maps.a, ab_type(bf16), dD, N, M, lddd * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                   !encode_2d(&maps.b, ab_type(bf16), A, K, M, lda * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))) ||
         !set_out(g, maps, dB, out, N, K, lddb, groups, stride_db))
         return GEMM_ERR_CUDA;
     g.groups = static_cast<int32_t>(groups);

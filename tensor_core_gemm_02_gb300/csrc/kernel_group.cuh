@@ -45,7 +45,7 @@ enum : int { kKindRows = 0, kKindSum = 1, kKindBatch = 2 };
 enum : int { kPrecAcc = 0, kPrecSums = 1, kPrecSplit = 2 };
 
 struct GroupMaps {
-    CUtensorMap a, b, d;           // 3-D (inner, rows, group); a is 2-D rows of a table when gathered
+    CUtensorMap a, b, d;           // stacks 3-D (inner, rows, group); one matrix's rows 2-D (D's always 3-D)
     CUtensorMap a_lo, b_lo, d_lo;  // the low parts (PREC_SPLIT; d_lo where D is written in two parts)
 };
 
@@ -180,6 +180,11 @@ struct GroupRows {
         base_last = __shfl_sync(0xffffffffu, start, who);
         blocks_last = __shfl_sync(0xffffffffu, blocks, who);
     }
+};
+
+template <bool V>
+struct Bool {
+    static constexpr bool value = V;
 };
 
 // One tile's place.
@@ -407,13 +412,15 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         rows[r] = v;
                 }
             }
-            for (int32_t kb = 0; kb < nkb; ++kb) {
+            // K block kb into the next stage; false if the kernel is aborting.  (Partial or not is
+            // a constant: as a condition at run time it cost a pair's main loop a quarter, 14336 x 4096
+            // summed over 4096 347 us against 246.)
+            auto fetch = [&](auto partial, int32_t kb) -> bool {
+                constexpr bool part = kSum && decltype(partial)::value;
                 if (!warp_wait_bounded<true>(empty_bar(s), ph ^ 1u, abort_flag, args.status, args.timeout_ns,
                                              kWhereProducerEmpty)) {
-                    alive = false;
-                    break;
+                    return false;
                 }
-                const bool part = kSum && rem != 0 && kb == nkb - 1;
                 const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
                 const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
                 const int32_t k = p.k0 + kb * Cfg::BK;
@@ -431,12 +438,21 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 __syncwarp();
                 // (a partial block is counted in this CTA, whose zeroing warp waits for it)
                 const uint32_t bar = part ? tail_bar(s) : lead(full_bar(s));
-                auto load = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
-                    if (PAIR && !part)
-                        tma_load_3d_pair(dst, m, bar, x, y, z);
-                    else
-                        tma_load_3d(dst, m, bar, x, y, z);
+                auto load = [&](auto stacked, uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
+                    if constexpr (decltype(stacked)::value) {
+                        if (PAIR && !part)
+                            tma_load_3d_pair(dst, m, bar, x, y, z);
+                        else
+                            tma_load_3d(dst, m, bar, x, y, z);
+                    } else {
+                        if (PAIR && !part)
+                            tma_load_2d_pair(dst, m, bar, x, y);
+                        else
+                            tma_load_2d(dst, m, bar, x, y);
+                    }
                 };
+                constexpr Bool<kBatch> kStackA{};   // (A is a stack, or rows of one matrix)
+                constexpr Bool<!kSum> kStackB{};
                 if (kRows && args.idx) {
                     if (PAIR)
                         tma_gather4_pair(sa + lane * 512u, &maps.a, bar, k, rows[0], rows[1], rows[2], rows[3]);
@@ -449,9 +465,9 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         const uint32_t to = sa + part2 * Cfg::A_BYTES;
                         if constexpr (kMnA) {
                             for (int j = 0; j < Cfg::BM / 64; ++j)
-                                load(to + j * 8192u, m, m0 + 64 * j, k, ga);
+                                load(kStackA, to + j * 8192u, m, m0 + 64 * j, k, ga);
                         } else {
-                            load(to, m, k, m0, ga);
+                            load(kStackA, to, m, k, m0, ga);
                         }
                     }
                 }
@@ -462,9 +478,9 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         const uint32_t to = sb + part2 * Cfg::B_BYTES;
                         if constexpr (kMnB) {
                             for (int j = 0; j < Cfg::BN_LOCAL / 64; ++j)
-                                load(to + j * 8192u, m, n0 + 64 * j, k, gb);
+                                load(kStackB, to + j * 8192u, m, n0 + 64 * j, k, gb);
                         } else {
-                            load(to, m, k, n0, gb);
+                            load(kStackB, to, m, k, n0, gb);
                         }
                     }
                 }
@@ -477,7 +493,13 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                     s = 0;
                     ph ^= 1u;
                 }
-            }
+                return true;
+            };
+            const int32_t whole = kSum && rem != 0 ? nkb - 1 : nkb;
+            for (int32_t kb = 0; kb < whole && alive; ++kb)
+                alive = fetch(Bool<false>{}, kb);
+            if (kSum && whole < nkb && alive)
+                alive = fetch(Bool<true>{}, whole);
         }
         if (!alive) {
             // every copy issued lands before the shared memory is released (bounded; the
@@ -526,18 +548,16 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 };
                 if (!wait_acc())
                     break;
-                for (int32_t kb = 0; kb < nkb; ++kb) {
+                auto multiply = [&](auto partial, int32_t kb) -> bool {
+                    constexpr bool part = kSum && decltype(partial)::value;
                     // (a chunk's sum goes to the epilogue, the next chunk starts from zero)
                     const bool begins = kSums ? kb % Cfg::CHUNK == 0 : kb == 0;
                     if (kSums && begins && kb > 0) {
                         next_acc();
-                        if (!wait_acc()) {
-                            alive = false;
-                            break;
-                        }
+                        if (!wait_acc())
+                            return false;
                     }
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
-                    const bool part = kSum && rem != 0 && kb == nkb - 1;
                     // (the peer's zeros: an acquire at cluster scope)
                     const bool got =
                         PAIR && part
@@ -545,10 +565,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                                                    kWhereMmaFull)
                             : wait_bounded<true>(full_bar(s), ph, abort_flag, args.status, args.timeout_ns,
                                                  kWhereMmaFull);
-                    if (!got) {
-                        alive = false;
-                        break;
-                    }
+                    if (!got)
+                        return false;
                     tc_fence_after_sync();
                     const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
                     const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
@@ -578,7 +596,13 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         s = 0;
                         ph ^= 1u;
                     }
-                }
+                    return true;
+                };
+                const int32_t whole = kSum && rem != 0 ? nkb - 1 : nkb;
+                for (int32_t kb = 0; kb < whole && alive; ++kb)
+                    alive = multiply(Bool<false>{}, kb);
+                if (kSum && whole < nkb && alive)
+                    alive = multiply(Bool<true>{}, whole);
                 if (!alive)
                     break;
                 next_acc();
