@@ -133,6 +133,23 @@ Span span_of(const Stack &s)
     return Span{one.p, one.bytes + static_cast<uint64_t>(s.depth - 1) * s.stride * s.m.esize};
 }
 
+// Few rows a group: the kernel that streams the weights, as (rows of a tile, CTAs a tile); rows
+// 0 where the tile kernel runs.
+struct Few {
+    int mp, cs;
+};
+Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
+{
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    const int64_t used = groups < M ? groups : M, rows = ceil_div(M, used);  // (of a group, on average)
+    if (K == 0 || (fk != 0 && fk != 2) || (fk == 0 && rows > 48))
+        return Few{0, 0};
+    const int mp = rows <= 8 ? 16 : (rows <= 16 ? 32 : 64);
+    const int64_t tiles = used * ceil_div(rows, mp) * ceil_div(N, 128);
+    return Few{mp, tiles >= 4 * sm_count || K < 256 ? 1 : 2};
+}
+
 bool bad_flag(int f) { return f != 0 && f != 1; }
 
 }  // namespace
@@ -194,7 +211,7 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     if (M == 0 || N == 0 || groups == 0)
         return GEMM_OK;
     auto most = [&](int tm, int bn) { return (M / tm + groups) * ceil_div(N, bn); };
-    if (most(128, 64) > kMaxDim)
+    if (most(16, 64) > kMaxDim)
         return GEMM_ERR_UNSUPPORTED;
     const int64_t rows = idx ? a_rows : M;
     const Mat a{A, lda, K > 0 ? rows : 0, K, 2, true}, d{D, ldd, M, N, out_size(out), false};
@@ -219,17 +236,25 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
         return st;
     const bool bf16 = dtype_is_bf16 == 1;
     const int prec = out == GEMM_OUT_F32 ? tcg::kPrecSums : tcg::kPrecAcc;
-    const tcg::host::GForm f = choose_form(ceil_div(K, 64), prec, dev->sm_count, tiles);
+    const Few few = choose_few(M, N, K, groups, dev->sm_count);
+    GForm f = choose_form(ceil_div(K, 64), prec, dev->sm_count, tiles);
     int grid = 0;
-    if ((st = group_grid(f, most(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK)
+    if (few.mp) {
+        f.pair = false;
+        f.bn = 128;
+        const int64_t n = most(few.mp, 128), sets = dev->sm_count / few.cs;
+        grid = static_cast<int>(few.cs * (n < sets ? n : sets));
+    } else if ((st = group_grid(f, most(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK) {
         return st;
+    }
     GroupMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     GroupArgs g;
     fill_group(g, bf16, out, dev);
     const bool a_ok = K == 0 || (idx ? encode_2d(&maps.a, ab_type(bf16), A, K, rows, lda * 2, 64, 1,
                                                  CU_TENSOR_MAP_SWIZZLE_128B)
-                                     : encode_2d(&maps.a, ab_type(bf16), A, K, M, lda * 2, 64, 128,
+                                     : encode_2d(&maps.a, ab_type(bf16), A, K, M, lda * 2, 64,
+                                                 static_cast<uint32_t>(few.mp ? few.mp : 128),
                                                  CU_TENSOR_MAP_SWIZZLE_128B));
     const bool b_ok = K == 0 || (trans_b ? set_operand(&maps.b, bf16, B, N, K, ldb, groups, stride_b, 64)
                                          : set_operand(&maps.b, bf16, B, K, N, ldb, groups, stride_b,
@@ -247,6 +272,11 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     g.idx = idx;
     g.table_rows = static_cast<int32_t>(rows);
     g.loads = K > 0 ? 1 : 0;
+    if (few.mp)
+        return tcg::launch_group_few(few.mp, few.cs, trans_b == 1, maps, g, grid, static_cast<cudaStream_t>(stream)) ==
+                       cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
     const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, prec, maps, g, grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }

@@ -185,6 +185,14 @@ __device__ __forceinline__ bool warp_wait_bounded(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+// As warp_wait_bounded, with the barrier read as an acquire at cluster scope.
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                                  uint32_t *status, uint64_t timeout_ns, uint32_t where)
+{
+    const bool ok = wait_bounded_cluster(bar, parity, abort_flag, status, timeout_ns, where);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // As warp_wait_bounded, with the loop inline: loads the waiting threads
 // still have in flight stay in flight (around a call, the live registers are
 // saved first, and saving a register waits for the load that fills it).

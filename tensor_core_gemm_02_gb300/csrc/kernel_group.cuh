@@ -299,6 +299,10 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         }
     }
     grid_dependency_wait();
+    // (the offsets come while the barriers and the tensor memory are set up)
+    GroupRows<TM> gr;
+    if constexpr (!kBatch)
+        gr.init(args.offsets, args.groups, args.rows, lane);
     tc_fence_before_sync();
     if (PAIR)
         cluster_sync_all();
@@ -310,14 +314,12 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         grid_launch_dependents();
 
     // ---- the tiles, as each warp finds them
-    GroupRows<TM> gr;
     int32_t num_tiles;
     if constexpr (kBatch) {
         const int32_t per = SYM ? (TM / BN) * (args.num_m_blocks * (args.num_m_blocks + 1) / 2)
                                 : args.num_m_blocks * args.num_n_blocks;
         num_tiles = args.groups * per;
     } else {
-        gr.init(args.offsets, args.groups, args.rows, lane);
         if (!gr.ok && blockIdx.x == 0 && threadIdx.x == 0)
             record_error(args.status, kStatusIndex, 0);
         if constexpr (kRows)

@@ -12,6 +12,10 @@ namespace tcg {
 // grid counts CTAs.  prec: kPrecAcc, or (bn 64 or 128) sums kept in registers.
 cudaError_t launch_group_rows(int bn, bool pair, bool b_major, int prec, const GroupMaps &maps, const GroupArgs &args,
                               int grid, cudaStream_t stream);
+// Few rows a group: tiles of mp (16, 32, 64) rows, each tile's sum shared by cs (1, 2) CTAs.
+// maps.a: boxes of mp rows (or a table's rows); maps.b: of 128 rows, or 64 x 64.
+cudaError_t launch_group_few(int mp, int cs, bool b_major, const GroupMaps &maps, const GroupArgs &args, int grid,
+                             cudaStream_t stream);
 cudaError_t launch_group_sum(int bn, bool pair, int prec, const GroupMaps &maps, const GroupArgs &args,
                              int grid, cudaStream_t stream);
 // (symmetric results: maj 0 or 3; others: maj 0 or 2; prec: kPrecAcc or kPrecSplit)

@@ -14,7 +14,7 @@ from tensor_core_gemm_02_gb300.workloads import OUT_BF16, OUT_F16, OUT_F32
 pytestmark = pytest.mark.gpu
 
 BF16, F16 = torch.bfloat16, torch.float16
-FORMS = {"auto": (0, 0), "single64": (1, 64), "single128": (1, 128), "single256": (1, 256), "pair256": (3, 256)}
+FORMS = {"auto": (0, 0), "few": (2, 0), "single64": (1, 64), "single128": (1, 128), "single256": (1, 256), "pair256": (3, 256)}
 KINDS = ((BF16, OUT_F32), (F16, OUT_BF16), (BF16, OUT_F16))
 # rows of each group, and rows outside every group in front and behind
 GROUPS = {
