@@ -396,11 +396,6 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
         (p.split && (!map_a(&maps.a_lo, p.A + p.a_lo) || !map_b(&maps.b_lo, p.B + p.b_lo))))
         return GEMM_ERR_CUDA;
     const int64_t cols = p.padded ? p.ldd : p.N;
-    if (p.d_lo != 0) {  // (a workspace: both parts alike)
-        if (!set_out(g, maps, static_cast<uint16_t *>(p.D) + p.d_lo, p.out, p.M, cols, p.ldd, p.count, p.stride_d))
-            return GEMM_ERR_CUDA;
-        maps.d_lo = maps.d;
-    }
     if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d))
         return GEMM_ERR_CUDA;
     g.c_lo = p.c_lo;

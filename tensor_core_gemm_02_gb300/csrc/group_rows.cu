@@ -3,15 +3,19 @@
 // order lists the positions 0 .. M - 1 by ids[i], equal ones in their order; ids outside
 // [0, groups) come last, in a bucket of their own.  offsets[g] is the number of ids below g.
 //
-// A warp takes a run of consecutive ids, 32 at a time: __match_any_sync names the lanes with
-// a lane's id, so the lowest of them adds their number to the warp's count (first pass) or
-// its place (second pass), and a lane's own place is that plus the number of such lanes
-// before it.  No atomics: the order of nothing depends on timing.  Between the passes the
-// counts of a thread block's 32 warps become places, bucket by bucket.  Up to 65536 ids one
-// block does it all; more are cut into chunks, a first kernel counts each chunk's, and every
-// block of the second adds up the counts before its own.
+// A warp takes a run of consecutive ids, 32 at a time.  First pass: each id counts one in its
+// warp's bucket (shared-memory atomics; a count does not depend on their order).  Then the
+// counts become places, bucket by bucket: behind all ids of lower buckets and, within one,
+// behind the thread blocks and warps before.  Second pass: the lanes with a lane's id are
+// those whose bits agree (a ballot a bit), a lane's place is its warp's next one plus the
+// number of such lanes before it, and the lowest of them moves the warp's next place on.  The
+// order of nothing depends on timing.  (__match_any_sync instead of the ballots, in one block:
+// 16384 ids of 64 groups 27 us.)
 //
-// Bound by latency: two passes over the ids, each 32 ids a warp and step.
+// Up to 32 a warp one thread block does it all, up to 131072 ids a cluster of eight, whose
+// blocks read one another's counts; more are cut into chunks, whose counts a first kernel
+// leaves in memory.  Bound by latency: a few dependent steps, each a round trip to shared
+// memory or L2.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -48,22 +52,7 @@ __device__ __forceinline__ void for_ids(const int32_t *ids, int64_t lo, int64_t 
     }
 }
 
-// counts[w (groups + 1) + b]: this warp's ids in bucket b
-__device__ __forceinline__ void count_ids(const int32_t *ids, int64_t lo, int64_t hi, int32_t groups,
-                                          uint32_t lane, int32_t *mine)
-{
-    for_ids(ids, lo, hi, groups, lane, [&](int64_t, int32_t b, bool there) {
-        const uint32_t live = __ballot_sync(0xffffffffu, there);
-        if (there) {
-            const uint32_t same = __match_any_sync(live, b);
-            if (lane == static_cast<uint32_t>(__ffs(same)) - 1u)
-                mine[b] += __popc(same);
-        }
-        __syncwarp();
-    });
-}
-
-// The chunk [lo, hi) of thread block `chunk`, cut into its warps' runs.
+// The ids [lo, hi) of a thread block, cut into its warps' runs.
 struct Run {
     int64_t lo, hi;
 };
@@ -75,28 +64,43 @@ __device__ __forceinline__ Run warp_run(int64_t lo, int64_t hi, uint32_t warp)
     return Run{a < hi ? a : hi, a + per < hi ? a + per : hi};
 }
 
+// First pass: counts[w nb + b], warp w's ids in bucket b, and all[b] their sum over the warps.
+__device__ __forceinline__ void count_ids(const int32_t *ids, const Run &r, int32_t groups, int32_t *counts,
+                                          int32_t *all)
+{
+    const int32_t nb = groups + 1;
+    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    for (int32_t i = threadIdx.x; i < nb * kSortWarps; i += kSortThreads)
+        counts[i] = 0;
+    __syncthreads();
+    for_ids(ids, r.lo, r.hi, groups, lane, [&](int64_t, int32_t b, bool there) {
+        if (there)
+            atomicAdd(counts + warp * nb + b, 1);
+    });
+    __syncthreads();
+    for (int32_t b = threadIdx.x; b < nb; b += kSortThreads) {
+        int32_t sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w)
+            sum += counts[w * nb + b];
+        all[b] = sum;
+    }
+}
+
 __global__ void __launch_bounds__(kSortThreads)
     group_count_kernel(const int32_t *ids, int64_t M, int64_t chunk, int32_t groups, int32_t *counts)
 {
     extern __shared__ int32_t sh[];
     const int32_t nb = groups + 1;
-    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
     grid_dependency_wait();
-    for (int32_t i = threadIdx.x; i < nb * kSortWarps; i += kSortThreads)
-        sh[i] = 0;
-    __syncthreads();
-    const int64_t lo = chunk * blockIdx.x, hi = lo + chunk < M ? lo + chunk : M;
-    const Run r = warp_run(lo, hi, warp);
-    count_ids(ids, r.lo, r.hi, groups, lane, sh + warp * nb);
-    __syncthreads();
-    for (int32_t b = threadIdx.x; b < nb; b += kSortThreads) {
-        int32_t sum = 0;
-        for (int w = 0; w < kSortWarps; ++w)
-            sum += sh[w * nb + b];
-        counts[static_cast<int64_t>(blockIdx.x) * nb + b] = sum;
-    }
+    const int64_t lo = chunk * blockIdx.x < M ? chunk * blockIdx.x : M, hi = lo + chunk < M ? lo + chunk : M;
+    count_ids(ids, warp_run(lo, hi, threadIdx.x / 32u), groups, sh,
+              counts + static_cast<int64_t>(blockIdx.x) * nb);
 }
 
+// CLUSTER: the grid is one cluster, whose blocks read one another's counts; otherwise
+// (several blocks) `counts` has every block's.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSortThreads)
     group_place_kernel(const int32_t *ids, int64_t M, int64_t chunk, int32_t groups, int32_t choices,
                        const int32_t *counts, int32_t *offsets, int32_t *order, int32_t *rows)
@@ -104,36 +108,32 @@ __global__ void __launch_bounds__(kSortThreads)
     extern __shared__ int32_t sh[];
     __shared__ int32_t warp_sum[kSortWarps];
     const int32_t nb = groups + 1;
+    int32_t *all = sh + nb * kSortWarps;
     const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int32_t i = threadIdx.x; i < nb * kSortWarps; i += kSortThreads)
-        sh[i] = 0;
-    __syncthreads();
-    const int64_t lo = chunk * blockIdx.x, hi = lo + chunk < M ? lo + chunk : M;
+    const int64_t lo = chunk * blockIdx.x < M ? chunk * blockIdx.x : M, hi = lo + chunk < M ? lo + chunk : M;
     const Run r = warp_run(lo, hi, warp);
-    count_ids(ids, r.lo, r.hi, groups, lane, sh + warp * nb);
-    __syncthreads();
-    // counts -> places: bucket b starts behind all ids of lower buckets and, within it, behind
-    // the chunks and warps before
+    count_ids(ids, r, groups, sh, all);
+    if (CLUSTER)
+        cluster_sync_all();
+    else
+        __syncthreads();
     int32_t carry = 0;
     for (int32_t b0 = 0; b0 < nb; b0 += kSortThreads) {
         const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
-        int32_t here = 0, before = 0, all = 0;
+        int32_t before = 0, total_b = 0;  // ids of the bucket in the blocks before, and in all
         if (b < nb) {
-            for (int w = 0; w < kSortWarps; ++w)
-                here += sh[w * nb + b];
-            all = here;
-            if (gridDim.x > 1) {
-                all = 0;
-                for (uint32_t c = 0; c < gridDim.x; ++c) {
-                    const int32_t n = __ldcg(counts + static_cast<int64_t>(c) * nb + b);
-                    before += c < blockIdx.x ? n : 0;
-                    all += n;
-                }
+#pragma unroll 8
+            for (uint32_t c = 0; c < gridDim.x; ++c) {
+                const int32_t n = gridDim.x == 1 ? all[b]
+                                  : CLUSTER      ? static_cast<int32_t>(ld_shared_cluster_u32(mapa_shared(smem_u32(all + b), c)))
+                                                 : __ldcg(counts + static_cast<int64_t>(c) * nb + b);
+                before += c < blockIdx.x ? n : 0;
+                total_b += n;
             }
         }
-        int32_t sum = all;
+        int32_t sum = total_b;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int32_t x = __shfl_up_sync(0xffffffffu, sum, d);
@@ -144,17 +144,19 @@ __global__ void __launch_bounds__(kSortThreads)
             warp_sum[warp] = sum;
         __syncthreads();
         int32_t lower = carry, total = 0;
+#pragma unroll
         for (uint32_t w = 0; w < kSortWarps; ++w) {
             const int32_t x = warp_sum[w];
             lower += w < warp ? x : 0;
             total += x;
         }
         carry += total;
-        const int32_t start = lower + sum - all;
+        const int32_t start = lower + sum - total_b;
         if (b < nb) {
             if (blockIdx.x == 0)
                 offsets[b] = start;
             int32_t at = start + before;
+#pragma unroll 8
             for (int w = 0; w < kSortWarps; ++w) {
                 const int32_t n = sh[w * nb + b];
                 sh[w * nb + b] = at;
@@ -164,12 +166,16 @@ __global__ void __launch_bounds__(kSortThreads)
         __syncthreads();
     }
     int32_t *mine = sh + warp * nb;
+    const int bits = 32 - __clz(groups);  // of a bucket's number, at most `groups`
     for_ids(ids, r.lo, r.hi, groups, lane, [&](int64_t i, int32_t b, bool there) {
-        const uint32_t live = __ballot_sync(0xffffffffu, there);
+        uint32_t same = __ballot_sync(0xffffffffu, there);
+        for (int k = 0; k < bits; ++k) {
+            const uint32_t bit = __ballot_sync(0xffffffffu, (b >> k) & 1);
+            same &= ((b >> k) & 1) ? bit : ~bit;
+        }
+        const int32_t at = mine[b] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
         if (there) {
-            const uint32_t same = __match_any_sync(live, b);
-            const int32_t at = mine[b] + __popc(same & ((1u << lane) - 1u));
-            __syncwarp(live);
             if (lane == static_cast<uint32_t>(__ffs(same)) - 1u)
                 mine[b] += __popc(same);
             order[at] = static_cast<int32_t>(i);
@@ -178,6 +184,8 @@ __global__ void __launch_bounds__(kSortThreads)
         }
         __syncwarp();
     });
+    if (CLUSTER)
+        cluster_sync_all();  // (every block has read this one's counts)
 }
 
 }  // namespace
@@ -186,29 +194,36 @@ cudaError_t launch_group_rows_sort(const int32_t *ids, int64_t M, int32_t groups
                                    int32_t *offsets, int32_t *order, int32_t *rows, int32_t *counts,
                                    int32_t chunks, cudaStream_t stream)
 {
-    const uint32_t smem = static_cast<uint32_t>((groups + 1) * kSortWarps * sizeof(int32_t));
-    static std::atomic<uint64_t> done_count{0}, done_place{0};
-    cudaError_t e;
-    if ((e = allow_smem(reinterpret_cast<const void *>(group_count_kernel), 1025 * 128, done_count)) !=
-            cudaSuccess ||
-        (e = allow_smem(reinterpret_cast<const void *>(group_place_kernel), 1025 * 128, done_place)) !=
-            cudaSuccess)
+    const uint32_t most = 1025 * (kSortWarps + 1) * sizeof(int32_t);
+    static std::atomic<uint64_t> done_count{0}, done_place{0}, done_cluster{0};
+    const bool cluster = chunks == 1 && M > kSortThreads;
+    const int64_t blocks = cluster ? 8 : chunks;
+    auto place = cluster ? group_place_kernel<true> : group_place_kernel<false>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(place), most, cluster ? done_cluster : done_place);
+    if (e != cudaSuccess)
         return e;
-    const int64_t chunk = chunks > 1 ? (M + chunks - 1) / chunks : M;
+    if (chunks > 1 && (e = allow_smem(reinterpret_cast<const void *>(group_count_kernel), most, done_count)) != cudaSuccess)
+        return e;
+    const int64_t chunk = (M + blocks - 1) / blocks;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(chunks), 1, 1);
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = static_cast<uint32_t>((groups + 1) * (kSortWarps + 1) * sizeof(int32_t));
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = TCG_PDL;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 8;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (chunks > 1 && (e = cudaLaunchKernelEx(&cfg, group_count_kernel, ids, M, chunk, groups, counts)) != cudaSuccess)
         return e;
-    return cudaLaunchKernelEx(&cfg, group_place_kernel, ids, M, chunk, groups, choices,
-                              static_cast<const int32_t *>(counts), offsets, order, rows);
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, place, ids, M, chunk, groups, choices, static_cast<const int32_t *>(counts),
+                              offsets, order, rows);
 }
 
 }  // namespace tcg

@@ -25,8 +25,8 @@
 //   PREC_SPLIT  as PREC_SUMS, and both operands are pairs of float16 matrices, a high part and
 //               the rest: high x high + high x low + low x high, 22 bits of each operand.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), warps 2-5
-// epilogue, (KIND_SUM) warp 6 zeroes.  Two TMEM accumulators: the epilogue of one tile
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), then four or
+// eight epilogue warps, (KIND_SUM) one that zeroes.  Two TMEM accumulators: the epilogue of one tile
 // runs beside the next tile's MMAs.  PAIR: the roles on a CTA pair and one 256 x 256 tile
 // (tcgen05 cta_group::2), each CTA loading its 128 rows of A and its half of B.  The
 // protocol is the tile kernel's (kernel_tile.cuh).  Every wait is bounded.
@@ -46,7 +46,7 @@ enum : int { kPrecAcc = 0, kPrecSums = 1, kPrecSplit = 2 };
 
 struct GroupMaps {
     CUtensorMap a, b, d;           // stacks 3-D (inner, rows, group); one matrix's rows 2-D (D's always 3-D)
-    CUtensorMap a_lo, b_lo, d_lo;  // the low parts (PREC_SPLIT; d_lo where D is written in two parts)
+    CUtensorMap a_lo, b_lo;        // the operands' low parts (PREC_SPLIT)
 };
 
 struct GroupArgs {
@@ -85,12 +85,18 @@ struct GroupCfg {
     static constexpr uint32_t A_BYTES = BM * 128u, B_BYTES = BN_LOCAL * 128u;
     static constexpr uint32_t STAGE_BYTES = PARTS * (A_BYTES + B_BYTES);
     static constexpr uint32_t OFF_A = 0, OFF_B = STAGES * PARTS * A_BYTES;
-    static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes, two a warp
+    static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes; two a warp, or (two groups) one
     static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_EPI + 8 * EPI_BUF;
     static constexpr uint32_t NUM_BARS = 3 * STAGES + 4;
     static constexpr uint32_t SMEM_ALLOC = OFF_BAR + NUM_BARS * 8 + 16 + 1024;
-    static constexpr int THREADS = 32 * (KIND_ == kKindSum ? 7 : 6);
+    // Epilogue groups of four warps: two, half of the columns each, but for the narrowest
+    // tiles.  (A warp's chain of TMEM load, conversion, shared image and store is all latency:
+    // about 1 us for 64 columns.)
+    static constexpr int EPI_GROUPS = BN >= 128 ? 2 : 1;
+    static constexpr int COLS = BN / EPI_GROUPS;
+    static constexpr int ZERO_WARP = 2 + 4 * EPI_GROUPS;  // (KIND_SUM)
+    static constexpr int THREADS = 32 * (ZERO_WARP + (KIND_ == kKindSum ? 1 : 0));
     static constexpr uint32_t TMEM_COLS = 2 * BN;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), PAIR ? 8 : 4);
+            mbar_init(acce_bar(b), (PAIR ? 8 : 4) * Cfg::EPI_GROUPS);
         }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             }
         }
         __syncwarp();
-    } else if (kSum && warp == 6) {
+    } else if (kSum && warp == Cfg::ZERO_WARP) {
         // ------------------------------------------------------------ zeroing warp
         if constexpr (kSum) {
             int s = 0;
@@ -651,38 +657,201 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         }
     } else {
         // ------------------------------------------------------------ epilogue
+        constexpr bool kF32 = kSums && !kBatch;  // (the products over groups sum in registers for float32 only)
+        constexpr int kCols = Cfg::COLS;
+        constexpr bool kOne = Cfg::EPI_GROUPS == 2;  // one buffer a warp
         const uint32_t q = warp & 3u;
-        const uint32_t buf0 = base + Cfg::OFF_EPI + q * 2u * Cfg::EPI_BUF;
-        const bool f32 = args.out_kind == kOutF32;
+        const int32_t col_g = kOne && warp >= 6u ? kCols : 0;  // first column of this group of warps
+        const uint32_t buf0 = base + Cfg::OFF_EPI + (kOne ? 4u * (warp >= 6u ? 1u : 0u) + q : 2u * q) * Cfg::EPI_BUF;
+        const bool f32 = kF32 || args.out_kind == kOutF32;
         const uint32_t esize = f32 ? 4u : 2u;
         const int32_t wide = f32 ? 32 : 64;  // columns of a 128-byte row
         // TMA stores whole 16 bytes of a row: D's descriptor ends with the last whole ones
         const int32_t n_tma = args.n_out & ~(f32 ? 3 : 7);
         const uint64_t policy = l2_policy_evict_first();
+        auto pack2 = [&](float x, float y) {
+            return args.out_kind == kOutBF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+        };
         int ab = 0;
         uint32_t aph = 0, slot = 0;
-        for (int32_t t = cta_set; t < num_tiles; t += cta_sets) {
+        bool alive = true;
+        for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
             const GroupTile p = locate(t);
             int32_t rem;
             const int32_t nkb = blocks_of(t, rem);
             const int32_t row0 = p.row0 + static_cast<int32_t>(role) * Cfg::BM + 32 * static_cast<int32_t>(q);
             const int32_t nrows = min(32, p.end - row0);
             const int32_t my_row = row0 + static_cast<int32_t>(lane);
+            const int32_t n_g = p.n0 + col_g;  // first column of D
+            const bool stores = nrows > 0 && n_g < args.N;
             bool zero = nkb == 0;
             if (kRows && args.idx && my_row < p.end) {
                 const int32_t v = __ldcg(args.idx + my_row);
                 zero = zero || v < 0 || v >= args.table_rows;
             }
-            // (SYM: the second half of a matrix's last diagonal block may lie past its end)
-            const int32_t chunks = max(1, min(BN / wide, (args.N - p.n0 + wide - 1) / wide));
             uint8_t *d_g = static_cast<uint8_t *>(args.D) + (kRows ? 0 : p.g * args.stride_d * esize);
-            const uint16_t *c_row = nullptr;
-            if (kBatch && args.C && my_row < p.end)
-                c_row = args.C + p.g * args.stride_c + static_cast<int64_t>(my_row) * args.ldc + p.n0;
-            // accumulators as they fill: the last (only) one's address, or (PREC_SUMS) all added up
-            // in registers and handed back
-            float sums[kSums ? BN : 1];
-            uint32_t acc0 = 0;
+            // C's high and low parts for 32 columns of this lane's row (from L2: written by the kernel
+            // before)
+            const uint16_t *c_row =
+                kBatch && args.C && my_row < p.end
+                    ? args.C + p.g * args.stride_c + static_cast<int64_t>(my_row) * args.ldc + n_g
+                    : nullptr;
+            struct CPart {
+                uint4 hi[4], lo[4];
+            };
+            auto load_c = [&](int32_t col, CPart &c) {
+                if constexpr (kBatch) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        c.hi[i] = c.lo[i] = make_uint4(0, 0, 0, 0);
+                        if (c_row && n_g + col + 8 * i < args.N) {
+                            c.hi[i] = __ldcg(reinterpret_cast<const uint4 *>(c_row + col + 8 * i));
+                            if (args.c_lo)
+                                c.lo[i] = __ldcg(reinterpret_cast<const uint4 *>(c_row + args.c_lo + col + 8 * i));
+                        }
+                    }
+                }
+            };
+            // alpha sum + beta C
+            auto finish = [&](float(&v)[32], const CPart &c) {
+                if (kBatch && args.C) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int sh = 16 * (i & 1);
+                        const uint32_t w = reinterpret_cast<const uint32_t *>(c.hi)[i / 2];
+                        const uint32_t wl = reinterpret_cast<const uint32_t *>(c.lo)[i / 2];
+                        const float x = cvt_f16_f32(static_cast<uint16_t>(w >> sh)) +
+                                        cvt_f16_f32(static_cast<uint16_t>(wl >> sh));
+                        v[i] = fma_rn(args.alpha, v[i], mul_rn(args.beta, x));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = zero ? 0.f : mul_rn(args.alpha, v[i]);
+                }
+            };
+            // a 128-byte row a lane, from column col of this group's, to D
+            auto put = [&](int32_t col, const uint32_t(&w)[32]) {
+                const int32_t col0 = n_g + col;
+                if (nrows <= 0 || col0 >= args.N)
+                    return;
+                const uint32_t buf = buf0 + (kOne ? 0u : slot * Cfg::EPI_BUF);
+                slot ^= 1u;
+                if (lane == 0) {  // the last store that used the buffer has read it
+                    if (kOne)
+                        bulk_wait_group_read<0>();
+                    else
+                        bulk_wait_group_read<1>();
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_shared_v4(buf + swz128(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                // a whole box by TMA; rows that end with the group (KIND_ROWS; the others' boxes
+                // end with their matrix), or columns past the last whole 16 bytes, by plain stores
+                const bool tma = args.d_tma && (!kRows || nrows == 32) && (col0 + wide <= n_tma || n_tma == args.n_out);
+                if (tma) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kBatch)  // (read by the next product)
+                            tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                        else
+                            tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.g, policy);
+                    }
+                } else {
+                    __syncwarp();
+                    store_image_rows(buf, lane, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
+                    __syncwarp();
+                }
+                if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
+                    bulk_commit_group();
+            };
+            // 32 columns from col, a second time: D[column][row], two neighbouring rows' values from
+            // a lane and its neighbour, two rows of D per pair of columns.  (All shuffles first: a
+            // store with its own condition after each took 180 cycles a pair.)
+            auto mirror = [&](int32_t col, const float(&v)[32], int64_t part) {
+                const bool odd = (lane & 1u) != 0u;
+                uint32_t x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+                    x[i] = odd ? pack_f16x2(other, v[2 * i + 1]) : pack_f16x2(v[2 * i], other);
+                }
+                const int32_t r = n_g + col + (odd ? 1 : 0), c = my_row & ~1;
+                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + static_cast<int64_t>(r) * args.ldd + c;
+                const int64_t step = 2 * args.ldd;
+                if (n_g + col + 32 <= args.N && nrows == 32) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        *reinterpret_cast<uint32_t *>(d + i * step) = x[i];
+                } else {
+                    // (an odd size: the last pair's second element goes into the row's padding)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (r + 2 * i < args.N && c < p.end)
+                            *reinterpret_cast<uint32_t *>(d + i * step) = x[i];
+                }
+            };
+            // 32 columns of this lane's row to a workspace, in 16-byte pieces (its rows are whole ones)
+            auto store_row = [&](int32_t col, const uint32_t(&w)[16], int64_t part) {
+                if (my_row >= p.end)
+                    return;
+                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + static_cast<int64_t>(my_row) * args.ldd + n_g + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n_g + col + 8 * i < args.n_out)
+                        *reinterpret_cast<uint4 *>(d + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            };
+            // 64 columns from col, their sums 32 at a time from take(half, v), C's elements from
+            // c (the first half's) and next(half) (those of the half after it)
+            auto piece = [&](int32_t col, CPart &c, auto take, auto next) {
+                uint32_t w[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    take(h, v);
+                    if (!stores)
+                        continue;
+                    finish(v, c);
+                    next(h);
+                    if (f32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = __float_as_uint(v[i]);
+                        put(col + 32 * h, w);
+                    }
+                    if constexpr (kF32)
+                        continue;
+                    else if (f32)
+                        continue;
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    if (SYM && p.mirror)
+                        mirror(col + 32 * h, v, 0);
+                    if (kBatch && args.d_lo) {
+                        store_row(col + 32 * h, x, 0);
+                        // what rounding to float16 left of the values
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] -= cvt_f16_f32(static_cast<uint16_t>(x[i / 2] >> (16 * (i & 1))));
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+                        store_row(col + 32 * h, x, args.d_lo);
+                        if (SYM && p.mirror)
+                            mirror(col + 32 * h, v, args.d_lo);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[16 * h + i] = x[i];
+                        if (h == 1)
+                            put(col, w);
+                    }
+                }
+            };
             auto hand_back = [&]() {
                 tc_fence_before_sync();
                 __syncwarp();
@@ -697,21 +866,23 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                     aph ^= 1u;
                 }
             };
-            bool alive = true;
-            const int32_t fills = kSums ? max(1, (nkb + Cfg::CHUNK - 1) / max(1, Cfg::CHUNK)) : 1;
-            for (int32_t f = 0; f < fills; ++f) {
-                if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
-                                             kWhereEpiAccFull)) {
-                    alive = false;
-                    break;
-                }
+            auto wait_full = [&]() {
+                alive = warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                                kWhereEpiAccFull);
                 tc_fence_after_sync();
-                acc0 = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN);
-                if constexpr (kSums) {
+                return tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN + col_g);
+            };
+            if constexpr (kSums) {
+                float sums[kCols];
+                const int32_t fills = max(1, (nkb + Cfg::CHUNK - 1) / Cfg::CHUNK);
+                for (int32_t f = 0; f < fills; ++f) {
+                    const uint32_t acc = wait_full();
+                    if (!alive)
+                        break;
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) {
+                    for (int c = 0; c < kCols / 32; ++c) {
                         uint32_t r[32];
-                        tc_ld_32x32b_x32(acc0 + 32u * c, r);
+                        tc_ld_32x32b_x32(acc + 32u * c, r);
                         tc_wait_ld(r);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -720,169 +891,51 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                     }
                     hand_back();
                 }
-            }
-            if (!alive)
-                break;
-            // 32 columns from col of this lane's row, in v: alpha sum + beta C
-            auto finish = [&](int32_t col, float(&v)[32]) {
-                if (kBatch && args.C) {
-                    uint4 c[4], cl[4];
+                if (!alive)
+                    break;
+                CPart c;
+                if (stores)
+                    load_c(0, c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool there = c_row && p.n0 + col + 8 * i < args.N;
-                        c[i] = there ? *reinterpret_cast<const uint4 *>(c_row + col + 8 * i) : make_uint4(0, 0, 0, 0);
-                        cl[i] = there && args.c_lo
-                                    ? *reinterpret_cast<const uint4 *>(c_row + args.c_lo + col + 8 * i)
-                                    : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int sh = 16 * (i & 1);
-                        const uint32_t w = reinterpret_cast<const uint32_t *>(c)[i / 2];
-                        const uint32_t wl = reinterpret_cast<const uint32_t *>(cl)[i / 2];
-                        const float x = cvt_f16_f32(static_cast<uint16_t>(w >> sh)) +
-                                        cvt_f16_f32(static_cast<uint16_t>(wl >> sh));
-                        v[i] = fma_rn(args.alpha, v[i], mul_rn(args.beta, x));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = zero ? 0.f : mul_rn(args.alpha, v[i]);
-                }
-            };
-            auto pack2 = [&](float a, float b) {
-                return args.out_kind == kOutBF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
-            };
-            // what rounding to float16 leaves of the values
-            auto rest = [&](float(&v)[32]) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] -= cvt_f16_f32(f32_to_f16_rn(v[i]));
-            };
-            // columns col .. col + 31 of the tile, a second time: D[column][row], two columns of
-            // D's row from a lane and its neighbour, two rows of D per pair of columns
-            auto mirror = [&](int32_t col, const float(&v)[32], int64_t part) {
-                const int32_t c = my_row & ~1;
-                const bool odd = (lane & 1u) != 0u;
-                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + c;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                    const uint32_t w = odd ? pack2(other, v[i + 1]) : pack2(v[i], other);
-                    const int32_t r = p.n0 + col + i + (odd ? 1 : 0);
-                    // (an odd size: the last pair's second element goes into the row's padding)
-                    if (r < args.N && c < p.end)
-                        *reinterpret_cast<uint32_t *>(d + static_cast<int64_t>(r) * args.ldd) = w;
-                }
-            };
-            // a 128-byte row a lane, from column col of the tile, to D (part 0) or its low part
-            auto put = [&](int32_t col, const uint32_t(&w)[32], bool low) {
-                const int32_t col0 = p.n0 + col;
-                if (nrows <= 0 || col0 >= args.N)
-                    return;
-                const uint32_t buf = buf0 + slot * Cfg::EPI_BUF;
-                slot ^= 1u;
-                if (lane == 0)
-                    bulk_wait_group_read<1>();  // the store before the last has left this buffer
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    st_shared_v4(buf + swz128(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                // a whole box by TMA; rows that end with the group (KIND_ROWS; the others' boxes
-                // end with their matrix), or columns past the last whole 16 bytes, by plain stores
-                const bool tma = args.d_tma && (!kRows || nrows == 32) && (col0 + wide <= n_tma || n_tma == args.n_out);
-                if (tma) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (kBatch)  // (read by the next product)
-                            tma_store_3d(low ? &maps.d_lo : &maps.d, buf, col0, row0, p.g);
-                        else
-                            tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.g, policy);
-                    }
-                } else {
-                    __syncwarp();
-                    store_image_rows(buf, lane, nrows, esize, d_g + (low ? args.d_lo * 2 : 0), args.ldd, row0, col0,
-                                     args.n_out, args.d_vec != 0);
-                    __syncwarp();
-                }
-                if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
-                    bulk_commit_group();
-            };
-            // 32 columns: from registers, or from the accumulator
-            auto take = [&](int c32, float(&v)[32]) {
-                if constexpr (kSums) {
-#pragma unroll
-                    for (int c = 0; c < BN / 32; ++c)  // (selects: registers have no addresses)
-                        if (c == c32) {
+                for (int col = 0; col < kCols; col += 64)
+                    piece(
+                        col, c,
+                        [&](int h, float(&v)[32]) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[i] = sums[32 * c + i];
-                        }
-                } else {
-                    uint32_t r[32];
-                    tc_ld_32x32b_x32(acc0 + 32u * static_cast<uint32_t>(c32), r);
-                    tc_wait_ld(r);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = __uint_as_float(r[i]);
-                }
-                finish(32 * c32, v);
-            };
-            const int per = wide / 32;
-            auto piece = [&](int c, bool last) {
-                const int32_t col = c * wide;
-                uint32_t w[32], wl[32];
-                const bool two = kBatch && args.d_lo != 0;
-                float v[32];
-                take(c * per, v);
-                if (SYM && p.mirror)
-                    mirror(col, v, 0);
-                if (f32) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack2(v[2 * i], v[2 * i + 1]);
-                    if (two) {
-                        rest(v);
-                        if (SYM && p.mirror)
-                            mirror(col, v, args.d_lo);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            wl[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
-                    }
-                    take(c * per + 1, v);
-                    if (SYM && p.mirror)
-                        mirror(col + 32, v, 0);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[16 + i] = pack2(v[2 * i], v[2 * i + 1]);
-                    if (two) {
-                        rest(v);
-                        if (SYM && p.mirror)
-                            mirror(col + 32, v, args.d_lo);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            wl[16 + i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
-                    }
-                }
-                if (!kSums && last)
-                    hand_back();
-                put(col, w, false);
-                if (two)
-                    put(col, wl, true);
-            };
-            if constexpr (kSums) {
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c)
-                    if (c < chunks)
-                        piece(c, false);
+                                v[i] = sums[col + 32 * h + i];
+                        },
+                        [&](int h) {
+                            if (col + 32 * h + 32 < kCols)
+                                load_c(col + 32 * h + 32, c);
+                        });
             } else {
-                for (int32_t c = 0; c < chunks; ++c)
-                    piece(c, c == chunks - 1);
+                // (C's first loads go out before the wait for the accumulator, the others as soon as the
+                // registers of the ones before are free)
+                CPart c;
+                if (stores)
+                    load_c(0, c);
+                const uint32_t acc = wait_full();
+                if (!alive)
+                    break;
+#pragma unroll 1
+                for (int32_t col = 0; col < kCols; col += 64)
+                    piece(
+                        col, c,
+                        [&](int h, float(&v)[32]) {
+                            uint32_t r[32];
+                            tc_ld_32x32b_x32(acc + static_cast<uint32_t>(col + 32 * h), r);
+                            tc_wait_ld(r);
+                            if (h == 1 && col + 64 >= kCols)
+                                hand_back();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __uint_as_float(r[i]);
+                        },
+                        [&](int h) {
+                            if (col + 32 * h + 32 < kCols)
+                                load_c(col + 32 * h + 32, c);
+                        });
             }
         }
         if (lane == 0)

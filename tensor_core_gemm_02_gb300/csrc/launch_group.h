@@ -25,8 +25,8 @@ cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, int prec, c
 // The stable order of M ids by value: offsets (groups + 1), order and rows (each M; rows
 // may be NULL: order[i] / choices).  counts: `chunks` x (groups + 1) int32 (unused for one
 // chunk).
-constexpr int64_t kGroupRowsChunk = 16384;  // ids a thread block sorts, where there are several
-constexpr int64_t kGroupRowsOne = 65536;    // up to this many, one does
+constexpr int64_t kGroupRowsChunk = 16384;  // ids a thread block sorts, where there are chunks
+constexpr int64_t kGroupRowsOne = 131072;   // up to this many, one launch does
 cudaError_t launch_group_rows_sort(const int32_t *ids, int64_t M, int32_t groups, int32_t choices,
                                    int32_t *offsets, int32_t *order, int32_t *rows, int32_t *counts,
                                    int32_t chunks, cudaStream_t stream);

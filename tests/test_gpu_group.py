@@ -291,8 +291,8 @@ def test_gradients_against_differences():
 
 # ---------------------------------------------------------------- rows by group
 
-@pytest.mark.parametrize("M,E,choices", [(0, 3, 1), (1, 1, 1), (32, 8, 2), (33, 8, 1), (1000, 0, 1), (1025, 1024, 1),
-                                         (16384, 64, 2), (65536, 256, 4), (65537, 5, 1), (200000, 1024, 2),
+@pytest.mark.parametrize("M,E,choices", [(0, 3, 1), (1, 1, 1), (32, 8, 2), (33, 8, 1), (1000, 0, 1), (1024, 7, 1), (1025, 1024, 1), (1030, 3, 2),
+                                         (16384, 64, 2), (65536, 256, 4), (65537, 5, 1), (131072, 1000, 2), (131073, 5, 1), (200000, 1024, 2),
                                          (3000000, 17, 1)])
 def test_group_rows(M, E, choices):
     gen = torch.Generator().manual_seed(M + E)
