@@ -82,8 +82,10 @@ void fill_group(GroupArgs &a, bool bf16, int out, const DeviceInfo *dev)
 }
 
 // D of a launch: `depth` matrices of rows x cols; false if the descriptor was refused.
+// d_lo != 0 (16 bits): in two parts, the second d_lo elements behind the first; narrow: boxes of
+// 32 columns.
 bool set_out(GroupArgs &a, GroupMaps &maps, void *D, int out, int64_t rows, int64_t cols, int64_t ld,
-             int64_t depth, int64_t stride)
+             int64_t depth, int64_t stride, int64_t d_lo = 0, bool narrow = false)
 {
     const int64_t es = out_size(out), per16 = 16 / es;
     a.D = D;
@@ -92,9 +94,13 @@ bool set_out(GroupArgs &a, GroupMaps &maps, void *D, int out, int64_t rows, int6
     a.n_out = static_cast<int32_t>(cols);
     a.d_vec = aligned16(D) && ld * es % 16 == 0 && (depth == 1 || stride * es % 16 == 0) ? 1 : 0;
     a.d_tma = a.d_vec && cols >= per16 ? 1 : 0;
-    return !a.d_tma || encode_3d(&maps.d, out_type(out), D, cols / per16 * per16, rows, ld * es, depth,
-                                 depth == 1 ? rows * ld * es : stride * es, static_cast<uint32_t>(128 / es), 32,
-                                 CU_TENSOR_MAP_SWIZZLE_128B);
+    a.d_lo = d_lo;
+    auto map = [&](CUtensorMap *m, const void *p) {
+        return encode_3d(m, out_type(out), p, cols / per16 * per16, rows, ld * es, depth,
+                         depth == 1 ? rows * ld * es : stride * es, narrow ? 32 : static_cast<uint32_t>(128 / es), 32,
+                         narrow && es == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    return !a.d_tma || (map(&maps.d, D) && (!d_lo || map(&maps.d_lo, static_cast<const uint16_t *>(D) + d_lo)));
 }
 
 // A stack of `depth` matrices of rows x cols 16-bit elements as an operand: boxes of 64
@@ -396,10 +402,15 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
         (p.split && (!map_a(&maps.a_lo, p.A + p.a_lo) || !map_b(&maps.b_lo, p.B + p.b_lo))))
         return GEMM_ERR_CUDA;
     const int64_t cols = p.padded ? p.ldd : p.N;
-    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d))
+    const bool c_tma = p.C && !p.split;
+    auto map_c = [&](CUtensorMap *m, const uint16_t *x) {
+        return encode_3d(m, ab_type(false), x, p.N, p.M, p.ldc * 2, p.count,
+                         p.count == 1 ? p.M * p.ldc * 2 : p.stride_c * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d, p.d_lo, p.d_lo || !p.split) ||
+        (c_tma && (!map_c(&maps.c, p.C) || (p.c_lo && !map_c(&maps.c_lo, p.C + p.c_lo)))))
         return GEMM_ERR_CUDA;
     g.c_lo = p.c_lo;
-    g.d_lo = p.d_lo;
     g.groups = static_cast<int32_t>(p.count);
     g.M = static_cast<int32_t>(p.M);
     g.N = static_cast<int32_t>(p.N);

@@ -47,6 +47,7 @@ enum : int { kPrecAcc = 0, kPrecSums = 1, kPrecSplit = 2 };
 struct GroupMaps {
     CUtensorMap a, b, d;           // stacks 3-D (inner, rows, group); one matrix's rows 2-D (D's always 3-D)
     CUtensorMap a_lo, b_lo;        // the operands' low parts (PREC_SPLIT)
+    CUtensorMap c, c_lo, d_lo;     // C and its low part (where it comes by TMA), D's low part: boxes of 32 columns
 };
 
 struct GroupArgs {
@@ -85,19 +86,22 @@ struct GroupCfg {
     static constexpr uint32_t A_BYTES = BM * 128u, B_BYTES = BN_LOCAL * 128u;
     static constexpr uint32_t STAGE_BYTES = PARTS * (A_BYTES + B_BYTES);
     static constexpr uint32_t OFF_A = 0, OFF_B = STAGES * PARTS * A_BYTES;
-    static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes; two a warp, or (two groups) one
+    static constexpr uint32_t EPI_BUF = 32 * 128;  // 32 rows x 128 bytes
     static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_EPI + 8 * EPI_BUF;
-    static constexpr uint32_t NUM_BARS = 3 * STAGES + 4;
-    static constexpr uint32_t SMEM_ALLOC = OFF_BAR + NUM_BARS * 8 + 16 + 1024;
     // Epilogue groups of four warps: two, half of the columns each, but for the narrowest
     // tiles.  (A warp's chain of TMEM load, conversion, shared image and store is all latency:
     // about 1 us for 64 columns.)
     static constexpr int EPI_GROUPS = BN >= 128 ? 2 : 1;
     static constexpr int COLS = BN / EPI_GROUPS;
+    // C by TMA, into the buffers that D leaves from: two a warp then, and a stage less
+    static constexpr bool C_TMA = KIND_ == kKindBatch && PREC_ == kPrecAcc;
+    static constexpr int EPI_BUFS = EPI_GROUPS == 1 || C_TMA ? 2 : 1;
+    static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * EPI_GROUPS * EPI_BUFS * EPI_BUF;
+    static constexpr uint32_t NUM_BARS = 3 * STAGES + 4 + (C_TMA ? 8 * EPI_GROUPS : 0);
     static constexpr int ZERO_WARP = 2 + 4 * EPI_GROUPS;  // (KIND_SUM)
     static constexpr int THREADS = 32 * (ZERO_WARP + (KIND_ == kKindSum ? 1 : 0));
     static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static constexpr uint32_t SMEM_ALLOC = OFF_BAR + NUM_BARS * 8 + 16 + 1024;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
     static_assert(!PAIR || BN == 256, "pairs: 256 x 256");
@@ -202,24 +206,33 @@ struct GroupTile {
     bool mirror;        // SYM: below the diagonal, stored a second time
 };
 
-__device__ __forceinline__ int32_t swz128(uint32_t row, uint32_t chunk)
+// Byte offset of 16-byte chunk `chunk` of row `row` in an image of 128-byte rows (128-byte
+// swizzle).
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk)
 {
-    return static_cast<int32_t>(row * 128u + ((chunk ^ (row & 7u)) << 4));
+    return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
-// Rows [0, nrows) of a 32 x 128-byte image to D at (row0, col0), columns below N: pieces of 16
-// bytes (four rows by eight pieces a pass, each row's 128 bytes together) where D has
-// them, single elements otherwise.
-__device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, int32_t nrows, uint32_t esize,
-                                                 void *D, int64_t ldd, int32_t row0, int32_t col0, int32_t N,
-                                                 bool vec)
+// The same for rows of 64 bytes (64-byte swizzle).
+__device__ __forceinline__ uint32_t swz64(uint32_t row, uint32_t chunk)
 {
-    const uint32_t chunk = lane % 8u;
+    return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+
+// Rows [0, nrows) of an image of 32 rows of 128 (64) bytes to D at (row0, col0), columns below
+// N: pieces of 16 bytes (four or eight rows a pass, each row's bytes together) where D has
+// them, single elements otherwise.
+__device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, bool narrow, int32_t nrows,
+                                                 uint32_t esize, void *D, int64_t ldd, int32_t row0,
+                                                 int32_t col0, int32_t N, bool vec)
+{
+    const uint32_t pieces = narrow ? 4u : 8u;
+    const uint32_t chunk = lane % pieces;
     const int32_t per = static_cast<int32_t>(16u / esize);
     const int32_t col = col0 + static_cast<int32_t>(chunk) * per;
-    for (int32_t r = static_cast<int32_t>(lane / 8u); r < nrows; r += 4) {
+    for (uint32_t r = lane / pieces; static_cast<int32_t>(r) < nrows; r += 32u / pieces) {
         uint32_t w[4];
-        ld_shared_v4(buf + swz128(r, chunk), w[0], w[1], w[2], w[3]);
+        ld_shared_v4(buf + (narrow ? swz64(r, chunk) : swz128(r, chunk)), w[0], w[1], w[2], w[3]);
         uint8_t *p = static_cast<uint8_t *>(D) + ((static_cast<int64_t>(row0) + r) * ldd + col) * esize;
         if (vec && col + per <= N) {
             *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -264,6 +277,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
     auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
+    // (C by TMA) epilogue warp w's buffer j holds its piece of C
+    auto c_bar = [&](uint32_t w, uint32_t j) { return bar0 + 8u * (3 * STAGES + 4 + 2 * w + j); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 8 * Cfg::NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
 
@@ -285,6 +300,10 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             mbar_init(accf_bar(b), 1);
             mbar_init(acce_bar(b), (PAIR ? 8 : 4) * Cfg::EPI_GROUPS);
         }
+        if (Cfg::C_TMA)
+            for (uint32_t w = 0; w < 4u * Cfg::EPI_GROUPS; ++w)
+                for (uint32_t j = 0; j < 2u; ++j)
+                    mbar_init(c_bar(w, j), 1);
         *abort_flag = 0u;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -659,10 +678,10 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         // ------------------------------------------------------------ epilogue
         constexpr bool kF32 = kSums && !kBatch;  // (the products over groups sum in registers for float32 only)
         constexpr int kCols = Cfg::COLS;
-        constexpr bool kOne = Cfg::EPI_GROUPS == 2;  // one buffer a warp
-        const uint32_t q = warp & 3u;
-        const int32_t col_g = kOne && warp >= 6u ? kCols : 0;  // first column of this group of warps
-        const uint32_t buf0 = base + Cfg::OFF_EPI + (kOne ? 4u * (warp >= 6u ? 1u : 0u) + q : 2u * q) * Cfg::EPI_BUF;
+        constexpr bool kOne = Cfg::EPI_BUFS == 1;  // one buffer a warp
+        const uint32_t q = warp & 3u, ew = (warp >= 6u ? 4u : 0u) + q;
+        const int32_t col_g = warp >= 6u ? kCols : 0;  // first column of this group of warps
+        const uint32_t buf0 = base + Cfg::OFF_EPI + Cfg::EPI_BUFS * ew * Cfg::EPI_BUF;
         const bool f32 = kF32 || args.out_kind == kOutF32;
         const uint32_t esize = f32 ? 4u : 2u;
         const int32_t wide = f32 ? 32 : 64;  // columns of a 128-byte row
@@ -674,6 +693,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         };
         int ab = 0;
         uint32_t aph = 0, slot = 0;
+        [[maybe_unused]] uint32_t c_ph = 0;  // (bit j) parity of c_bar j's next phase
         bool alive = true;
         for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
             const GroupTile p = locate(t);
@@ -690,8 +710,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 zero = zero || v < 0 || v >= args.table_rows;
             }
             uint8_t *d_g = static_cast<uint8_t *>(args.D) + (kRows ? 0 : p.g * args.stride_d * esize);
-            // C's high and low parts for 32 columns of this lane's row (from L2: written by the kernel
-            // before)
+            // (PREC_SPLIT) C's high and low parts for 32 columns of this lane's row
             const uint16_t *c_row =
                 kBatch && args.C && my_row < p.end
                     ? args.C + p.g * args.stride_c + static_cast<int64_t>(my_row) * args.ldc + n_g
@@ -700,21 +719,21 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 uint4 hi[4], lo[4];
             };
             auto load_c = [&](int32_t col, CPart &c) {
-                if constexpr (kBatch) {
+                if constexpr (kSplit) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         c.hi[i] = c.lo[i] = make_uint4(0, 0, 0, 0);
                         if (c_row && n_g + col + 8 * i < args.N) {
-                            c.hi[i] = __ldcg(reinterpret_cast<const uint4 *>(c_row + col + 8 * i));
+                            c.hi[i] = *reinterpret_cast<const uint4 *>(c_row + col + 8 * i);
                             if (args.c_lo)
-                                c.lo[i] = __ldcg(reinterpret_cast<const uint4 *>(c_row + args.c_lo + col + 8 * i));
+                                c.lo[i] = *reinterpret_cast<const uint4 *>(c_row + args.c_lo + col + 8 * i);
                         }
                     }
                 }
             };
             // alpha sum + beta C
             auto finish = [&](float(&v)[32], const CPart &c) {
-                if (kBatch && args.C) {
+                if (kSplit && args.C) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int sh = 16 * (i & 1);
@@ -761,47 +780,76 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                     }
                 } else {
                     __syncwarp();
-                    store_image_rows(buf, lane, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
+                    store_image_rows(buf, lane, false, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
                     __syncwarp();
                 }
                 if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
                     bulk_commit_group();
             };
-            // 32 columns from col, a second time: D[column][row], two neighbouring rows' values from
-            // a lane and its neighbour, two rows of D per pair of columns.  (All shuffles first: a
-            // store with its own condition after each took 180 cycles a pair.)
-            auto mirror = [&](int32_t col, const float(&v)[32], int64_t part) {
-                const bool odd = (lane & 1u) != 0u;
-                uint32_t x[16];
+            // 32 columns as the image of their transpose, 32 rows of 64 bytes: two neighbouring rows'
+            // values from a lane and its neighbour make a word, two of its rows' words a conflict-free
+            // store.  (Those words stored to D from here: 8 x 1000 x 1000 20 us against 26 with a
+            // condition after each shuffle.)
+            auto transpose = [&](uint32_t buf, const float (&v)[32]) {
+                const uint32_t odd = lane & 1u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-                    x[i] = odd ? pack_f16x2(other, v[2 * i + 1]) : pack_f16x2(v[2 * i], other);
-                }
-                const int32_t r = n_g + col + (odd ? 1 : 0), c = my_row & ~1;
-                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + static_cast<int64_t>(r) * args.ldd + c;
-                const int64_t step = 2 * args.ldd;
-                if (n_g + col + 32 <= args.N && nrows == 32) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        *reinterpret_cast<uint32_t *>(d + i * step) = x[i];
-                } else {
-                    // (an odd size: the last pair's second element goes into the row's padding)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (r + 2 * i < args.N && c < p.end)
-                            *reinterpret_cast<uint32_t *>(d + i * step) = x[i];
+                for (uint32_t k = 0; k < 16u; ++k) {
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * k] : v[2 * k + 1], 1);
+                    const uint32_t w = odd ? pack_f16x2(other, v[2 * k + 1]) : pack_f16x2(v[2 * k], other);
+                    st_shared_u32(buf + swz64(2 * k + odd, lane >> 3) + ((lane & 6u) << 1), w);
                 }
             };
-            // 32 columns of this lane's row to a workspace, in 16-byte pieces (its rows are whole ones)
-            auto store_row = [&](int32_t col, const uint32_t(&w)[16], int64_t part) {
-                if (my_row >= p.end)
+            // (PREC_SPLIT) 32 columns of a workspace in two parts: two images of 64-byte rows, and
+            // boxes of them.  (Each lane its own row in 16-byte stores instead: 8 x 1000 x 1367 52 ->
+            // 76 us.)
+            auto free_buffer = [&]() {
+                const uint32_t buf = buf0 + (kOne ? 0u : slot * Cfg::EPI_BUF);
+                slot ^= 1u;
+                if (lane == 0) {
+                    if (kOne)
+                        bulk_wait_group_read<0>();
+                    else
+                        bulk_wait_group_read<1>();
+                }
+                __syncwarp();
+                return buf;
+            };
+            auto send_two = [&](uint32_t buf, int32_t x, int32_t y) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&maps.d, buf, x, y, p.g);
+                    tma_store_3d(&maps.d_lo, buf + 2048u, x, y, p.g);
+                    bulk_commit_group();
+                }
+            };
+            auto put_two = [&](int32_t col, float(&v)[32], const uint32_t(&hi)[16]) {
+                const int32_t col0 = n_g + col;
+                if (nrows <= 0 || col0 >= args.N)
                     return;
-                uint16_t *d = reinterpret_cast<uint16_t *>(d_g) + part + static_cast<int64_t>(my_row) * args.ldd + n_g + col;
+                uint32_t buf = free_buffer();
+                if (SYM && p.mirror)
+                    transpose(buf, v);
+                // what rounding to float16 left of the values
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n_g + col + 8 * i < args.n_out)
-                        *reinterpret_cast<uint4 *>(d + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int i = 0; i < 32; ++i)
+                    v[i] -= cvt_f16_f32(static_cast<uint16_t>(hi[i / 2] >> (16 * (i & 1))));
+                if (SYM && p.mirror) {
+                    transpose(buf + 2048u, v);
+                    send_two(buf, row0, col0);
+                    buf = free_buffer();
+                }
+                uint32_t lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    lo[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i) {
+                    const uint32_t o = swz64(lane, i);
+                    st_shared_v4(buf + o, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                    st_shared_v4(buf + 2048u + o, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                }
+                send_two(buf, col0, row0);
             };
             // 64 columns from col, their sums 32 at a time from take(half, v), C's elements from
             // c (the first half's) and next(half) (those of the half after it)
@@ -820,35 +868,22 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         for (int i = 0; i < 32; ++i)
                             w[i] = __float_as_uint(v[i]);
                         put(col + 32 * h, w);
+                        continue;
                     }
-                    if constexpr (kF32)
-                        continue;
-                    else if (f32)
-                        continue;
-                    uint32_t x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[i] = pack2(v[2 * i], v[2 * i + 1]);
-                    if (SYM && p.mirror)
-                        mirror(col + 32 * h, v, 0);
-                    if (kBatch && args.d_lo) {
-                        store_row(col + 32 * h, x, 0);
-                        // what rounding to float16 left of the values
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] -= cvt_f16_f32(static_cast<uint16_t>(x[i / 2] >> (16 * (i & 1))));
+                    if constexpr (!kF32) {
+                        uint32_t x[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            x[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
-                        store_row(col + 32 * h, x, args.d_lo);
-                        if (SYM && p.mirror)
-                            mirror(col + 32 * h, v, args.d_lo);
-                    } else {
+                            x[i] = pack2(v[2 * i], v[2 * i + 1]);
+                        if (kSplit && args.d_lo) {
+                            put_two(col + 32 * h, v, x);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[16 * h + i] = x[i];
-                        if (h == 1)
-                            put(col, w);
+                            for (int i = 0; i < 16; ++i)
+                                w[16 * h + i] = x[i];
+                            if (h == 1)
+                                put(col, w);
+                        }
                     }
                 }
             };
@@ -909,12 +944,137 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                             if (col + 32 * h + 32 < kCols)
                                 load_c(col + 32 * h + 32, c);
                         });
+            } else if constexpr (Cfg::C_TMA) {
+                // KIND_BATCH.  C by TMA, 32 columns (and their low parts) a buffer, the first two while
+                // the tile's MMAs run; D takes C's place and leaves from there, and (SYM) its transpose
+                // from the low parts' place.  (C by loads of each lane's own row: 32 x 1000 x 1000 113
+                // against 91 us.)
+                {
+                    const bool has_c = args.C != nullptr;
+                    const int32_t units = stores ? min(kCols / 32, (args.N - n_g + 31) / 32) : 0;
+                    auto load_unit = [&](int32_t u) {  // (lane 0; the buffer's last store has read it)
+                        const uint32_t j = (slot + static_cast<uint32_t>(u)) & 1u, to = buf0 + j * Cfg::EPI_BUF;
+                        mbar_arrive_expect_tx(c_bar(ew, j), args.c_lo ? 4096u : 2048u);
+                        tma_load_3d(to, &maps.c, c_bar(ew, j), n_g + 32 * u, row0, p.g);
+                        if (args.c_lo)
+                            tma_load_3d(to + 2048u, &maps.c_lo, c_bar(ew, j), n_g + 32 * u, row0, p.g);
+                    };
+                    if (lane == 0 && has_c && units > 0) {
+                        bulk_wait_group_read<0>();
+                        for (int32_t u = 0; u < min(units, 2); ++u)
+                            load_unit(u);
+                    }
+                    const uint32_t acc = wait_full();
+                    int32_t landed = 0;  // pieces of C seen to have landed
+#pragma unroll 1
+                    for (int32_t u = 0; u < kCols / 32 && alive; ++u) {
+                        const uint32_t j = (slot + static_cast<uint32_t>(u)) & 1u, buf = buf0 + j * Cfg::EPI_BUF;
+                        uint32_t r[32];
+                        tc_ld_32x32b_x32(acc + 32u * static_cast<uint32_t>(u), r);
+                        tc_wait_ld(r);
+                        if (u == kCols / 32 - 1)
+                            hand_back();
+                        if (u >= units)
+                            continue;
+                        if (has_c) {
+                            if (!warp_wait_bounded<true>(c_bar(ew, j), (c_ph >> j) & 1u, abort_flag, args.status,
+                                                         args.timeout_ns, kWhereEpiC)) {
+                                alive = false;
+                                break;
+                            }
+                            c_ph ^= 1u << j;
+                            ++landed;
+                        } else if (lane == 0) {
+                            bulk_wait_group_read<1>();  // the store before the last has left this buffer
+                        }
+                        float v[32];
+                        if (!has_c) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = mul_rn(args.alpha, __uint_as_float(r[i]));
+                        } else
+#pragma unroll
+                        for (uint32_t i = 0; i < 4u; ++i) {
+                            uint32_t h[4], l[4] = {0u, 0u, 0u, 0u};
+                            ld_shared_v4(buf + swz64(lane, i), h[0], h[1], h[2], h[3]);
+                            if (args.c_lo)
+                                ld_shared_v4(buf + 2048u + swz64(lane, i), l[0], l[1], l[2], l[3]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int sh = 16 * (e & 1);
+                                const float x = cvt_f16_f32(static_cast<uint16_t>(h[e / 2] >> sh)) +
+                                                cvt_f16_f32(static_cast<uint16_t>(l[e / 2] >> sh));
+                                v[8 * i + e] = fma_rn(args.alpha, __uint_as_float(r[8 * i + e]), mul_rn(args.beta, x));
+                            }
+                        }
+                        // the buffer before: refilled while this piece leaves
+                        if (has_c && lane == 0 && u >= 1 && u + 1 < units) {
+                            bulk_wait_group_read<0>();
+                            load_unit(u + 1);
+                        }
+                        __syncwarp();  // (every lane has read C)
+                        const int32_t col = 32 * u, col0 = n_g + col;
+                        if (f32) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                st_shared_v4(buf + swz128(lane, i), __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                        } else {
+                            uint32_t x[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                x[i] = pack2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                            for (uint32_t i = 0; i < 4u; ++i)
+                                st_shared_v4(buf + swz64(lane, i), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            if (SYM) {
+                                if (p.mirror)
+                                    transpose(buf + 2048u, v);
+                            } else if (args.d_lo) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] -= cvt_f16_f32(static_cast<uint16_t>(x[i / 2] >> (16 * (i & 1))));
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    x[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                                for (uint32_t i = 0; i < 4u; ++i)
+                                    st_shared_v4(buf + 2048u + swz64(lane, i), x[4 * i], x[4 * i + 1], x[4 * i + 2],
+                                                 x[4 * i + 3]);
+                            }
+                        }
+                        if (args.d_tma && (col0 + 32 <= n_tma || n_tma == args.n_out)) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                                if (SYM) {
+                                    if (p.mirror)
+                                        tma_store_3d(&maps.d, buf + 2048u, row0, col0, p.g);
+                                } else if (args.d_lo) {
+                                    tma_store_3d(&maps.d_lo, buf + 2048u, col0, row0, p.g);
+                                }
+                            }
+                        } else {
+                            __syncwarp();
+                            store_image_rows(buf, lane, !f32, nrows, esize, d_g, args.ldd, row0, col0, args.n_out,
+                                             args.d_vec != 0);
+                            fence_proxy_async_smem();  // (the buffer is a TMA load's next)
+                            __syncwarp();
+                        }
+                        if (lane == 0)
+                            bulk_commit_group();
+                    }
+                    if (!alive && has_c && lane == 0) {
+                        // pieces of C under way land before the shared memory is released
+                        for (int32_t u = landed; u < min(units, landed + 2); ++u)
+                            wait_drain(c_bar(ew, (slot + static_cast<uint32_t>(u)) & 1u),
+                                       (c_ph >> ((slot + static_cast<uint32_t>(u)) & 1u)) & 1u, 10000000ull);
+                    }
+                    slot += static_cast<uint32_t>(units);  // (the buffers in turn, also from tile to tile)
+                }
             } else {
-                // (C's first loads go out before the wait for the accumulator, the others as soon as the
-                // registers of the ones before are free)
-                CPart c;
-                if (stores)
-                    load_c(0, c);
+                CPart c;  // (no C)
                 const uint32_t acc = wait_full();
                 if (!alive)
                     break;
@@ -932,10 +1092,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                             for (int i = 0; i < 32; ++i)
                                 v[i] = __uint_as_float(r[i]);
                         },
-                        [&](int h) {
-                            if (col + 32 * h + 32 < kCols)
-                                load_c(col + 32 * h + 32, c);
-                        });
+                        [](int) {});
             }
         }
         if (lane == 0)

@@ -39,16 +39,17 @@ template <int KIND, int MAJ, bool SYM>
 cudaError_t group_launch_forms(int bn, bool pair, const GroupMaps &maps, const GroupArgs &args, int grid,
                                cudaStream_t stream)
 {
+    constexpr int kLess = KIND == kKindBatch ? 1 : 0;  // (C's buffers)
     if (pair)
-        return bn == 256 ? group_launch_impl<256, 6, true, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream)
+        return bn == 256 ? group_launch_impl<256, 6 - kLess, true, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream)
                          : cudaErrorInvalidValue;
     if (bn == 128)
-        return group_launch_impl<128, 6, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
+        return group_launch_impl<128, 6 - kLess, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     if (bn == 64)
         return group_launch_impl<64, 8, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     if constexpr (!SYM) {
         if (bn == 256)
-            return group_launch_impl<256, 4, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
+            return group_launch_impl<256, 4 - kLess, false, KIND, MAJ, SYM, kPrecAcc>(maps, args, grid, stream);
     }
     return cudaErrorInvalidValue;
 }
