@@ -24,10 +24,15 @@ constexpr int kGroupM = 16;           // block rows per tile-order group, as the
 struct GForm {
     int bn;
     bool pair;
+    int cs;  // CTAs that share a tile's sum
     int64_t block_ns, fixed_ns;
 };
-// (float32 results, and operands in two parts: single CTAs of 64 or 128 columns)
-constexpr GForm kForms[4] = {{64, false, 300, 300}, {128, false, 300, 500}, {256, false, 390, 600}, {256, true, 280, 1500}};
+constexpr GForm kForms[4] = {{64, false, 1, 300, 300}, {128, false, 1, 300, 500}, {256, false, 1, 390, 600},
+                             {256, true, 1, 280, 1500}};
+// (float32 results)
+constexpr GForm kSumForms[2] = {{64, false, 1, 300, 500}, {128, false, 1, 300, 800}};
+// (operands in two parts)
+constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 1500}, {128, false, 1, 600, 2000}, {64, false, 2, 440, 3000}};
 
 // The form of the least waves x time of a tile.  tiles(tile_m, bn): tiles of the problem
 // (0: the form does not apply).
@@ -36,33 +41,35 @@ GForm choose_form(int64_t k_blocks, int prec, int sm_count, F tiles)
 {
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
+    const GForm *forms = prec == kPrecSplit ? kSplitForms : (prec == kPrecSums ? kSumForms : kForms);
+    const int n_forms = prec == kPrecSplit ? 3 : (prec == kPrecSums ? 2 : 4);
     const GForm *best = nullptr;
     int64_t best_ns = 0;
-    for (const GForm &f : kForms) {
-        const int64_t n = tiles(f.pair ? 256 : 128, f.bn), sets = f.pair ? sm_count / 2 : sm_count;
-        if (n <= 0 || sets <= 0 || (prec != kPrecAcc && f.bn > 128))
+    for (const GForm *f = forms; f != forms + n_forms; ++f) {
+        const int64_t n = tiles(f->pair ? 256 : 128, f->bn), sets = sm_count / (f->pair ? 2 : f->cs);
+        if (n <= 0 || sets <= 0)
             continue;
-        if ((fk == 1 && !f.pair && f.bn == fbn) || (fk == 3 && f.pair))
-            return f;
-        const int64_t ns = ceil_div(n, sets) * (k_blocks * f.block_ns + f.fixed_ns);
+        if ((fk == 1 && !f->pair && f->cs == 1 && f->bn == fbn) || (fk == 3 && (f->pair || f->cs == 2)))
+            return *f;
+        const int64_t ns = ceil_div(n, sets) * (ceil_div(k_blocks, f->cs) * f->block_ns + f->fixed_ns);
         if (!best || ns < best_ns) {
-            best = &f;
+            best = f;
             best_ns = ns;
         }
     }
-    return best ? *best : kForms[1];
+    return best ? *best : forms[1];
 }
 
 // CTAs of a launch over at most `tiles` tiles.
 gemm_status group_grid(const GForm &f, int64_t tiles, const DeviceInfo *dev, int *grid)
 {
-    int64_t sets = dev->sm_count;
+    int64_t sets = dev->sm_count / f.cs;
     if (f.pair) {
         sets = tcg::tile_max_clusters(256, true, 1, 1);  // (the same shared memory)
         if (sets <= 0)
             return GEMM_ERR_CUDA;
     }
-    *grid = static_cast<int>((f.pair ? 2 : 1) * (tiles < sets ? tiles : sets));
+    *grid = static_cast<int>((f.pair ? 2 : f.cs) * (tiles < sets ? tiles : sets));
     return GEMM_OK;
 }
 
@@ -424,7 +431,7 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     g.ldc = p.ldc;
     g.stride_c = p.stride_c;
     g.loads = 1;
-    const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, prec, maps, g, grid, stream);
+    const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, prec, f.cs, maps, g, grid, stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -23,7 +23,12 @@
 //   PREC_SUMS   the accumulator is emptied every four K blocks into float32 registers, which
 //               round to nearest (float32 results: 1000 x 1367 summed over 1000 1.2e-6 -> 3e-7).
 //   PREC_SPLIT  as PREC_SUMS, and both operands are pairs of float16 matrices, a high part and
-//               the rest: high x high + high x low + low x high, 22 bits of each operand.
+//               the rest: high x high + high x low + low x high, 22 bits of each operand.  Twelve
+//               MMAs a K block: two issuing warps, half of its K steps each (a lone thread's
+//               ~117 cycles an MMA took longer than loading the block).  CS = 2: the CTAs of a
+//               cluster share a tile's sum, half of its K blocks each, where the tiles alone
+//               leave SMs idle; the rows of a tile are finished half by each, which gets the
+//               other's sums of them through its shared memory.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), then four or
 // eight epilogue warps, (KIND_SUM) one that zeroes.  Two TMEM accumulators: the epilogue of one tile
@@ -75,8 +80,10 @@ struct GroupArgs {
     uint64_t timeout_ns;
 };
 
-template <int BN_, int STAGES_, bool PAIR_, int KIND_, int PREC_>
+template <int BN_, int STAGES_, bool PAIR_, int KIND_, int PREC_, int CS_ = 1>
 struct GroupCfg {
+    static constexpr int CS = CS_;
+    static constexpr int ISS = PREC_ == kPrecSplit ? 2 : 1;  // MMA issuers
     static constexpr int PARTS = PREC_ == kPrecSplit ? 2 : 1;  // boxes of an operand in a stage
     static constexpr int CHUNK = PREC_ == kPrecAcc ? 0 : 4;    // K blocks an accumulator takes (0: all)
     static constexpr bool PAIR = PAIR_;
@@ -96,11 +103,15 @@ struct GroupCfg {
     // C by TMA, into the buffers that D leaves from: two a warp then, and a stage less
     static constexpr bool C_TMA = KIND_ == kKindBatch && PREC_ == kPrecAcc;
     static constexpr int EPI_BUFS = EPI_GROUPS == 1 || C_TMA ? 2 : 1;
-    static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * EPI_GROUPS * EPI_BUFS * EPI_BUF;
-    static constexpr uint32_t NUM_BARS = 3 * STAGES + 4 + (C_TMA ? 8 * EPI_GROUPS : 0);
-    static constexpr int ZERO_WARP = 2 + 4 * EPI_GROUPS;  // (KIND_SUM)
-    static constexpr int THREADS = 32 * (ZERO_WARP + (KIND_ == kKindSum ? 1 : 0));
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    // (CS = 2) the other CTA's sums of two warps' rows
+    static constexpr uint32_t RED_BYTES = CS == 2 ? 32u * COLS * 4u : 0u;
+    static constexpr uint32_t OFF_RED = OFF_EPI + 4 * EPI_GROUPS * EPI_BUFS * EPI_BUF;
+    static constexpr uint32_t OFF_BAR = OFF_RED + 2 * RED_BYTES;
+    static constexpr uint32_t NUM_BARS = 3 * STAGES + 4 + (C_TMA ? 8 * EPI_GROUPS : 0) + (CS == 2 ? 8 : 0);
+    static_assert(CS == 1 || (CS == 2 && !PAIR && PREC_ == kPrecSplit && EPI_GROUPS == 1), "shared sums");
+    static constexpr int LAST_WARP = 2 + 4 * EPI_GROUPS;  // zeroes (KIND_SUM), or the second MMA issuer
+    static constexpr int THREADS = 32 * (LAST_WARP + (KIND_ == kKindSum || ISS == 2 ? 1 : 0));
+    static constexpr uint32_t TMEM_COLS = 2 * BN * ISS;
     static constexpr uint32_t SMEM_ALLOC = OFF_BAR + NUM_BARS * 8 + 16 + 1024;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
@@ -250,11 +261,12 @@ __device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, bo
     }
 }
 
-template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC>
-__global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREADS, 1)
+template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC, int CS = 1>
+__global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::THREADS, 1)
     group_gemm_kernel(const __grid_constant__ GroupMaps maps, const GroupArgs args)
 {
-    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC>;
+    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>;
+    constexpr int CL = PAIR ? 2 : CS;  // CTAs of a cluster
     constexpr bool kSums = PREC != kPrecAcc, kSplit = PREC == kPrecSplit;
     constexpr bool kRows = KIND == kKindRows, kSum = KIND == kKindSum, kBatch = KIND == kKindBatch;
     constexpr bool kMnA = (MAJ & 1) != 0, kMnB = (MAJ & 2) != 0;
@@ -278,14 +290,19 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
     auto accf_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
     // (C by TMA) epilogue warp w's buffer j holds its piece of C
+    // (CS = 2) the other CTA's sums of warp q's rows are there / have been read (arrives at
+    // the writer)
+    auto redf_bar = [&](uint32_t q) { return bar0 + 8u * (3 * STAGES + 4 + q); };
+    auto rede_bar = [&](uint32_t q) { return bar0 + 8u * (3 * STAGES + 8 + q); };
     auto c_bar = [&](uint32_t w, uint32_t j) { return bar0 + 8u * (3 * STAGES + 4 + 2 * w + j); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 8 * Cfg::NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
 
     const uint32_t role = PAIR ? cluster_ctarank() : 0u;
     const bool leader = role == 0u;
-    const int32_t cta_set = static_cast<int32_t>(blockIdx.x) / (PAIR ? 2 : 1);
-    const int32_t cta_sets = static_cast<int32_t>(gridDim.x) / (PAIR ? 2 : 1);
+    const uint32_t share = CS == 2 ? cluster_ctarank() : 0u;  // which part of a shared sum
+    const int32_t cta_set = static_cast<int32_t>(blockIdx.x) / CL;
+    const int32_t cta_sets = static_cast<int32_t>(gridDim.x) / CL;
     auto lead = [&](uint32_t bar) { return PAIR ? mapa_shared(bar, 0u) : bar; };
 
     if (warp == 0 && lane == 0) {
@@ -293,13 +310,18 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             // (KIND_SUM on pairs: two arrivals, since a partial block is handed over by both
             // CTAs' zeroing warps; the leader's producer arrives twice for a whole one)
             mbar_init(full_bar(s), kSum && PAIR ? 2 : 1);
-            mbar_init(empty_bar(s), 1);
+            mbar_init(empty_bar(s), Cfg::ISS);
             mbar_init(tail_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(accf_bar(b), 1);
+            mbar_init(accf_bar(b), Cfg::ISS);
             mbar_init(acce_bar(b), (PAIR ? 8 : 4) * Cfg::EPI_GROUPS);
         }
+        if (CS == 2)
+            for (uint32_t q = 0; q < 4u; ++q) {
+                mbar_init(redf_bar(q), 1);
+                mbar_init(rede_bar(q), 1);
+            }
         if (Cfg::C_TMA)
             for (uint32_t w = 0; w < 4u * Cfg::EPI_GROUPS; ++w)
                 for (uint32_t j = 0; j < 2u; ++j)
@@ -329,7 +351,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
     if constexpr (!kBatch)
         gr.init(args.offsets, args.groups, args.rows, lane);
     tc_fence_before_sync();
-    if (PAIR)
+    if (CL > 1)
         cluster_sync_all();
     else
         __syncthreads();
@@ -400,9 +422,14 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         return p;
     };
     const int32_t k_blocks = (args.K + Cfg::BK - 1) / Cfg::BK;
-    // K blocks of tile t (KIND_SUM: of its group)
+    // (CS = 2) this CTA's K blocks of a tile: from kb_first, kb_mine of them
+    const int32_t kb_first = CS == 2 ? static_cast<int32_t>(share) * (k_blocks / 2) : 0;
+    const int32_t kb_mine = CS == 2 ? (share == 0u ? k_blocks / 2 : k_blocks - k_blocks / 2) : k_blocks;
+    // K blocks of tile t (KIND_SUM: of its group) that this CTA multiplies
     auto blocks_of = [&](int32_t t, int32_t &rem) -> int32_t {
         rem = 0;
+        if constexpr (CS == 2)
+            return kb_mine;
         if constexpr (kSum) {
             gr.load(t / (args.num_m_blocks * args.num_n_blocks));
             const int32_t n = gr.hi_last - gr.lo_last;
@@ -450,7 +477,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 }
                 const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
                 const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
-                const int32_t k = p.k0 + kb * Cfg::BK;
+                const int32_t k = p.k0 + (kb_first + kb) * Cfg::BK;
                 if (lane == 0) {
                     const uint32_t extra = first ? args.extra_tx : 0u;
                     if (part) {
@@ -544,9 +571,12 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                     wait_drain(full_bar(ds), dph, 10000000ull);
             }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp == 1 || (Cfg::ISS == 2 && warp == Cfg::LAST_WARP)) {
+        // ------------------------------------------------------------ MMA issuers
         if (lane == 0 && leader) {
+            // (two issuers: the first or the second half of every block's K steps, into an
+            // accumulator of its own)
+            const int e = Cfg::ISS == 2 && warp != 1 ? 1 : 0;
             const uint32_t idesc = idesc_f16_f32acc(args.ab_bf16 != 0, TM, BN, kMnA, kMnB);
             int s = 0, ab = 0;
             uint32_t ph = 0, aph = 0;
@@ -584,7 +614,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         if (!wait_acc())
                             return false;
                     }
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((ab * Cfg::ISS + e) * BN);
                     // (the peer's zeros: an acquire at cluster scope)
                     const bool got =
                         PAIR && part
@@ -608,9 +638,10 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         const uint64_t ad = kMnA ? sdesc_mn_sw128(pa) : sdesc_k_sw128(pa);
                         const uint64_t bd = kMnB ? sdesc_mn_sw128(pb) : sdesc_k_sw128(pb);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k2 = 0; k2 < 4 / Cfg::ISS; ++k2) {
+                            const int k = Cfg::ISS == 2 ? 2 * e + k2 : k2;
                             if (k < steps) {
-                                const uint32_t acc = !begins || k > 0 || pr > (kSplit ? 0 : 2) ? 1u : 0u;
+                                const uint32_t acc = !begins || k2 > 0 || pr > (kSplit ? 0 : 2) ? 1u : 0u;
                                 if (PAIR)
                                     tc_mma_f16_pair(d_tmem, ad + kStepA * k, bd + kStepB * k, idesc, acc);
                                 else
@@ -636,7 +667,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             }
         }
         __syncwarp();
-    } else if (kSum && warp == Cfg::ZERO_WARP) {
+    } else if (kSum && warp == Cfg::LAST_WARP) {
         // ------------------------------------------------------------ zeroing warp
         if constexpr (kSum) {
             int s = 0;
@@ -693,6 +724,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
         };
         int ab = 0;
         uint32_t aph = 0, slot = 0;
+        [[maybe_unused]] uint32_t shared_tiles = 0;  // (CS = 2) tiles handed over so far
         [[maybe_unused]] uint32_t c_ph = 0;  // (bit j) parity of c_bar j's next phase
         bool alive = true;
         for (int32_t t = cta_set; t < num_tiles && alive; t += cta_sets) {
@@ -704,7 +736,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             const int32_t my_row = row0 + static_cast<int32_t>(lane);
             const int32_t n_g = p.n0 + col_g;  // first column of D
             const bool stores = nrows > 0 && n_g < args.N;
-            bool zero = nkb == 0;
+            bool zero = CS == 1 && nkb == 0;
             if (kRows && args.idx && my_row < p.end) {
                 const int32_t v = __ldcg(args.idx + my_row);
                 zero = zero || v < 0 || v >= args.table_rows;
@@ -905,7 +937,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                 alive = warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
                                                 kWhereEpiAccFull);
                 tc_fence_after_sync();
-                return tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * BN + col_g);
+                return tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * Cfg::ISS * BN + col_g);
             };
             if constexpr (kSums) {
                 float sums[kCols];
@@ -923,11 +955,57 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
                         for (int i = 0; i < 32; ++i)
                             sums[32 * c + i] = f == 0 ? __uint_as_float(r[i])
                                                       : __fadd_rn(sums[32 * c + i], __uint_as_float(r[i]));
+                        if constexpr (Cfg::ISS == 2) {
+                            tc_ld_32x32b_x32(acc + 32u * c + BN, r);
+                            tc_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                sums[32 * c + i] = __fadd_rn(sums[32 * c + i], __uint_as_float(r[i]));
+                        }
                     }
                     hand_back();
                 }
                 if (!alive)
                     break;
+                if constexpr (CS == 2) {
+                    if (nkb == 0) {  // (one K block: the other CTA's)
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i)
+                            sums[i] = 0.f;
+                    }
+                    const uint32_t at = base + Cfg::OFF_RED + (q & 1u) * Cfg::RED_BYTES + lane * 4u;
+                    if ((q >> 1) != share) {
+                        // the other CTA finishes these rows
+                        if (shared_tiles > 0 && !warp_wait_cluster(rede_bar(q), (shared_tiles - 1u) & 1u, abort_flag,
+                                                                   args.status, args.timeout_ns, kWhereEpiC)) {
+                            alive = false;
+                            break;
+                        }
+                        const uint32_t to = mapa_shared(at, share ^ 1u);
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i)
+                            st_shared_cluster_u32(to + 128u * static_cast<uint32_t>(i), __float_as_uint(sums[i]));
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(mapa_shared(redf_bar(q), share ^ 1u));
+                        ++shared_tiles;
+                        continue;
+                    }
+                    if (!warp_wait_cluster(redf_bar(q), shared_tiles & 1u, abort_flag, args.status, args.timeout_ns,
+                                           kWhereEpiC)) {
+                        alive = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        sums[i] = __fadd_rn(sums[i], __uint_as_float(ld_shared_u32(at + 128u * static_cast<uint32_t>(i))));
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(mapa_shared(rede_bar(q), share ^ 1u));
+                    ++shared_tiles;
+                }
+                if (!stores)
+                    continue;
                 CPart c;
                 if (stores)
                     load_c(0, c);
@@ -1110,10 +1188,11 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC>::THREAD
             while (global_timer_ns() - t0 < 100000ull) {
             }
         }
-        cluster_sync_all();
-    } else {
-        __syncthreads();
     }
+    if (CL > 1)
+        cluster_sync_all();  // (the other CTA's work may use this one's shared memory until here)
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         if (PAIR)

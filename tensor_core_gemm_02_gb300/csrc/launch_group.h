@@ -18,8 +18,9 @@ cudaError_t launch_group_few(int mp, int cs, bool b_major, const GroupMaps &maps
                              cudaStream_t stream);
 cudaError_t launch_group_sum(int bn, bool pair, int prec, const GroupMaps &maps, const GroupArgs &args,
                              int grid, cudaStream_t stream);
-// (symmetric results: maj 0 or 3; others: maj 0 or 2; prec: kPrecAcc or kPrecSplit)
-cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, int prec, const GroupMaps &maps,
+// (symmetric results: maj 0 or 3; others: maj 0 or 2; prec: kPrecAcc or kPrecSplit,
+// the latter with bn 64 also on cs = 2 CTAs a tile)
+cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, int prec, int cs, const GroupMaps &maps,
                                const GroupArgs &args, int grid, cudaStream_t stream);
 
 // The stable order of M ids by value: offsets (groups + 1), order and rows (each M; rows

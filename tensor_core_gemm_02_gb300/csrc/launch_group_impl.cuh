@@ -5,11 +5,11 @@
 
 namespace tcg {
 
-template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC>
+template <int BN, int STAGES, bool PAIR, int KIND, int MAJ, bool SYM, int PREC, int CS = 1>
 cudaError_t group_launch_impl(const GroupMaps &maps, const GroupArgs &args, int grid, cudaStream_t stream)
 {
-    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC>;
-    auto kfn = group_gemm_kernel<BN, STAGES, PAIR, KIND, MAJ, SYM, PREC>;
+    using Cfg = GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>;
+    auto kfn = group_gemm_kernel<BN, STAGES, PAIR, KIND, MAJ, SYM, PREC, CS>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kfn), Cfg::SMEM_ALLOC, done);
     if (e != cudaSuccess)
@@ -23,7 +23,7 @@ cudaError_t group_launch_impl(const GroupMaps &maps, const GroupArgs &args, int 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = TCG_PDL;
     cfg.numAttrs = 1;
-    if (PAIR) {
+    if (PAIR || CS > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = 2;
         attr[1].val.clusterDim.y = 1;
