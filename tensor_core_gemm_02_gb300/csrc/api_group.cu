@@ -414,7 +414,8 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
         return encode_3d(m, ab_type(false), x, p.N, p.M, p.ldc * 2, p.count,
                          p.count == 1 ? p.M * p.ldc * 2 : p.stride_c * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     };
-    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d, p.d_lo, p.d_lo || !p.split) ||
+    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d, p.d_lo,
+                 p.d_lo || !p.split || f.cs == 2) ||
         (c_tma && (!map_c(&maps.c, p.C) || (p.c_lo && !map_c(&maps.c_lo, p.C + p.c_lo)))))
         return GEMM_ERR_CUDA;
     g.c_lo = p.c_lo;

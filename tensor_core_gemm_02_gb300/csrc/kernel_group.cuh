@@ -27,8 +27,8 @@
 //               MMAs a K block: two issuing warps, half of its K steps each (a lone thread's
 //               ~117 cycles an MMA took longer than loading the block).  CS = 2: the CTAs of a
 //               cluster share a tile's sum, half of its K blocks each, where the tiles alone
-//               leave SMs idle; the rows of a tile are finished half by each, which gets the
-//               other's sums of them through its shared memory.
+//               leave SMs idle; each finishes half of the tile's columns, with the other's sums
+//               of them through its shared memory.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), then four or
 // eight epilogue warps, (KIND_SUM) one that zeroes.  Two TMEM accumulators: the epilogue of one tile
@@ -103,10 +103,10 @@ struct GroupCfg {
     // C by TMA, into the buffers that D leaves from: two a warp then, and a stage less
     static constexpr bool C_TMA = KIND_ == kKindBatch && PREC_ == kPrecAcc;
     static constexpr int EPI_BUFS = EPI_GROUPS == 1 || C_TMA ? 2 : 1;
-    // (CS = 2) the other CTA's sums of two warps' rows
-    static constexpr uint32_t RED_BYTES = CS == 2 ? 32u * COLS * 4u : 0u;
+    // (CS = 2) the other CTA's sums of a warp's rows, half of the columns
+    static constexpr uint32_t RED_BYTES = CS == 2 ? 32u * COLS / 2 * 4u : 0u;
     static constexpr uint32_t OFF_RED = OFF_EPI + 4 * EPI_GROUPS * EPI_BUFS * EPI_BUF;
-    static constexpr uint32_t OFF_BAR = OFF_RED + 2 * RED_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_RED + 4 * RED_BYTES;
     static constexpr uint32_t NUM_BARS = 3 * STAGES + 4 + (C_TMA ? 8 * EPI_GROUPS : 0) + (CS == 2 ? 8 : 0);
     static_assert(CS == 1 || (CS == 2 && !PAIR && PREC_ == kPrecSplit && EPI_GROUPS == 1), "shared sums");
     static constexpr int LAST_WARP = 2 + 4 * EPI_GROUPS;  // zeroes (KIND_SUM), or the second MMA issuer
@@ -715,7 +715,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
         const uint32_t buf0 = base + Cfg::OFF_EPI + Cfg::EPI_BUFS * ew * Cfg::EPI_BUF;
         const bool f32 = kF32 || args.out_kind == kOutF32;
         const uint32_t esize = f32 ? 4u : 2u;
-        const int32_t wide = f32 ? 32 : 64;  // columns of a 128-byte row
+        const bool narrow = CS == 2 && !f32;         // (images of 64-byte rows)
+        const int32_t wide = f32 || narrow ? 32 : 64;  // columns of an image's row
         // TMA stores whole 16 bytes of a row: D's descriptor ends with the last whole ones
         const int32_t n_tma = args.n_out & ~(f32 ? 3 : 7);
         const uint64_t policy = l2_policy_evict_first();
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                         v[i] = zero ? 0.f : mul_rn(args.alpha, v[i]);
                 }
             };
-            // a 128-byte row a lane, from column col of this group's, to D
+            // a row of an image a lane, from column col of this group's, to D
             auto put = [&](int32_t col, const uint32_t(&w)[32]) {
                 const int32_t col0 = n_g + col;
                 if (nrows <= 0 || col0 >= args.N)
@@ -797,7 +798,9 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    st_shared_v4(buf + swz128(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    if (!narrow || i < 4)
+                        st_shared_v4(buf + (narrow ? swz64(lane, i) : swz128(lane, i)), w[4 * i], w[4 * i + 1],
+                                     w[4 * i + 2], w[4 * i + 3]);
                 // a whole box by TMA; rows that end with the group (KIND_ROWS; the others' boxes
                 // end with their matrix), or columns past the last whole 16 bytes, by plain stores
                 const bool tma = args.d_tma && (!kRows || nrows == 32) && (col0 + wide <= n_tma || n_tma == args.n_out);
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     }
                 } else {
                     __syncwarp();
-                    store_image_rows(buf, lane, false, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
+                    store_image_rows(buf, lane, narrow, nrows, esize, d_g, args.ldd, row0, col0, args.n_out, args.d_vec != 0);
                     __syncwarp();
                 }
                 if (lane == 0)  // (every use of a buffer is a group: the wait above counts them)
@@ -941,6 +944,11 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             };
             if constexpr (kSums) {
                 float sums[kCols];
+                // (CS = 2) the columns this CTA finishes, and C's elements there
+                const int32_t half = CS == 2 ? 32 * static_cast<int32_t>(share) : 0;
+                [[maybe_unused]] CPart c_early;
+                if (CS == 2 && stores)
+                    load_c(half, c_early);
                 const int32_t fills = max(1, (nkb + Cfg::CHUNK - 1) / Cfg::CHUNK);
                 for (int32_t f = 0; f < fills; ++f) {
                     const uint32_t acc = wait_full();
@@ -968,41 +976,54 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 if (!alive)
                     break;
                 if constexpr (CS == 2) {
-                    if (nkb == 0) {  // (one K block: the other CTA's)
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            sums[i] = 0.f;
+                    // the halves change places; each CTA finishes 32 columns
+                    float v[32];
+                    const uint32_t at = base + Cfg::OFF_RED + q * Cfg::RED_BYTES + lane * 4u;
+                    const uint32_t to = mapa_shared(at, share ^ 1u);
+                    if (shared_tiles > 0 && !warp_wait_cluster(rede_bar(q), (shared_tiles - 1u) & 1u, abort_flag,
+                                                               args.status, args.timeout_ns, kWhereEpiC)) {
+                        alive = false;
+                        break;
                     }
-                    const uint32_t at = base + Cfg::OFF_RED + (q & 1u) * Cfg::RED_BYTES + lane * 4u;
-                    if ((q >> 1) != share) {
-                        // the other CTA finishes these rows
-                        if (shared_tiles > 0 && !warp_wait_cluster(rede_bar(q), (shared_tiles - 1u) & 1u, abort_flag,
-                                                                   args.status, args.timeout_ns, kWhereEpiC)) {
-                            alive = false;
-                            break;
-                        }
-                        const uint32_t to = mapa_shared(at, share ^ 1u);
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            st_shared_cluster_u32(to + 128u * static_cast<uint32_t>(i), __float_as_uint(sums[i]));
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster(mapa_shared(redf_bar(q), share ^ 1u));
-                        ++shared_tiles;
-                        continue;
+                    for (int i = 0; i < 32; ++i) {
+                        // (one K block: all of it the second CTA's)
+                        const float lo = nkb > 0 ? sums[i] : 0.f, hi = nkb > 0 ? sums[32 + i] : 0.f;
+                        st_shared_cluster_u32(to + 128u * static_cast<uint32_t>(i), __float_as_uint(share ? lo : hi));
+                        v[i] = share ? hi : lo;
                     }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(mapa_shared(redf_bar(q), share ^ 1u));
                     if (!warp_wait_cluster(redf_bar(q), shared_tiles & 1u, abort_flag, args.status, args.timeout_ns,
                                            kWhereEpiC)) {
                         alive = false;
                         break;
                     }
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        sums[i] = __fadd_rn(sums[i], __uint_as_float(ld_shared_u32(at + 128u * static_cast<uint32_t>(i))));
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __fadd_rn(v[i], __uint_as_float(ld_shared_u32(at + 128u * static_cast<uint32_t>(i))));
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(mapa_shared(rede_bar(q), share ^ 1u));
                     ++shared_tiles;
+                    if (!stores)
+                        continue;
+                    finish(v, c_early);
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    if (args.d_lo) {
+                        put_two(half, v, x);
+                    } else {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = f32 ? __float_as_uint(v[i]) : x[i % 16];
+                        put(half, w);
+                    }
+                    continue;
                 }
                 if (!stores)
                     continue;
