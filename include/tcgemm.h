@@ -593,9 +593,9 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *                    overlap is GEMM_ERR_ALIAS.
  *  Rounding: the norm and every sum are float32.  Between the products the iterate X is held
  *  as two float16 matrices, a high part and the rest (22 bits), P and b P + c P^2 in float16.
- *  The products take the high part of X; all of their operands in two parts in the last step
- *  of a float16 Y and in every step of a float32 Y (three products for one), so that the
- *  steps' error stays below the rounding of Y.  All are scaled by 2^12: the elements of the
+ *  The products take the high part of X; all of their operands in two parts (three products
+ *  for one) in every step of a float32 Y, in the last one of a float16 Y, and in two more,
+ *  also of a bfloat16 Y, where min(M, N) < 256.  All are scaled by 2^12: the elements of the
  *  iterates, of P and of b P + c P^2 have to stay below 16, as they do where the singular
  *  values stay below 2.  The last step is rounded once, to Y's type.
  *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.

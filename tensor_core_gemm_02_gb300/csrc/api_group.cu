@@ -475,11 +475,15 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
         return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // The iterate is held in two float16 parts, since what its rounding loses in one step the
-    // next ones multiply.  The products take the high parts, or, in the last `exact` steps, both:
-    // as many steps as it takes for their error to stay below the rounding of Y's type
-    // (1000 x 1367, relative to 64 bits, without Y's rounding: no step 2.7e-4, the last 1.2e-4,
-    // all 1e-6; one float16 part of X, 3.1e-3).
-    const int exact = out == GEMM_OUT_F32 ? steps : (out == GEMM_OUT_F16 ? 1 : 0);
+    // next ones multiply (1000 x 1367, relative to 64 bits: one part 3.1e-3, two 2.7e-4).  The
+    // products take the high parts, or, in the last `exact` steps, both, as Y's type asks for
+    // (emulated, with 0, 1, 2, 3 such steps: a momentum of 1000 x 1000 3.0e-4, 1.3e-4, 9.8e-5, 2.2e-5,
+    // random numbers 1.3e-3, 9.5e-4, 3.8e-4, 8e-6; of 64 x 64 1.7e-3, 1.3e-3, 7.4e-4, 1.8e-4 and 2.1e-3,
+    // 1.8e-3, 1.5e-3, 6.4e-4; bfloat16 rounds by 1.7e-3, float16 by 2.1e-4).  Small matrices, which
+    // wait for their launches anyway, get two more.
+    const int more = s < 256 ? 2 : 0;
+    const int wanted = out == GEMM_OUT_F32 ? steps : (out == GEMM_OUT_F16 ? 1 + more : more);
+    const int exact = wanted < steps ? wanted : steps;
     // workspace of a matrix: two iterates, the product of one with itself, and the polynomial of that
     const int64_t ldi = ceil_div(N, 8) * 8, ldp = ceil_div(s, 8) * 8;
     const int64_t size_i = ceil_div(M * ldi, 64) * 64, size_p = ceil_div(s * ldp, 64) * 64;

@@ -53,7 +53,8 @@ def recurrence(x, coefs, steps, eps, out):
     # the norm: float32 sums of N squares (2^-24 each, pairwise in part: at most the chain of a
     # thread), the root, the division and a product; then the iterate's two parts
     e = 2.0 ** -16 * x.norm().item() + (s * l) ** 0.5 * 2.0 ** -37
-    exact = {torch.float32: steps, torch.float16: 1, torch.bfloat16: 0}[out]
+    more = 2 if s < 256 else 0
+    exact = {torch.float32: steps, torch.float16: 1 + more, torch.bfloat16: more}[out]
     for i in range(steps):
         h = 2.0 ** -22 if i >= steps - exact else 2.0 ** -11
         p = x @ x.T
