@@ -291,7 +291,7 @@ def _timed_out(call):
 def test_a_wait_that_runs_out(form):
     """A stage that never fills: the kernels give up, say so, and the next call works."""
     binding.gemm_debug_force_tile(*FORMS[form])
-    A, B, dD = quarters((300, 328), 1), quarters((3, 260, 328), 2), quarters((300, 260), 3)
+    A, B, dD = quarters((300, 328), 1), quarters((3, 264, 328), 2), quarters((300, 264), 3)
     off = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda")
     for out in (binding.OUT_F32, binding.OUT_BF16):
         want = binding.gemm_grouped(A, B, off, out=out)
