@@ -547,7 +547,7 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.
  *  K == 0            the groups' rows are 0.
  *  Sums are float32, multiplied by alpha (mul.rn) and rounded once; the same bits every time.
- *  (Of float32 results the sums are added up in registers, rounded to nearest, every 256 of
+ *  (Of float32 results the sums are added up in registers, rounded to nearest, every 512 of
  *  K; of the others in the tensor cores' accumulators throughout.)
  *  Other errors and execution as gemm_f16.
  */

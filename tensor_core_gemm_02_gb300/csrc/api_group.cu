@@ -27,10 +27,12 @@ struct GForm {
     int cs;  // CTAs that share a tile's sum
     int64_t block_ns, fixed_ns;
 };
-constexpr GForm kForms[4] = {{64, false, 1, 300, 300}, {128, false, 1, 300, 500}, {256, false, 1, 390, 600},
-                             {256, true, 1, 280, 1500}};
-// (float32 results)
-constexpr GForm kSumForms[2] = {{64, false, 1, 300, 500}, {128, false, 1, 300, 800}};
+// Measured, us a tile, 2 / 8 / 32 and more blocks: 128 x 256 2.35 / 4.1, pairs 3.0 / 3.6 / 12.7;
+// float32 results, 128 columns 1.5 / - / 0.5 a block, pairs 6.3 / - / 26.8 (64 blocks).
+constexpr GForm kForms[4] = {{64, false, 1, 300, 800}, {128, false, 1, 300, 1000}, {256, false, 1, 330, 1700},
+                             {256, true, 1, 285, 2000}};
+// (float32 results, sums in registers)
+constexpr GForm kSumForms[3] = {{64, false, 1, 300, 700}, {128, false, 1, 480, 800}, {256, true, 1, 320, 7500}};
 // (operands in two parts)
 constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 1500}, {128, false, 1, 600, 2000}, {64, false, 2, 440, 3000}};
 
@@ -42,7 +44,7 @@ GForm choose_form(int64_t k_blocks, int prec, int sm_count, F tiles)
     int fk = 0, fbn = 0;
     forced_tile(&fk, &fbn);
     const GForm *forms = prec == kPrecSplit ? kSplitForms : (prec == kPrecSums ? kSumForms : kForms);
-    const int n_forms = prec == kPrecSplit ? 3 : (prec == kPrecSums ? 2 : 4);
+    const int n_forms = prec == kPrecAcc ? 4 : 3;
     const GForm *best = nullptr;
     int64_t best_ns = 0;
     for (const GForm *f = forms; f != forms + n_forms; ++f) {
@@ -160,7 +162,7 @@ Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
         return Few{0, 0};
     const int mp = rows <= 8 ? 16 : (rows <= 16 ? 32 : 64);
     const int64_t tiles = used * ceil_div(rows, mp) * ceil_div(N, 128);
-    return Few{mp, tiles >= 4 * sm_count || K < 256 ? 1 : 2};
+    return Few{mp, tiles >= 4 * sm_count || K < 1024 ? 1 : 2};
 }
 
 bool bad_flag(int f) { return f != 0 && f != 1; }

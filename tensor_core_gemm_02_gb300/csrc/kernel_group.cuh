@@ -20,8 +20,9 @@
 // does not fit, so the error of a long sum grows with its steps.  How much of that is let
 // stand is a template parameter:
 //   PREC_ACC    one accumulator for the whole sum (results of 16 bits).
-//   PREC_SUMS   the accumulator is emptied every four K blocks into float32 registers, which
-//               round to nearest (float32 results: 1000 x 1367 summed over 1000 1.2e-6 -> 3e-7).
+//   PREC_SUMS   the accumulator is emptied every eight (PREC_SPLIT: four) K blocks into float32
+//               registers, which round to nearest (float32 results, relative error of sums
+//               over 1024 1.2e-6 -> XXX).
 //   PREC_SPLIT  as PREC_SUMS, and both operands are pairs of float16 matrices, a high part and
 //               the rest: high x high + high x low + low x high, 22 bits of each operand.  Twelve
 //               MMAs a K block: two issuing warps, half of its K steps each (a lone thread's
@@ -85,7 +86,7 @@ struct GroupCfg {
     static constexpr int CS = CS_;
     static constexpr int ISS = PREC_ == kPrecSplit ? 2 : 1;  // MMA issuers
     static constexpr int PARTS = PREC_ == kPrecSplit ? 2 : 1;  // boxes of an operand in a stage
-    static constexpr int CHUNK = PREC_ == kPrecAcc ? 0 : 4;    // K blocks an accumulator takes (0: all)
+    static constexpr int CHUNK = PREC_ == kPrecAcc ? 0 : (PREC_ == kPrecSums ? 8 : 4);  // K blocks an accumulator takes (0: all)
     static constexpr bool PAIR = PAIR_;
     static constexpr int BM = 128, BN = BN_, BK = 64, STAGES = STAGES_;
     static constexpr int TILE_M = PAIR ? 256 : 128;
@@ -97,8 +98,8 @@ struct GroupCfg {
     static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES;
     // Epilogue groups of four warps: two, half of the columns each, but for the narrowest
     // tiles.  (A warp's chain of TMEM load, conversion, shared image and store is all latency:
-    // about 1 us for 64 columns.)
-    static constexpr int EPI_GROUPS = BN >= 128 ? 2 : 1;
+    // about 1 us for 64 columns.)  Four where 256 columns' sums stay in registers.
+    static constexpr int EPI_GROUPS = BN >= 128 ? (BN == 256 && PREC_ != kPrecAcc ? 4 : 2) : 1;
     static constexpr int COLS = BN / EPI_GROUPS;
     // C by TMA, into the buffers that D leaves from: two a warp then, and a stage less
     static constexpr bool C_TMA = KIND_ == kKindBatch && PREC_ == kPrecAcc;
@@ -116,7 +117,7 @@ struct GroupCfg {
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
     static_assert(!PAIR || BN == 256, "pairs: 256 x 256");
-    static_assert(PREC_ == kPrecAcc || (BN <= 128 && !PAIR), "a row's sums in a thread's registers");
+    static_assert(PREC_ != kPrecSplit || (BN <= 128 && !PAIR), "a row's sums in a thread's registers");
 };
 
 // The groups' rows, as one warp knows them.  Lane l keeps the block rows of groups l per
@@ -231,32 +232,75 @@ __device__ __forceinline__ uint32_t swz64(uint32_t row, uint32_t chunk)
 }
 
 // Rows [0, nrows) of an image of 32 rows of 128 (64) bytes to D at (row0, col0), columns below
-// N: pieces of 16 bytes (four or eight rows a pass, each row's bytes together) where D has
-// them, single elements otherwise.
+// N.  vec: D's rows are whole 16 bytes apart: pieces of 16 bytes, four or eight rows a pass, each
+// row's bytes together.  Otherwise a row a pass, lanes along the columns: float32 elements, or 16-bit
+// ones in pairs that begin where D's row has a 4-byte boundary.  (Pieces of 16 bytes taken apart
+// there: 16 x 1000 x 1367 of 100 rows each 85 us.)
 __device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, bool narrow, int32_t nrows,
                                                  uint32_t esize, void *D, int64_t ldd, int32_t row0,
                                                  int32_t col0, int32_t N, bool vec)
 {
-    const uint32_t pieces = narrow ? 4u : 8u;
-    const uint32_t chunk = lane % pieces;
-    const int32_t per = static_cast<int32_t>(16u / esize);
-    const int32_t col = col0 + static_cast<int32_t>(chunk) * per;
-    for (uint32_t r = lane / pieces; static_cast<int32_t>(r) < nrows; r += 32u / pieces) {
+    if (vec) {
+        const uint32_t pieces = narrow ? 4u : 8u;
+        const uint32_t chunk = lane % pieces;
+        const int32_t per = static_cast<int32_t>(16u / esize);
+        const int32_t col = col0 + static_cast<int32_t>(chunk) * per;
+        for (uint32_t r = lane / pieces; static_cast<int32_t>(r) < nrows; r += 32u / pieces) {
+            uint32_t w[4];
+            ld_shared_v4(buf + (narrow ? swz64(r, chunk) : swz128(r, chunk)), w[0], w[1], w[2], w[3]);
+            uint8_t *p = static_cast<uint8_t *>(D) + ((static_cast<int64_t>(row0) + r) * ldd + col) * esize;
+            if (col + per <= N) {
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else if (esize == 4u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col + i < N)
+                        reinterpret_cast<uint32_t *>(p)[i] = w[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col + i < N)
+                        reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+            }
+        }
+        return;
+    }
+    // (four rows at once, so that their loads, shuffles and stores overlap)
+    const uint32_t words = narrow ? 16u : 32u;
+    const uint32_t in_row = lane % words;
+    uint8_t *p = static_cast<uint8_t *>(D) + (static_cast<int64_t>(row0) * ldd + col0) * esize;
+    const int64_t pitch = ldd * esize;
+    const int32_t left = N - col0;  // columns of the row, at most
+    for (int32_t r0 = 0; r0 < nrows; r0 += 4, p += 4 * pitch) {
         uint32_t w[4];
-        ld_shared_v4(buf + (narrow ? swz64(r, chunk) : swz128(r, chunk)), w[0], w[1], w[2], w[3]);
-        uint8_t *p = static_cast<uint8_t *>(D) + ((static_cast<int64_t>(row0) + r) * ldd + col) * esize;
-        if (vec && col + per <= N) {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (esize == 4u) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; ++i) {
+            const uint32_t r = static_cast<uint32_t>(r0) + i;
+            w[i] = ld_shared_u32(buf + (narrow ? swz64(r, in_row / 4u) : swz128(r, in_row / 4u)) + in_row % 4u * 4u);
+        }
+        if (esize == 4u) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (col + i < N)
-                    reinterpret_cast<uint32_t *>(p)[i] = w[i];
-        } else {
+                if (r0 + i < nrows && static_cast<int32_t>(lane) < left)
+                    reinterpret_cast<uint32_t *>(p + i * pitch)[lane] = w[i];
+            continue;
+        }
+        const int32_t c = 2 * static_cast<int32_t>(lane);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < N)
-                    reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        for (int i = 0; i < 4; ++i) {
+            uint16_t *h = reinterpret_cast<uint16_t *>(p + i * pitch);
+            const bool odd = (reinterpret_cast<uintptr_t>(h) & 2u) != 0;
+            const uint32_t next = __shfl_down_sync(0xffffffffu, w[i], 1);
+            const uint32_t pair = odd ? (w[i] >> 16) | (next << 16) : w[i];
+            const int32_t e = c + (odd ? 1 : 0);  // the pair's first element
+            const bool row = r0 + i < nrows && lane < words;
+            const bool both = e + 1 < left && !(odd && lane == words - 1u);
+            if (row && both)
+                *reinterpret_cast<uint32_t *>(h + e) = pair;
+            if (row && !both && e < left)
+                h[e] = static_cast<uint16_t>(pair);
+            if (row && odd && lane == 0u && left > 0)
+                h[0] = static_cast<uint16_t>(w[i]);
         }
     }
 }
@@ -710,8 +754,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
         constexpr bool kF32 = kSums && !kBatch;  // (the products over groups sum in registers for float32 only)
         constexpr int kCols = Cfg::COLS;
         constexpr bool kOne = Cfg::EPI_BUFS == 1;  // one buffer a warp
-        const uint32_t q = warp & 3u, ew = (warp >= 6u ? 4u : 0u) + q;
-        const int32_t col_g = warp >= 6u ? kCols : 0;  // first column of this group of warps
+        const uint32_t q = warp & 3u, ew = (warp - 2u) / 4u * 4u + q;
+        const int32_t col_g = static_cast<int32_t>((warp - 2u) / 4u) * kCols;  // first column of this group of warps
         const uint32_t buf0 = base + Cfg::OFF_EPI + Cfg::EPI_BUFS * ew * Cfg::EPI_BUF;
         const bool f32 = kF32 || args.out_kind == kOutF32;
         const uint32_t esize = f32 ? 4u : 2u;
@@ -937,8 +981,13 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 }
             };
             auto wait_full = [&]() {
-                alive = warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
-                                                kWhereEpiAccFull);
+                // (PREC_SUMS: inline, or the call would save the sums' registers)
+                if constexpr (kSums)
+                    alive = warp_wait_bounded_inline(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                                     kWhereEpiAccFull);
+                else
+                    alive = warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                                    kWhereEpiAccFull);
                 tc_fence_after_sync();
                 return tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * Cfg::ISS * BN + col_g);
             };
@@ -954,6 +1003,18 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     const uint32_t acc = wait_full();
                     if (!alive)
                         break;
+                    if constexpr (Cfg::EPI_GROUPS == 4) {  // (18 warps: about 100 registers each)
+#pragma unroll
+                        for (int c = 0; c < kCols / 16; ++c) {
+                            uint32_t r[16];
+                            tc_ld_32x32b_x16(acc + 16u * c, r);
+                            tc_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sums[16 * c + i] = f == 0 ? __uint_as_float(r[i])
+                                                          : __fadd_rn(sums[16 * c + i], __uint_as_float(r[i]));
+                        }
+                    } else
 #pragma unroll
                     for (int c = 0; c < kCols / 32; ++c) {
                         uint32_t r[32];
@@ -1027,6 +1088,17 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 }
                 if (!stores)
                     continue;
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int col = 0; col < kCols; col += 32) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = zero ? 0u : __float_as_uint(mul_rn(args.alpha, sums[col + i]));
+                        put(col, w);
+                    }
+                    continue;
+                }
                 CPart c;
                 if (stores)
                     load_c(0, c);

@@ -9,7 +9,7 @@ namespace tcg {
 
 // A form of the group kernel: single CTAs with 128 x bn tiles (bn 64, 128, 256), or
 // (pair) CTA pairs with 256 x 256 ones.  maj: bit 0 A stored with K outermost, bit 1 B.
-// grid counts CTAs.  prec: kPrecAcc, or (bn 64 or 128) sums kept in registers.
+// grid counts CTAs.  prec: kPrecAcc, or sums kept in registers (bn 64 or 128, or pairs).
 cudaError_t launch_group_rows(int bn, bool pair, bool b_major, int prec, const GroupMaps &maps, const GroupArgs &args,
                               int grid, cudaStream_t stream);
 // Few rows a group: tiles of mp (16, 32, 64) rows, each tile's sum shared by cs (1, 2) CTAs.

@@ -54,11 +54,15 @@ cudaError_t group_launch_forms(int bn, bool pair, const GroupMaps &maps, const G
     return cudaErrorInvalidValue;
 }
 
-// The forms that keep float32 sums in registers.
+// The forms that keep float32 sums in registers (bn 256: CTA pairs).
 template <int KIND, int MAJ, bool SYM, int PREC>
 cudaError_t group_launch_sums(int bn, const GroupMaps &maps, const GroupArgs &args, int grid, cudaStream_t stream)
 {
     constexpr int kDeep = PREC == kPrecSplit ? 2 : 1;
+    if constexpr (PREC == kPrecSums) {
+        if (bn == 256)
+            return group_launch_impl<256, 5, true, KIND, MAJ, SYM, PREC>(maps, args, grid, stream);
+    }
     if (bn == 128)
         return group_launch_impl<128, 6 / kDeep, false, KIND, MAJ, SYM, PREC>(maps, args, grid, stream);
     if (bn == 64)

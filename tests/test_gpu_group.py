@@ -37,8 +37,8 @@ def _clean():
 
 
 def sum_bound(K, out):
-    """As gated_ref's; float32 results are added up in registers every 256 of K, each time one rounding."""
-    return ref.sum_bound(K) if out != OUT_F32 else ref.sum_bound(min(K, 256)) + K / 256 * 2.0 ** -24
+    """As gated_ref's; float32 results are added up in registers every 512 of K, each time one rounding."""
+    return ref.sum_bound(K) if out != OUT_F32 else ref.sum_bound(min(K, 512)) + K / 512 * 2.0 ** -24
 
 
 def offsets_of(counts, front):
