@@ -281,8 +281,8 @@ __device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, bo
         if (esize == 4u) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (r0 + i < nrows && static_cast<int32_t>(lane) < left)
-                    reinterpret_cast<uint32_t *>(p + i * pitch)[lane] = w[i];
+                st_global_u32_if(r0 + i < nrows && static_cast<int32_t>(lane) < left,
+                                 reinterpret_cast<uint32_t *>(p + i * pitch) + lane, w[i]);
             continue;
         }
         const int32_t c = 2 * static_cast<int32_t>(lane);
@@ -295,12 +295,9 @@ __device__ __forceinline__ void store_image_rows(uint32_t buf, uint32_t lane, bo
             const int32_t e = c + (odd ? 1 : 0);  // the pair's first element
             const bool row = r0 + i < nrows && lane < words;
             const bool both = e + 1 < left && !(odd && lane == words - 1u);
-            if (row && both)
-                *reinterpret_cast<uint32_t *>(h + e) = pair;
-            if (row && !both && e < left)
-                h[e] = static_cast<uint16_t>(pair);
-            if (row && odd && lane == 0u && left > 0)
-                h[0] = static_cast<uint16_t>(w[i]);
+            st_global_u32_if(row && both, h + e, pair);
+            st_global_u16_if(row && !both && e < left, h + e, pair);
+            st_global_u16_if(row && odd && lane == 0u && left > 0, h, w[i]);
         }
     }
 }

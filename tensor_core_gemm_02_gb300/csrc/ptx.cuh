@@ -909,6 +909,21 @@ __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Stores under a predicate (a branch around each of several stores costs more than they do).
+__device__ __forceinline__ void st_global_u32_if(bool on, void *p, uint32_t v)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+                 "r"(static_cast<uint32_t>(on))
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global_u16_if(bool on, void *p, uint32_t v)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(p),
+                 "h"(static_cast<unsigned short>(v)), "r"(static_cast<uint32_t>(on))
+                 : "memory");
+}
+
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c,
                                              uint32_t &d)
 {
