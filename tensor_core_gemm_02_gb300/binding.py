@@ -496,20 +496,25 @@ def gemm_group_rows(ids, groups, offsets=None, order=None, rows=None, *, stream=
     int32) where each group's rows begin, order the positions in ids.flatten() by group, equal
     ones in their order, those of no group last, and rows = order // choices (choices 1 for
     1-D ids), which gemm_grouped takes as its idx."""
-    if ids.dim() not in (1, 2):
+    shape, i32 = ids.shape, torch.int32
+    if len(shape) not in (1, 2):
         raise ValueError("ids must be 1-D or tokens x choices")
-    choices = max(1, ids.shape[1]) if ids.dim() == 2 else 1
-    M, new, i32 = ids.numel(), _allocator(ids.device), torch.int32
-    offsets = new((groups + 1,), (1,), i32) if offsets is None else offsets
-    order = new((M,), (1,), i32) if order is None else order
-    rows = new((M,), (1,), i32) if rows is None else rows
-    args = (M, groups, choices, _ints("ids", ids, ids.shape), _ints("offsets", offsets, (groups + 1,)),
-            _ints("order", order, (M,)), _ints("rows", rows, (M,)))
-    _on_device(ids, offsets, order, rows)
-    st = load_library().gemm_group_rows(*args, _stream_ptr(stream))
+    choices = max(1, shape[1]) if len(shape) == 2 else 1
+    M = ids.numel()
+    new = _allocator(ids.device)
+    ptrs, outs = [_ints("ids", ids, shape)], []
+    for name, t, n in (("offsets", offsets, groups + 1), ("order", order, M), ("rows", rows, M)):
+        if t is None:
+            t = new((n,), (1,), i32)
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_ints(name, t, (n,)))
+        outs.append(t)
+    _on_device(ids, *outs)
+    st = load_library().gemm_group_rows(M, groups, choices, *ptrs, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_group_rows")
-    return offsets, order, rows
+    return tuple(outs)
 
 
 def gemm_grouped(A, B, offsets, D=None, *, idx=None, trans_b=False, alpha=1.0, out=OUT_F32, stream=None):
