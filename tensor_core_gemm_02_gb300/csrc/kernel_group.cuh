@@ -466,6 +466,11 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
     // (CS = 2) this CTA's K blocks of a tile: from kb_first, kb_mine of them
     const int32_t kb_first = CS == 2 ? static_cast<int32_t>(share) * (k_blocks / 2) : 0;
     const int32_t kb_mine = CS == 2 ? (share == 0u ? k_blocks / 2 : k_blocks - k_blocks / 2) : k_blocks;
+    // (KIND_SUM) A partial block is loaded this many blocks before the end of its tile and
+    // multiplied at the end, so that its zeros are there in time: loaded last, it held up
+    // every tile (four groups of 1025 rows, 4096 x 4096: 101.8 us against 87 of 1024).
+    constexpr int32_t kEarly = 3;
+    static_assert(!kSum || STAGES > kEarly, "the blocks after a partial one fit beside it");
     // K blocks of tile t (KIND_SUM: of its group) that this CTA multiplies
     auto blocks_of = [&](int32_t t, int32_t &rem) -> int32_t {
         rem = 0;
@@ -591,10 +596,15 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 return true;
             };
             const int32_t whole = kSum && rem != 0 ? nkb - 1 : nkb;
-            for (int32_t kb = 0; kb < whole && alive; ++kb)
+            const int32_t early = kSum && rem != 0 ? max(0, whole - kEarly) : whole;
+            for (int32_t kb = 0; kb < early && alive; ++kb)
                 alive = fetch(Bool<false>{}, kb);
-            if (kSum && whole < nkb && alive)
-                alive = fetch(Bool<true>{}, whole);
+            if constexpr (kSum) {
+                if (rem != 0 && alive)
+                    alive = fetch(Bool<true>{}, whole);
+                for (int32_t kb = early; kb < whole && alive; ++kb)
+                    alive = fetch(Bool<false>{}, kb);
+            }
         }
         if (!alive) {
             // every copy issued lands before the shared memory is released (bounded; the
@@ -646,7 +656,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 };
                 if (!wait_acc())
                     break;
-                auto multiply = [&](auto partial, int32_t kb) -> bool {
+                // K block kb, on stage st (phase sph of its barrier)
+                auto multiply = [&](auto partial, int32_t kb, int st, uint32_t sph) -> bool {
                     constexpr bool part = kSum && decltype(partial)::value;
                     // (a chunk's sum goes to the epilogue, the next chunk starts from zero)
                     const bool begins = kSums ? kb % Cfg::CHUNK == 0 : kb == 0;
@@ -659,15 +670,15 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     // (the peer's zeros: an acquire at cluster scope)
                     const bool got =
                         PAIR && part
-                            ? wait_bounded_cluster(full_bar(s), ph, abort_flag, args.status, args.timeout_ns,
+                            ? wait_bounded_cluster(full_bar(st), sph, abort_flag, args.status, args.timeout_ns,
                                                    kWhereMmaFull)
-                            : wait_bounded<true>(full_bar(s), ph, abort_flag, args.status, args.timeout_ns,
+                            : wait_bounded<true>(full_bar(st), sph, abort_flag, args.status, args.timeout_ns,
                                                  kWhereMmaFull);
                     if (!got)
                         return false;
                     tc_fence_after_sync();
-                    const uint32_t sa = base + Cfg::OFF_A + s * (Cfg::PARTS * Cfg::A_BYTES);
-                    const uint32_t sb = base + Cfg::OFF_B + s * (Cfg::PARTS * Cfg::B_BYTES);
+                    const uint32_t sa = base + Cfg::OFF_A + st * (Cfg::PARTS * Cfg::A_BYTES);
+                    const uint32_t sb = base + Cfg::OFF_B + st * (Cfg::PARTS * Cfg::B_BYTES);
                     constexpr uint32_t kStepA = kMnA ? 128u : 2u, kStepB = kMnB ? 128u : 2u;
                     // (of a partial block only the K steps that hold rows of the group)
                     const int steps = part ? (rem + 15) / 16 : 4;
@@ -690,18 +701,33 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                             }
                         }
                     }
-                    commit_to(empty_bar(s));
+                    commit_to(empty_bar(st));
+                    return true;
+                };
+                auto next_stage = [&]() {
                     if (++s == STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
-                    return true;
                 };
                 const int32_t whole = kSum && rem != 0 ? nkb - 1 : nkb;
-                for (int32_t kb = 0; kb < whole && alive; ++kb)
-                    alive = multiply(Bool<false>{}, kb);
-                if (kSum && whole < nkb && alive)
-                    alive = multiply(Bool<true>{}, whole);
+                const int32_t early = kSum && rem != 0 ? max(0, whole - kEarly) : whole;
+                for (int32_t kb = 0; kb < early && alive; ++kb) {
+                    alive = multiply(Bool<false>{}, kb, s, ph);
+                    next_stage();
+                }
+                if constexpr (kSum) {
+                    if (rem != 0 && alive) {
+                        const int st = s;
+                        const uint32_t sph = ph;
+                        next_stage();
+                        for (int32_t kb = early; kb < whole && alive; ++kb) {
+                            alive = multiply(Bool<false>{}, kb, s, ph);
+                            next_stage();
+                        }
+                        alive = alive && multiply(Bool<true>{}, whole, st, sph);
+                    }
+                }
                 if (!alive)
                     break;
                 next_acc();
@@ -717,7 +743,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 int32_t rem;
                 const int32_t nkb = blocks_of(t, rem);
                 if (rem != 0) {
-                    const int at = (s + nkb - 1) % STAGES;
+                    const int at = (s + max(0, nkb - 1 - kEarly)) % STAGES;
                     if (!warp_wait_bounded(tail_bar(at), (tail_ph >> at) & 1u, abort_flag, args.status,
                                            args.timeout_ns, kWhereMmaFull))
                         break;
