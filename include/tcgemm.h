@@ -33,8 +33,10 @@
  * device, a small status word in its own device globals and a host-side cache
  * of TMA descriptors; per device and stream, the skinny (M <= 64) path keeps
  * a workspace for split tiles, the FP4 paths buffers for converted weights
- * or re-pitched scales, and gemm_trans and gemm_gated_backward one or two for
- * the float32 parts of long sums over few tiles (splits > 1).  Each is allocated
+ * or re-pitched scales, gemm_trans and gemm_gated_backward one or two for
+ * the float32 parts of long sums over few tiles (splits > 1), gemm_orthogonalize
+ * one for its iterates, and gemm_group_rows one for counts (more than 131072
+ * ids).  Each is allocated
  * by the first call that needs it; a call that needs more gets a new one of at
  * least twice the size, and the old one stays until the process ends (together
  * the old ones are no larger than the newest), since a captured graph may hold
@@ -533,7 +535,8 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  * offsets[groups] on keep what they hold.  The offsets are read on the device: the host
  * need not know them, and a captured call follows them.
  *
- *  groups            in [0, 1024] (GEMM_ERR_UNSUPPORTED above); 0: nothing is done.
+ *  M, N, K           below 2^31 - 512; groups in [0, 1024] (GEMM_ERR_UNSUPPORTED above); groups
+ *                    0: nothing is done.
  *  offsets           groups + 1 int32, not falling, in [0, M].  Where they are not, nothing
  *                    is computed and GEMM_ERR_INDEX is recorded in the device status word.
  *  M                 rows of D (and of A without idx; entries of idx).
@@ -591,7 +594,8 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *  steps             1 to 100; a, b, c finite; eps >= 0.
  *  Y                 may be X exactly (same pointer, type, pitch and stride); any other
  *                    overlap is GEMM_ERR_ALIAS.
- *  Rounding: the norm and every sum are float32.  Between the products the iterate X is held
+ *  Rounding: the norm and every sum are float32 (so the squares of X's elements have to
+ *  be float32 numbers: |x| from about 1e-19 to 1e18).  Between the products the iterate X is held
  *  as two float16 matrices, a high part and the rest (22 bits), P and b P + c P^2 in float16.
  *  The products take the high part of X; all of their operands in two parts (three products
  *  for one) in every step of a float32 Y, in the last one of a float16 Y, and in two more,
@@ -710,7 +714,11 @@ gemm_status gemm_debug_inject(int mode);
  * with packed codes, M <= 64, K > 0; other calls keep the automatic choice;
  * forcing 11 - 14 keeps gemm_e2m1 on the tile kernel at M <= 64), kernel 2 = the skinny kernel with bn = 0 or 128
  * (problems it can run: M <= 64, K > 0, not gathered or seeded), kernel 0 =
- * automatic choice (the default).  Tile forms apply to every problem the tile
+ * automatic choice (the default).  The products over groups (gemm_grouped,
+ * gemm_grouped_weights and gemm_orthogonalize's) take kernels 1 and 3 likewise,
+ * the latter with operands in two parts as two CTAs that share a tile, and
+ * gemm_grouped kernel 2 as its kernel for few rows a group; where there is no
+ * such form they keep the automatic choice.  Tile forms apply to every problem the tile
  * kernel runs, M <= 64 ones included; FP4 weights keep their own paths, and
  * problems the forced form cannot run (K == 0 for clusters and pairs) keep
  * the automatic choice.  Returns GEMM_ERR_INVALID_ARG for other values.

@@ -11,6 +11,7 @@ from __future__ import annotations
 __all__ = [
     "gemm", "gemm_f16", "gemm_bf16", "gemm_gather_rows", "gemm_check_device_status",
     "gemm_gated", "gemm_gated_backward", "gemm_gated_e2m1", "gemm_quantize_e2m1", "gemm_trans",
+    "gemm_group_rows", "gemm_grouped", "gemm_grouped_weights", "gemm_orthogonalize",
     "gemm_status_string", "GemmError", "load_library",
 ]
 

@@ -17,6 +17,7 @@ namespace host {
 namespace {
 
 constexpr int64_t kMaxGroups = 1024;  // (a warp keeps 32 groups a lane)
+constexpr int64_t kMaxRows = kMaxDim - 512;  // (a tile's rows past the last one are 32-bit numbers too)
 constexpr int kGroupM = 16;           // block rows per tile-order group, as the plain forms
 
 // A form of the group kernel, with the time of a tile's K block and of its fixed part in ns
@@ -221,7 +222,7 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     if (bad_flag(dtype_is_bf16) || bad_flag(trans_b) || M < 0 || N < 0 || K < 0 || groups < 0 || !out_ok(out) ||
         (idx && a_rows < 1))
         return GEMM_ERR_INVALID_ARG;
-    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || (idx && a_rows > kMaxDim) || groups > kMaxGroups)
+    if (M > kMaxRows || N > kMaxRows || K > kMaxRows || (idx && a_rows > kMaxDim) || groups > kMaxGroups)
         return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0 || groups == 0)
         return GEMM_OK;
@@ -302,7 +303,7 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
 {
     if (bad_flag(dtype_is_bf16) || M < 0 || N < 0 || K < 0 || groups < 0 || !out_ok(out))
         return GEMM_ERR_INVALID_ARG;
-    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > kMaxGroups)
+    if (M > kMaxRows || N > kMaxRows || K > kMaxRows || groups > kMaxGroups)
         return GEMM_ERR_UNSUPPORTED;
     if (N == 0 || K == 0 || groups == 0)
         return GEMM_OK;
@@ -456,7 +457,7 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     if (count < 0 || M < 0 || N < 0 || !out_ok(type) || !out_ok(out) || steps < 1 || steps > 100 ||
         !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !(eps >= 0.0f))
         return GEMM_ERR_INVALID_ARG;
-    if (count > kMaxDim || M > kMaxDim || N > kMaxDim)
+    if (count > kMaxDim || M > kMaxRows || N > kMaxRows)
         return GEMM_ERR_UNSUPPORTED;
     if (count == 0 || M == 0 || N == 0)
         return GEMM_OK;

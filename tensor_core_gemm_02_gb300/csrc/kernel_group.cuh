@@ -22,7 +22,7 @@
 //   PREC_ACC    one accumulator for the whole sum (results of 16 bits).
 //   PREC_SUMS   the accumulator is emptied every eight (PREC_SPLIT: four) K blocks into float32
 //               registers, which round to nearest (float32 results, relative error of sums
-//               over 1024 1.2e-6 -> XXX).
+//               over 1024 1.2e-6 -> 6e-7).
 //   PREC_SPLIT  as PREC_SUMS, and both operands are pairs of float16 matrices, a high part and
 //               the rest: high x high + high x low + low x high, 22 bits of each operand.  Twelve
 //               MMAs a K block: two issuing warps, half of its K steps each (a lone thread's
@@ -36,6 +36,15 @@
 // runs beside the next tile's MMAs.  PAIR: the roles on a CTA pair and one 256 x 256 tile
 // (tcgen05 cta_group::2), each CTA loading its 128 rows of A and its half of B.  The
 // protocol is the tile kernel's (kernel_tile.cuh).  Every wait is bounded.
+//
+// Bounds and figures.  KIND_ROWS and KIND_SUM of long sums are bound by the tensor cores under
+// the power cap (16384 rows in eight uneven groups, 14336 x 4096 bf16: 1.19 to 1.22 ms forward,
+// 1.25 to 1.27 the input's gradient, 1.21 the weights'; 1.5 to 1.6 PFLOP/s; tensor pipe active 85 %
+// of cycles at 4096 rows and 4096 x 4096), of short ones by the results' way out (eight groups
+// of 128 rows: 940 MB of bf16 gradients 224 us, float32 1.9 GB 290).  KIND_BATCH likewise: 4096 x
+// 4096 x 14336, half of a symmetric product 148 us, the update 290 (1.66 and 1.65 PFLOP/s); where
+// the tiles are few, by the rate L2 feeds an SM (128 x 128 tiles: 63 bytes a clock).  Rows of D that
+// are not 16 bytes apart go out as words (16 x 1000 x 1367 from 100 rows each 36 us, 1368 20).
 //
 // Why tiles from device offsets and not from a list: a list is a second kernel before
 // every call.  Each warp that needs coordinates reads the offsets (at most 1024 groups,

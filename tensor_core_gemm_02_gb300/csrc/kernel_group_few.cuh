@@ -14,6 +14,11 @@
 // peers' shared memory; each then adds the parts in order and stores its rows: no workspace,
 // no atomics, the same bits every time.
 //
+// Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 138 us (6.8 TB/s; the tile kernel 141 to 160),
+// two of one row 38.5 (6.1 TB/s; one CTA a tile 56, the tile kernel 60); 2 of 64 groups, 2816 x 1024
+// 6.9 (launch, offsets, first loads, join).  More rows: 64 a group 161 against the tile kernel's 163,
+// 100 of 2816 x 1024 91 against 84, hence the change at 48.
+//
 //   warp 0     producer: per stage two K blocks of B (boxes of 64 x 128, or stored K x N two
 //              boxes of 64 x 64) and of A (a box of MP rows, or MP / 4 tile::gather4)
 //   warps 1-2  MMA issuers, one for each of a stage's K blocks, into accumulators of their own
