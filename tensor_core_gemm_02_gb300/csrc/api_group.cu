@@ -150,7 +150,11 @@ Span span_of(const Stack &s)
 }
 
 // Few rows a group: the kernel that streams the weights, as (rows of a tile, CTAs a tile); rows
-// 0 where the tile kernel runs.
+// 0 where the tile kernel runs.  Measured, us, groups x N x K of so many rows, bf16: tiles of 16 / 32 /
+// 64 rows, 8 x 14336 x 4096 of 4 141 / 137 / 138, of 12 143 / 139 / 140, of 24 154 / 141 / 141, of 40 183 /
+// 159 / 142 (the tile kernel 143 to 149); 2 x 2816 x 1024 of 1 6.4 / 6.7 / 7.9 (9.0).  One / two CTAs a tile:
+// 2 x 4096 x 14336 (64 tiles) 42.7 / 39.2, 2 x 14336 x 4096 (224) 39.0 / 39.1, 2 x 2816 x 1024 (44) 6.4 / 6.7,
+// 32 x 2816 x 1024 (704) 31.6 / 39.0: two where they have SMs of their own and a long sum to share.
 struct Few {
     int mp, cs;
 };
@@ -163,7 +167,7 @@ Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
         return Few{0, 0};
     const int mp = rows <= 8 ? 16 : (rows <= 16 ? 32 : 64);
     const int64_t tiles = used * ceil_div(rows, mp) * ceil_div(N, 128);
-    return Few{mp, tiles >= 4 * sm_count || K < 1024 ? 1 : 2};
+    return Few{mp, 2 * tiles <= sm_count && K >= 4096 ? 2 : 1};
 }
 
 bool bad_flag(int f) { return f != 0 && f != 1; }

@@ -7,17 +7,16 @@
 // A tile is 128 columns of D by MP rows of a group; its tiles come from the offsets as in
 // kernel_group.cuh.
 //
-// Split: CS CTAs of a cluster share each tile's sum, CTA c the c-th part of its K blocks.
-// With one CTA a tile few groups leave SMs idle or a last wave half empty (two groups of
-// 14336 x 4096 are 224 tiles for 152 SMs).  Each CTA ends with the sums of its part for 128
-// columns x MP rows, keeps those of its own MP / CS rows and writes the others into the
-// peers' shared memory; each then adds the parts in order and stores its rows: no workspace,
-// no atomics, the same bits every time.
+// Split: CS CTAs of a cluster share each tile's sum, CTA c the c-th part of its K blocks, where
+// there are fewer tiles than SMs and the sums are long.  Each CTA ends with the sums of its part
+// for 128 columns x MP rows, keeps those of its own MP / CS rows and writes the others into the
+// peer's shared memory; each then adds the parts in order and stores its rows: no workspace, no
+// atomics, the same bits every time.
 //
-// Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 138 us (6.8 TB/s; the tile kernel 141 to 160),
-// two of one row 38.5 (6.1 TB/s; one CTA a tile 56, the tile kernel 60); 2 of 64 groups, 2816 x 1024
-// 6.9 (launch, offsets, first loads, join).  More rows: 64 a group 161 against the tile kernel's 163,
-// 100 of 2816 x 1024 91 against 84, hence the change at 48.
+// Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 138 us (6.8 TB/s), two of one row 39 (6.0 TB/s; the
+// tile kernel 65); 2 of 64 groups, 2816 x 1024 6.4 us (launch, offsets, first loads, epilogue).  More
+// rows: 64 a group 161 against the tile kernel's 163, 100 of 2816 x 1024 91 against 84, hence the
+// change at 48.
 //
 //   warp 0     producer: per stage two K blocks of B (boxes of 64 x 128, or stored K x N two
 //              boxes of 64 x 64) and of A (a box of MP rows, or MP / 4 tile::gather4)

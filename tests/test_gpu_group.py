@@ -133,6 +133,15 @@ def test_grouped_normal(trans_b, counts, N, K):
         check_grouped(counts, 0, 0, N, K, trans_b, dtype, out, False, idx=True)
 
 
+@pytest.mark.parametrize("trans_b", [False, True])
+@pytest.mark.parametrize("counts", [[3, 0, 5, 1], [12, 16], [40, 60, 2], [1]])
+def test_few_rows_and_long_sums(trans_b, counts):
+    """Fewer tiles than half of the SMs: two CTAs share each tile's sum."""
+    for i, K in enumerate((4096, 4104, 8200)):
+        dtype, out = KINDS[i]
+        check_grouped(counts, 0, 2, 200, K, trans_b, dtype, out, True, idx=i == 1)
+
+
 def test_grouped_largest_number_of_groups():
     gen = torch.Generator().manual_seed(3)
     counts = torch.randint(0, 4, (1024,), generator=gen).tolist()
