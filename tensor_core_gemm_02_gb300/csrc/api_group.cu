@@ -35,7 +35,7 @@ constexpr GForm kForms[4] = {{64, false, 1, 300, 800}, {128, false, 1, 300, 1000
 // (float32 results, sums in registers)
 constexpr GForm kSumForms[3] = {{64, false, 1, 300, 700}, {128, false, 1, 480, 800}, {256, true, 1, 320, 7500}};
 // (operands in two parts)
-constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 1500}, {128, false, 1, 600, 2000}, {64, false, 2, 440, 3000}};
+constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 3500}, {128, false, 1, 600, 4500}, {64, false, 2, 440, 2000}};
 
 // The form of the least waves x time of a tile.  tiles(tile_m, bn): tiles of the problem
 // (0: the form does not apply).
