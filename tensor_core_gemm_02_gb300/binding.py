@@ -10,6 +10,7 @@ anything some other way.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -116,6 +117,13 @@ def _stream_ptr(stream) -> int:
     if stream is None:
         return _raw_stream(_current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(stream):
+    """A context in which torch's own operations run on the stream of the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -530,14 +538,18 @@ def gemm_grouped(A, B, offsets, D=None, *, idx=None, trans_b=False, alpha=1.0, o
     N = cb if trans_b else rb
     if (rb if trans_b else cb) != K:
         raise ValueError("A and B disagree on K")
-    if D is None:
-        D = torch.zeros((M, N), dtype=_DTYPE_OF_OUT[out], device=A.device)
+    new = D is None
+    if new:
+        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
     a, lda = _mat("A", A, table, K, dt)
     args = (M, N, K, groups, bf16, a, table, lda,
             None if idx is None else _ints("idx", idx, (M,)), _ints("offsets", offsets, (groups + 1,)),
             1 if trans_b else 0, *_stack("B", B, groups, rb, cb, dt), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]),
             out, alpha)
     _on_device(A, B, offsets, idx, D)
+    if new:
+        with _on_stream(stream):
+            D.zero_()
     st = load_library().gemm_grouped(*args, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_grouped")

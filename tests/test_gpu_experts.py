@@ -179,6 +179,27 @@ def test_replay_after_a_larger_call():
     assert all(bool((t == 7).all()) for t in others)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_stream_that_is_not_the_current_one(raw):
+    """Every step of a call, a new output's zeros too, is on the stream it is given, whatever else the
+    current one still has to do."""
+    A, B, dD = quarters((150, 136), 1), quarters((3, 200, 136), 2), quarters((150, 200), 3)
+    ids = torch.randint(-1, 3, (150,), dtype=torch.int32, device="cuda")
+    off = binding.gemm_group_rows(ids, 3)[0]
+    calls = [lambda **k: binding.gemm_group_rows(ids, 3, **k)[1], lambda **k: binding.gemm_grouped(A, B, off, **k),
+             lambda **k: binding.gemm_grouped(dD, B, off, trans_b=True, out=binding.OUT_BF16, **k),
+             lambda **k: binding.gemm_grouped_weights(dD, A, off, **k), lambda **k: binding.gemm_orthogonalize(B, **k)]
+    want = [c() for c in calls]
+    s, busy = torch.cuda.Stream(), torch.empty(1 << 31, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(100):
+        busy.fill_(1)
+    got = [c(stream=s.cuda_stream if raw else s) for c in calls]
+    torch.cuda.synchronize()
+    for i, (g, w) in enumerate(zip(got, want)):
+        assert torch.equal(g, w), i
+
+
 def _ortho(i):
     X = torch.randn((2, 100 + 40 * i, 150), device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
     return lambda: binding.gemm_orthogonalize(X)

@@ -276,6 +276,33 @@ def test_weights_without_rows():
     assert (dB == 0).all()
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_elements_past_32_bits(form):
+    """Matrices of a stack and rows so far apart that element numbers do not fit 32 bits."""
+    binding.gemm_debug_force_tile(*FORMS[form])
+    gen = torch.Generator().manual_seed(3)
+    counts, N, K, far = [30, 5, 45], 200, 136, (1 << 31) + 64
+    off = offsets_of(counts, 0)
+    big = torch.empty(2 * far + 300 * 512, dtype=F16, device="cuda")  # (8.6 GB)
+    A, dD, small = wide(80, K, F16, gen, True), wide(80, N, F16, gen, True), stack(3, N, K, F16, gen, True)
+    B = big.as_strided((3, N, K), (far, K, 1))
+    B.copy_(small)
+    want = binding.gemm_grouped(A, small, off), binding.gemm_grouped(dD, small, off, trans_b=True)
+    assert torch.equal(binding.gemm_grouped(A, B, off), want[0])
+    assert torch.equal(binding.gemm_grouped(dD, B, off, trans_b=True), want[1])
+    wantB = binding.gemm_grouped_weights(dD, A, off, out=binding.OUT_F16)
+    binding.gemm_grouped_weights(dD, A, off, B, out=binding.OUT_F16)
+    assert torch.equal(B, wantB)
+    pitch = 1 << 25  # (80 rows of it: 2^31 is passed at row 64)
+    rows = big.as_strided((80, N), (pitch, 1))
+    binding.gemm_grouped(A, small, off, rows, out=binding.OUT_F16)
+    assert torch.equal(rows, want[0].half())
+    rows = big.as_strided((80, K), (pitch, 1))
+    rows.copy_(A)
+    assert torch.equal(binding.gemm_grouped(rows, small, off), want[0])
+    assert torch.equal(binding.gemm_grouped_weights(dD, rows, off, out=binding.OUT_F16), wantB)
+
+
 def test_gradients_against_differences():
     """dA and dB of sum(dD * D) against central differences of the product itself, which is linear in
     each operand: on quarter-integers both are exact."""

@@ -187,3 +187,14 @@ def test_a_stack_larger_than_the_workspace():
     Y = binding.gemm_orthogonalize(X, steps=2)
     for i in (0, 1, 9999, 13000, 19999):
         assert torch.equal(Y[i], binding.gemm_orthogonalize(X[i], steps=2)), i
+
+
+def test_elements_past_32_bits():
+    """Matrices so far apart that element numbers do not fit 32 bits."""
+    X, far = stack(3, 90, 70, torch.bfloat16, 4), (1 << 31) + 5
+    big = torch.empty(2 * far + 90 * 70, dtype=torch.bfloat16, device="cuda").as_strided((3, 90, 70), (far, 70, 1))
+    big.copy_(X)
+    want = binding.gemm_orthogonalize(X, steps=2)
+    assert torch.equal(binding.gemm_orthogonalize(big, steps=2), want)
+    binding.gemm_orthogonalize(X, big, steps=2)
+    assert torch.equal(big, want)
