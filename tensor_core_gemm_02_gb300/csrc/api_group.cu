@@ -37,6 +37,10 @@ constexpr GForm kSumForms[3] = {{64, false, 1, 300, 700}, {128, false, 1, 480, 8
 // (operands in two parts)
 constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 3500}, {128, false, 1, 600, 4500}, {64, false, 2, 440, 2000}};
 
+// Shorter sums than these K blocks are not shared: their halves' exchange takes what they save (64 x
+// 128 x 512 150 us, shared 220; 512 x 512 133, shared 108).
+constexpr int64_t kSharedBlocks = 8;
+
 // The form of the least waves x time of a tile.  tiles(tile_m, bn): tiles of the problem
 // (0: the form does not apply).
 template <class F>
@@ -50,7 +54,7 @@ GForm choose_form(int64_t k_blocks, int prec, int sm_count, F tiles)
     int64_t best_ns = 0;
     for (const GForm *f = forms; f != forms + n_forms; ++f) {
         const int64_t n = tiles(f->pair ? 256 : 128, f->bn), sets = sm_count / (f->pair ? 2 : f->cs);
-        if (n <= 0 || sets <= 0)
+        if (n <= 0 || sets <= 0 || (f->cs > 1 && k_blocks < kSharedBlocks))
             continue;
         if ((fk == 1 && !f->pair && f->cs == 1 && f->bn == fbn) || (fk == 3 && (f->pair || f->cs == 2)))
             return *f;

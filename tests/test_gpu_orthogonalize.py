@@ -198,3 +198,10 @@ def test_elements_past_32_bits():
     assert torch.equal(binding.gemm_orthogonalize(big, steps=2), want)
     binding.gemm_orthogonalize(X, big, steps=2)
     assert torch.equal(big, want)
+
+
+@pytest.mark.parametrize("form", [(1, 64), (1, 128), (3, 256), (0, 0)])
+@pytest.mark.parametrize("count,m,n", [(3, 700, 900), (2, 1100, 380), (1, 2000, 1030)])
+def test_more_tiles_than_ctas_hold(form, count, m, n):
+    binding.gemm_debug_force_tile(*form)
+    check(stack(count, m, n, torch.float32, m + n), MUON, 2)
