@@ -505,24 +505,33 @@ def gemm_group_rows(ids, groups, offsets=None, order=None, rows=None, *, stream=
     ones in their order, those of no group last, and rows = order // choices (choices 1 for
     1-D ids), which gemm_grouped takes as its idx."""
     shape, i32 = ids.shape, torch.int32
-    if len(shape) not in (1, 2):
+    if len(shape) == 1:
+        choices = 1
+    elif len(shape) == 2:
+        choices = shape[1] or 1
+    else:
         raise ValueError("ids must be 1-D or tokens x choices")
-    choices = max(1, shape[1]) if len(shape) == 2 else 1
-    M = ids.numel()
-    new = _allocator(ids.device)
-    ptrs, outs = [_ints("ids", ids, shape)], []
-    for name, t, n in (("offsets", offsets, groups + 1), ("order", order, M), ("rows", rows, M)):
-        if t is None:
-            t = new((n,), (1,), i32)
-            ptrs.append(t.data_ptr())
-        else:
-            ptrs.append(_ints(name, t, (n,)))
-        outs.append(t)
-    _on_device(ids, *outs)
-    st = load_library().gemm_group_rows(M, groups, choices, *ptrs, _stream_ptr(stream))
+    M, p, new = ids.numel(), _ints("ids", ids, shape), _allocator(ids.device)
+    if offsets is None:
+        offsets = new((groups + 1,), (1,), i32)
+        p_off = offsets.data_ptr()
+    else:
+        p_off = _ints("offsets", offsets, (groups + 1,))
+    if order is None:
+        order = new((M,), (1,), i32)
+        p_order = order.data_ptr()
+    else:
+        p_order = _ints("order", order, (M,))
+    if rows is None:
+        rows = new((M,), (1,), i32)
+        p_rows = rows.data_ptr()
+    else:
+        p_rows = _ints("rows", rows, (M,))
+    _on_device(ids, offsets, order, rows)
+    st = load_library().gemm_group_rows(M, groups, choices, p, p_off, p_order, p_rows, _stream_ptr(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_group_rows")
-    return tuple(outs)
+    return offsets, order, rows
 
 
 def gemm_grouped(A, B, offsets, D=None, *, idx=None, trans_b=False, alpha=1.0, out=OUT_F32, stream=None):
