@@ -30,10 +30,10 @@ struct GForm {
 };
 // Measured, us a tile, 2 / 8 / 32 and more blocks: 128 x 256 2.35 / 4.1, pairs 3.0 / 3.6 / 12.7;
 // float32 results, 128 columns 1.5 / - / 0.5 a block, pairs 6.3 / - / 26.8 (64 blocks).
-constexpr GForm kForms[4] = {{64, false, 1, 300, 800}, {128, false, 1, 300, 1000}, {256, false, 1, 330, 1700},
+constexpr GForm kForms[4] = {{64, false, 1, 200, 800}, {128, false, 1, 300, 1000}, {256, false, 1, 330, 1700},
                              {256, true, 1, 285, 2000}};
 // (float32 results, sums in registers)
-constexpr GForm kSumForms[3] = {{64, false, 1, 300, 700}, {128, false, 1, 480, 800}, {256, true, 1, 320, 7500}};
+constexpr GForm kSumForms[3] = {{64, false, 1, 200, 700}, {128, false, 1, 480, 800}, {256, true, 1, 320, 7500}};
 // (operands in two parts)
 constexpr GForm kSplitForms[3] = {{64, false, 1, 440, 3500}, {128, false, 1, 600, 4500}, {64, false, 2, 440, 2000}};
 

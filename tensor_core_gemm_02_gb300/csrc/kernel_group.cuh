@@ -93,7 +93,8 @@ struct GroupArgs {
 template <int BN_, int STAGES_, bool PAIR_, int KIND_, int PREC_, int CS_ = 1>
 struct GroupCfg {
     static constexpr int CS = CS_;
-    static constexpr int ISS = PREC_ == kPrecSplit ? 2 : 1;  // MMA issuers
+    // MMA issuers: two where one thread's MMAs take longer than the loads
+    static constexpr int ISS = PREC_ == kPrecSplit || (BN_ == 64 && KIND_ != kKindSum) ? 2 : 1;
     static constexpr int PARTS = PREC_ == kPrecSplit ? 2 : 1;  // boxes of an operand in a stage
     static constexpr int CHUNK = PREC_ == kPrecAcc ? 0 : (PREC_ == kPrecSums ? 8 : 4);  // K blocks an accumulator takes (0: all)
     static constexpr bool PAIR = PAIR_;
@@ -1023,6 +1024,17 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 tc_fence_after_sync();
                 return tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(ab * Cfg::ISS * BN + col_g);
             };
+            // (two issuers) the second one's sums of 32 columns, added to the first one's
+            auto add_second = [&](uint32_t at, uint32_t(&r)[32]) {
+                if constexpr (Cfg::ISS == 2) {
+                    uint32_t r2[32];
+                    tc_ld_32x32b_x32(at + BN, r2);
+                    tc_wait_ld(r2);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        r[i] = __float_as_uint(__fadd_rn(__uint_as_float(r[i]), __uint_as_float(r2[i])));
+                }
+            };
             if constexpr (kSums) {
                 float sums[kCols];
                 // (CS = 2) the columns this CTA finishes, and C's elements there
@@ -1175,6 +1187,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                         uint32_t r[32];
                         tc_ld_32x32b_x32(acc + 32u * static_cast<uint32_t>(u), r);
                         tc_wait_ld(r);
+                        add_second(acc + 32u * static_cast<uint32_t>(u), r);
                         if (u == kCols / 32 - 1)
                             hand_back();
                         if (u >= units)
@@ -1289,6 +1302,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                             uint32_t r[32];
                             tc_ld_32x32b_x32(acc + static_cast<uint32_t>(col + 32 * h), r);
                             tc_wait_ld(r);
+                            add_second(acc + static_cast<uint32_t>(col + 32 * h), r);
                             if (h == 1 && col + 64 >= kCols)
                                 hand_back();
 #pragma unroll
