@@ -22,43 +22,44 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 1024;
 
-// Eight elements of a row from column c (those below N), as float32.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void *X, int64_t at, int32_t n, bool vec, float (&v)[8])
+// W elements of a row from element `at` of X on (those below n), as float32: eight at once where
+// rows are whole 16 bytes apart, or two.
+template <int TYPE, int W>
+__device__ __forceinline__ void load_piece(const void *X, int64_t at, int32_t n, float (&v)[W])
 {
     if (TYPE == kOutF32) {
         const float *p = static_cast<const float *>(X) + at;
-        if (vec && n >= 8) {
+        if (W == 8 && n >= 8) {
             const float4 a = __ldcg(reinterpret_cast<const float4 *>(p));
             const float4 b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            v[0] = a.x, v[1] = a.y, v[2 % W] = a.z, v[3 % W] = a.w;
+            v[4 % W] = b.x, v[5 % W] = b.y, v[6 % W] = b.z, v[7 % W] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < W; ++i)
                 v[i] = i < n ? __ldcg(p + i) : 0.f;
         }
     } else {
         const unsigned short *p = static_cast<const unsigned short *>(X) + at;
         uint32_t w[4] = {0, 0, 0, 0};
-        if (vec && n >= 8) {
+        if (W == 8 && n >= 8) {
             const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(p));
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < W; ++i)
                 if (i < n)
                     w[i / 2] |= static_cast<uint32_t>(__ldcg(p + i)) << (16 * (i & 1));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < W; ++i) {
             const unsigned short h = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
             v[i] = TYPE == kOutBF16 ? cvt_bf16_f32(h) : cvt_f16_f32(h);
         }
     }
 }
 
-// The pieces of eight columns that a thread takes, one every `step`, as row and piece of it
+// The pieces of a row that a thread takes, one every `step`, as row and piece of it
 // (one division at the start: 64-bit ones for every piece cost more than the memory).
 struct Walk {
     int64_t row, d_row;
@@ -94,43 +95,46 @@ __device__ __forceinline__ float block_sum(float x)
     return s;
 }
 
-template <int TYPE>
+// (In pieces of eight rows that are not 16 bytes apart would ask for every 32-byte sector up to
+// eight times: 8 x 1000 x 1367, the whole of gemm_orthogonalize, float16 535 -> 523 us, float32 922
+// -> 895 with pieces of two.)
+template <int TYPE, int W>
 __global__ void __launch_bounds__(kThreads)
-    square_sums_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, bool vec,
-                       float *partial)
+    square_sums_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, float *partial)
 {
     const int32_t parts = static_cast<int32_t>(gridDim.x), g = static_cast<int32_t>(blockIdx.y);
-    const int32_t per_row = (N + 7) / 8;
+    const int32_t per_row = (N + W - 1) / W;
     grid_dependency_wait();
     grid_launch_dependents();
+    constexpr int kAhead = W == 8 ? 4 : 8;  // pieces in flight
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     Walk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<int64_t>(parts) * kThreads, per_row);
     while (w.row < M) {
-        float v[4][8];
+        float v[kAhead][W];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            load8<TYPE>(X, g * stride_x + w.row * ldx + 8 * w.at, w.row < M ? N - 8 * w.at : 0, vec, v[j]);
+        for (int j = 0; j < kAhead; ++j) {
+            load_piece<TYPE, W>(X, g * stride_x + w.row * ldx + W * w.at, w.row < M ? N - W * w.at : 0, v[j]);
             w.next();
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum[j] = fmaf(v[j][e], v[j][e], sum[j]);
+            for (int e = 0; e < W; ++e)
+                sum[j % 4] = fmaf(v[j][e], v[j][e], sum[j % 4]);
     }
     const float s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
     if (threadIdx.x == 0)
         partial[static_cast<int64_t>(g) * parts + blockIdx.x] = s;
 }
 
-template <int TYPE>
+template <int TYPE, int W>
 __global__ void __launch_bounds__(kThreads)
-    normalize_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, bool vec,
-                     const float *partial, int32_t parts, float scale, float eps, uint16_t *Xs, int64_t lds,
-                     int64_t stride_s, int64_t lo)
+    normalize_kernel(const void *X, int64_t ldx, int64_t stride_x, int32_t M, int32_t N, const float *partial,
+                     int32_t parts, float scale, float eps, uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo)
 {
     const int32_t g = static_cast<int32_t>(blockIdx.y);
-    const int32_t per_row = (N + 7) / 8;
+    constexpr int kAhead = W == 8 ? 4 : 8;  // pieces in flight
+    const int32_t per_row = (N + 7) / 8 * (8 / W);  // (rows of Xs are whole 16 bytes: the last pieces fill the padding)
     grid_dependency_wait();
     grid_launch_dependents();
     float sum = 0.f;
@@ -140,31 +144,35 @@ __global__ void __launch_bounds__(kThreads)
     Walk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kThreads,
            per_row);
     while (w.row < M) {
-        float v[4][8];
-        int64_t to[4];
+        float v[kAhead][W];
+        int64_t to[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             const bool there = w.row < M;
-            load8<TYPE>(X, g * stride_x + w.row * ldx + 8 * w.at, there ? N - 8 * w.at : 0, vec, v[j]);
-            to[j] = there ? w.row * lds + 8 * w.at : -1;
+            load_piece<TYPE, W>(X, g * stride_x + w.row * ldx + W * w.at, there ? N - W * w.at : 0, v[j]);
+            to[j] = there ? w.row * lds + W * w.at : -1;
             w.next();
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             if (to[j] < 0)
                 break;
-            uint32_t hi[4], low[4];
+            uint32_t hi[W / 2], low[W / 2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < W / 2; ++e) {
                 const float x0 = v[j][2 * e] * f, x1 = v[j][2 * e + 1] * f;
                 hi[e] = pack_f16x2(x0, x1);
                 low[e] = pack_f16x2(x0 - cvt_f16_f32(static_cast<unsigned short>(hi[e])),
                                     x1 - cvt_f16_f32(static_cast<unsigned short>(hi[e] >> 16)));
             }
-            // (rows of Xs are whole 16 bytes: the last piece fills the padding)
             uint16_t *p = Xs + g * stride_s + to[j];
-            *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(p + lo) = make_uint4(low[0], low[1], low[2], low[3]);
+            if constexpr (W == 8) {
+                *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(p + lo) = make_uint4(low[0], low[1], low[2], low[3]);
+            } else {
+                *reinterpret_cast<uint32_t *>(p) = hi[0];
+                *reinterpret_cast<uint32_t *>(p + lo) = low[0];
+            }
         }
     }
 }
@@ -208,22 +216,30 @@ int orthogonalize_parts(int64_t M, int64_t N)
 cudaError_t launch_square_sums(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
                                int32_t count, float *partial, int parts, cudaStream_t stream)
 {
-    auto k = type == kOutF32    ? square_sums_kernel<kOutF32>
-             : type == kOutBF16 ? square_sums_kernel<kOutBF16>
-                                : square_sums_kernel<kOutF16>;
-    return launch(k, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(count)), stream, X, ldx, stride_x,
-                  M, N, vec_ok(X, ldx, stride_x, type), partial);
+    const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(count));
+    auto go = [&](auto k) { return launch(k, grid, stream, X, ldx, stride_x, M, N, partial); };
+    const bool vec = vec_ok(X, ldx, stride_x, type);
+    if (type == kOutF32)
+        return vec ? go(square_sums_kernel<kOutF32, 8>) : go(square_sums_kernel<kOutF32, 2>);
+    if (type == kOutBF16)
+        return vec ? go(square_sums_kernel<kOutBF16, 8>) : go(square_sums_kernel<kOutBF16, 2>);
+    return vec ? go(square_sums_kernel<kOutF16, 8>) : go(square_sums_kernel<kOutF16, 2>);
 }
 
 cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int type, int32_t M, int32_t N,
                              int32_t count, const float *partial, int parts, float scale, float eps,
                              uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo, cudaStream_t stream)
 {
-    auto k = type == kOutF32    ? normalize_kernel<kOutF32>
-             : type == kOutBF16 ? normalize_kernel<kOutBF16>
-                                : normalize_kernel<kOutF16>;
-    return launch(k, dim3(blocks_for(M, N, 4), static_cast<unsigned>(count)), stream, X, ldx, stride_x, M, N,
-                  vec_ok(X, ldx, stride_x, type), partial, parts, scale, eps, Xs, lds, stride_s, lo);
+    const dim3 grid(blocks_for(M, N, 4), static_cast<unsigned>(count));
+    auto go = [&](auto k) {
+        return launch(k, grid, stream, X, ldx, stride_x, M, N, partial, parts, scale, eps, Xs, lds, stride_s, lo);
+    };
+    const bool vec = vec_ok(X, ldx, stride_x, type);
+    if (type == kOutF32)
+        return vec ? go(normalize_kernel<kOutF32, 8>) : go(normalize_kernel<kOutF32, 2>);
+    if (type == kOutBF16)
+        return vec ? go(normalize_kernel<kOutBF16, 8>) : go(normalize_kernel<kOutBF16, 2>);
+    return vec ? go(normalize_kernel<kOutF16, 8>) : go(normalize_kernel<kOutF16, 2>);
 }
 
 }  // namespace tcg

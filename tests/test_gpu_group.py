@@ -124,6 +124,18 @@ def test_grouped_outputs_of_any_pitch(form):
                 check_grouped(counts, front, behind, N, 72, False, dtype, out, True, pad=pad)
 
 
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("N", [1, 2, 3, 31, 33, 34, 35, 65, 66, 67, 98, 130, 257, 258])
+def test_row_ends_between_words(form, N):
+    """Rows of D of an odd pitch end at any place of a piece of 32 or 64 columns; the column behind
+    keeps what it holds."""
+    binding.gemm_debug_force_tile(*FORMS[form])
+    for out in (OUT_F32, OUT_BF16, OUT_F16):
+        for exact in (True, False):
+            check_grouped([35, 0, 6], 0, 2, N, 24, False, F16, out, exact, pad=1)
+            check_weights([35, 0, 6], 0, 2, 24, N, F16, out, exact, pad=1)
+
+
 @pytest.mark.parametrize("trans_b", [False, True])
 @pytest.mark.parametrize("counts,N,K", [([700, 3, 0, 900], 777, 1000), ([2, 1, 0, 1] * 8, 1030, 2056),
                                         ([40, 0, 90, 20], 4096, 4100), ([16] * 20, 264, 328), ([64, 1, 33], 130, 8200)])
@@ -284,7 +296,7 @@ def test_elements_past_32_bits(form):
     counts, N, K, far = [30, 5, 45], 200, 136, (1 << 31) + 64
     off = offsets_of(counts, 0)
     big = torch.empty(2 * far + 300 * 512, dtype=F16, device="cuda")  # (8.6 GB)
-    A, dD, small = wide(80, K, F16, gen, True), wide(80, N, F16, gen, True), stack(3, N, K, F16, gen, True)
+    A, dD, small = wide(80, K, F16, gen), wide(80, N, F16, gen), stack(3, N, K, F16, gen, True)
     B = big.as_strided((3, N, K), (far, K, 1))
     B.copy_(small)
     want = binding.gemm_grouped(A, small, off), binding.gemm_grouped(dD, small, off, trans_b=True)

@@ -161,6 +161,16 @@ def test_padding_is_left_alone():
     assert torch.isfinite(buf[:, :60, :45]).all()
 
 
+@pytest.mark.parametrize("n", [33, 34, 66, 67, 98, 129, 130, 259])
+def test_row_ends_between_words(n):
+    X = stack(2, 70, n, torch.float32, n)
+    for out in (torch.float32, torch.bfloat16, torch.float16):
+        buf = torch.full((2, 71, n + 3 - n % 2), 7.0, dtype=out, device="cuda")
+        check(X, MUON, 2, out, Y=buf[:, :70, :n])
+        assert (buf[:, 70:] == 7).all() and (buf[:, :, n:] == 7).all()
+        assert torch.equal(buf[:, :70, :n], binding.gemm_orthogonalize(X, torch.empty((2, 70, n + 8 - n % 8), dtype=out, device="cuda")[:, :, :n], steps=2))
+
+
 def test_zeros_and_what_is_not_finite():
     X = stack(4, 50, 80, torch.float32, 6)
     good = binding.gemm_orthogonalize(X)
