@@ -387,7 +387,28 @@ struct BatchProduct {
     // and D where not 0
     bool split;
     int64_t a_lo, b_lo, c_lo, d_lo;
+    int64_t parts;  // (sym) D: so many matrices of parts of each sum; 0: whole sums
 };
+
+// Parts for the sums of `count` symmetric s x s products over l: as many as leave the tiles (of 64
+// columns) to the SMs in one wave, eight K blocks each at least, where the blocks saved (of operands in
+// two parts those that two CTAs a tile would not save) take longer than the launch that adds the parts,
+// about 5 us.  Five steps, whole sums / parts, us: bf16 20000 x 41 472 / 165, 128 x 8192 214 / 119, 512 x
+// 4096 160 / 129, 512 x 2048 118.8 / 119.9, 256 x 1024 88 / 90; float32 512 x 4096 195 / 176, 128 x 2048
+// 130 / 113, 512 x 2048 143.5 / 142.7, 2816 x 1024 259 / 273.
+int64_t sum_parts(int64_t count, int64_t s, int64_t l, bool split, int sm_count)
+{
+    const int64_t mb = ceil_div(s, 128), tiles = count * mb * (mb + 1), blocks = ceil_div(l, 64);
+    int64_t parts = sm_count / tiles;
+    parts = parts < blocks / 8 ? parts : blocks / 8;
+    if (parts < 2)
+        return 1;
+    const int64_t saved_ns = split ? (blocks / 2 - blocks / parts) * kSplitForms[0].block_ns
+                                   : (blocks - blocks / parts) * kForms[0].block_ns;
+    if (saved_ns < (split ? 3000 : 5000))
+        return 1;
+    return ceil_div(blocks, ceil_div(blocks, parts));  // (no part is empty)
+}
 
 gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t stream)
 {
@@ -398,10 +419,11 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
         return p.count * mb * ceil_div(p.N, bn);
     };
     const int prec = p.split ? tcg::kPrecSplit : tcg::kPrecAcc;
-    const GForm f = choose_form(ceil_div(p.K, 64), prec, dev->sm_count, tiles);
+    const int64_t parts = p.parts > 1 ? p.parts : 1, k_blocks = ceil_div(p.K, 64);
+    const GForm f = parts > 1 ? (p.split ? kSplitForms[0] : kForms[0]) : choose_form(k_blocks, prec, dev->sm_count, tiles);
     const int tm = f.pair ? 256 : 128, b_rows = f.pair ? f.bn / 2 : f.bn;
     int grid = 0;
-    gemm_status st = group_grid(f, tiles(tm, f.bn), dev, &grid);
+    gemm_status st = group_grid(f, parts * tiles(tm, f.bn), dev, &grid);
     if (st != GEMM_OK)
         return st;
     GroupMaps maps;
@@ -425,7 +447,7 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
         return encode_3d(m, ab_type(false), x, p.N, p.M, p.ldc * 2, p.count,
                          p.count == 1 ? p.M * p.ldc * 2 : p.stride_c * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     };
-    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count, p.stride_d, p.d_lo,
+    if (!set_out(g, maps, p.D, p.out, p.M, cols, p.ldd, p.count * parts, p.stride_d, p.d_lo,
                  p.d_lo || !p.split || f.cs == 2) ||
         (c_tma && (!map_c(&maps.c, p.C) || (p.c_lo && !map_c(&maps.c_lo, p.C + p.c_lo)))))
         return GEMM_ERR_CUDA;
@@ -442,6 +464,8 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     g.C = p.C;
     g.ldc = p.ldc;
     g.stride_c = p.stride_c;
+    g.parts = static_cast<int32_t>(parts);
+    g.part_blocks = static_cast<int32_t>(ceil_div(k_blocks, parts));
     g.loads = 1;
     const cudaError_t e = tcg::launch_group_batch(f.bn, f.pair, p.maj, p.sym, prec, f.cs, maps, g, grid, stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
@@ -508,12 +532,19 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     at_once = at_once > 1 ? at_once : 1;
     std::unique_lock<std::mutex> hold(buffer_mutex(dev->index, cs));
     void *w = nullptr;
-    if ((st = get_dequant_buffer(dev->index, cs, kBufOrthogonalize, static_cast<size_t>(at_once * each), &w)) != GEMM_OK)
+    // parts of the sums of X X^T (with one operand part or two), float32
+    const int64_t parts_of[2] = {sum_parts(at_once, s, l, false, dev->sm_count), sum_parts(at_once, s, l, true, dev->sm_count)};
+    const int64_t most_parts = parts_of[0] > parts_of[1] ? parts_of[0] : parts_of[1];
+    const int64_t ldq = ceil_div(s, 4) * 4, size_q = ceil_div(s * ldq, 64) * 64;
+    const int64_t bytes_q = most_parts > 1 ? at_once * most_parts * size_q * 4 : 0;
+    const int64_t bytes = ceil_div(at_once * each, 256) * 256;
+    if ((st = get_dequant_buffer(dev->index, cs, kBufOrthogonalize, static_cast<size_t>(bytes + bytes_q), &w)) != GEMM_OK)
         return st;
     const int64_t lo_i = at_once * size_i, lo_p = at_once * size_p;  // to the low parts
     uint16_t *iter[2] = {static_cast<uint16_t *>(w), static_cast<uint16_t *>(w) + 2 * lo_i};
     uint16_t *prod = iter[1] + 2 * lo_i, *poly = prod + 2 * lo_p;
     float *partial = reinterpret_cast<float *>(poly + 2 * lo_p);
+    float *sums = reinterpret_cast<float *>(static_cast<uint8_t *>(w) + bytes);
     for (int64_t first = 0; first < count; first += at_once) {
         const int64_t n = count - first < at_once ? count - first : at_once;
         const void *xf = static_cast<const uint8_t *>(X) + first * stride_x * out_size(type);
@@ -546,8 +577,27 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
             p.split = both;
             p.a_lo = p.b_lo = lo_i;
             p.d_lo = both ? lo_p : 0;
+            const int64_t shared = parts_of[both];
+            if (shared > 1) {
+                p.parts = shared;
+                p.D = sums;
+                p.ldd = ldq;
+                p.stride_d = size_q;
+                p.out = GEMM_OUT_F32;
+                p.d_lo = 0;
+            }
             if ((st = run_batch(p, dev, cs)) != GEMM_OK)
                 return st;
+            if (shared > 1) {
+                if (tcg::launch_join_parts(sums, ldq, size_q, static_cast<int32_t>(shared), static_cast<int32_t>(s),
+                                           static_cast<int32_t>(n), prod, ldp, size_p, both ? lo_p : 0, cs) != cudaSuccess)
+                    return GEMM_ERR_CUDA;
+                p.parts = 0;
+                p.ldd = ldp;
+                p.stride_d = size_p;
+                p.out = GEMM_OUT_F16;
+                p.d_lo = both ? lo_p : 0;
+            }
             // Q = kProductScale (b P + c P^2)
             p.K = s;
             p.maj = 0;

@@ -84,6 +84,7 @@ struct GroupArgs {
     const uint16_t *C;       // KIND_BATCH: f16, 16-byte aligned rows (NULL: none)
     int64_t ldc, stride_c;
     int64_t c_lo, d_lo;      // KIND_BATCH: elements from C, D to their low parts (0: none)
+    int32_t parts, part_blocks;  // SYM: a tile's sum in so many parts of so many K blocks, each a matrix of D
     int32_t loads;           // there is something to multiply (K > 0; KIND_SUM: rows > 0)
     uint32_t extra_tx;
     uint32_t *status;
@@ -224,7 +225,8 @@ struct GroupTile {
     int32_t g;          // group
     int32_t row0, end;  // its first row (PAIR: of the pair's tile) and the end of the rows it may store
     int32_t n0;         // first column
-    int32_t k0;         // KIND_SUM: first row of the sum
+    int32_t gd;         // matrix of D
+    int32_t k0;         // first row of the sum (KIND_SUM, SYM)
     bool mirror;        // SYM: below the diagonal, stored a second time
 };
 
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
     if constexpr (kBatch) {
         const int32_t per = SYM ? (TM / BN) * (args.num_m_blocks * (args.num_m_blocks + 1) / 2)
                                 : args.num_m_blocks * args.num_n_blocks;
-        num_tiles = args.groups * per;
+        num_tiles = args.groups * per * (SYM ? args.parts : 1);
     } else {
         if (!gr.ok && blockIdx.x == 0 && threadIdx.x == 0)
             record_error(args.status, kStatusIndex, 0);
@@ -440,7 +442,14 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             // block row mb of a matrix has the TM / BN (mb + 1) tiles up to the diagonal
             constexpr int32_t q = TM / BN;
             const int32_t per = q * (blocks * (blocks + 1) / 2);
+            int32_t part = 0;
+            if (args.parts > 1) {
+                part = t % args.parts;
+                t /= args.parts;
+            }
             p.g = t / per;
+            p.gd = p.g * args.parts + part;
+            p.k0 = part * args.part_blocks * Cfg::BK;
             r = t - p.g * per;
             const int32_t u = r / q;
             int32_t mb = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(u) + 1.0f) - 1.0f) * 0.5f);
@@ -452,11 +461,11 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             p.row0 = mb * TM;
             p.n0 = nb * BN;
             p.end = args.M;
-            p.mirror = nb / q != mb;
+            p.mirror = nb / q != mb && args.parts == 1;
             return p;
         } else {
             const int32_t per = blocks * args.num_n_blocks;
-            p.g = t / per;
+            p.g = p.gd = t / per;
             r = t - p.g * per;
             p.end = args.M;
             if constexpr (kSum) {
@@ -492,6 +501,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             rem = n % Cfg::BK;
             return (n + Cfg::BK - 1) / Cfg::BK;
         }
+        if (SYM && args.parts > 1)
+            return min(args.part_blocks, k_blocks - t % args.parts * args.part_blocks);
         return k_blocks;
     };
 
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 const int32_t v = __ldcg(args.idx + my_row);
                 zero = zero || v < 0 || v >= args.table_rows;
             }
-            uint8_t *d_g = static_cast<uint8_t *>(args.D) + (kRows ? 0 : p.g * args.stride_d * esize);
+            uint8_t *d_g = static_cast<uint8_t *>(args.D) + (kRows ? 0 : p.gd * args.stride_d * esize);
             // (PREC_SPLIT) C's high and low parts for 32 columns of this lane's row
             const uint16_t *c_row =
                 kBatch && args.C && my_row < p.end
@@ -886,9 +897,9 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     __syncwarp();
                     if (lane == 0) {
                         if (kBatch)  // (read by the next product)
-                            tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                            tma_store_3d(&maps.d, buf, col0, row0, p.gd);
                         else
-                            tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.g, policy);
+                            tma_store_3d_hint(&maps.d, buf, col0, row0, kRows ? 0 : p.gd, policy);
                     }
                 } else {
                     __syncwarp();
@@ -1263,7 +1274,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) {
-                                tma_store_3d(&maps.d, buf, col0, row0, p.g);
+                                tma_store_3d(&maps.d, buf, col0, row0, p.gd);
                                 if (SYM) {
                                     if (p.mirror)
                                         tma_store_3d(&maps.d, buf + 2048u, row0, col0, p.g);

@@ -41,4 +41,9 @@ cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int t
                              int32_t count, const float *partial, int parts, float scale, float eps,
                              uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo, cudaStream_t stream);
 
+// Symmetric matrices P (s x s, float16, and, lo != 0, their low parts lo elements behind) from `parts`
+// float32 matrices each, whose sums' elements on and below the diagonal are P's.
+cudaError_t launch_join_parts(const float *Q, int64_t ldq, int64_t stride_q, int32_t parts, int32_t s, int32_t count,
+                              uint16_t *P, int64_t ldp, int64_t stride_p, int64_t lo, cudaStream_t stream);
+
 }  // namespace tcg

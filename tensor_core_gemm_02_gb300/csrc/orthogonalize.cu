@@ -177,6 +177,61 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// One 32 x 32 block on or below the diagonal: the parts' sums in order, written here and, transposed,
+// above the diagonal.
+__global__ void __launch_bounds__(kThreads)
+    join_parts_kernel(const float *Q, int64_t ldq, int64_t stride_q, int32_t parts, int32_t s, uint16_t *P,
+                      int64_t ldp, int64_t stride_p, int64_t lo)
+{
+    __shared__ float sum[32][33];
+    const int32_t t = static_cast<int32_t>(blockIdx.x);
+    int32_t bi = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
+    while (bi * (bi + 1) / 2 > t)
+        --bi;
+    while ((bi + 1) * (bi + 2) / 2 <= t)
+        ++bi;
+    const int32_t r0 = 32 * bi, c0 = 32 * (t - bi * (bi + 1) / 2), g = static_cast<int32_t>(blockIdx.y);
+    const int32_t lane = static_cast<int32_t>(threadIdx.x) % 32, warp = static_cast<int32_t>(threadIdx.x) / 32;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const float *q = Q + static_cast<int64_t>(g) * parts * stride_q;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int32_t k = 0; k < parts; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t r = r0 + warp + 8 * j, c = c0 + lane;
+            if (r < s && c < s)
+                v[j] += __ldcg(q + k * stride_q + r * ldq + c);
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sum[warp + 8 * j][lane] = v[j];
+    __syncthreads();
+    uint16_t *p = P + g * stride_p;
+    for (int32_t i = static_cast<int32_t>(threadIdx.x); i < 32 * 16; i += kThreads) {
+        const int32_t a = i / 16, b = i % 16 * 2;  // row and first column of a pair
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (m == 1 && r0 == c0)
+                break;
+            // (a diagonal block's elements above the diagonal are those below it)
+            const bool f0 = m == 1 || (r0 == c0 && b > a), f1 = m == 1 || (r0 == c0 && b + 1 > a);
+            const float x0 = f0 ? sum[b][a] : sum[a][b], x1 = f1 ? sum[b + 1][a] : sum[a][b + 1];
+            const int32_t row = (m ? c0 : r0) + a, col = (m ? r0 : c0) + b;
+            if (row >= s || col >= s)
+                continue;
+            const uint32_t hi = pack_f16x2(x0, x1);  // (an odd s: the second one is padding)
+            uint16_t *to = p + row * ldp + col;
+            *reinterpret_cast<uint32_t *>(to) = hi;
+            if (lo)
+                *reinterpret_cast<uint32_t *>(to + lo) =
+                    pack_f16x2(x0 - cvt_f16_f32(static_cast<unsigned short>(hi)),
+                               x1 - cvt_f16_f32(static_cast<unsigned short>(hi >> 16)));
+        }
+    }
+}
+
 bool vec_ok(const void *X, int64_t ldx, int64_t stride_x, int type)
 {
     const int64_t es = type == kOutF32 ? 4 : 2;
@@ -240,6 +295,14 @@ cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int t
     if (type == kOutBF16)
         return vec ? go(normalize_kernel<kOutBF16, 8>) : go(normalize_kernel<kOutBF16, 2>);
     return vec ? go(normalize_kernel<kOutF16, 8>) : go(normalize_kernel<kOutF16, 2>);
+}
+
+cudaError_t launch_join_parts(const float *Q, int64_t ldq, int64_t stride_q, int32_t parts, int32_t s, int32_t count,
+                              uint16_t *P, int64_t ldp, int64_t stride_p, int64_t lo, cudaStream_t stream)
+{
+    const unsigned nb = (static_cast<unsigned>(s) + 31) / 32;
+    return launch(join_parts_kernel, dim3(nb * (nb + 1) / 2, static_cast<unsigned>(count)), stream, Q, ldq, stride_q,
+                  parts, s, P, ldp, stride_p, lo);
 }
 
 }  // namespace tcg

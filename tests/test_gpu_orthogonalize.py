@@ -215,3 +215,14 @@ def test_elements_past_32_bits():
 def test_more_tiles_than_ctas_hold(form, count, m, n):
     binding.gemm_debug_force_tile(*form)
     check(stack(count, m, n, torch.float32, m + n), MUON, 2)
+
+
+@pytest.mark.parametrize("count,m,n", [(1, 41, 3000), (1, 3001, 41), (2, 2500, 130), (1, 260, 5000), (3, 64, 2117), (1, 6000, 1),
+                                       (1, 257, 2600), (5, 4096, 16)])
+def test_long_sums_of_few_tiles(count, m, n):
+    """The sums of X X^T (X^T X) in parts, which a kernel of its own adds."""
+    for dtype, out in ((torch.float32, torch.float32), (torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)):
+        check(stack(count, m, n, dtype, m + n), MUON, 1, out)
+        check(stack(count, m, n, dtype, m + n), QUINTIC, 4, out)
+    X = stack(count, m, n, torch.bfloat16, 3)
+    assert torch.equal(binding.gemm_orthogonalize(X), binding.gemm_orthogonalize(X))
