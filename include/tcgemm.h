@@ -604,7 +604,7 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *  values stay below 2.  The last step is rounded once, to Y's type.
  *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.
  *  Workspace: per device and stream, up to 1 GiB or one matrix's (8 M N + 8 min(M, N)^2
- *  bytes) if that is more, and some MB for long sums of few tiles, kept as the other
+ *  bytes, rows padded to 64 elements) if that is more, and some MB for long sums of few tiles, kept as the other
  *  workspaces are.
  *  Other errors and execution as gemm_f16 (2 + 3 steps kernels, with long sums of few
  *  tiles 2 + 4 steps, more for a large stack).

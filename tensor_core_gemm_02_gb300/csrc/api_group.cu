@@ -441,7 +441,7 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     if (!map_a(&maps.a, p.A) || !map_b(&maps.b, p.B) ||
         (p.split && (!map_a(&maps.a_lo, p.A + p.a_lo) || !map_b(&maps.b_lo, p.B + p.b_lo))))
         return GEMM_ERR_CUDA;
-    const int64_t cols = p.padded ? p.ldd : p.N;
+    const int64_t whole = ceil_div(p.N, 8) * 8, cols = !p.padded ? p.N : (whole < p.ldd ? whole : p.ldd);
     const bool c_tma = p.C && !p.split;
     auto map_c = [&](CUtensorMap *m, const uint16_t *x) {
         return encode_3d(m, ab_type(false), x, p.N, p.M, p.ldc * 2, p.count,
@@ -519,8 +519,10 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     const int more = s < 256 ? 2 : 0;
     const int wanted = out == GEMM_OUT_F32 ? steps : (out == GEMM_OUT_F16 ? 1 + more : more);
     const int exact = wanted < steps ? wanted : steps;
-    // workspace of a matrix: two iterates, the product of one with itself, and the polynomial of that
-    const int64_t ldi = ceil_div(N, 8) * 8, ldp = ceil_div(s, 8) * 8;
+    // workspace of a matrix: two iterates, the product of one with itself, and the polynomial of that;
+    // rows begin on 128-byte lines, or every row of a box would be two requests to L2 (8 x 1000 x 1367
+    // float16 528 us with rows of 8 elements' multiples, 427; 32 x 1000 x 1000 1357, 1055)
+    const int64_t ldi = ceil_div(N, 64) * 64, ldp = ceil_div(s, 64) * 64;
     const int64_t size_i = ceil_div(M * ldi, 64) * 64, size_p = ceil_div(s * ldp, 64) * 64;
     const int parts = tcg::orthogonalize_parts(M, N);
     const int64_t each = 2 * (4 * size_i + 4 * size_p) + 4 * static_cast<int64_t>(parts);
