@@ -15,7 +15,7 @@
 // Up to 32 a warp one thread block does it all, up to 131072 ids a cluster of eight, whose
 // blocks read one another's counts; more are cut into chunks, whose counts a first kernel
 // leaves in memory.  Bound by latency: a few dependent steps, each a round trip to shared
-// memory or L2 (16384 ids of 64 groups 10.8 us, the call's host time 10 to 11).
+// memory or L2 (16384 ids of 64 groups 10.8 us, the call's host time 9 to 10).
 #include <cuda_runtime.h>
 
 #include "common.cuh"

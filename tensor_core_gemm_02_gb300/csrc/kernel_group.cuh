@@ -14,7 +14,8 @@
 //   KIND_BATCH  D_g = alpha A_g B_g^T + beta C_g for a stack of equal sizes, in either
 //               storage, C in 16 bits.  SYM: D_g is known to be symmetric (A A^T, or
 //               the square of a symmetric matrix): only the tiles that reach the
-//               diagonal or lie below it are computed, and each is stored twice.
+//               diagonal or lie below it are computed, and each is stored twice.  A long sum of
+//               few tiles can be cut into parts, each a tile of its own into a matrix of its own.
 //
 // Sums.  The tensor cores add each K step of 16 to a float32 accumulator and drop what
 // does not fit, so the error of a long sum grows with its steps.  How much of that is let
@@ -31,20 +32,23 @@
 //               leave SMs idle; each finishes half of the tile's columns, with the other's sums
 //               of them through its shared memory.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread), then four or
-// eight epilogue warps, (KIND_SUM) one that zeroes.  Two TMEM accumulators: the epilogue of one tile
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (tcgen05.mma by one thread; 64 columns wide tiles have
+// two, whose K blocks of 24 KB come faster than a thread's four MMAs go: a symmetric 1024 x 1024 over 2816
+// 17.7 -> 16.0 us), then four or eight epilogue warps, (KIND_SUM) one that zeroes.  Two TMEM accumulators: the epilogue of one tile
 // runs beside the next tile's MMAs.  PAIR: the roles on a CTA pair and one 256 x 256 tile
 // (tcgen05 cta_group::2), each CTA loading its 128 rows of A and its half of B.  The
 // protocol is the tile kernel's (kernel_tile.cuh).  Every wait is bounded.
 //
 // Bounds and figures.  KIND_ROWS and KIND_SUM of long sums are bound by the tensor cores under
 // the power cap (16384 rows in eight uneven groups, 14336 x 4096 bf16: 1.19 to 1.22 ms forward,
-// 1.25 to 1.27 the input's gradient, 1.21 the weights'; 1.5 to 1.6 PFLOP/s; tensor pipe active 85 %
-// of cycles at 4096 rows and 4096 x 4096), of short ones by the results' way out (eight groups
+// 1.24 to 1.27 the input's gradient, 1.20 the weights'; 1.5 to 1.6 PFLOP/s; tensor pipe active 92, 90
+// and 82 % of cycles), of short ones by the results' way out (eight groups
 // of 128 rows: 940 MB of bf16 gradients 224 us, float32 1.9 GB 290).  KIND_BATCH likewise: 4096 x
 // 4096 x 14336, half of a symmetric product 148 us, the update 290 (1.66 and 1.65 PFLOP/s); where
-// the tiles are few, by the rate L2 feeds an SM (128 x 128 tiles: 63 bytes a clock).  Rows of D that
-// are not 16 bytes apart go out as words (16 x 1000 x 1367 from 100 rows each 36 us, 1368 20).
+// the tiles are few, by the rate L2 feeds an SM (at most 63 bytes a clock) and whole waves of tiles
+// (operands in two parts, the update of 2816 x 1024: 16 K blocks of 64 KB take 8.5 us, two waves and the
+// last epilogue 23).  Rows of D that are not 16 bytes apart go out as words (16 x 1000 x 1367 from 100
+// rows each 36 us, 1368 20).
 //
 // Why tiles from device offsets and not from a list: a list is a second kernel before
 // every call.  Each warp that needs coordinates reads the offsets (at most 1024 groups,
