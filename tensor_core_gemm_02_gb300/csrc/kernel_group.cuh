@@ -402,11 +402,13 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             tmem_relinquish();
         }
     }
-    grid_dependency_wait();
-    // (the offsets come while the barriers and the tensor memory are set up)
+    // (the offsets come while the barriers and the tensor memory are set up; without any, that is
+    // done before the kernel before ends: between CTAs 500 clocks of every launch)
     GroupRows<TM> gr;
-    if constexpr (!kBatch)
+    if constexpr (!kBatch) {
+        grid_dependency_wait();
         gr.init(args.offsets, args.groups, args.rows, lane);
+    }
     tc_fence_before_sync();
     if (CL > 1)
         cluster_sync_all();
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
         __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    if constexpr (kBatch)
+        grid_dependency_wait();
     if (threadIdx.x == 0)
         grid_launch_dependents();
 
@@ -1124,7 +1128,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     for (int i = 0; i < 32; ++i)
                         v[i] = __fadd_rn(v[i], __uint_as_float(ld_shared_u32(at + 128u * static_cast<uint32_t>(i))));
                     __syncwarp();
-                    if (lane == 0)
+                    // (not after the last tile: the writer may have ended)
+                    if (lane == 0 && t + cta_sets < num_tiles)
                         mbar_arrive_cluster(mapa_shared(rede_bar(q), share ^ 1u));
                     ++shared_tiles;
                     if (!stores)
@@ -1343,9 +1348,17 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             }
         }
     }
-    if (CL > 1)
-        cluster_sync_all();  // (the other CTA's work may use this one's shared memory until here)
-    else
+    // The other CTA's work may use this one's shared memory until here.  (CS = 2: not where all
+    // went well.  Its sums have been waited for, and so has every arrival at this CTA's barriers.
+    // Of a kernel of 9 us the barrier took 0.6.)
+    bool together = PAIR;
+    if (CS == 2) {
+        __syncthreads();
+        together = *abort_flag != 0u;
+    }
+    if (together)
+        cluster_sync_all();
+    else if (CS == 1)
         __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
