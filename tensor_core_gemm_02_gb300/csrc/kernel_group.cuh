@@ -141,7 +141,8 @@ template <int TILE_M>
 struct GroupRows {
     const int32_t *off;
     int32_t groups, rows, per;
-    int32_t first, mine;  // block rows before this lane's groups, and of them
+    int32_t lo[2], hi[2];  // rows of this lane's groups (up to two: with 64 groups find() loads nothing)
+    int32_t first, mine;   // block rows before this lane's groups, and of them
     int32_t total;        // block rows of all groups (0 where the offsets are not valid)
     bool ok;
     // the group found last: its rows, its first block row and their number
@@ -160,11 +161,20 @@ struct GroupRows {
         mine = 0;
         bool good = true;
         const int32_t g0 = static_cast<int32_t>(lane) * per;
-        for (int32_t g = g0; g < min(g0 + per, n); ++g) {
-            const int32_t lo = at(g), hi = at(g + 1);
-            good = good && lo >= 0 && lo <= hi && hi <= limit;
-            mine += good ? (hi - lo + TILE_M - 1) / TILE_M : 0;
+        auto count = [&](int32_t l, int32_t h) {
+            good = good && l >= 0 && l <= h && h <= limit;
+            mine += good ? (h - l + TILE_M - 1) / TILE_M : 0;
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool there = i < per && g0 + i < n;
+            lo[i] = there ? at(g0 + i) : 0;
+            hi[i] = there ? at(g0 + i + 1) : 0;
         }
+        count(lo[0], hi[0]);
+        count(lo[1], hi[1]);
+        for (int32_t g = g0 + 2; g < min(g0 + per, n); ++g)
+            count(at(g), at(g + 1));
         ok = __all_sync(0xffffffffu, good);
         int32_t sum = mine;
 #pragma unroll
@@ -195,6 +205,18 @@ struct GroupRows {
         if (q >= base_last && q < base_last + blocks_last)
             return;
         const int chunk = __ffs(__ballot_sync(0xffffffffu, q >= first && q < first + mine)) - 1;
+        if (per <= 2) {
+            const int32_t l0 = __shfl_sync(0xffffffffu, lo[0], chunk), h0 = __shfl_sync(0xffffffffu, hi[0], chunk);
+            const int32_t l1 = __shfl_sync(0xffffffffu, lo[1], chunk), h1 = __shfl_sync(0xffffffffu, hi[1], chunk);
+            const int32_t start = __shfl_sync(0xffffffffu, first, chunk), b0 = (h0 - l0 + TILE_M - 1) / TILE_M;
+            const bool second = q >= start + b0;
+            g_last = chunk * per + (second ? 1 : 0);
+            lo_last = second ? l1 : l0;
+            hi_last = second ? h1 : h0;
+            base_last = second ? start + b0 : start;
+            blocks_last = (hi_last - lo_last + TILE_M - 1) / TILE_M;
+            return;
+        }
         const int32_t g = chunk * per + static_cast<int32_t>(lane);
         int32_t l = 0, h = 0;
         if (static_cast<int32_t>(lane) < per && g < groups) {
@@ -532,13 +554,18 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             if (kRows && args.idx) {
                 // lane l fetches rows 4 l .. 4 l + 3, four per gather4; rows past the group's,
                 // and those whose index is not a row of the table, fetch row 0
-                for (int r = 0; r < 4; ++r) {
+                int32_t v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {  // (at once: each is a round trip to L2)
                     const int32_t m = m0 + 4 * static_cast<int32_t>(lane) + r;
-                    const int32_t v = m < p.end ? __ldcg(args.idx + m) : 0;
-                    if (v < 0 || v >= args.table_rows)
+                    v[r] = m < p.end ? __ldcg(args.idx + m) : 0;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (v[r] < 0 || v[r] >= args.table_rows)
                         record_error(args.status, kStatusIndex, 0);
                     else
-                        rows[r] = v;
+                        rows[r] = v[r];
                 }
             }
             // K block kb into the next stage; false if the kernel is aborting.  (Partial or not is

@@ -143,13 +143,18 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
             int32_t rows[4] = {0, 0, 0, 0};
             const bool gather_lane = lane < MP / 4;
             if (args.idx && gather_lane) {
+                int32_t v[4];
+#pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int32_t m = row0 + 4 * static_cast<int32_t>(lane) + r;
-                    const int32_t v = m < end ? __ldcg(args.idx + m) : 0;
-                    if (v < 0 || v >= args.table_rows)
+                    v[r] = m < end ? __ldcg(args.idx + m) : 0;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (v[r] < 0 || v[r] >= args.table_rows)
                         record_error(args.status, kStatusIndex, 0);
                     else
-                        rows[r] = v;
+                        rows[r] = v[r];
                 }
             }
             for (int32_t i = 0; i < nst; ++i) {
@@ -253,20 +258,26 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
         for (int32_t t = set; t < num_tiles; t += sets) {
             locate(t);
             const int32_t n = n0 + 32 * static_cast<int32_t>(q) + static_cast<int32_t>(lane);
-            // (a bad index makes its row zero: bit j, row j of this CTA's)
-            uint64_t bad = 0;
-            if (args.idx) {
+            int32_t row_idx[(kMine + 31) / 32];  // (loaded while the tile's MMAs run)
 #pragma unroll
-                for (int j0 = 0; j0 < kMine; j0 += 32) {
-                    const int32_t m = row0 + static_cast<int32_t>(rank) * kMine + j0 + static_cast<int32_t>(lane);
-                    const int32_t v = static_cast<int32_t>(lane) + j0 < kMine && m < end ? __ldcg(args.idx + m) : 0;
-                    bad |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, v < 0 || v >= args.table_rows)) << j0;
-                }
+            for (int j0 = 0; j0 < kMine; j0 += 32) {
+                const int32_t m = row0 + static_cast<int32_t>(rank) * kMine + j0 + static_cast<int32_t>(lane);
+                row_idx[j0 / 32] =
+                    args.idx && static_cast<int32_t>(lane) + j0 < kMine && m < end ? __ldcg(args.idx + m) : 0;
             }
             if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
                                          kWhereEpiAccFull))
                 break;
             tc_fence_after_sync();
+            // (a bad index makes its row zero: bit j, row j of this CTA's)
+            uint64_t bad = 0;
+            if (args.idx) {
+#pragma unroll
+                for (int j0 = 0; j0 < kMine; j0 += 32) {
+                    const int32_t v = row_idx[j0 / 32];
+                    bad |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, v < 0 || v >= args.table_rows)) << j0;
+                }
+            }
             const uint32_t acc = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(2 * ab * MP);
             // 8 rows' sums from row j: both issuers'
             float v[kMine];
