@@ -35,8 +35,8 @@
  * a workspace for split tiles, the FP4 paths buffers for converted weights
  * or re-pitched scales, gemm_trans and gemm_gated_backward one or two for
  * the float32 parts of long sums over few tiles (splits > 1), gemm_orthogonalize
- * one for its iterates, and gemm_group_rows one for counts (more than 131072
- * ids).  Each is allocated
+ * one for its iterates, gemm_group_rows one for counts (more than 131072 ids),
+ * and gemm_grouped one for the gathered rows of larger calls.  Each is allocated
  * by the first call that needs it; a call that needs more gets a new one of at
  * least twice the size, and the old one stays until the process ends (together
  * the old ones are no larger than the newest), since a captured graph may hold
@@ -544,7 +544,8 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *                    aligned, lda a multiple of 8.  a_rows is not read without idx.
  *  idx               NULL, or M int32 rows of A, read for rows of a group only; they may
  *                    repeat.  An index outside [0, a_rows) makes its row zero and records
- *                    GEMM_ERR_INDEX.
+ *                    GEMM_ERR_INDEX.  (Larger calls first lay the rows out in order, in a kept
+ *                    workspace of M x K elements, rows padded to 64.)
  *  B, ldb, stride_b  `groups` matrices, ldb a multiple of 8, the starts of consecutive ones
  *                    stride_b elements apart (a multiple of 8, no less than a matrix).
  *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.

@@ -174,6 +174,19 @@ Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
     return Few{mp, 2 * tiles <= sm_count && K >= 4096 ? 2 : 1};
 }
 
+// Gathered rows of A: whether a kernel that lays them out in order comes first.  The products' own
+// gathers cost about 36 ns for four rows and 64 columns where the tiles are 128 rows high, and 1.5 us a
+// tile where the rows of a group are few; the kernel a launch and each row in and out.  (us, own / in
+// order first: 16384 rows, 4096 x 4096 1038 / 326; 8 x 500, 4096 x 512 47.5 / 27.3; 777 rows, 2743 x 1000
+// 30.8 / 19.1; 60 groups of 163, 5489 x 118 175 / 55; 43 of 4, 8640 x 298 71 / 44; 8 of 4, 14336 x 4096
+// 146.4 / 144.5.)
+bool gather_first(int64_t M, int64_t K, const GForm &f, const Few &few, int64_t waves)
+{
+    const int64_t block_ns = f.block_ns < 32 * 36 ? 32 * 36 - f.block_ns : 0;
+    const int64_t own_ns = few.mp ? waves * 1500 : waves * ceil_div(K, 64) * block_ns;
+    return own_ns > 4000 + M * K / 1250;
+}
+
 bool bad_flag(int f) { return f != 0 && f != 1; }
 
 }  // namespace
@@ -263,19 +276,40 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     const Few few = choose_few(M, N, K, groups, dev->sm_count);
     GForm f = choose_form(ceil_div(K, 64), prec, dev->sm_count, tiles);
     int grid = 0;
+    int64_t waves = 0;  // (the tiles in rows are known on average only)
     if (few.mp) {
         f.pair = false;
         f.bn = 128;
         const int64_t n = most(few.mp, 128), sets = dev->sm_count / few.cs;
         grid = static_cast<int>(few.cs * (n < sets ? n : sets));
+        waves = ceil_div(tiles(few.mp, 128), sets);
     } else if ((st = group_grid(f, most(f.pair ? 256 : 128, f.bn), dev, &grid)) != GEMM_OK) {
         return st;
+    } else {
+        waves = ceil_div(tiles(f.pair ? 256 : 128, f.bn), dev->sm_count / (f.pair ? 2 : 1));
     }
     GroupMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     GroupArgs g;
     fill_group(g, bf16, out, dev);
-    const bool a_ok = K == 0 || (idx ? encode_2d(&maps.a, ab_type(bf16), A, K, rows, lda * 2, 64, 1,
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool first = idx && K > 0 && gather_first(M, K, f, few, waves);
+    std::unique_lock<std::mutex> hold;
+    if (first) {
+        const int64_t ldw = ceil_div(K, 64) * 64;
+        void *w = nullptr;
+        hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, cs));
+        if ((st = get_dequant_buffer(dev->index, cs, kBufGathered, static_cast<size_t>(M * ldw) * 2, &w)) != GEMM_OK)
+            return st;
+        if (tcg::launch_group_gather(A, static_cast<int32_t>(rows), lda, idx, offsets, static_cast<int32_t>(groups),
+                                     static_cast<int32_t>(M), static_cast<int32_t>(K), w, ldw, g.status,
+                                     dev->sm_count, cs) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        A = w;
+        lda = ldw;
+    }
+    const bool own = idx && !first;
+    const bool a_ok = K == 0 || (own ? encode_2d(&maps.a, ab_type(bf16), A, K, rows, lda * 2, 64, 1,
                                                  CU_TENSOR_MAP_SWIZZLE_128B)
                                      : encode_2d(&maps.a, ab_type(bf16), A, K, M, lda * 2, 64,
                                                  static_cast<uint32_t>(few.mp ? few.mp : 128),
@@ -295,13 +329,14 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     g.alpha = alpha;
     g.idx = idx;
     g.table_rows = static_cast<int32_t>(rows);
+    g.gather = own ? 1 : 0;
     g.loads = K > 0 ? 1 : 0;
     if (few.mp)
-        return tcg::launch_group_few(few.mp, few.cs, trans_b == 1, maps, g, grid, static_cast<cudaStream_t>(stream)) ==
+        return tcg::launch_group_few(few.mp, few.cs, trans_b == 1, maps, g, grid, cs) ==
                        cudaSuccess
                    ? GEMM_OK
                    : GEMM_ERR_CUDA;
-    const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, prec, maps, g, grid, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = tcg::launch_group_rows(f.bn, f.pair, trans_b == 1, prec, maps, g, grid, cs);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -114,7 +114,7 @@ gemm_status reset_static_scratch(int device);
 // gemm_gated_e2m1), the parts of sums (kBufParts and the one after it), gemm_orthogonalize's
 // iterates and gemm_group_rows' counts.
 enum { kBufWeights = 0, kBufScales = 1, kBufScalesA = 2, kBufScalesB = 3, kBufScalesB2 = 4, kBufParts = 5,
-       kBufOrthogonalize = 7, kBufGroupRows = 8 };
+       kBufOrthogonalize = 7, kBufGroupRows = 8, kBufGathered = 9 };
 gemm_status get_dequant_buffer(int device, cudaStream_t stream, int use, size_t bytes, void **out);
 
 // To be held from get_dequant_buffer to the last launch that reads the buffer, where a

@@ -80,6 +80,7 @@ struct GroupArgs {
     int32_t out_kind, ab_bf16;
     const int32_t *idx;      // KIND_ROWS: row i of A is row idx[i] of a table (NULL: row i)
     int32_t table_rows;
+    int32_t gather;          // idx is followed here (0: A is those rows already)
     int32_t d_tma;           // D goes out through TMA where a box is whole
     int32_t d_vec;           // D's rows are whole 16 bytes apart, its base 16-byte aligned
     void *D;
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
             const int32_t n0 = p.n0 + static_cast<int32_t>(role) * Cfg::BN_LOCAL;
             const int32_t ga = kBatch ? p.g : 0, gb = kSum ? 0 : p.g;
             int32_t rows[4] = {0, 0, 0, 0};
-            if (kRows && args.idx) {
+            if (kRows && args.gather) {
                 // lane l fetches rows 4 l .. 4 l + 3, four per gather4; rows past the group's,
                 // and those whose index is not a row of the table, fetch row 0
                 int32_t v[4];
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                 };
                 constexpr Bool<kBatch> kStackA{};   // (A is a stack, or rows of one matrix)
                 constexpr Bool<!kSum> kStackB{};
-                if (kRows && args.idx) {
+                if (kRows && args.gather) {
                     if (PAIR)
                         tma_gather4_pair(sa + lane * 512u, &maps.a, bar, k, rows[0], rows[1], rows[2], rows[3]);
                     else

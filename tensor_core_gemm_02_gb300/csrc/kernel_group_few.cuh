@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
             locate(t);
             int32_t rows[4] = {0, 0, 0, 0};
             const bool gather_lane = lane < MP / 4;
-            if (args.idx && gather_lane) {
+            if (args.gather && gather_lane) {
                 int32_t v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
                         }
                     }
                     const uint32_t to = sa + MP * 128u * j;
-                    if (args.idx) {
+                    if (args.gather) {
                         if (gather_lane)
                             tma_gather4(to + lane * 512u, &maps.a, full_bar(s), k, rows[0], rows[1], rows[2], rows[3]);
                     } else if (lane == 0) {

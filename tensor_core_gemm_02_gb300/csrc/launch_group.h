@@ -23,6 +23,12 @@ cudaError_t launch_group_sum(int bn, bool pair, int prec, const GroupMaps &maps,
 cudaError_t launch_group_batch(int bn, bool pair, int maj, bool sym, int prec, int cs, const GroupMaps &maps,
                                const GroupArgs &args, int grid, cudaStream_t stream);
 
+// W[i] = table[idx[i]] (M rows of K 16-bit elements, 16-byte aligned rows in both) for the rows that
+// the groups' offsets name; zeros, and an error recorded, where idx[i] is not a row of the table.
+cudaError_t launch_group_gather(const void *table, int32_t table_rows, int64_t lda, const int32_t *idx,
+                                const int32_t *offsets, int32_t groups, int32_t M, int32_t K, void *W, int64_t ldw,
+                                uint32_t *status, int sm_count, cudaStream_t stream);
+
 // The stable order of M ids by value: offsets (groups + 1), order and rows (each M; rows
 // may be NULL: order[i] / choices).  counts: `chunks` x (groups + 1) int32 (unused for one
 // chunk).

@@ -249,6 +249,46 @@ def test_threads(make, one):
     assert not failures, failures[:5]
 
 
+def _gathered(i):
+    A, B = quarters((900, 520), i), quarters((4, 2056, 520), 9 + i)
+    idx = torch.randint(0, 900, (3000 + 100 * i,), dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 1500 + i, 1500 + i, 2200, 3000], dtype=torch.int32, device="cuda")
+    return lambda: binding.gemm_grouped(A, B, off, idx=idx)
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_threads_with_gathered_rows(one):
+    test_threads(_gathered, one)
+
+
+def test_gathered_rows_replayed_after_a_larger_call():
+    """The rows laid out in order are a graph's own: on two streams at once, and after a larger call."""
+    calls = [_gathered(i) for i in range(2)]
+    want = [c().clone() for c in calls]
+    streams, graphs, got = [torch.cuda.Stream() for _ in calls], [torch.cuda.CUDAGraph() for _ in calls], []
+    torch.cuda.synchronize()
+    for c, s, g in zip(calls, streams, graphs):
+        with torch.cuda.graph(g, stream=s):
+            got.append(c())
+    A, B = quarters((100, 2056), 5), quarters((1, 2056, 2056), 6)
+    off = torch.tensor([0, 9000], dtype=torch.int32, device="cuda")
+    idx = torch.randint(0, 100, (9000,), dtype=torch.int32, device="cuda")
+    with torch.cuda.stream(streams[0]):
+        larger = binding.gemm_grouped(A, B, off, idx=idx)
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        [t.zero_() for t in got]
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 7).all()) for t in others)
+    assert torch.equal(larger, binding.gemm_grouped(A[idx.long()].contiguous(), B, off))
+
+
 @pytest.mark.parametrize("what", ["_ortho", "_sort", "_grouped"])
 def test_first_call_of_a_process_inside_a_capture_on_a_new_thread(what):
     code = textwrap.dedent(f"""

@@ -234,6 +234,46 @@ def test_bad_row_indices_make_zero_rows(form):
 
 # ---------------------------------------------------------------- the gradients of the weights
 
+# enough tiles that the rows are laid out in order first
+GATHERED = [([1500, 0, 700, 801], 5, 30, 2056, 519), ([3] * 100, 0, 7, 4000, 264), ([40] * 30, 2, 0, 3000, 1000), ([4000], 0, 0, 1030, 64)]
+
+
+@pytest.mark.parametrize("trans_b", [False, True])
+@pytest.mark.parametrize("counts,front,behind,N,K", GATHERED)
+def test_gathered_rows_of_large_calls(trans_b, counts, front, behind, N, K):
+    for dtype, out in KINDS:
+        check_grouped(counts, front, behind, N, K, trans_b, dtype, out, True, idx=True)
+        check_grouped(counts, front, behind, N, K, trans_b, dtype, out, False, idx=True)
+
+
+@pytest.mark.parametrize("counts,front,behind,N,K", GATHERED)
+def test_bad_row_indices_of_large_calls(counts, front, behind, N, K):
+    """Their rows are zero whatever B holds, and the error is recorded; indices of rows outside every
+    group are not read."""
+    gen = torch.Generator().manual_seed(5)
+    M = front + sum(counts) + behind
+    table, B = wide(50, K, F16, gen, exact=True), stack(len(counts), N, K, F16, gen, True)
+    idx = torch.randint(0, 50, (M,), generator=gen).int()
+    idx[:front] = -5
+    idx[M - behind:] = 1 << 30
+    idx = idx.cuda()
+    off = offsets_of(counts, front)
+    D = new_out(M, N, OUT_F32)[:, :N]
+    want = binding.gemm_grouped(table, B, off, D, idx=idx).clone()
+    assert device_status() == binding.GEMM_OK
+    bad = [front, front + 2, front + sum(counts) - 1]
+    for i, v in zip(bad, (-1, 50, (1 << 31) - 1)):
+        idx[i] = v
+        want[i] = 0
+    B[:, 0, 0] = float("inf")
+    keep = torch.ones(N, dtype=torch.bool)
+    keep[0] = False
+    binding.gemm_grouped(table, B, off, D, idx=idx)
+    assert device_status() == binding.GEMM_ERR_INDEX
+    assert torch.equal(D[:, keep], want[:, keep])
+    assert (D[bad] == 0).all()
+
+
 def check_weights(counts, front, behind, N, K, dtype, out, exact, pad=8):
     gen = torch.Generator().manual_seed(N + K)
     M = front + sum(counts) + behind
