@@ -603,6 +603,8 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *  also of a bfloat16 Y, where min(M, N) < 256.  All are scaled by 2^12: the elements of the
  *  iterates, of P and of b P + c P^2 have to stay below 16, as they do where the singular
  *  values stay below 2.  The last step is rounded once, to Y's type.
+ *  (Small matrices, min(M, N) <= 64 and what fits shared memory, where one launch for all
+ *  steps is faster: float32 throughout, no workspace.)
  *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.
  *  Workspace: per device and stream, up to 1 GiB or one matrix's (8 M N + 8 min(M, N)^2
  *  bytes, rows padded to 64 elements) if that is more, and some MB for long sums of few tiles, kept as the other

@@ -506,6 +506,42 @@ gemm_status run_batch(const BatchProduct &p, const DeviceInfo *dev, cudaStream_t
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
+constexpr int64_t kSmallColumns = 1 << 16;  // (a block's elements are 32-bit numbers)
+// Thread blocks a matrix for all steps in one launch (1 or 8), or 0 where the tile kernels are faster
+// or the matrix does not fit.  Five steps, the tile kernels / one launch, us: bf16 1 x 38 x 24 68 / 19, 1 x
+// 1070 x 18 95 / 27, 9 x 128 x 34 84 / 32, 1 x 16 x 4096 87 / 38, 100 x 721 x 20 164 / 61, 1000 x 16 x 64 234 /
+// 59, 300 x 32 x 128 107 / 45, 1 x 64 x 512 79 / 77, 1 x 64 x 1024 87 / 103, 1 x 2048 x 48 101 / 116, 16 x 64 x 1024 95 / 204.
+int small_blocks(int64_t count, int64_t s, int64_t l, int steps, int out, int sm_count)
+{
+    int fk = 0, fbn = 0;
+    forced_tile(&fk, &fbn);
+    if (fk != 0 || s > 64 || count > kMaxDim / 8)
+        return 0;
+    const int64_t s4 = ceil_div(s, 4) * 4, blocks = ceil_div(l, 64);
+    // the tile kernels': launches, K blocks of X X^T (long sums are shared), waves of tiles
+    const int64_t more = ceil_div(count * ceil_div(l, 128), sm_count) - 1;
+    int64_t best_ns = (2 + 3 * static_cast<int64_t>(steps)) * 3600 + steps * ((blocks < 30 ? blocks : 30) * 200 + more * 4500);
+    if (out == GEMM_OUT_F32)
+        best_ns += best_ns / 8;
+    int best = 0;
+    for (int c = 1; c <= 8; c += 7) {
+        const int64_t lc = ceil_div(l, c);
+        const size_t shared = tcg::orthogonalize_small_shared(s, l, c);
+        if (lc > kSmallColumns || shared > tcg::kSmallShared)
+            continue;
+        // FMAs of a block's step, 100 a ns; passes over s x s, and what a step waits for; waves (a
+        // cluster wants eight free SMs of one group, two small blocks share an SM)
+        const int64_t step_ns = (2 * s4 * s4 * lc + s4 * s4 * s4) / 100 + s4 * s4 * 8 / 10 + (c == 1 ? 1700 : 3500);
+        const int64_t at_once = c == 8 ? sm_count / 11 : (shared <= tcg::kSmallShared / 2 ? sm_count * 7 / 5 : sm_count);
+        const int64_t ns = ceil_div(count, at_once) * (steps * step_ns + 4000);
+        if (ns < best_ns) {
+            best = c;
+            best_ns = ns;
+        }
+    }
+    return best;
+}
+
 // Powers of two that keep the float16 iterates (elements up to 1 and a little) and their
 // products with themselves (as small as the product of two of their elements) away from
 // float16's subnormal numbers.
@@ -544,6 +580,27 @@ extern "C" gemm_status gemm_orthogonalize(int64_t count, int64_t M, int64_t N, i
     if ((st = device_info(&dev)) != GEMM_OK)
         return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (const int blocks = small_blocks(count, s, l, steps, out, dev->sm_count)) {
+        tcg::SmallArgs q{};
+        q.X = X;
+        q.ldx = ldx;
+        q.stride_x = stride_x;
+        q.type = type;
+        q.Y = Y;
+        q.ldy = ldy;
+        q.stride_y = stride_y;
+        q.out = out;
+        q.s = static_cast<int32_t>(s);
+        q.l = static_cast<int32_t>(l);
+        q.tall = wide ? 0 : 1;
+        q.steps = steps;
+        q.cluster = blocks;
+        q.a = a;
+        q.b = b;
+        q.c = c;
+        q.eps = eps;
+        return tcg::launch_orthogonalize_small(q, count, cs) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    }
     // The iterate is held in two float16 parts, since what its rounding loses in one step the
     // next ones multiply (1000 x 1367, relative to 64 bits: one part 3.1e-3, two 2.7e-4).  The
     // products take the high parts, or, in the last `exact` steps, both, as Y's type asks for

@@ -47,6 +47,24 @@ cudaError_t launch_normalize(const void *X, int64_t ldx, int64_t stride_x, int t
                              int32_t count, const float *partial, int parts, float scale, float eps,
                              uint16_t *Xs, int64_t lds, int64_t stride_s, int64_t lo, cudaStream_t stream);
 
+// All steps on `count` small matrices in one launch, a matrix by `cluster` (1 or 8) thread blocks; s <= 64
+// and l its sides, the shared memory of a block at most kSmallShared bytes.
+constexpr size_t kSmallShared = 220 * 1024;
+struct SmallArgs {
+    const void *X;
+    int64_t ldx, stride_x;
+    int32_t type;
+    void *Y;
+    int64_t ldy, stride_y;
+    int32_t out;
+    int32_t s, l, tall;  // tall: X is l x s
+    int32_t steps, cluster;
+    float a, b, c, eps;
+    int32_t lc, px, ps;  // (the launch's: columns of a block, pitches)
+};
+size_t orthogonalize_small_shared(int64_t s, int64_t l, int cluster);
+cudaError_t launch_orthogonalize_small(SmallArgs a, int64_t count, cudaStream_t stream);
+
 // Symmetric matrices P (s x s, float16, and, lo != 0, their low parts lo elements behind) from `parts`
 // float32 matrices each, whose sums' elements on and below the diagonal are P's.
 cudaError_t launch_join_parts(const float *Q, int64_t ldq, int64_t stride_q, int32_t parts, int32_t s, int32_t count,

@@ -226,3 +226,56 @@ def test_long_sums_of_few_tiles(count, m, n):
         check(stack(count, m, n, dtype, m + n), QUINTIC, 4, out)
     X = stack(count, m, n, torch.bfloat16, 3)
     assert torch.equal(binding.gemm_orthogonalize(X), binding.gemm_orthogonalize(X))
+
+
+SMALL = [(1, 16, 4096), (1, 4096, 16), (2, 64, 1000), (2, 1001, 63), (200, 16, 64), (30, 33, 17), (1, 5, 9), (3, 61, 61), (20, 1, 300),
+         (1, 2, 2), (40, 40, 130)]
+
+
+@pytest.mark.parametrize("count,m,n", SMALL)
+def test_small_matrices(count, m, n):
+    """One launch, in float32 throughout, which the bound of the two float16 parts covers: each of its
+    roundings is 2^-24 of a value or of a term of a sum, of at most as many terms."""
+    for dtype, out in ((torch.float32, torch.float32), (torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)):
+        check(stack(count, m, n, dtype, m + n), MUON, 1, out)
+        check(stack(count, m, n, dtype, m + n), QUINTIC, 5, out)
+    X = stack(count, m, n, torch.float32, 3)
+    Y = binding.gemm_orthogonalize(X)
+    assert torch.equal(Y, binding.gemm_orthogonalize(X))
+    buf = torch.full((count, m + 1, n + 5), 7.0, device="cuda")
+    binding.gemm_orthogonalize(X, buf[:, :m, :n])
+    assert torch.equal(buf[:, :m, :n], Y) and (buf[:, m:] == 7).all() and (buf[:, :, n:] == 7).all()
+    binding.gemm_orthogonalize(X, X)
+    assert torch.equal(X, Y)
+
+
+@pytest.mark.parametrize("count,m,n", [(4, 16, 2000), (4, 300, 40), (30, 20, 30)])
+def test_small_matrices_that_are_not_finite(count, m, n):
+    X = stack(count, m, n, torch.float32, 6)
+    good = binding.gemm_orthogonalize(X)
+    X[0] = 0
+    X[2, 3, 3] = float("inf")
+    X[3, m - 1, n - 1] = float("nan")
+    Y = binding.gemm_orthogonalize(X)
+    assert (Y[0] == 0).all() and torch.equal(Y[1], good[1]) and torch.equal(Y[4:], good[4:])
+    assert torch.isnan(Y[2]).all() and torch.isnan(Y[3]).all()
+    assert torch.isnan(binding.gemm_orthogonalize(torch.zeros(m, n, device="cuda"), eps=0.0)).all()
+
+
+def test_small_matrices_captured_and_one_behind_another():
+    X = stack(3, 24, 700, torch.bfloat16, 9)
+    want = X
+    for _ in range(3):
+        want = binding.gemm_orthogonalize(want, steps=2)
+    Y, s, graph = torch.empty_like(want), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        binding.gemm_orthogonalize(X, Y, steps=2)
+        binding.gemm_orthogonalize(Y, Y, steps=2)
+        binding.gemm_orthogonalize(Y, Y, steps=2)
+    for _ in range(2):
+        Y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
