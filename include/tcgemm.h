@@ -545,7 +545,7 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *  idx               NULL, or M int32 rows of A, read for rows of a group only; they may
  *                    repeat.  An index outside [0, a_rows) makes its row zero and records
  *                    GEMM_ERR_INDEX.  (Larger calls first lay the rows out in order, in a kept
- *                    workspace of M x K elements, rows padded to 64.)
+ *                    workspace of M x K elements, rows padded to 64, up to 8 GiB.)
  *  B, ldb, stride_b  `groups` matrices, ldb a multiple of 8, the starts of consecutive ones
  *                    stride_b elements apart (a multiple of 8, no less than a matrix).
  *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.

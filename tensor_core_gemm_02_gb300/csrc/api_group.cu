@@ -180,8 +180,11 @@ Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
 // order first: 16384 rows, 4096 x 4096 1038 / 326; 8 x 500, 4096 x 512 47.5 / 27.3; 777 rows, 2743 x 1000
 // 30.8 / 19.1; 60 groups of 163, 5489 x 118 175 / 55; 43 of 4, 8640 x 298 71 / 44; 8 of 4, 14336 x 4096
 // 146.4 / 144.5.)
+constexpr int64_t kGatheredBytes = int64_t(8) << 30;  // (more is not kept for them)
 bool gather_first(int64_t M, int64_t K, const GForm &f, const Few &few, int64_t waves)
 {
+    if (ceil_div(K, 64) * 128 > kGatheredBytes / M)
+        return false;
     const int64_t block_ns = f.block_ns < 32 * 36 ? 32 * 36 - f.block_ns : 0;
     const int64_t own_ns = few.mp ? waves * 1500 : waves * ceil_div(K, 64) * block_ns;
     return own_ns > 4000 + M * K / 1250;

@@ -246,6 +246,19 @@ def test_gathered_rows_of_large_calls(trans_b, counts, front, behind, N, K):
         check_grouped(counts, front, behind, N, K, trans_b, dtype, out, False, idx=True)
 
 
+def test_more_gathered_rows_than_are_laid_out():
+    """Rows of which the workspace would pass 8 GiB are gathered by the product itself."""
+    gen = torch.Generator().manual_seed(8)
+    M, N, K = (1 << 21) + 128, 8, 2048
+    table, B = wide(50, K, F16, gen, exact=True), stack(2, N, K, F16, gen, True)
+    idx = torch.randint(0, 50, (M,), generator=gen).int()
+    off = torch.tensor([0, 1 << 20, M], dtype=torch.int32, device="cuda")
+    D = binding.gemm_grouped(table, B, off, idx=idx.cuda())
+    every = torch.stack([table.double() @ b.double().T for b in B])  # (group, row of the table, N)
+    g = (torch.arange(M) >= 1 << 20).long()
+    assert torch.equal(D, every[g.cuda(), idx.long().cuda()].float())
+
+
 @pytest.mark.parametrize("counts,front,behind,N,K", GATHERED)
 def test_bad_row_indices_of_large_calls(counts, front, behind, N, K):
     """Their rows are zero whatever B holds, and the error is recorded; indices of rows outside every
