@@ -174,7 +174,7 @@ def prepare(case, seed):
         s["db"] = torch.zeros((e, n, _pad8(k)), dtype=out, device=DEV)[:, :, :k]
         return s
     choices = case["choices"]
-    s["a"] = _normal(gen, (max(1, m // choices) if choices else m, k), dt)
+    s["a"] = _normal(gen, (m // choices if choices else m, k), dt)
     s["idx"] = None
     if choices:
         s["idx"] = (torch.argsort(ids, stable=True) // choices).to(torch.int32)
