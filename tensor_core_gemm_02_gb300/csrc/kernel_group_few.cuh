@@ -13,6 +13,11 @@
 // peer's shared memory; each then adds the parts in order and stores its rows: no workspace, no
 // atomics, the same bits every time.
 //
+// Float32 results: the accumulators, which drop what does not fit them, are emptied every eight stages
+// (512 of K each) into float32 registers, which round to nearest; while one tile buffer is read the MMAs go
+// on in the other.  (Positive operands, relative error, one accumulator / emptied: K of 14336 4.6e-5 / 3.0e-6,
+// 57344 1.9e-4 / 3.1e-6.)  For results of 16 bits one accumulator takes an issuer's whole share.
+//
 // Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 138 us (6.8 TB/s), two of one row 39 (6.0 TB/s; the
 // tile kernel 65); 2 of 64 groups, 2816 x 1024 6.4 us (launch, offsets, first loads, epilogue).  More
 // rows: 64 a group 161 against the tile kernel's 163, 100 of 2816 x 1024 91 against 84, hence the
@@ -36,6 +41,7 @@ struct FewCfg {
     static constexpr uint32_t B_BYTES = BN * 128u * KBOX, A_BYTES = MP * 128u * KBOX;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = MP == 16 ? 6 : (MP == 32 ? 5 : 4);
+    static constexpr int CHUNK = 8;  // stages, a K block each an issuer, between roundings of float32 results
     static constexpr uint32_t OFF_B = 0, OFF_A = STAGES * B_BYTES;
     // sums from the peer: two tiles' in turn, MP / CS rows of 128 floats
     static constexpr uint32_t RED_BYTES = CS > 1 ? MP / CS * BN * 4u : 0u;
@@ -118,7 +124,9 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
     // this CTA's stages of every tile
     const int32_t all = (args.K + 127) / 128;
     const int32_t st0 = static_cast<int32_t>(static_cast<int64_t>(all) * rank / CS);
-    const int32_t nst = static_cast<int32_t>(static_cast<int64_t>(all) * (rank + 1) / CS) - st0;
+    const int32_t nst = static_cast<int32_t>(static_cast<int64_t>(all) * (rank + 1) / CS) - st0;  // (K > 0, CS = 2: long)
+    // stages that an accumulator takes
+    const int32_t fill = args.out_kind == kOutF32 ? Cfg::CHUNK : nst;
 
     // (whole warp) a tile's first row, the end of its group's and its first column
     int32_t g = 0, row0 = 0, end = 0, n0 = 0;
@@ -214,37 +222,42 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
             uint32_t ph = 0, aph = 0;
             bool alive = true;
             for (int32_t t = set; t < num_tiles && alive; t += sets) {
-                if (!wait_bounded<true>(acce_bar(ab), aph ^ 1u, abort_flag, args.status, args.timeout_ns,
-                                        kWhereMmaAccEmpty))
-                    break;
-                tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * ab + e) * MP);
-                for (int32_t i = 0; i < nst; ++i) {
-                    if (!wait_bounded(full_bar(s), ph, abort_flag, args.status, args.timeout_ns, kWhereMmaFull)) {
+                for (int32_t i0 = 0; i0 < nst && alive; i0 += fill) {
+                    if (!wait_bounded<true>(acce_bar(ab), aph ^ 1u, abort_flag, args.status, args.timeout_ns,
+                                            kWhereMmaAccEmpty)) {
                         alive = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES + 16384u * e;
-                    const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES + MP * 128u * e;
-                    const uint64_t wd = MAJB ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
-                    const uint64_t xd = sdesc_k_sw128(sa);
-                    constexpr uint32_t kStepW = MAJB ? 128u : 2u;
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * ab + e) * MP);
+                    const int32_t here = min(fill, nst - i0);
+                    for (int32_t i = 0; i < here; ++i) {
+                        if (!wait_bounded(full_bar(s), ph, abort_flag, args.status, args.timeout_ns, kWhereMmaFull)) {
+                            alive = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t sb = base + Cfg::OFF_B + s * Cfg::B_BYTES + 16384u * e;
+                        const uint32_t sa = base + Cfg::OFF_A + s * Cfg::A_BYTES + MP * 128u * e;
+                        const uint64_t wd = MAJB ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
+                        const uint64_t xd = sdesc_k_sw128(sa);
+                        constexpr uint32_t kStepW = MAJB ? 128u : 2u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f16(d_tmem, wd + kStepW * k, xd + 2u * k, idesc, (i | k) != 0 ? 1u : 0u);
-                    tc_commit(empty_bar(s));
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f16(d_tmem, wd + kStepW * k, xd + 2u * k, idesc, (i | k) != 0 ? 1u : 0u);
+                        tc_commit(empty_bar(s));
+                        if (++s == STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
-                }
-                if (!alive)
-                    break;
-                tc_commit(accf_bar(ab));
-                if (++ab == 2) {
-                    ab = 0;
-                    aph ^= 1u;
+                    if (!alive)
+                        break;
+                    tc_commit(accf_bar(ab));
+                    if (++ab == 2) {
+                        ab = 0;
+                        aph ^= 1u;
+                    }
                 }
             }
         }
@@ -253,8 +266,9 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
         // ------------------------------------------------------------ epilogue
         const uint32_t q = warp & 3u;
         constexpr int kMine = MP / CS;  // rows this CTA finishes
-        int ab = 0;
-        uint32_t aph = 0, use = 0;  // use: times both buffers have been used before
+        int ab = 0, rb = 0;  // accumulators; the peer's sums
+        uint32_t aph = 0, use = 0;  // use: times both buffers of the peer's sums have been used before
+        bool alive = true;
         for (int32_t t = set; t < num_tiles; t += sets) {
             locate(t);
             const int32_t n = n0 + 32 * static_cast<int32_t>(q) + static_cast<int32_t>(lane);
@@ -265,69 +279,91 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
                 row_idx[j0 / 32] =
                     args.idx && static_cast<int32_t>(lane) + j0 < kMine && m < end ? __ldcg(args.idx + m) : 0;
             }
-            if (!warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
-                                         kWhereEpiAccFull))
+            // v: the sums of this CTA's rows, both issuers'; w: of the peer's
+            float v[kMine], w[CS > 1 ? kMine : 1];
+            const int mine0 = static_cast<int>(rank) * kMine;
+            const auto take = [&](auto more) {
+                constexpr bool kMore = decltype(more)::value;
+                tc_fence_after_sync();
+                const uint32_t acc = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(2 * ab * MP);
+                // 8 rows' from row j
+                auto take8 = [&](int j, float *to) {
+                    uint32_t a[8], b[8];
+                    tc_ld_32x32b_x8(acc + static_cast<uint32_t>(j), a);
+                    tc_ld_32x32b_x8(acc + static_cast<uint32_t>(MP + j), b);
+                    tc_wait_ld8(a);
+                    tc_wait_ld8(b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = __fadd_rn(__uint_as_float(a[i]), __uint_as_float(b[i]));
+                        to[i] = kMore ? __fadd_rn(to[i], x) : x;
+                    }
+                };
+#pragma unroll
+                for (int j = 0; j < kMine; j += 8) {
+                    take8(mine0 + j, v + j);
+                    if constexpr (CS > 1)
+                        take8(static_cast<int>(rank ^ 1u) * kMine + j, w + j);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(acce_bar(ab));
+                if (++ab == 2) {
+                    ab = 0;
+                    aph ^= 1u;
+                }
+            };
+            alive = warp_wait_bounded<true>(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                            kWhereEpiAccFull);
+            if (!alive)
                 break;
-            tc_fence_after_sync();
+            take(Bool<false>{});
+            for (int32_t i = fill; i < nst; i += fill) {
+                // (inline, or the call would save the sums' registers)
+                alive = warp_wait_bounded_inline(accf_bar(ab), aph, abort_flag, args.status, args.timeout_ns,
+                                                 kWhereEpiAccFull);
+                if (!alive)
+                    break;
+                take(Bool<true>{});
+            }
+            if (!alive)
+                break;
             // (a bad index makes its row zero: bit j, row j of this CTA's)
             uint64_t bad = 0;
             if (args.idx) {
 #pragma unroll
                 for (int j0 = 0; j0 < kMine; j0 += 32) {
-                    const int32_t v = row_idx[j0 / 32];
-                    bad |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, v < 0 || v >= args.table_rows)) << j0;
+                    const int32_t r = row_idx[j0 / 32];
+                    bad |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, r < 0 || r >= args.table_rows)) << j0;
                 }
             }
-            const uint32_t acc = tmem_base + ((32u * q) << 16) + static_cast<uint32_t>(2 * ab * MP);
-            // 8 rows' sums from row j: both issuers'
-            float v[kMine];
-            auto take8 = [&](int j, float *to) {
-                uint32_t a[8], b[8];
-                tc_ld_32x32b_x8(acc + static_cast<uint32_t>(j), a);
-                tc_ld_32x32b_x8(acc + static_cast<uint32_t>(MP + j), b);
-                tc_wait_ld8(a);
-                tc_wait_ld8(b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    to[i] = nst > 0 ? __fadd_rn(__uint_as_float(a[i]), __uint_as_float(b[i])) : 0.f;
-            };
-            const int mine0 = static_cast<int>(rank) * kMine;
-#pragma unroll
-            for (int j = 0; j < kMine; j += 8)
-                take8(mine0 + j, v + j);
             if constexpr (CS > 1) {
                 const uint32_t peer = rank ^ 1u;
                 // the peer has read the buffer's last sums
-                if (use > 0 && !warp_wait_cluster(rede_bar(ab, q), (use - 1u) & 1u, abort_flag, args.status,
+                if (use > 0 && !warp_wait_cluster(rede_bar(rb, q), (use - 1u) & 1u, abort_flag, args.status,
                                                   args.timeout_ns, kWhereEpiC))
                     break;
-                const uint32_t to = mapa_shared(base + Cfg::OFF_RED + ab * Cfg::RED_BYTES + (32u * q + lane) * 4u, peer);
+                const uint32_t to = mapa_shared(base + Cfg::OFF_RED + rb * Cfg::RED_BYTES + (32u * q + lane) * 4u, peer);
 #pragma unroll
-                for (int j = 0; j < kMine; j += 8) {
-                    float w[8];
-                    take8(static_cast<int>(peer) * kMine + j, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_cluster_u32(to + static_cast<uint32_t>(j + i) * 512u, __float_as_uint(w[i]));
-                }
+                for (int j = 0; j < kMine; ++j)
+                    st_shared_cluster_u32(to + static_cast<uint32_t>(j) * 512u, __float_as_uint(w[j]));
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(mapa_shared(redf_bar(ab, q), peer));
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(acce_bar(ab));
-            if constexpr (CS > 1) {
-                if (!warp_wait_cluster(redf_bar(ab, q), use & 1u, abort_flag, args.status, args.timeout_ns, kWhereEpiC))
+                    mbar_arrive_cluster(mapa_shared(redf_bar(rb, q), peer));
+                if (!warp_wait_cluster(redf_bar(rb, q), use & 1u, abort_flag, args.status, args.timeout_ns, kWhereEpiC))
                     break;
-                const uint32_t from = base + Cfg::OFF_RED + ab * Cfg::RED_BYTES + (32u * q + lane) * 4u;
+                const uint32_t from = base + Cfg::OFF_RED + rb * Cfg::RED_BYTES + (32u * q + lane) * 4u;
 #pragma unroll
                 for (int j = 0; j < kMine; ++j)
                     v[j] = __fadd_rn(v[j], __uint_as_float(ld_shared_u32(from + static_cast<uint32_t>(j) * 512u)));
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(mapa_shared(rede_bar(ab, q), rank ^ 1u));
+                    mbar_arrive_cluster(mapa_shared(rede_bar(rb, q), peer));
+                if (++rb == 2) {
+                    rb = 0;
+                    ++use;
+                }
             }
             if (n < args.N) {
 #pragma unroll
@@ -343,11 +379,6 @@ __global__ void __launch_bounds__(FewCfg<MP, CS>::THREADS, 1)
                                 args.out_kind == kOutBF16 ? f32_to_bf16_rn(x) : f32_to_f16_rn(x);
                     }
                 }
-            }
-            if (++ab == 2) {
-                ab = 0;
-                aph ^= 1u;
-                ++use;
             }
         }
         __syncwarp();

@@ -154,6 +154,25 @@ def test_few_rows_and_long_sums(trans_b, counts):
         check_grouped(counts, 0, 2, 200, K, trans_b, dtype, out, True, idx=i == 1)
 
 
+@pytest.mark.parametrize("form", ["auto", "few"])
+@pytest.mark.parametrize("trans_b", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 5, 1], 200, 14336), ([3, 0, 5, 1], 200, 114696), ([12, 16], 130, 65544),
+                                        ([40, 30], 130, 65544), ([1] * 80, 8, 57352), ([40] * 80, 8, 28680)])
+def test_float32_sums_of_one_sign(form, trans_b, counts, N, K):
+    """Positive operands: nothing cancels, and what each step of a long sum drops adds up.  (The last two on
+    one CTA a tile, the others on two.)"""
+    binding.gemm_debug_force_tile(*FORMS[form])
+    gen = torch.Generator().manual_seed(K)
+    M = sum(counts)
+    A, B = wide(M, K, F16, gen).abs_(), stack(len(counts), K if trans_b else N, N if trans_b else K, F16, gen, False).abs_()
+    s, t = grouped64(A, B, counts, 0, trans_b)
+    assert torch.equal(s, t)
+    D = binding.gemm_grouped(A, B, offsets_of(counts, 0), trans_b=trans_b, alpha=0.5)
+    want = 0.5 * s
+    b = 0.5 * sum_bound(K, OUT_F32) * t + 2.0 ** -23 * want
+    assert_close(D, want, b + ref.rounding(want + b, OUT_F32), (counts, N, K))
+
+
 def test_grouped_largest_number_of_groups():
     gen = torch.Generator().manual_seed(3)
     counts = torch.randint(0, 4, (1024,), generator=gen).tolist()
