@@ -239,4 +239,12 @@ __device__ __forceinline__ void tile_coords(int32_t t, const GemmArgs &a, int32_
     nb = r / rows;
 }
 
+// scale / (sqrt(squares) + eps); the largest number in the place of an infinity that comes from a divisor
+// above 0 (a matrix of zeros with a tiny eps: times 0 it has to give 0), not of one that comes from 0.
+__device__ __forceinline__ float norm_factor(float scale, float squares, float eps)
+{
+    const float d = sqrtf(squares) + eps, f = scale / d;
+    return d > 0.f && f > 3.402823466e38f ? 3.402823466e38f : f;
+}
+
 }  // namespace tcg

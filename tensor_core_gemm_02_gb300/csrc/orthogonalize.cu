@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
     float sum = 0.f;
     for (int32_t i = static_cast<int32_t>(threadIdx.x); i < parts; i += kThreads)
         sum += __ldcg(partial + static_cast<int64_t>(g) * parts + i);
-    const float f = scale / (sqrtf(block_sum(sum)) + eps);
+    const float f = norm_factor(scale, block_sum(sum), eps);
     Walk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kThreads,
            per_row);
     while (w.row < M) {

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) orthogonalize_small_kernel(const 
     float total = 0.f;
     for (int32_t c = 0; c < C; ++c)
         total += totals[c];
-    const float f = 1.0f / (sqrtf(total) + a.eps);
+    const float f = norm_factor(1.0f, total, a.eps);
     for (int32_t i = tid; i < s4 * px; i += kThreads)
         x[i] *= f;
     __syncthreads();

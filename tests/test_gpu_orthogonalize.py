@@ -184,6 +184,20 @@ def test_zeros_and_what_is_not_finite():
     assert torch.isnan(binding.gemm_orthogonalize(torch.zeros(4, 4, device="cuda"), eps=0.0)).all()
 
 
+@pytest.mark.parametrize("eps", [1e-30, 1e-36, 1e-44])
+@pytest.mark.parametrize("m,n", [(50, 80), (300, 200), (16, 1000), (130, 3000)])
+def test_zeros_whatever_eps(m, n, eps):
+    """A matrix of zeros gives zeros for every eps above 0, one whose reciprocal is no float32 number
+    among them; its neighbours, whose norm such an eps does not change, are what they are without."""
+    X = stack(3, m, n, torch.float32, 6)
+    good = binding.gemm_orthogonalize(X, eps=0.0)
+    X[1] = 0
+    Y = binding.gemm_orthogonalize(X, eps=eps)
+    assert (Y[1] == 0).all()
+    assert torch.equal(Y[0], good[0]) and torch.equal(Y[2], good[2])
+    assert torch.isnan(binding.gemm_orthogonalize(X, eps=0.0)[1]).all()
+
+
 def test_same_bits_every_time():
     X = stack(5, 300, 200, torch.bfloat16, 8)
     a = binding.gemm_orthogonalize(X)
