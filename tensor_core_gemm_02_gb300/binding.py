@@ -7,6 +7,10 @@ C function of the same name and raise :class:`GemmError` on a non-OK status.
 Every step of the computation runs in the library's CUDA kernels; there is no
 fallback.  If the library is missing this module raises instead of computing
 anything some other way.
+
+Where a call makes its output, the memory is that of the stream the call is given (of the
+current one without any); used on another stream, the usual rules of torch apply to it
+(``Tensor.record_stream``).
 """
 from __future__ import annotations
 
@@ -144,9 +148,10 @@ def _check(status: int, where: str):
         raise GemmError(status, where)
 
 
-def _out_tensor(D, M, N, out, device):
+def _out_tensor(D, M, N, out, device, stream):
     if D is None:
-        return torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=device)
+        with _on_stream(stream):
+            return torch.empty((M, N), dtype=_DTYPE_OF_OUT[out], device=device)
     if _OUT_OF_DTYPE.get(D.dtype) != out:
         raise TypeError("D's dtype does not match `out`")
     return D
@@ -161,7 +166,7 @@ def _plain(name, dtype, A, B, C, D, alpha, beta, out, stream):
         raise ValueError("A and B disagree on K")
     if C is not None and (C.dtype != torch.float32 or tuple(C.shape) != (M, N)):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, A.device)
+    D = _out_tensor(D, M, N, out, A.device, stream)
     st = getattr(load_library(), name)(
         M, N, K, _ptr(A), _ld(A), _ptr(B), _ld(B), _ptr(C), _ld(C) if C is not None else 0,
         _ptr(D), _ld(D), out, float(alpha), float(beta), _stream_ptr(stream))
@@ -193,7 +198,7 @@ def gemm_gather_rows(table, idx, B, C=None, D=None, *, alpha=1.0, beta=1.0, out=
         raise ValueError("table and B disagree on K")
     if C is not None and (C.dtype != torch.float32 or tuple(C.shape) != (M, N)):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, table.device)
+    D = _out_tensor(D, M, N, out, table.device, stream)
     st = load_library().gemm_gather_rows(
         M, N, K, 1 if table.dtype == torch.bfloat16 else 0, _ptr(table), rows, _ld(table),
         _ptr(idx), _ptr(B), _ld(B), _ptr(C), _ld(C) if C is not None else 0, _ptr(D), _ld(D),
@@ -247,7 +252,7 @@ def gemm_bf16_e2m1(A, Bq, Bs, C=None, D=None, *, alpha=1.0, beta=1.0, out=OUT_F3
         raise ValueError("Bq must be N x K/2 and Bs K/32 x N")
     if C is not None and (C.dtype != torch.float32 or tuple(C.shape) != (M, N)):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, A.device)
+    D = _out_tensor(D, M, N, out, A.device, stream)
     st = load_library().gemm_bf16_e2m1(
         M, N, K, _ptr(A), _ld(A), _ptr(Bq), _ld(Bq), _ptr(Bs), _ld(Bs), _ptr(C),
         _ld(C) if C is not None else 0, _ptr(D), _ld(D), out, float(alpha), float(beta),
@@ -275,7 +280,7 @@ def gemm_e2m1(Aq, As, Bq, Bs, C=None, D=None, *, alpha=1.0, beta=1.0, out=OUT_F3
         raise ValueError("Aq must be M x K/2, Bq N x K/2, As K/32 x M and Bs K/32 x N")
     if C is not None and (C.dtype != torch.float32 or tuple(C.shape) != (M, N)):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, Aq.device)
+    D = _out_tensor(D, M, N, out, Aq.device, stream)
     st = load_library().gemm_e2m1(
         M, N, K, _ptr(Aq), _ld(Aq), _ptr(As), _ld(As), _ptr(Bq), _ld(Bq), _ptr(Bs), _ld(Bs),
         _ptr(C), _ld(C) if C is not None else 0, _ptr(D), _ld(D), out, float(alpha), float(beta),
@@ -337,8 +342,15 @@ _empty_strided_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guard
                               "_empty_strided_cuda", None)
 
 
-def _allocator(device):
-    """A function (size, stride, dtype) -> uninitialised tensor on the device."""
+def _allocator(device, stream):
+    """A function (size, stride, dtype) -> uninitialised tensor on the device, from the memory of the
+    stream that the call is given: torch hands out a stream's freed memory to that stream again while
+    kernels on it may still use it."""
+    if stream is not None:
+        def new(size, strides, dtype):
+            with _on_stream(stream):
+                return torch.empty_strided(size, strides, dtype=dtype, device=device)
+        return new
     if _empty_strided_cuda is not None and device.type == "cuda" and device.index == _current_device():
         return _empty_strided_cuda
     return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device=device)
@@ -354,7 +366,7 @@ def gemm_gated(A, Bg, Bu, D=None, *, G=None, U=None, act=ACT_SILU, out=OUT_F32, 
     M, K = A.shape
     N = Bg.shape[0]
     if D is None:
-        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+        D = _allocator(A.device, stream)((M, N), (N, 1), _DTYPE_OF_OUT[out])
     args = (M, N, K, bf16, *_mat("A", A, M, K, dt), *_mat("Bg", Bg, N, K, dt), *_mat("Bu", Bu, N, K, dt),
             *_mat_or_null("G", G, M, N, dt), *_mat_or_null("U", U, M, N, dt),
             *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act))
@@ -372,7 +384,7 @@ def gemm_gated_e2m1(Aq, As, Bgq, Bgs, Buq, Bus, D=None, *, act=ACT_SILU, out=OUT
     N = Bgq.shape[0]
     blocks, u8 = half // 16, torch.uint8
     if D is None:
-        D = _allocator(Aq.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+        D = _allocator(Aq.device, stream)((M, N), (N, 1), _DTYPE_OF_OUT[out])
     args = (M, N, 2 * half, *_mat("Aq", Aq, M, half, u8), *_mat("As", As, blocks, M, u8),
             *_mat("Bgq", Bgq, N, half, u8), *_mat("Bgs", Bgs, blocks, N, u8), *_mat("Buq", Buq, N, half, u8),
             *_mat("Bus", Bus, blocks, N, u8), *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, _act(act))
@@ -390,7 +402,7 @@ def gemm_gated_backward(dD, G, U, A, Bg, Bu, *, dG=None, dU=None, dA=None, dBg=N
     dA = dG @ Bg + dU @ Bu, dBg = dG.T @ A and dBu = dU.T @ A in `out`'s type.
     dG may be G and dU may be U.  need_input / need_weights leave out dA / dBg
     and dBu (then None).  Returns (dA, dBg, dBu, dG, dU)."""
-    dt, new, ot = dD.dtype, _allocator(dD.device), _DTYPE_OF_OUT[out]
+    dt, new, ot = dD.dtype, _allocator(dD.device, stream), _DTYPE_OF_OUT[out]
     bf16 = _bf16_flag("dD", dt)
     M, N = dD.shape
     K = A.shape[1] if need_weights else (Bg.shape[1] if need_input else 0)
@@ -439,7 +451,7 @@ def gemm_trans(A, B, C=None, D=None, *, trans_a=False, trans_b=False, alpha=1.0,
     if K != Kb:
         raise ValueError("A and B disagree on K")
     if D is None:
-        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+        D = _allocator(A.device, stream)((M, N), (N, 1), _DTYPE_OF_OUT[out])
     args = (M, N, K, bf16, 1 if trans_a else 0, *_mat("A", A, ra, ca, dt), 1 if trans_b else 0,
             *_mat("B", B, rb, cb, dt), *_mat_or_null("C", C, M, N, torch.float32),
             *_mat("D", D, M, N, _DTYPE_OF_OUT[out]), out, alpha, beta)
@@ -462,7 +474,7 @@ def gemm_quantize_e2m1(X, Q=None, S=None, *, Y=None, stream=None):
     M, K = X.shape
     half, blocks = K // 2, K // 32
     if Q is None or S is None:
-        new = _allocator(X.device)
+        new = _allocator(X.device, stream)
         if Q is None:
             Q = new((M, half), (half, 1), u8)
         if S is None:  # (rows of whole 16 bytes, which the products read in place)
@@ -511,7 +523,7 @@ def gemm_group_rows(ids, groups, offsets=None, order=None, rows=None, *, stream=
         choices = shape[1] or 1
     else:
         raise ValueError("ids must be 1-D or tokens x choices")
-    M, p, new = ids.numel(), _ints("ids", ids, shape), _allocator(ids.device)
+    M, p, new = ids.numel(), _ints("ids", ids, shape), _allocator(ids.device, stream)
     if offsets is None:
         offsets = new((groups + 1,), (1,), i32)
         p_off = offsets.data_ptr()
@@ -549,7 +561,7 @@ def gemm_grouped(A, B, offsets, D=None, *, idx=None, trans_b=False, alpha=1.0, o
         raise ValueError("A and B disagree on K")
     new = D is None
     if new:
-        D = _allocator(A.device)((M, N), (N, 1), _DTYPE_OF_OUT[out])
+        D = _allocator(A.device, stream)((M, N), (N, 1), _DTYPE_OF_OUT[out])
     a, lda = _mat("A", A, table, K, dt)
     args = (M, N, K, groups, bf16, a, table, lda,
             None if idx is None else _ints("idx", idx, (M,)), _ints("offsets", offsets, (groups + 1,)),
@@ -575,7 +587,7 @@ def gemm_grouped_weights(dD, A, offsets, dB=None, *, alpha=1.0, out=OUT_F32, str
     K = A.shape[1]
     groups = offsets.shape[0] - 1
     if dB is None:
-        dB = _allocator(dD.device)((groups, N, K), (N * K, K, 1), _DTYPE_OF_OUT[out])
+        dB = _allocator(dD.device, stream)((groups, N, K), (N * K, K, 1), _DTYPE_OF_OUT[out])
     args = (M, N, K, groups, bf16, *_mat("dD", dD, M, N, dt), *_mat("A", A, M, K, dt),
             _ints("offsets", offsets, (groups + 1,)), *_stack("dB", dB, groups, N, K, _DTYPE_OF_OUT[out]), out, alpha)
     _on_device(dD, A, offsets, dB)
@@ -596,7 +608,8 @@ def gemm_orthogonalize(X, Y=None, *, steps=5, coefs=(3.4445, -4.7750, 2.0315), e
     if X.dim() not in (2, 3):
         raise ValueError("X must be M x N or count x M x N")
     if Y is None:
-        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        with _on_stream(stream):
+            Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
     out = _OUT_OF_DTYPE.get(Y.dtype)
     if out is None:
         raise TypeError("Y must be float32, bfloat16 or float16")
@@ -625,7 +638,7 @@ def gemm_seeded(A, B, C, D=None, *, out=OUT_F32, stream=None):
         raise ValueError("A and B disagree on K")
     if C is None or C.dtype != torch.float32 or tuple(C.shape) != (M, N):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, A.device)
+    D = _out_tensor(D, M, N, out, A.device, stream)
     st = load_library().gemm_seeded(
         M, N, K, 1 if A.dtype == torch.bfloat16 else 0, _ptr(A), _ld(A), _ptr(B), _ld(B),
         _ptr(C), _ld(C), _ptr(D), _ld(D), out, _stream_ptr(stream))
@@ -662,7 +675,7 @@ def gemm_skinny_noalloc(A, B, C=None, D=None, *, alpha=1.0, beta=1.0, out=OUT_F3
         raise ValueError("A and B disagree on K")
     if C is not None and (C.dtype != torch.float32 or tuple(C.shape) != (M, N)):
         raise ValueError("C must be float32 M x N")
-    D = _out_tensor(D, M, N, out, A.device)
+    D = _out_tensor(D, M, N, out, A.device, stream)
     st = load_library().gemm_skinny_noalloc(
         M, N, K, 1 if A.dtype == torch.bfloat16 else 0, _ptr(A), _ld(A), _ptr(B), _ld(B),
         _ptr(C), _ld(C) if C is not None else 0, _ptr(D), _ld(D), out, float(alpha),

@@ -200,6 +200,31 @@ def test_a_stream_that_is_not_the_current_one(raw):
         assert torch.equal(g, w), i
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_on_another_stream_and_memory_still_in_use(raw):
+    """The current stream has still to write blocks of the outputs' sizes when they are freed: the
+    outputs of a call on another stream are not laid there."""
+    A, B, dD = quarters((150, 136), 1), quarters((3, 200, 136), 2), quarters((150, 200), 3)
+    ids = torch.randint(-1, 3, (150,), dtype=torch.int32, device="cuda")
+    off = binding.gemm_group_rows(ids, 3)[0]
+    calls = [lambda **k: binding.gemm_group_rows(ids, 3, **k)[1], lambda **k: binding.gemm_grouped(A, B, off, **k),
+             lambda **k: binding.gemm_grouped(dD, B, off, trans_b=True, out=binding.OUT_BF16, **k),
+             lambda **k: binding.gemm_grouped_weights(dD, A, off, **k), lambda **k: binding.gemm_orthogonalize(B, **k),
+             lambda **k: binding.gemm_bf16(A, B[0], **k), lambda **k: binding.gemm_trans(dD, A, trans_a=True, trans_b=True, **k)]
+    want = [c() for c in calls]
+    s, busy = torch.cuda.Stream(), torch.empty(1 << 31, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(100):
+        busy.fill_(1)
+    freed = [torch.empty_like(w).fill_(99) for w in want for _ in range(8)]
+    del freed
+    got = [c(stream=s.cuda_stream if raw else s) for c in calls]
+    torch.cuda.synchronize()
+    for i, (g, w) in enumerate(zip(got, want)):
+        assert torch.equal(g, w), i
+    assert torch.equal(calls[1](stream=0), want[1])
+
+
 def _ortho(i):
     X = torch.randn((2, 100 + 40 * i, 150), device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
     return lambda: binding.gemm_orthogonalize(X)

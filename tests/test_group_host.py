@@ -138,3 +138,61 @@ def test_stack_pitches():
     y = torch.zeros(1, 1, 21, dtype=torch.bfloat16)
     _, ld, _ = binding._stack("y", y, 1, 1, 21, torch.bfloat16)
     assert ld == 24
+
+
+def _calls():
+    """Every wrapper that makes its outputs where it is given none: (call, number of new tensors)."""
+    z, h = torch.zeros, dict(dtype=torch.bfloat16)
+    u8 = dict(dtype=torch.uint8)
+    A, B, C, off = z(4, 32, **h), z(8, 32, **h), z(4, 8), z(4, dtype=torch.int32)
+    W, q, s, G = z(3, 8, 32, **h), z(4, 16, **u8), z(1, 4, **u8), z(4, 8, **h)
+    b = binding
+    return {
+        "gemm": (lambda **k: b.gemm(A, B, C, **k), 1),
+        "gemm_f16": (lambda **k: b.gemm_f16(A.half(), B.half(), **k), 1),
+        "gemm_gather_rows": (lambda **k: b.gemm_gather_rows(A, off, B, **k), 1),
+        "gemm_seeded": (lambda **k: b.gemm_seeded(A, B, C, **k), 1),
+        "gemm_skinny_noalloc": (lambda **k: b.gemm_skinny_noalloc(A, B, **k), 1),
+        "gemm_bf16_e2m1": (lambda **k: b.gemm_bf16_e2m1(A, q, s, **k), 1),
+        "gemm_e2m1": (lambda **k: b.gemm_e2m1(q, s, q, s, **k), 1),
+        "gemm_gated": (lambda **k: b.gemm_gated(A, B, B, **k), 1),
+        "gemm_gated_e2m1": (lambda **k: b.gemm_gated_e2m1(q, s, q, s, q, s, **k), 1),
+        "gemm_gated_backward": (lambda **k: b.gemm_gated_backward(G, G, G, A, B, B, **k), 5),
+        "gemm_trans": (lambda **k: b.gemm_trans(A, B, **k), 1),
+        "gemm_quantize_e2m1": (lambda **k: b.gemm_quantize_e2m1(A, **k), 2),
+        "gemm_group_rows": (lambda **k: b.gemm_group_rows(off, 3, **k), 3),
+        "gemm_grouped": (lambda **k: b.gemm_grouped(A, W, off, **k), 1),
+        "gemm_grouped_weights": (lambda **k: b.gemm_grouped_weights(A, A, off, **k), 1),
+        "gemm_orthogonalize": (lambda **k: b.gemm_orthogonalize(A, **k), 1),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_new_outputs_belong_to_the_stream_of_the_call(monkeypatch, name):
+    """torch gives a stream's freed memory to that stream again while its kernels may still use it: an
+    output that another stream writes has to come from that stream's memory."""
+    call, count = _calls()[name]
+
+    class Stream:
+        cuda_stream = 0x70
+
+    class Context:
+        def __enter__(self):
+            where.append(stream)
+
+        def __exit__(self, *_):
+            where.pop()
+
+    class Library:
+        def __getattr__(self, entry):
+            return lambda *args: used.append(args[-1]) or 0
+
+    stream, where, made, used = Stream(), [None], [], []
+    monkeypatch.setattr(binding, "load_library", lambda: Library())
+    monkeypatch.setattr(binding, "_on_device", lambda *t: None)
+    monkeypatch.setattr(binding, "_on_stream", lambda s: Context() if s is stream else pytest.fail("another stream"))
+    for made_by in ("empty", "empty_strided"):
+        real = getattr(torch, made_by)
+        monkeypatch.setattr(torch, made_by, lambda *a, real=real, **k: made.append(where[-1]) or real(*a, **k))
+    call(stream=stream)
+    assert made == [stream] * count and used == [stream.cuda_stream]
