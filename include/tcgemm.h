@@ -545,7 +545,10 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *  idx               NULL, or M int32 rows of A, read for rows of a group only; they may
  *                    repeat.  An index outside [0, a_rows) makes its row zero and records
  *                    GEMM_ERR_INDEX.  (Larger calls first lay the rows out in order, in a kept
- *                    workspace of M x K elements, rows padded to 64, up to 8 GiB.)
+ *                    workspace of M x K elements, rows padded to 64, its size a power of two:
+ *                    per device and stream up to 8 GiB, with outgrown ones less than 16.  Where
+ *                    that is too little or cannot be had, the product gathers them itself: the
+ *                    same results, at large M and K up to three times the time.)
  *  B, ldb, stride_b  `groups` matrices, ldb a multiple of 8, the starts of consecutive ones
  *                    stride_b elements apart (a multiple of 8, no less than a matrix).
  *  D, ldd, out       M x N as gemm_f16; must not overlap A, B, idx or offsets.
@@ -701,7 +704,8 @@ gemm_status gemm_set_wait_timeout(uint64_t ns);
  * Test hook.  mode 1: the next launches add 16 bytes to the transaction
  * count the first shared-memory stage expects, so that stage never completes
  * and its bounded wait runs out (all copies still land; nothing faults).
- * mode 0 turns it off.
+ * mode 2: the library gets no further device memory (it asks for none; buffers
+ * it already keeps are used).  mode 0 turns either off.
  */
 gemm_status gemm_debug_inject(int mode);
 

@@ -109,6 +109,8 @@ namespace {
 // no part.
 gemm_status new_buffer(size_t bytes, bool zeroed, void **out)
 {
+    if (g_inject.load() == 2)  // (as if there were no memory)
+        return GEMM_ERR_CUDA;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess)
         return GEMM_ERR_CUDA;
@@ -127,8 +129,10 @@ gemm_status new_buffer(size_t bytes, bool zeroed, void **out)
             cudaFree(p);
     }
     cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess) {
+        cudaGetLastError();  // (it is this call's answer, not the next launch's)
         return GEMM_ERR_CUDA;
+    }
     *out = p;
     return GEMM_OK;
 }
@@ -1217,7 +1221,7 @@ gemm_status gemm_debug_force_tile(int kernel, int bn)
 
 gemm_status gemm_debug_inject(int mode)
 {
-    if (mode != 0 && mode != 1)
+    if (mode < 0 || mode > 2)
         return GEMM_ERR_INVALID_ARG;
     g_inject.store(mode);
     return GEMM_OK;

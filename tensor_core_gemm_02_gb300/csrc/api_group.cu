@@ -180,7 +180,7 @@ Few choose_few(int64_t M, int64_t N, int64_t K, int64_t groups, int sm_count)
 // order first: 16384 rows, 4096 x 4096 1038 / 326; 8 x 500, 4096 x 512 47.5 / 27.3; 777 rows, 2743 x 1000
 // 30.8 / 19.1; 60 groups of 163, 5489 x 118 175 / 55; 43 of 4, 8640 x 298 71 / 44; 8 of 4, 14336 x 4096
 // 146.4 / 144.5.)
-constexpr int64_t kGatheredBytes = int64_t(8) << 30;  // (more is not kept for them)
+constexpr int64_t kGatheredBytes = int64_t(8) << 30;  // of a buffer for them, at most
 bool gather_first(int64_t M, int64_t K, const GForm &f, const Few &few, int64_t waves)
 {
     if (ceil_div(K, 64) * 128 > kGatheredBytes / M)
@@ -188,6 +188,16 @@ bool gather_first(int64_t M, int64_t K, const GForm &f, const Few &few, int64_t 
     const int64_t block_ns = f.block_ns < 32 * 36 ? 32 * 36 - f.block_ns : 0;
     const int64_t own_ns = few.mp ? waves * 1500 : waves * ceil_div(K, 64) * block_ns;
     return own_ns > 4000 + M * K / 1250;
+}
+
+// The buffer's size for so many bytes (kGatheredBytes at most): the next power of two.  A larger call then finds
+// a buffer of its own size or gets one twice as large, and none is larger than kGatheredBytes.
+size_t gathered_size(int64_t bytes)
+{
+    size_t size = 1 << 20;
+    while (size < static_cast<size_t>(bytes))
+        size *= 2;
+    return size;
 }
 
 bool bad_flag(int f) { return f != 0 && f != 1; }
@@ -296,14 +306,16 @@ gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dt
     GroupArgs g;
     fill_group(g, bf16, out, dev);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool first = idx && K > 0 && gather_first(M, K, f, few, waves);
+    bool first = idx && K > 0 && gather_first(M, K, f, few, waves);
     std::unique_lock<std::mutex> hold;
+    const int64_t ldw = ceil_div(K, 64) * 64;
+    void *w = nullptr;
     if (first) {
-        const int64_t ldw = ceil_div(K, 64) * 64;
-        void *w = nullptr;
         hold = std::unique_lock<std::mutex>(buffer_mutex(dev->index, cs));
-        if ((st = get_dequant_buffer(dev->index, cs, kBufGathered, static_cast<size_t>(M * ldw) * 2, &w)) != GEMM_OK)
-            return st;
+        // (where there is no memory for them, the product gathers the rows itself)
+        first = get_dequant_buffer(dev->index, cs, kBufGathered, gathered_size(M * ldw * 2), &w) == GEMM_OK;
+    }
+    if (first) {
         if (tcg::launch_group_gather(A, static_cast<int32_t>(rows), lda, idx, offsets, static_cast<int32_t>(groups),
                                      static_cast<int32_t>(M), static_cast<int32_t>(K), w, ldw, g.status,
                                      dev->sm_count, cs) != cudaSuccess)

@@ -314,6 +314,48 @@ def test_gathered_rows_replayed_after_a_larger_call():
     assert torch.equal(larger, binding.gemm_grouped(A[idx.long()].contiguous(), B, off))
 
 
+def test_gathered_rows_without_memory_for_them():
+    """Where the workspace cannot be had the product gathers the rows itself: the same bits, also
+    captured, and the calls after it have the workspace again.  (A stream of its own, which keeps
+    none yet.)"""
+    call, s, graph = _gathered(0), torch.cuda.Stream(priority=-1), torch.cuda.CUDAGraph()
+    want, X = call().clone(), torch.randn((2, 300, 200), device="cuda")
+    torch.cuda.synchronize()
+    binding.gemm_debug_inject(2)
+    with torch.cuda.stream(s):
+        got = call()
+        with pytest.raises(binding.GemmError):
+            binding.gemm_orthogonalize(X)  # (which has no other way)
+    with torch.cuda.graph(graph, stream=s):
+        kept = call()
+    binding.gemm_debug_inject(0)
+    graph.replay()
+    with torch.cuda.stream(s):
+        again = call()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(kept, want) and torch.equal(again, want)
+
+
+def test_memory_kept_for_gathered_rows():
+    """A call of 5 GiB and one of 7.9 keep 8 GiB between them."""
+    M, N = 1 << 20, 512
+    idx = torch.randint(0, 50, (M,), dtype=torch.int32, device="cuda")
+    off, D = torch.tensor([0, M], dtype=torch.int32, device="cuda"), torch.empty((M, N), dtype=BF16, device="cuda")
+    operands = [(quarters((50, K), K), quarters((1, N, K), 1)) for K in (2560, 4032)]
+    s, free = torch.cuda.Stream(priority=-1), []
+    for A, B in operands:
+        want = (A.double() @ B[0].double().T).to(BF16)[idx.long()]
+        torch.cuda.synchronize()
+        free.append(torch.cuda.mem_get_info()[0])
+        binding.gemm_grouped(A, B, off, D, idx=idx, out=binding.OUT_BF16, stream=s)
+        torch.cuda.synchronize()
+        free.append(torch.cuda.mem_get_info()[0])
+        assert torch.equal(D, want)
+        del want
+    taken = (free[0] - free[1]) + (free[2] - free[3])
+    assert 7 << 30 < taken < (8 << 30) + (64 << 20), taken
+
+
 @pytest.mark.parametrize("what", ["_ortho", "_sort", "_grouped"])
 def test_first_call_of_a_process_inside_a_capture_on_a_new_thread(what):
     code = textwrap.dedent(f"""

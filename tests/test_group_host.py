@@ -196,3 +196,7 @@ def test_new_outputs_belong_to_the_stream_of_the_call(monkeypatch, name):
         monkeypatch.setattr(torch, made_by, lambda *a, real=real, **k: made.append(where[-1]) or real(*a, **k))
     call(stream=stream)
     assert made == [stream] * count and used == [stream.cuda_stream]
+
+
+def test_inject_modes(lib):
+    assert [lib.gemm_debug_inject(m) for m in (2, 1, 3, -1, 0)] == [0, 0, 1, 1, 0]
