@@ -369,11 +369,11 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
     auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
-    // (C by TMA) epilogue warp w's buffer j holds its piece of C
     // (CS = 2) the other CTA's sums of warp q's rows are there / have been read (arrives at
     // the writer)
     auto redf_bar = [&](uint32_t q) { return bar0 + 8u * (3 * STAGES + 4 + q); };
     auto rede_bar = [&](uint32_t q) { return bar0 + 8u * (3 * STAGES + 8 + q); };
+    // (C by TMA) epilogue warp w's buffer j holds its piece of C
     auto c_bar = [&](uint32_t w, uint32_t j) { return bar0 + 8u * (3 * STAGES + 4 + 2 * w + j); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 8 * Cfg::NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
         return p;
     };
     const int32_t k_blocks = (args.K + Cfg::BK - 1) / Cfg::BK;
-    // (CS = 2) this CTA's K blocks of a tile: from kb_first, kb_mine of them
+    // (CS = 2) this CTA's K blocks of a tile: from kb_first, kb_mine of them (not 0: sums of fewer
+    // than eight blocks are not shared)
     const int32_t kb_first = CS == 2 ? static_cast<int32_t>(share) * (k_blocks / 2) : 0;
     const int32_t kb_mine = CS == 2 ? (share == 0u ? k_blocks / 2 : k_blocks - k_blocks / 2) : k_blocks;
     // (KIND_SUM) A partial block is loaded this many blocks before the end of its tile and
@@ -1139,10 +1140,9 @@ __global__ void __launch_bounds__(GroupCfg<BN, STAGES, PAIR, KIND, PREC, CS>::TH
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        // (one K block: all of it the second CTA's)
-                        const float lo = nkb > 0 ? sums[i] : 0.f, hi = nkb > 0 ? sums[32 + i] : 0.f;
-                        st_shared_cluster_u32(to + 128u * static_cast<uint32_t>(i), __float_as_uint(share ? lo : hi));
-                        v[i] = share ? hi : lo;
+                        st_shared_cluster_u32(to + 128u * static_cast<uint32_t>(i),
+                                              __float_as_uint(share ? sums[i] : sums[32 + i]));
+                        v[i] = share ? sums[32 + i] : sums[i];
                     }
                     __syncwarp();
                     if (lane == 0)

@@ -198,6 +198,14 @@ def test_zeros_whatever_eps(m, n, eps):
     assert torch.isnan(binding.gemm_orthogonalize(X, eps=0.0)[1]).all()
 
 
+@pytest.mark.parametrize("count,m,n", [(2, 448, 449), (1, 449, 512), (2, 512, 448), (1, 513, 449)])
+def test_sums_at_the_length_that_two_ctas_share(count, m, n):
+    """Seven, eight and nine blocks of 64: sums of eight and more are shared where that form is forced."""
+    binding.gemm_debug_force_tile(3, 256)
+    check(stack(count, m, n, torch.float32, m + n), MUON, 1)
+    check(stack(count, m, n, torch.bfloat16, m + n), MUON, 2, torch.float32)
+
+
 def test_same_bits_every_time():
     X = stack(5, 300, 200, torch.bfloat16, 8)
     a = binding.gemm_orthogonalize(X)
