@@ -135,6 +135,30 @@ def test_singular_values_reach_one():
     assert (torch.linalg.svdvals(y) - 1).abs().max() < 16 * 2.0 ** -11
 
 
+# Near orthogonal rows (P = I, a + b + c = 1, slope 0) the last step alone moves a singular value: what P's sum
+# drops, at most sum_bound(l) of its diagonal, by |b + 2 c|; what P P's and the update's drop, sum_bound(s), by c
+# and |b + c|; the operands' 22 bits and the last rounding, 2^-22 each, at most six times together.  For QUINTIC
+# and 96 x 200: 5.5e-6; errors of no common sign across a row average out, the rest of 1e-5 is for them.
+SINGULAR = 1e-5
+
+
+def test_singular_values_follow_the_recurrence():
+    """A float32 result's singular values against those of the recurrence in 64 bits: with the products X X^T and
+    b P + c P^2 in one float16 they are off by 2e-4 (test_orthogonalize_bounds.py plants that)."""
+    x = spread_matrix()
+    want = torch.linalg.svdvals(recurrence(x, QUINTIC, 14, EPS, torch.float32)[0])
+    y = binding.gemm_orthogonalize(x.cuda(), steps=14, coefs=QUINTIC).cpu().double()
+    assert (torch.linalg.svdvals(y) - want).abs().max() < SINGULAR
+
+
+def spread_matrix():
+    """96 x 200 with singular values from 0.1 to 1."""
+    gen = torch.Generator().manual_seed(0)
+    u, _ = torch.linalg.qr(torch.randn(96, 96, generator=gen, dtype=torch.float64))
+    v, _ = torch.linalg.qr(torch.randn(200, 96, generator=gen, dtype=torch.float64))
+    return ((u * torch.linspace(0.1, 1.0, 96, dtype=torch.float64)) @ v.T).float()
+
+
 @pytest.mark.parametrize("scale", [1e-12, 1e-3, 1.0, 1e6])
 def test_scales(scale):
     """The norm is divided out: small and large matrices alike."""
