@@ -310,6 +310,9 @@ def _bf16_flag(name, dtype) -> int:
     return 0
 
 
+_MAX_DIM = (1 << 31) - 1  # elements of a dimension or a pitch
+
+
 def _mat(name, t, rows, cols, dtype):
     """(pointer, leading dimension) of a rows x cols matrix argument of that dtype."""
     if t.dtype is not dtype:
@@ -320,7 +323,7 @@ def _mat(name, t, rows, cols, dtype):
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows < 2 or not cols:  # (one row: its pitch says nothing; no columns: not used)
-        ld = max(ld, cols) if cols else 0
+        ld = (max(ld, cols) if ld <= _MAX_DIM else (cols + 7) // 8 * 8) if cols else 0
     return t.data_ptr(), ld
 
 
@@ -499,6 +502,8 @@ def _stack(name, t, depth, rows, cols, dtype):
         raise ValueError(f"{name} must have unit column stride")
     if rows < 2 or not cols:  # (one row: its pitch says nothing; no columns: not used)
         ld = (max(ld, cols) + 7) // 8 * 8 if depth < 2 or not cols else max(stride, ld, cols)
+        if ld > _MAX_DIM:
+            ld = (cols + 7) // 8 * 8
     return t.data_ptr(), ld, stride
 
 

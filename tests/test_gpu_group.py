@@ -387,6 +387,18 @@ def test_elements_past_32_bits(form):
     assert torch.equal(binding.gemm_grouped_weights(dD, rows, off, out=binding.OUT_F16), wantB)
 
 
+def test_weights_of_one_row_far_apart():
+    gen = torch.Generator().manual_seed(3)
+    far, off = (1 << 31) + 8, offsets_of([30, 5, 45], 0)
+    A, dD, small = wide(80, 136, F16, gen), wide(80, 1, F16, gen), stack(3, 1, 136, F16, gen, True)
+    B = torch.empty(2 * far + 136, dtype=F16, device="cuda").as_strided((3, 1, 136), (far, far, 1))
+    B.copy_(small)
+    assert torch.equal(binding.gemm_grouped(A, B, off), binding.gemm_grouped(A, small, off))
+    want = binding.gemm_grouped_weights(dD, A, off, out=binding.OUT_F16)
+    binding.gemm_grouped_weights(dD, A, off, B, out=binding.OUT_F16)
+    assert torch.equal(B, want)
+
+
 def test_gradients_against_differences():
     """dA and dB of sum(dD * D) against central differences of the product itself, which is linear in
     each operand: on quarter-integers both are exact."""

@@ -256,6 +256,19 @@ def test_elements_past_32_bits():
     assert torch.equal(big, want)
 
 
+def test_single_rows_far_apart():
+    """Matrices of one row, further apart than the largest pitch."""
+    X, far = stack(3, 1, 70, torch.bfloat16, 4), (1 << 31) + 8
+    big = torch.empty(2 * far + 70, dtype=torch.bfloat16, device="cuda").as_strided((3, 1, 70), (far, far, 1))
+    for form in ((0, 0), (1, 64)):
+        binding.gemm_debug_force_tile(*form)
+        want = binding.gemm_orthogonalize(X, steps=2)
+        big.copy_(X)
+        assert torch.equal(binding.gemm_orthogonalize(big, steps=2), want)
+        binding.gemm_orthogonalize(X, big, steps=2)
+        assert torch.equal(big, want)
+
+
 @pytest.mark.parametrize("form", [(1, 64), (1, 128), (3, 256), (0, 0)])
 @pytest.mark.parametrize("count,m,n", [(3, 700, 900), (2, 1100, 380), (1, 2000, 1030)])
 def test_more_tiles_than_ctas_hold(form, count, m, n):

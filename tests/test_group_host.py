@@ -200,3 +200,15 @@ def test_new_outputs_belong_to_the_stream_of_the_call(monkeypatch, name):
 
 def test_inject_modes(lib):
     assert [lib.gemm_debug_inject(m) for m in (2, 1, 3, -1, 0)] == [0, 0, 1, 1, 0]
+
+
+@pytest.mark.parametrize("depth", [1, 3])
+def test_single_rows_far_apart(depth):
+    """The pitch of a matrix of one row is made up: it does not pass the limit of pitches (2^31 - 1) where the
+    matrices, or a slice's rows, lie further apart than that."""
+    far = (1 << 31) + 8
+    x = torch.empty_strided((depth, 1, 20), (far, far, 1), dtype=torch.bfloat16, device="meta")
+    _, ld, stride = binding._stack("x", x, depth, 1, 20, torch.bfloat16)
+    assert ld == 24 and stride == far
+    if depth == 1:
+        assert binding._mat("x", x[0], 1, 20, torch.bfloat16)[1] == 24
