@@ -230,6 +230,21 @@ def test_sums_at_the_length_that_two_ctas_share(count, m, n):
     check(stack(count, m, n, torch.bfloat16, m + n), MUON, 2, torch.float32)
 
 
+def test_iterates_past_their_range():
+    """An element of 16 and more between the steps is not finite in Y; the other matrices of the stack
+    are not concerned, nor is the last step's result."""
+    X = stack(3, 300, 200, torch.float32, 6)
+    good = binding.gemm_orthogonalize(X, steps=2)
+    X[1] = 0
+    X[1, 7, 9] = 5.0
+    Y = binding.gemm_orthogonalize(X, steps=2, coefs=(1.0, -0.5, 0.0))
+    assert torch.isfinite(Y).all()
+    assert not torch.isfinite(binding.gemm_orthogonalize(X, steps=2, coefs=(20.0, -0.5, 0.0))[1, 7, 9])
+    one = binding.gemm_orthogonalize(X, steps=1, coefs=(20.0, -0.5, 0.0))
+    assert abs(one[1, 7, 9].item() - 19.5) < 1e-4
+    assert torch.equal(binding.gemm_orthogonalize(X, steps=2)[::2], good[::2])
+
+
 def test_same_bits_every_time():
     X = stack(5, 300, 200, torch.bfloat16, 8)
     a = binding.gemm_orthogonalize(X)
