@@ -556,6 +556,9 @@ gemm_status gemm_group_rows(int64_t M, int64_t groups, int64_t choices, const in
  *  Sums are float32, multiplied by alpha (mul.rn) and rounded once; the same bits every time.
  *  (Of float32 results the sums are added up in registers, rounded to nearest, every 512 of
  *  K; of the others in the tensor cores' accumulators throughout.)
+ *  The kernel is chosen by the average number of rows of a group, M / min(groups, M), since the
+ *  host does not know the offsets: where a few of many groups have nearly all rows, a call
+ *  may run as if for few rows, right but slower.
  *  Other errors and execution as gemm_f16.
  */
 gemm_status gemm_grouped(int64_t M, int64_t N, int64_t K, int64_t groups, int dtype_is_bf16,
@@ -605,13 +608,14 @@ gemm_status gemm_grouped_weights(int64_t M, int64_t N, int64_t K, int64_t groups
  *  for one) in every step of a float32 Y, in the last one of a float16 Y, and in two more,
  *  also of a bfloat16 Y, where min(M, N) < 256.  All are scaled by 2^12: the elements of the
  *  iterates, of P and of b P + c P^2 have to stay below 16, as they do where the singular
- *  values stay below 2.  The last step is rounded once, to Y's type.
+ *  values stay below 2 (past that Y gets infinities or NaN, and no error is recorded).  The last
+ *  step is rounded once, to Y's type.
  *  (Small matrices, min(M, N) <= 64 and what fits shared memory, where one launch for all
  *  steps is faster: float32 throughout, no workspace.)
  *  A matrix with an infinity or a NaN gives NaN; one of zeros gives zeros if eps > 0.
- *  Workspace: per device and stream, up to 1 GiB or one matrix's (8 M N + 8 min(M, N)^2
- *  bytes, rows padded to 64 elements) if that is more, and some MB for long sums of few tiles, kept as the other
- *  workspaces are.
+ *  Workspace: a call takes up to 1 GiB or one matrix's (8 M N + 8 min(M, N)^2 bytes, rows
+ *  padded to 64 elements) if that is more, and some MB for long sums of few tiles.  It is kept per
+ *  device and stream, and grows, as the other workspaces do.
  *  Other errors and execution as gemm_f16 (2 + 3 steps kernels, with long sums of few
  *  tiles 2 + 4 steps, more for a large stack).
  */

@@ -606,7 +606,8 @@ def gemm_orthogonalize(X, Y=None, *, steps=5, coefs=(3.4445, -4.7750, 2.0315), e
     """Newton-Schulz steps on X (M x N, or a stack count x M x N; float32, bf16 or f16): X / (|X| + eps),
     then `steps` times X <- a X + (b P + c P @ P) X with P = X @ X.T and (a, b, c) = coefs,
     which move the singular values towards 1.  Y has X's shape and, unless given, its dtype;
-    Y may be X.  Returns Y."""
+    Y may be X.  Returns Y.  (Steps that let singular values grow past 2 may give infinities or
+    NaN: between steps the iterates are held in float16, in two parts.)"""
     kind = _OUT_OF_DTYPE.get(X.dtype)
     if kind is None:
         raise TypeError("X must be float32, bfloat16 or float16")

@@ -158,7 +158,8 @@ Span span_of(const Stack &s)
 // 64 rows, 8 x 14336 x 4096 of 4 141 / 137 / 138, of 12 143 / 139 / 140, of 24 154 / 141 / 141, of 40 183 /
 // 159 / 142 (the tile kernel 143 to 149); 2 x 2816 x 1024 of 1 6.4 / 6.7 / 7.9 (9.0).  One / two CTAs a tile:
 // 2 x 4096 x 14336 (64 tiles) 42.7 / 39.2, 2 x 14336 x 4096 (224) 39.0 / 39.1, 2 x 2816 x 1024 (44) 6.4 / 6.7,
-// 32 x 2816 x 1024 (704) 31.6 / 39.0: two where they have SMs of their own and a long sum to share.
+// 32 x 2816 x 1024 (704) 31.6 / 39.0: two where they have SMs of their own and a long sum to share.  (Each list of
+// one run; from one GPU to another they differ by up to 4 %.)
 struct Few {
     int mp, cs;
 };

@@ -40,8 +40,8 @@
 // protocol is the tile kernel's (kernel_tile.cuh).  Every wait is bounded.
 //
 // Bounds and figures.  KIND_ROWS and KIND_SUM of long sums are bound by the tensor cores under
-// the power cap (16384 rows in eight uneven groups, 14336 x 4096 bf16: 1.19 to 1.22 ms forward,
-// 1.24 to 1.27 the input's gradient, 1.20 the weights'; 1.5 to 1.6 PFLOP/s; tensor pipe active 92, 90
+// the power cap (16384 rows in eight uneven groups, 14336 x 4096 bf16: 1.19 to 1.20 ms forward,
+// 1.25 to 1.26 the input's gradient, 1.20 to 1.22 the weights'; 1.5 to 1.6 PFLOP/s; tensor pipe active 90, 87
 // and 82 % of cycles), of short ones by the results' way out (eight groups
 // of 128 rows: 940 MB of bf16 gradients 224 us, float32 1.9 GB 290).  KIND_BATCH likewise: 4096 x
 // 4096 x 14336, half of a symmetric product 148 us, the update 290 (1.66 and 1.65 PFLOP/s); where

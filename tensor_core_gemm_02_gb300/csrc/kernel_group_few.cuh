@@ -18,10 +18,10 @@
 // on in the other.  (Positive operands, relative error, one accumulator / emptied: K of 14336 4.6e-5 / 3.0e-6,
 // 57344 1.9e-4 / 3.1e-6.)  For results of 16 bits one accumulator takes an issuer's whole share.
 //
-// Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 138 us (6.8 TB/s), two of one row 39 (6.0 TB/s; the
-// tile kernel 65); 2 of 64 groups, 2816 x 1024 6.4 us (launch, offsets, first loads, epilogue).  More
-// rows: 64 a group 161 against the tile kernel's 163, 100 of 2816 x 1024 91 against 84, hence the
-// change at 48.
+// Bound by HBM: 8 groups of 4 rows, 14336 x 4096 bf16 141 to 143 us (6.6 TB/s; float32 143 to 144), two of one
+// row 40 to 43 (5.4 to 5.8 TB/s; the tile kernel 83); 2 of 64 groups, 2816 x 1024 7.1 us (launch, offsets,
+// first loads, epilogue).  More rows, bf16: 48 a group of 8 x 14336 x 4096 146 against the tile kernel's 152, 64 148
+// against 151, 100 of 8 x 2816 x 1024 17.6 against 14.8, hence the change at 48.
 //
 //   warp 0     producer: per stage two K blocks of B (boxes of 64 x 128, or stored K x N two
 //              boxes of 64 x 64) and of A (a box of MP rows, or MP / 4 tile::gather4)
