@@ -432,3 +432,13 @@ def test_a_wait_that_runs_out(form):
         X = torch.randn((2, 300, 290), device="cuda").to(dtype)
         want = binding.gemm_orthogonalize(X, steps=1)
         assert torch.equal(_timed_out(lambda: binding.gemm_orthogonalize(X, steps=1)), want)
+
+
+@pytest.mark.parametrize("out", [binding.OUT_F32, binding.OUT_BF16])
+@pytest.mark.parametrize("counts,N", [([3, 0, 5, 1], 200), ([1] * 80, 8)])
+def test_a_wait_that_runs_out_in_a_long_sum(counts, N, out):
+    """Few rows, sums of many fills of the accumulators, on two CTAs a tile and on one."""
+    A, B = quarters((sum(counts), 14336), 1), quarters((len(counts), N, 14336), 2)
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    want = binding.gemm_grouped(A, B, off, out=out)
+    assert torch.equal(_timed_out(lambda: binding.gemm_grouped(A, B, off, out=out)), want)
